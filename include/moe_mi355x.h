@@ -29,7 +29,8 @@
  *     for moe_last_error() (per calling thread); nothing was enqueued.
  *     A launch failure reported by the HIP runtime returns MOE_ERR_HIP.
  *   - Device contents are not validated: expert ids must lie in [0, E) and
- *     logits must be finite, otherwise results are undefined.
+ *     logits must be finite, otherwise results are undefined (the calls that
+ *     take masked logits or ids out of range say so).
  *   - Determinism: identical inputs, shapes and device give byte-identical
  *     outputs.  No kernel accumulates floating point values with atomics.
  *   - All device pointers must be 16-byte aligned.
@@ -57,6 +58,9 @@ typedef enum {
 typedef enum {
   MOE_BF16 = 0,   /* BF16 activations and weights                         */
   MOE_MXFP8 = 1,  /* E4M3 codes with one E8M0 scale per 32 along K          */
+  MOE_INT8 = 2,   /* INT8 codes with one FP32 scale per row: an output type of
+                     moe_add_rmsnorm; the batched calls do not take it
+                     (moe_experts_int8 is the INT8 form of the layer)        */
   /* not element types: they make the enum span every int, so that an unknown
    * value passed by a caller is a valid value of the type that the library
    * rejects (MOE_ERR_SHAPE) rather than undefined behaviour in C++ */
@@ -325,6 +329,157 @@ int moe_backward_batched_mxfp8(const uint16_t* x, const uint8_t* w_gate_up,
 size_t moe_backward_mxfp8_workspace_bytes(int T, int H, int I, int E, int k);
 
 /*
+ * moe_add_rmsnorm -- residual sum and root-mean-square norm in front of the
+ * layer, with the output in the form that the experts read.
+ *
+ *   s = bf16(x + residual)   (s = x without a residual)
+ *   y = s * w / sqrt(mean over H of s^2 + eps)
+ * in FP32 from the stored (rounded) s; each output is rounded once from FP32, the
+ * 8-bit codes not through BF16.
+ *
+ *   x            [T, H] BF16
+ *   residual     [T, H] BF16, or NULL
+ *   weight       [H] BF16
+ *   residual_out [T, H] BF16 out: s; NULL: not kept.  Needs a residual.
+ *   y            [T, H] BF16 out; may be NULL if qtype asks for codes
+ *   qtype        MOE_BF16: no 8-bit output (codes and scales are ignored);
+ *                MOE_MXFP8: codes [T, H] E4M3, scales [T, H/32] E8M0 of y by the
+ *                rule of moe_quantize_mxfp8; MOE_INT8: codes [T, H] int8, scales
+ *                [T] float of y by the rule of moe_quantize_int8
+ * In place: residual_out may be x or residual, and y may be x or residual (the
+ * same pointer, not an overlap), but not both the same one; nothing else may
+ * overlap.
+ * Limits: T >= 0 (0 enqueues nothing), H a multiple of 32, 32 <= H <= 16384, eps
+ * finite and above 0.  A row with a non-finite value, or whose squares' sum leaves
+ * FP32 (magnitudes of 1e17 and more), has undefined contents; other rows are not
+ * affected.
+ */
+int moe_add_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int T,
+                    int H, float eps, uint16_t* residual_out, uint16_t* y, moe_dtype qtype,
+                    void* codes, void* scales, void* stream);
+
+/*
+ * moe_add_rmsnorm_backward -- gradients of moe_add_rmsnorm for sum(dy * y) +
+ * sum(ds * s), BF16 (the 8-bit outputs take the gradient of the y that they
+ * stand for).
+ *
+ *   s       [T, H] BF16: residual_out of the forward (x if it had no residual)
+ *   weight  [H] BF16
+ *   dy      [T, H] BF16
+ *   ds      [T, H] BF16: the gradient that reaches residual_out from elsewhere, or NULL
+ *   dx      [T, H] BF16 out: the gradient of s, which is that of x and that of
+ *           residual; may be dy or ds (the same pointer)
+ *   dweight [H] BF16 out: summed over the rows in FP32 in a fixed order (zeros for T = 0)
+ *   workspace >= moe_add_rmsnorm_backward_workspace_bytes(T, H) bytes, contents ignored
+ * Limits as for moe_add_rmsnorm.
+ */
+int moe_add_rmsnorm_backward(const uint16_t* s, const uint16_t* weight, const uint16_t* dy,
+                             const uint16_t* ds, int T, int H, float eps, uint16_t* dx,
+                             uint16_t* dweight, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+size_t moe_add_rmsnorm_backward_workspace_bytes(int T, int H);
+
+/*
+ * moe_route_scored -- top-k expert routing by scores, beside moe_route_topk.
+ *
+ *   p_e = exp(l_e) / sum exp(l)  (MOE_SCORE_SOFTMAX)  or  1 / (1 + exp(-l_e))  (MOE_SCORE_SIGMOID)
+ *   c_e = p_e + bias_e                       (the bias steers the choice only)
+ *   The E experts form n_groups consecutive groups of E / n_groups.  A group scores
+ *   the sum of its group_top (1 or 2) largest c; the topk_groups groups with the
+ *   largest score (ties: the lower group) take part.
+ *   Slots: the k largest c among their experts, c descending, index ascending.
+ *   topk_w = scale * p / (renormalize ? sum of the k selected p : 1)
+ *
+ * The choice is made on exact comparisons: without a bias on the FP32 logits
+ * themselves (as moe_route_topk; -0 and +0 tie), with one on c in FP64; group
+ * scores are FP64.  The weights are FP32.
+ *
+ *   logits   [T, E] float32.  A logit of -3.3895e38 (BF16's lowest finite value) or
+ *            less, -inf or NaN masks the expert: p = 0, it adds nothing to a group's
+ *            score, and it is selected (weight 0, lowest index first) only where
+ *            fewer than k experts of the selected groups take part.  A group with
+ *            no expert that takes part ranks last.  +inf counts as FLT_MAX.
+ *            Weights whose selected scores sum to 0 are 0.
+ *   bias     [E] float32, or NULL; no NaN or +inf
+ *   topk_idx [T, k] int32 out, always within [0, E) and distinct within a row
+ *   topk_w   [T, k] float32 out
+ * Limits: T >= 0 (0 enqueues nothing), E <= 1024, 1 <= k <= 32, n_groups <= 64 and
+ * a divisor of E, 1 <= topk_groups <= n_groups, k <= topk_groups * (E / n_groups),
+ * scale finite.
+ */
+typedef enum {
+  MOE_SCORE_SOFTMAX = 0,
+  MOE_SCORE_SIGMOID = 1,
+  MOE_SCORE_RANGE_MIN_ = -0x7FFFFFFF - 1,   /* as in moe_dtype: any int is a value of the type */
+  MOE_SCORE_RANGE_MAX_ = 0x7FFFFFFF
+} moe_score;
+
+int moe_route_scored(const float* logits, const float* bias, int T, int E, int k, int n_groups,
+                     int topk_groups, int group_top, moe_score score, int renormalize, float scale,
+                     int32_t* topk_idx, float* topk_w, void* stream);
+
+/*
+ * moe_route_scored_backward -- gradient of topk_w with the selection held fixed
+ * (as moe_backward_batched, whose d_topk_w it takes):
+ *   dlogits[t, e] = sum over slots j of d_topk_w[t, j] * d topk_w[t, j] / d l_e
+ * Softmax scores without renormalisation reach every expert that takes part; the
+ * others reach the selected experts only.  The bias has no gradient.
+ *
+ *   logits, topk_idx   as given to and returned by moe_route_scored (a masked
+ *                      expert gets 0; ids outside [0, E) are ignored)
+ *   d_topk_w [T, k] float32
+ *   dlogits  [T, E] float32 out, every element
+ * Limits: T >= 0 (0 enqueues nothing), E <= 1024, 1 <= k <= min(E, 32), scale finite.
+ */
+int moe_route_scored_backward(const float* logits, const int32_t* topk_idx, const float* d_topk_w,
+                              int T, int E, int k, moe_score score, int renormalize, float scale,
+                              float* dlogits, void* stream);
+
+/*
+ * moe_quantize_int8 -- INT8 codes of a BF16 matrix, one FP32 scale per row.
+ *
+ *   src    [rows, K] BF16
+ *   codes  [rows, K] int8 out: v * (127 / amax) rounded to nearest even, in [-127, 127]
+ *   scales [rows] float out: amax / 127, amax = max |v| of the row
+ * A row whose magnitudes all lie below 2^-100 takes scale 0 and codes 0.
+ * Limits: 0 <= rows < 2^29, K a multiple of 32, 32 <= K <= 16384.
+ */
+int moe_quantize_int8(const uint16_t* src, int64_t rows, int K, int8_t* codes, float* scales,
+                      void* stream);
+
+/*
+ * moe_experts_int8 -- the layer's expert products in 8-bit integers with scales
+ * for each token and output channel, from routed INT8 activations to the weighted
+ * sum, for any number of tokens.
+ *
+ *   g, u  = x_scales[t] * w_gate_up_scales[e, n] * (x[t] . w_gate_up[e, n])
+ *   a     = silu(g) * u                     (FP32, not rounded)
+ *   hq,sh = INT8 codes and scale of a by the rule of moe_quantize_int8
+ *   y     = sh * w_down_scales[e, n] * (hq . w_down[e, n])
+ *   out[t] = sum over slots j = 0..k-1, in that order, of topk_w[t, j] * y[t, j]
+ * with exact INT32 dot products; the rest FP32, out rounded once to BF16.
+ *
+ *   x         [T, H] int8,  x_scales [T] float         (moe_quantize_int8, moe_add_rmsnorm)
+ *   w_gate_up [E, 2I, H] int8, rows [0, I) gate and [I, 2I) up;  w_gate_up_scales [E, 2I] float
+ *   w_down    [E, H, I] int8;  w_down_scales [E, H] float
+ *   topk_idx, topk_w [T, k].  A slot whose id lies outside [0, E) (an expert held
+ *             elsewhere, a padded token) adds nothing; a token without any other
+ *             slot gets zeros.
+ *   out       [T, H] BF16 out
+ *   workspace >= moe_experts_int8_workspace_bytes(T, H, I, E, k), contents ignored
+ * Limits: T >= 0 (0 enqueues nothing), H and I multiples of 256 up to 16384, 1 <= k
+ * <= min(E, 32), E <= 1024; T*H, T*k*H, T*k*I and 2*I*H each below 2^31.
+ */
+int moe_experts_int8(const int8_t* x, const float* x_scales, const int8_t* w_gate_up,
+                     const float* w_gate_up_scales, const int8_t* w_down,
+                     const float* w_down_scales, const int32_t* topk_idx, const float* topk_w,
+                     int T, int H, int I, int E, int k, uint16_t* out, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+size_t moe_experts_int8_workspace_bytes(int T, int H, int I, int E, int k);
+
+/*
  * Kernel timing hook for benchmarks and profilers (not on any page).
  * moe_profile_kernel(kernel, start, stop): from now on, the calling thread's
  * launches of `kernel` are bracketed by hipEventRecord(start) and
@@ -339,7 +494,7 @@ typedef enum {
   MOE_KERNEL_DECODE_GATE_UP = 2,
   MOE_KERNEL_DECODE_DOWN = 3,
   MOE_KERNEL_GROUP = 4,          /* expert grouping of the batched path        */
-  MOE_KERNEL_QUANT = 5,          /* moe_quantize_mxfp8                         */
+  MOE_KERNEL_QUANT = 5,          /* moe_quantize_mxfp8, moe_quantize_int8      */
   MOE_KERNEL_GEMM_GATE_UP = 6,
   MOE_KERNEL_GEMM_DOWN = 7,      /* batched down projection and the weighted combine
                                     (which runs interleaved with it in column parts) */
@@ -352,7 +507,12 @@ typedef enum {
   MOE_KERNEL_DECODE_FUSED = 14,  /* single-launch decode (T <= 16): the whole layer */
   MOE_KERNEL_BWD_REQUANT = 15,   /* MXFP8 backward: x, dout and both weights encoded
                                     along the backward's reduction axes           */
-  MOE_KERNEL_COUNT = 16
+  MOE_KERNEL_NORM = 16,          /* moe_add_rmsnorm                            */
+  MOE_KERNEL_NORM_BACKWARD = 17, /* moe_add_rmsnorm_backward                   */
+  MOE_KERNEL_ROUTE_BACKWARD = 18,/* moe_route_scored_backward (moe_route_scored: ROUTE) */
+  MOE_KERNEL_INT8_GATE_UP = 19,  /* moe_experts_int8: gate/up product and SwiGLU */
+  MOE_KERNEL_INT8_DOWN = 20,     /* moe_experts_int8: down product and the weighted sum */
+  MOE_KERNEL_COUNT = 21
 } moe_kernel_id;
 
 int moe_profile_kernel(int kernel, void* start_event, void* stop_event);

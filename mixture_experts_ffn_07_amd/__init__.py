@@ -19,15 +19,18 @@ LIB_PATH = os.path.join(_HERE, "lib", "libmoe_mi355x.so")
 
 MOE_OK, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_ALIGN = 0, -1, -2, -3
 MOE_ERR_WORKSPACE, MOE_ERR_UNSUPPORTED, MOE_ERR_HIP = -4, -5, -6
-MOE_BF16, MOE_MXFP8 = 0, 1
+MOE_BF16, MOE_MXFP8, MOE_INT8 = 0, 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 KERNELS = {"none": 0, "route": 1, "decode_gate_up": 2, "decode_down": 3, "group": 4,
            "quant": 5, "gemm_gate_up": 6, "gemm_down": 7, "combine": 8, "bwd_gate_up": 9,
            "bwd_down": 10, "bwd_input": 11, "bwd_wdown": 12, "bwd_wgate_up": 13,
-           "decode_fused": 14, "bwd_requant": 15}
+           "decode_fused": 14, "bwd_requant": 15, "norm": 16, "norm_backward": 17,
+           "route_backward": 18, "int8_gate_up": 19, "int8_down": 20}
 MOE_DEBUG_PERMUTE_ORDER, MOE_DEBUG_DECODE_FUSED = 1, 2
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_F = ctypes.c_float
 _SZ = ctypes.c_size_t
 _SIGS = {
     "moe_route_topk": (_I, [_P, _I, _I, _I, _P, _P, _P]),
@@ -45,6 +48,14 @@ _SIGS = {
     "moe_backward_batched_mxfp8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P,
                                         _P, _P, _P, _P, _P, _SZ, _P]),
     "moe_backward_mxfp8_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "moe_add_rmsnorm": (_I, [_P, _P, _P, _I, _I, _F, _P, _P, _I, _P, _P, _P]),
+    "moe_add_rmsnorm_backward": (_I, [_P, _P, _P, _P, _I, _I, _F, _P, _P, _P, _SZ, _P]),
+    "moe_add_rmsnorm_backward_workspace_bytes": (_SZ, [_I, _I]),
+    "moe_route_scored": (_I, [_P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P]),
+    "moe_route_scored_backward": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _F, _P, _P]),
+    "moe_quantize_int8": (_I, [_P, ctypes.c_int64, _I, _P, _P, _P]),
+    "moe_experts_int8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _SZ, _P]),
+    "moe_experts_int8_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
     "moe_profile_kernel": (_I, [_I, _P, _P]),
     "moe_set_debug_options": (_I, [ctypes.c_uint, ctypes.c_uint32]),
     "moe_status_string": (ctypes.c_char_p, [_I]),
@@ -408,6 +419,206 @@ def moe_backward_batched_mxfp8(x, w_gate_up, w_gate_up_scales, w_down, w_down_sc
     return dx, dw_gate_up, dw_down, d_topk_w, dlogits
 
 
+class _on:
+    """Device and stream of a call: `with _on(stream, x, ...) as s` checks that the given
+    tensors live on one GPU, makes it the current device for the call (the library launches
+    on the current device) and yields the stream handle - the caller's, or that device's
+    current stream."""
+
+    def __init__(self, stream, *tensors):
+        dev = tensors[0].device
+        for t in tensors:
+            if t is not None and t.device != dev:
+                raise ValueError(f"tensors on {dev} and {t.device}: one call takes one device")
+        if dev.type != "cuda":
+            raise ValueError("tensors passed to the library must live on the GPU")
+        self.stream = stream
+        self.dev = dev
+        self.guard = None
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.dev.index:
+            self.guard = torch.cuda.device(self.dev)
+            self.guard.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def moe_add_rmsnorm(x, weight, eps: float, residual=None, residual_out=None, y=None,
+                    qtype: int = MOE_BF16, codes=None, scales=None, stream=None):
+    """Residual sum and RMS norm of [T, H] rows; returns (residual_out, y, codes, scales).
+
+    qtype MOE_BF16: y (BF16) only; MOE_MXFP8 / MOE_INT8: codes and scales, and y where a
+    buffer for it is given.  residual_out is allocated when a residual is given without it,
+    and None without a residual."""
+    if x.dim() != 2:
+        raise ValueError("x must be [T, H]")
+    T, H = x.shape
+    dev = x.device
+    _u16(x)
+    _need(weight, "weight", (H,), _BF16)
+    _need(residual, "residual", (T, H), _BF16, optional=True)
+    if residual_out is None and residual is not None:
+        residual_out = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+    _need(residual_out, "residual_out", (T, H), _BF16, optional=True)
+    if y is None and qtype == MOE_BF16:
+        y = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+    _need(y, "y", (T, H), _BF16, optional=True)
+    if qtype == MOE_BF16:
+        codes = scales = None
+    else:
+        mx = qtype == MOE_MXFP8
+        cdt, sdt = (torch.uint8, torch.uint8) if mx else (torch.int8, torch.float32)
+        sshape = (T, H // 32) if mx else (T,)
+        if codes is None:
+            codes = torch.empty(T, H, dtype=cdt, device=dev)
+        if scales is None:
+            scales = torch.empty(sshape, dtype=sdt, device=dev)
+        _need(codes, "codes", (T, H), cdt)
+        _need(scales, "scales", sshape, sdt)
+    with _on(stream, x, weight, residual, residual_out, y, codes, scales) as s:
+        _check("moe_add_rmsnorm", lib.moe_add_rmsnorm(
+            _ptr(x), _ptr(residual), _ptr(weight), T, H, eps, _ptr(residual_out), _ptr(y), qtype,
+            _ptr(codes), _ptr(scales), s))
+    return residual_out, y, codes, scales
+
+
+def moe_add_rmsnorm_backward_workspace_bytes(T: int, H: int) -> int:
+    return int(lib.moe_add_rmsnorm_backward_workspace_bytes(T, H))
+
+
+def moe_add_rmsnorm_backward(s, weight, dy, eps: float, ds=None, dx=None, dweight=None, ws=None,
+                             stream=None):
+    """Gradients of moe_add_rmsnorm from its residual sum s (x without a residual); ds is the
+    gradient that reaches s from elsewhere.  Returns (dx, dweight); dx is the gradient of x
+    and of the residual."""
+    if s.dim() != 2:
+        raise ValueError("s must be [T, H]")
+    T, H = s.shape
+    _u16(s)
+    _need(weight, "weight", (H,), _BF16)
+    _need(dy, "dy", (T, H), _BF16)
+    _need(ds, "ds", (T, H), _BF16, optional=True)
+    if dx is None:
+        dx = torch.empty(T, H, dtype=torch.bfloat16, device=s.device)
+    if dweight is None:
+        dweight = torch.empty(H, dtype=torch.bfloat16, device=s.device)
+    _need(dx, "dx", (T, H), _BF16)
+    _need(dweight, "dweight", (H,), _BF16)
+    need = moe_add_rmsnorm_backward_workspace_bytes(T, H)
+    if ws is None:
+        ws = workspace(need, s.device)
+    _need_ws(ws, need)
+    with _on(stream, s, weight, dy, ds, dx, dweight, ws) as st:
+        _check("moe_add_rmsnorm_backward", lib.moe_add_rmsnorm_backward(
+            _ptr(s), _ptr(weight), _ptr(dy), _ptr(ds), T, H, eps, _ptr(dx), _ptr(dweight), _ptr(ws),
+            ws.numel(), st))
+    return dx, dweight
+
+
+def moe_route_scored(logits, k: int, bias=None, score: int = MOE_SCORE_SOFTMAX, n_groups: int = 1,
+                     topk_groups: int = 1, group_top: int = 1, renormalize: bool = True,
+                     scale: float = 1.0, topk_idx=None, topk_w=None, stream=None):
+    """logits [T, E] float32 (-inf masks an expert), bias [E] float32 or None ->
+    (topk_idx [T, k] int32, topk_w [T, k] float32)."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T, E]")
+    T, E = logits.shape
+    _need(logits, "logits", (T, E), torch.float32)
+    _need(bias, "bias", (E,), torch.float32, optional=True)
+    if topk_idx is None:
+        topk_idx = torch.empty(T, max(k, 0), dtype=torch.int32, device=logits.device)
+    if topk_w is None:
+        topk_w = torch.empty(T, max(k, 0), dtype=torch.float32, device=logits.device)
+    _need(topk_idx, "topk_idx", (T, k), torch.int32)
+    _need(topk_w, "topk_w", (T, k), torch.float32)
+    with _on(stream, logits, bias, topk_idx, topk_w) as s:
+        _check("moe_route_scored", lib.moe_route_scored(
+            _ptr(logits), _ptr(bias), T, E, k, n_groups, topk_groups, group_top, score,
+            1 if renormalize else 0, scale, _ptr(topk_idx), _ptr(topk_w), s))
+    return topk_idx, topk_w
+
+
+def moe_route_scored_backward(logits, topk_idx, d_topk_w, score: int = MOE_SCORE_SOFTMAX,
+                              renormalize: bool = True, scale: float = 1.0, dlogits=None,
+                              stream=None):
+    """Gradient of moe_route_scored's weights (selection held fixed) -> dlogits [T, E] float32."""
+    if logits.dim() != 2 or topk_idx.dim() != 2:
+        raise ValueError("logits must be [T, E] and topk_idx [T, k]")
+    T, E = logits.shape
+    k = topk_idx.shape[1]
+    _need(logits, "logits", (T, E), torch.float32)
+    _need(topk_idx, "topk_idx", (T, k), torch.int32)
+    _need(d_topk_w, "d_topk_w", (T, k), torch.float32)
+    if dlogits is None:
+        dlogits = torch.empty(T, E, dtype=torch.float32, device=logits.device)
+    _need(dlogits, "dlogits", (T, E), torch.float32)
+    with _on(stream, logits, topk_idx, d_topk_w, dlogits) as s:
+        _check("moe_route_scored_backward", lib.moe_route_scored_backward(
+            _ptr(logits), _ptr(topk_idx), _ptr(d_topk_w), T, E, k, score, 1 if renormalize else 0,
+            scale, _ptr(dlogits), s))
+    return dlogits
+
+
+def moe_quantize_int8(src, codes=None, scales=None, stream=None):
+    """src [rows, K] BF16 -> (codes [rows, K] int8, scales [rows] float32)."""
+    if src.dim() != 2:
+        raise ValueError("src must be [rows, K]")
+    rows, K = src.shape
+    _u16(src)
+    if codes is None:
+        codes = torch.empty(rows, K, dtype=torch.int8, device=src.device)
+    if scales is None:
+        scales = torch.empty(rows, dtype=torch.float32, device=src.device)
+    _need(codes, "codes", (rows, K), torch.int8)
+    _need(scales, "scales", (rows,), torch.float32)
+    with _on(stream, src, codes, scales) as s:
+        _check("moe_quantize_int8", lib.moe_quantize_int8(_ptr(src), rows, K, _ptr(codes),
+                                                          _ptr(scales), s))
+    return codes, scales
+
+
+def moe_experts_int8_workspace_bytes(T: int, H: int, I: int, E: int, k: int) -> int:
+    return int(lib.moe_experts_int8_workspace_bytes(T, H, I, E, k))
+
+
+def moe_experts_int8(x, x_scales, w_gate_up, w_gate_up_scales, w_down, w_down_scales, topk_idx,
+                     topk_w, out=None, ws=None, stream=None):
+    """The routed experts' FFN in INT8 (codes with per-token and per-channel scales) -> out
+    [T, H] BF16.  Slots whose expert id lies outside [0, E) add nothing."""
+    if x.dim() != 2 or w_gate_up.dim() != 3 or topk_idx.dim() != 2:
+        raise ValueError("x must be [T, H], w_gate_up [E, 2I, H], topk_idx [T, k]")
+    T, H = x.shape
+    E, I2, _ = w_gate_up.shape
+    I = I2 // 2
+    k = topk_idx.shape[1]
+    _need(x, "x", (T, H), torch.int8)
+    _need(x_scales, "x_scales", (T,), torch.float32)
+    _need(w_gate_up, "w_gate_up", (E, 2 * I, H), torch.int8)
+    _need(w_gate_up_scales, "w_gate_up_scales", (E, 2 * I), torch.float32)
+    _need(w_down, "w_down", (E, H, I), torch.int8)
+    _need(w_down_scales, "w_down_scales", (E, H), torch.float32)
+    _need(topk_idx, "topk_idx", (T, k), torch.int32)
+    _need(topk_w, "topk_w", (T, k), torch.float32)
+    if out is None:
+        out = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
+    _need(out, "out", (T, H), _BF16)
+    need = moe_experts_int8_workspace_bytes(T, H, I, E, k)
+    if ws is None:
+        ws = workspace(need, x.device)
+    _need_ws(ws, need)
+    with _on(stream, x, x_scales, w_gate_up, w_gate_up_scales, w_down, w_down_scales, topk_idx,
+             topk_w, out, ws) as s:
+        _check("moe_experts_int8", lib.moe_experts_int8(
+            _ptr(x), _ptr(x_scales), _ptr(w_gate_up), _ptr(w_gate_up_scales), _ptr(w_down),
+            _ptr(w_down_scales), _ptr(topk_idx), _ptr(topk_w), T, H, I, E, k, _ptr(out), _ptr(ws),
+            ws.numel(), s))
+    return out
+
+
 def moe_profile_kernel(kernel, start_event: Optional[int], stop_event: Optional[int]) -> None:
     """Bracket the named kernel's launches with the given hipEvent_t handles."""
     kid = KERNELS[kernel] if isinstance(kernel, str) else int(kernel)
@@ -422,4 +633,8 @@ __all__ = ["lib", "LIB_PATH", "MoeError", "moe_route_topk", "moe_decode_forward"
            "moe_backward_workspace_bytes", "moe_backward_batched_mxfp8",
            "moe_backward_mxfp8_workspace_bytes", "moe_profile_kernel", "workspace",
            "moe_set_debug_options", "MOE_DEBUG_PERMUTE_ORDER", "MOE_DEBUG_DECODE_FUSED",
-           "MOE_BF16", "MOE_MXFP8", "KERNELS"]
+           "moe_add_rmsnorm", "moe_add_rmsnorm_backward",
+           "moe_add_rmsnorm_backward_workspace_bytes", "moe_route_scored",
+           "moe_route_scored_backward", "moe_quantize_int8", "moe_experts_int8",
+           "moe_experts_int8_workspace_bytes", "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID",
+           "MOE_BF16", "MOE_MXFP8", "MOE_INT8", "KERNELS"]

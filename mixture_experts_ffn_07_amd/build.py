@@ -22,7 +22,7 @@ CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "lib")
 LIB = os.path.join(OUT_DIR, "libmoe_mi355x.so")
 SOURCES = ["abi.cpp", "route.hip", "decode.hip", "batched.hip", "gemm_large.hip", "backward.hip",
-           "scratch.hip"]
+           "scratch.hip", "norm.hip", "route_scored.hip", "int8.hip"]
 
 
 def hipcc() -> str:

@@ -3,6 +3,7 @@
 // a GPU.  The HIP runtime is first touched by the first valid launch.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <mutex>
@@ -410,6 +411,171 @@ int moe_gate_up_3d_batched_train(const uint16_t* x, const uint16_t* w_gate_up,
                                                 E, k, MOE_BF16, h, nullptr, workspace,
                                                 static_cast<hipStream_t>(stream), cus, gu),
                     "moe_gate_up_3d_batched_train launch");
+}
+
+static int check_norm(int T, int H, float eps) {
+  if (T < 0) return fail(MOE_ERR_SHAPE, "T=%d < 0", T);
+  if (H < 32 || H % 32 || H > moe::kNormMaxH)
+    return fail(MOE_ERR_SHAPE, "H=%d is not a multiple of 32 in [32, %d]", H, moe::kNormMaxH);
+  if (!(eps > 0.0f) || !std::isfinite(eps))
+    return fail(MOE_ERR_SHAPE, "eps=%g is not finite and above 0", static_cast<double>(eps));
+  return MOE_OK;
+}
+
+int moe_add_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t* weight, int T,
+                    int H, float eps, uint16_t* residual_out, uint16_t* y, moe_dtype qtype,
+                    void* codes, void* scales, void* stream) {
+  if (int st = check_norm(T, H, eps)) return st;
+  if (qtype != MOE_BF16 && qtype != MOE_MXFP8 && qtype != MOE_INT8)
+    return fail(MOE_ERR_SHAPE, "qtype=%d", qtype);
+  if (residual_out && !residual)
+    return fail(MOE_ERR_NULL, "residual_out needs a residual (without one the sum is x)");
+  if (T == 0) return ok();
+  if (!x || !weight) return fail(MOE_ERR_NULL, "x and weight are required");
+  const bool q = qtype != MOE_BF16;
+  if (q && (!codes || !scales)) return fail(MOE_ERR_NULL, "8-bit output needs codes and scales");
+  if (!q && !y) return fail(MOE_ERR_NULL, "y is required without 8-bit output");
+  if (y && y == residual_out) return fail(MOE_ERR_UNSUPPORTED, "y and residual_out are the same buffer");
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(weight) || !aligned16(residual_out) ||
+      !aligned16(y) || (q && (!aligned16(codes) || !aligned16(scales))))
+    return fail(MOE_ERR_ALIGN, "device pointers must be 16-byte aligned");
+  int cus = 0;
+  if (int st = device_info(&cus)) return st;
+  return hip_status(moe::launch_add_rmsnorm(x, residual, weight, T, H, eps, residual_out, y, qtype,
+                                            static_cast<uint8_t*>(codes), scales,
+                                            static_cast<hipStream_t>(stream), cus),
+                    "moe_add_rmsnorm launch");
+}
+
+size_t moe_add_rmsnorm_backward_workspace_bytes(int T, int H) {
+  if (T < 0 || H <= 0) return 0;
+  const size_t rows = static_cast<size_t>(moe::norm_backward_rows(T));
+  return (rows > 0 ? rows : 1) * static_cast<size_t>(H) * sizeof(float);
+}
+
+int moe_add_rmsnorm_backward(const uint16_t* s, const uint16_t* weight, const uint16_t* dy,
+                             const uint16_t* ds, int T, int H, float eps, uint16_t* dx,
+                             uint16_t* dweight, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  if (int st = check_norm(T, H, eps)) return st;
+  if (!dweight || (T > 0 && (!s || !weight || !dy || !dx)))
+    return fail(MOE_ERR_NULL, "s, weight, dy, dx and dweight are required");
+  if (!workspace) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
+  const size_t need = moe_add_rmsnorm_backward_workspace_bytes(T, H);
+  if (workspace_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "workspace %zu bytes < %zu required", workspace_bytes, need);
+  if (!aligned16(s) || !aligned16(weight) || !aligned16(dy) || !aligned16(ds) || !aligned16(dx) ||
+      !aligned16(dweight) || !aligned16(workspace))
+    return fail(MOE_ERR_ALIGN, "device pointers must be 16-byte aligned");
+  int cus = 0;
+  if (int st = device_info(&cus)) return st;
+  return hip_status(moe::launch_add_rmsnorm_backward(s, weight, dy, ds, T, H, eps, dx, dweight,
+                                                     static_cast<float*>(workspace),
+                                                     static_cast<hipStream_t>(stream)),
+                    "moe_add_rmsnorm_backward launch");
+}
+
+static int check_scored(int T, int E, int k, moe_score score, float scale) {
+  if (T < 0) return fail(MOE_ERR_SHAPE, "T=%d < 0", T);
+  if (E < 1 || E > 1024) return fail(MOE_ERR_SHAPE, "E=%d outside [1, 1024]", E);
+  if (k < 1 || k > E || k > 32) return fail(MOE_ERR_SHAPE, "k=%d outside [1, min(E=%d, 32)]", k, E);
+  if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID)
+    return fail(MOE_ERR_SHAPE, "score=%d", score);
+  if (!std::isfinite(scale)) return fail(MOE_ERR_SHAPE, "scale is not finite");
+  return MOE_OK;
+}
+
+int moe_route_scored(const float* logits, const float* bias, int T, int E, int k, int n_groups,
+                     int topk_groups, int group_top, moe_score score, int renormalize, float scale,
+                     int32_t* topk_idx, float* topk_w, void* stream) {
+  if (int st = check_scored(T, E, k, score, scale)) return st;
+  if (n_groups < 1 || n_groups > 64 || E % n_groups)
+    return fail(MOE_ERR_SHAPE, "n_groups=%d is not a divisor of E=%d in [1, 64]", n_groups, E);
+  if (topk_groups < 1 || topk_groups > n_groups)
+    return fail(MOE_ERR_SHAPE, "topk_groups=%d outside [1, n_groups=%d]", topk_groups, n_groups);
+  if (group_top != 1 && group_top != 2) return fail(MOE_ERR_SHAPE, "group_top=%d is not 1 or 2", group_top);
+  if (k > topk_groups * (E / n_groups))
+    return fail(MOE_ERR_SHAPE, "k=%d > %d experts in the selected groups", k, topk_groups * (E / n_groups));
+  if (T == 0) return ok();
+  if (!logits || !topk_idx || !topk_w)
+    return fail(MOE_ERR_NULL, "logits, topk_idx and topk_w are required");
+  if (!aligned16(logits) || !aligned16(bias) || !aligned16(topk_idx) || !aligned16(topk_w))
+    return fail(MOE_ERR_ALIGN, "device pointers must be 16-byte aligned");
+  int cus = 0;
+  if (int st = device_info(&cus)) return st;
+  const moe::ScoredRoute p{E, k, n_groups, topk_groups, group_top, score == MOE_SCORE_SIGMOID,
+                           renormalize != 0, scale};
+  return hip_status(moe::launch_route_scored(logits, bias, T, p, topk_idx, topk_w,
+                                             static_cast<hipStream_t>(stream)),
+                    "moe_route_scored launch");
+}
+
+int moe_route_scored_backward(const float* logits, const int32_t* topk_idx, const float* d_topk_w,
+                              int T, int E, int k, moe_score score, int renormalize, float scale,
+                              float* dlogits, void* stream) {
+  if (int st = check_scored(T, E, k, score, scale)) return st;
+  if (T == 0) return ok();
+  if (!logits || !topk_idx || !d_topk_w || !dlogits)
+    return fail(MOE_ERR_NULL, "logits, topk_idx, d_topk_w and dlogits are required");
+  if (!aligned16(logits) || !aligned16(topk_idx) || !aligned16(d_topk_w) || !aligned16(dlogits))
+    return fail(MOE_ERR_ALIGN, "device pointers must be 16-byte aligned");
+  int cus = 0;
+  if (int st = device_info(&cus)) return st;
+  const moe::ScoredRoute p{E, k, 1, 1, 1, score == MOE_SCORE_SIGMOID, renormalize != 0, scale};
+  return hip_status(moe::launch_route_scored_backward(logits, topk_idx, d_topk_w, T, p, dlogits,
+                                                      static_cast<hipStream_t>(stream)),
+                    "moe_route_scored_backward launch");
+}
+
+int moe_quantize_int8(const uint16_t* src, int64_t rows, int K, int8_t* codes, float* scales,
+                      void* stream) {
+  if (rows < 0 || rows >= (1LL << 29))
+    return fail(MOE_ERR_SHAPE, "rows=%lld outside [0, 2^29)", static_cast<long long>(rows));
+  if (K < 32 || K % 32 || K > moe::kNormMaxH)
+    return fail(MOE_ERR_SHAPE, "K=%d is not a multiple of 32 in [32, %d]", K, moe::kNormMaxH);
+  if (rows == 0) return ok();
+  if (!src || !codes || !scales) return fail(MOE_ERR_NULL, "src, codes and scales are required");
+  if (!aligned16(src) || !aligned16(codes) || !aligned16(scales))
+    return fail(MOE_ERR_ALIGN, "device pointers must be 16-byte aligned");
+  int cus = 0;
+  if (int st = device_info(&cus)) return st;
+  return hip_status(moe::launch_quant_int8(src, rows, K, reinterpret_cast<uint8_t*>(codes), scales,
+                                           static_cast<hipStream_t>(stream), cus),
+                    "moe_quantize_int8 launch");
+}
+
+size_t moe_experts_int8_workspace_bytes(int T, int H, int I, int E, int k) {
+  if (T < 1 || H <= 0 || I <= 0 || E < 1 || k < 1) return 0;
+  return moe::int8_ws_layout(T, H, I, E, k).total;
+}
+
+int moe_experts_int8(const int8_t* x, const float* x_scales, const int8_t* w_gate_up,
+                     const float* w_gate_up_scales, const int8_t* w_down,
+                     const float* w_down_scales, const int32_t* topk_idx, const float* topk_w,
+                     int T, int H, int I, int E, int k, uint16_t* out, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  if (int st = check_common(T, H, I, E, k, 256, 256)) return st;
+  if (H > moe::kNormMaxH || I > moe::kNormMaxH)
+    return fail(MOE_ERR_SHAPE, "H=%d or I=%d above %d", H, I, moe::kNormMaxH);
+  if (int st = check_offsets(T, H, I, k)) return st;
+  if (T == 0) return ok();
+  if (!x || !x_scales || !w_gate_up || !w_gate_up_scales || !w_down || !w_down_scales ||
+      !topk_idx || !topk_w || !out)
+    return fail(MOE_ERR_NULL, "every input and output pointer is required");
+  if (!workspace) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
+  const size_t need = moe::int8_ws_layout(T, H, I, E, k).total;
+  if (workspace_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "workspace %zu bytes < %zu required", workspace_bytes, need);
+  if (!aligned16(x) || !aligned16(x_scales) || !aligned16(w_gate_up) ||
+      !aligned16(w_gate_up_scales) || !aligned16(w_down) || !aligned16(w_down_scales) ||
+      !aligned16(topk_idx) || !aligned16(topk_w) || !aligned16(out) || !aligned16(workspace))
+    return fail(MOE_ERR_ALIGN, "device pointers must be 16-byte aligned");
+  int cus = 0;
+  if (int st = device_info(&cus)) return st;
+  return hip_status(moe::launch_experts_int8(x, x_scales, w_gate_up, w_gate_up_scales, w_down,
+                                             w_down_scales, topk_idx, topk_w, T, H, I, E, k, out,
+                                             workspace, static_cast<hipStream_t>(stream), cus),
+                    "moe_experts_int8 launch");
 }
 
 }  // extern "C"

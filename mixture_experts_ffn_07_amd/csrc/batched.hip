@@ -979,6 +979,14 @@ hipError_t launch_group_experts(const int32_t* idx, int P, int E, int BM, int* c
   return hipGetLastError();
 }
 
+hipError_t launch_combine_slots(const float* y, const int* row_of, const float* w, int T, int H,
+                                int k, uint16_t* out, int col0, int cols, int ldy, hipStream_t s,
+                                int num_cus) {
+  hipLaunchKernelGGL(combine_slots, combine_grid(T, cols, num_cus), dim3(256), 0, s, y, row_of, w, T, H,
+                     k, out, order_key(), col0, cols, ldy);
+  return hipGetLastError();
+}
+
 hipError_t launch_quant_mx(const uint16_t* src, int64_t rows, int K, uint8_t* codes,
                            uint8_t* scales, hipStream_t s) {
   const int64_t n_blocks = rows * (K / 32);

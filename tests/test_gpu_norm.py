@@ -1,0 +1,249 @@
+"""moe_add_rmsnorm and its backward against the FP64 formulas.
+
+Bounds.  BF16 outputs are rounded once from FP32: half a step, 2^-8 of the value,
+plus the FP32 error before it.  That is at most 40 roundings on the way to the mean
+of squares (8 or 16 terms per lane, 6 + 15 adds across lanes and waves, squares,
+the division; halved by the root) and 4 after it: 24 * 2^-24 < 2^-18 relative.
+MXFP8: half an E4M3 step, 2^-4 of the value (2^-10 of the scale below its normal
+range), values past 448 scales saturate.  INT8: half a code.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import block as B
+from oracle import formats as F
+
+pytestmark = pytest.mark.gpu
+
+F32 = 2.0 ** -18
+EPS = 1e-6
+
+
+@pytest.fixture(scope="module")
+def M():
+    import mixture_experts_ffn_07_amd as M
+    yield M
+    M.moe_set_debug_options(0, 0)
+
+
+def _inputs(T, H, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x, res = r(T, H) * 3, r(T, H)
+    x[:, ::97] *= 40
+    return x.bfloat16(), res.bfloat16(), (1 + 0.3 * r(H)).bfloat16()
+
+
+def _f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def _check_bf16(got, ref, slack=0.0):
+    g = _f64(got)
+    over = np.abs(g - ref) - (np.abs(ref) * (2.0 ** -8 + F32) + slack)
+    assert np.all(over <= 0), f"{over.max():.3e} over the bound at {np.unravel_index(over.argmax(), over.shape)}"
+
+
+def _check_mx(codes, scales, y):
+    s = scales.cpu().numpy().astype(np.int64) - 127
+    _, ref_s = F.mx_quantize(y)
+    ref_s = ref_s.astype(np.int64) - 127
+    amax = np.abs(y.reshape(*s.shape, 32)).max(axis=-1)
+    lg = np.log2(np.where(amax > 0, amax, 1.5))
+    border = np.abs(lg - np.rint(lg)) < 1e-5       # FP32 may fall on the other side of a power of two
+    assert np.all((s == ref_s) | (border & (np.abs(s - ref_s) == 1)))
+    step = 2.0 ** s[..., None]
+    got = F.e4m3_decode(codes.cpu().numpy()).reshape(*s.shape, 32) * step
+    ref = np.clip(y.reshape(*s.shape, 32), -448 * step, 448 * step)
+    assert np.all(np.abs(got - ref) <= np.maximum(np.abs(ref) * 2.0 ** -4, step * 2.0 ** -10) * (1 + 1e-3))
+
+
+def _check_int8(codes, scales, y):
+    sc = scales.double().cpu().numpy()
+    ref = np.abs(y).max(axis=1) / 127
+    assert np.all(np.abs(sc - ref) <= ref * F32)
+    c = codes.cpu().numpy().astype(np.float64)
+    assert np.abs(c).max(initial=0) <= 127
+    err = np.abs(c * sc[:, None] - y)
+    # half a code, and FP32's error of a value of up to 127 codes on either side of the border
+    assert np.all(err <= sc[:, None] * (0.5 + 2 * 127 * F32) + 1e-45)
+
+
+SHAPES = [(1, 32), (1, 4096), (3, 96), (7, 2048), (2, 8192), (5, 8224), (2, 16384), (33, 7168),
+          (1025, 512), (600, 6144), (2049, 1056)]
+
+
+@pytest.mark.parametrize("T,H", SHAPES)
+@pytest.mark.parametrize("res", [False, True])
+def test_norm_bf16(M, T, H, res):
+    print(f"[norm] bf16 T={T} H={H} res={res}", flush=True)
+    x, r, w = _inputs(T, H, T + H)
+    s, y, codes, scales = M.moe_add_rmsnorm(x, w, EPS, residual=r if res else None)
+    rs, ry = B.add_rmsnorm(_f64(x), _f64(w), EPS, _f64(r) if res else None)
+    assert codes is None and scales is None
+    if res:
+        assert np.array_equal(_f64(s), rs)
+    else:
+        assert s is None
+    _check_bf16(y, ry)
+
+
+@pytest.mark.parametrize("T,H", SHAPES)
+@pytest.mark.parametrize("q", ["mxfp8", "int8"])
+def test_norm_8bit(M, T, H, q):
+    print(f"[norm] {q} T={T} H={H}", flush=True)
+    x, r, w = _inputs(T, H, 2 * T + H)
+    y = torch.full_like(x, float("nan")) if T % 2 else None
+    s, y2, codes, scales = M.moe_add_rmsnorm(x, w, EPS, residual=r, y=y,
+                                             qtype=M.MOE_MXFP8 if q == "mxfp8" else M.MOE_INT8)
+    rs, ry = B.add_rmsnorm(_f64(x), _f64(w), EPS, _f64(r))
+    assert np.array_equal(_f64(s), rs)
+    if y is None:
+        assert y2 is None
+    else:
+        _check_bf16(y, ry)
+    (_check_mx if q == "mxfp8" else _check_int8)(codes, scales, ry)
+
+
+def test_norm_zero_rows_and_small_values(M):
+    x = torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda")
+    x[1] = 1e-20                                       # far below eps: y = x / sqrt(eps)
+    x[2, 5] = -3e4
+    x[3] = torch.finfo(torch.bfloat16).tiny
+    w = torch.ones(256, dtype=torch.bfloat16, device="cuda")
+    _, ry = B.add_rmsnorm(_f64(x), _f64(w), EPS)
+    _, y, _, _ = M.moe_add_rmsnorm(x, w, EPS)
+    _check_bf16(y, ry, slack=2.0 ** -133)              # BF16's smallest step
+    _, _, c, s = M.moe_add_rmsnorm(x, w, EPS, qtype=M.MOE_MXFP8)
+    assert not c[0].any() and not s[0].any()           # all-zero blocks: codes 0, scale 2^-127
+    _check_mx(c[1:3], s[1:3], ry[1:3])
+    _, _, c, s = M.moe_add_rmsnorm(x, w, EPS, qtype=M.MOE_INT8)
+    assert not c[0].any() and s[0] == 0 and not c[3].any() and s[3] == 0
+    _check_int8(c[1:3], s[1:3], ry[1:3])
+
+
+def test_norm_row_with_infinity_leaves_the_others(M):
+    x, r, w = _inputs(5, 2048, 3)
+    ref = M.moe_add_rmsnorm(x, w, EPS, residual=r, qtype=M.MOE_INT8, y=torch.empty_like(x))
+    bad = x.clone()
+    bad[2, 100], bad[2, 7] = float("inf"), float("nan")
+    got = M.moe_add_rmsnorm(bad, w, EPS, residual=r, qtype=M.MOE_INT8, y=torch.empty_like(x))
+    keep = [0, 1, 3, 4]
+    for a, b in zip(ref, got):
+        assert torch.equal(a[keep], b[keep])
+
+
+@pytest.mark.parametrize("T", [3, 700])
+def test_norm_in_place(M, T):
+    x, r, w = _inputs(T, 4096, 4)
+    s, y, _, _ = M.moe_add_rmsnorm(x, w, EPS, residual=r)
+    x1, r1 = x.clone(), r.clone()
+    M.moe_add_rmsnorm(x1, w, EPS, residual=r1, residual_out=r1, y=x1)
+    assert torch.equal(x1, y) and torch.equal(r1, s)
+    x1, r1 = x.clone(), r.clone()
+    M.moe_add_rmsnorm(x1, w, EPS, residual=r1, residual_out=x1, y=r1)
+    assert torch.equal(x1, s) and torch.equal(r1, y)
+    dy, ds = _inputs(T, 4096, 5)[:2]
+    dx, dw = M.moe_add_rmsnorm_backward(s, w, dy, EPS, ds=ds)
+    for inout in ("dy", "ds"):
+        a = {"dy": dy.clone(), "ds": ds.clone()}
+        _, dw1 = M.moe_add_rmsnorm_backward(s, w, a["dy"], EPS, ds=a["ds"], dx=a[inout])
+        assert torch.equal(a[inout], dx) and torch.equal(dw1, dw)
+
+
+def test_norm_empty_batch(M):
+    x = torch.empty(0, 512, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(512, dtype=torch.bfloat16, device="cuda")
+    _, y, _, _ = M.moe_add_rmsnorm(x, w, EPS)
+    assert y.shape == (0, 512)
+    dx, dw = M.moe_add_rmsnorm_backward(x, w, x, EPS)
+    assert dx.shape == (0, 512) and not dw.any()
+
+
+@pytest.mark.parametrize("T,H", SHAPES + [(511, 768), (513, 768), (3000, 64)])
+@pytest.mark.parametrize("res", [False, True])
+def test_norm_backward(M, T, H, res):
+    print(f"[norm backward] T={T} H={H} ds={res}", flush=True)
+    s, ds, w = _inputs(T, H, 3 * T + H)
+    dy = _inputs(T, H, 5 * T + H)[1]
+    dx, dw = M.moe_add_rmsnorm_backward(s, w, dy, EPS, ds=ds if res else None)
+    rdx, rdw = B.add_rmsnorm_backward(_f64(s), _f64(w), _f64(dy), EPS, _f64(ds) if res else None)
+    s64, w64, dy64 = _f64(s), _f64(w), _f64(dy)
+    q = 1 / np.sqrt((s64 ** 2).mean(axis=1, keepdims=True) + EPS)
+    n = s64 * q
+    # FP32: each term q w dy, q n m, ds with a relative error F32 (m: that of sum |n w dy|)
+    m_abs = np.abs(n * w64 * dy64).mean(axis=1, keepdims=True)
+    terms = q * (np.abs(w64 * dy64) + 2 * np.abs(n) * m_abs) + (np.abs(_f64(ds)) if res else 0)
+    _check_bf16(dx, rdx, slack=terms * F32)
+    # the sum over rows: at most T / 512 + 1 terms per lane, 32 + 16 partial sums
+    count = T / 512 + 1 + 48
+    _check_bf16(dw, rdw, slack=np.abs(dy64 * n).sum(axis=0) * (count * 2.0 ** -24 + F32))
+
+
+def test_norm_gradient_against_differences_of_the_kernel_formula(M):
+    """sum(dy y) moved along a direction v: the directional difference of the FP64 formula
+    equals <dx, v> within dx's rounding."""
+    s, v, w = _inputs(9, 512, 11)
+    dy = _inputs(9, 512, 12)[1]
+    dx, dw = M.moe_add_rmsnorm_backward(s, w, dy, EPS)
+    s64, w64, dy64, v64 = (_f64(t) for t in (s, w, dy, v))
+    f = lambda a, b: (dy64 * B.add_rmsnorm(a, b, EPS)[1]).sum()  # noqa: E731
+    h = 1e-4
+    num = (f(s64 + h * v64, w64) - f(s64 - h * v64, w64)) / (2 * h)
+    tol = (np.abs(_f64(dx) * v64)).sum() * (2.0 ** -8 + F32) + 1e-4 * abs(num)
+    assert abs((_f64(dx) * v64).sum() - num) <= tol
+    u64 = np.random.default_rng(0).normal(size=512)
+    num = (f(s64, w64 + h * u64) - f(s64, w64 - h * u64)) / (2 * h)
+    tol = np.abs(_f64(dw) * u64).sum() * (2.0 ** -8 + F32) + 1e-6 * abs(num)
+    assert abs((_f64(dw) * u64).sum() - num) <= tol
+
+
+@pytest.mark.parametrize("T,H", [(1, 256), (5, 2048), (700, 7168)])
+def test_quantize_int8(M, T, H):
+    x, _, _ = _inputs(T, H, 21)
+    if T > 2:
+        x[1] = 0
+        x[2] = 1e-35
+    c, s = M.moe_quantize_int8(x)
+    rc, rs = B.int8_rows(_f64(x))
+    assert np.all(np.abs(s.double().cpu().numpy() - rs) <= rs * 2.0 ** -24)
+    c = c.cpu().numpy().astype(np.float64)
+    diff = c != rc
+    assert np.all(np.abs(c - rc) <= 1)
+    # only where v 127 / amax lies at a border: two FP32 roundings of a value of up to 127
+    v = _f64(x) / np.where(rs > 0, rs, 1)[:, None]
+    assert np.all(np.abs(np.abs(v[diff]) % 1 - 0.5) < 127 * 2.0 ** -22)
+    if T > 2:
+        assert not c[1].any() and not c[2].any() and s[1] == 0 and s[2] == 0
+
+
+def _all(M, x, r, w, dy, stream=None):
+    s, y, c, sc = M.moe_add_rmsnorm(x, w, EPS, residual=r, y=torch.empty_like(x), qtype=M.MOE_MXFP8, stream=stream)
+    _, _, c8, s8 = M.moe_add_rmsnorm(x, w, EPS, residual=r, qtype=M.MOE_INT8, stream=stream)
+    dx, dw = M.moe_add_rmsnorm_backward(s, w, dy, EPS, ds=r, stream=stream)
+    return [s, y, c, sc, c8, s8, dx, dw]
+
+
+@pytest.mark.parametrize("T,H", [(5, 4096), (777, 2048)])
+def test_norm_is_deterministic_and_order_free(M, T, H):
+    x, r, w = _inputs(T, H, 31)
+    dy = _inputs(T, H, 32)[0]
+    ref = _all(M, x, r, w, dy)
+    for seed in range(4):
+        M.moe_set_debug_options(M.MOE_DEBUG_PERMUTE_ORDER if seed else 0, seed)
+        for a, b in zip(ref, _all(M, x, r, w, dy)):
+            assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+    M.moe_set_debug_options(0, 0)
+
+
+def test_norm_on_a_side_stream(M):
+    x, r, w = _inputs(300, 2048, 41)
+    dy = _inputs(300, 2048, 42)[0]
+    ref = _all(M, x, r, w, dy)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = _all(M, x, r, w, dy, stream=side)            # the handle given, not the current stream
+    side.synchronize()
+    for a, b in zip(ref, got):
+        assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))

@@ -1,0 +1,233 @@
+"""moe_route_scored and its backward against the FP64 oracle: indices exact, weights and
+gradients to FP32's error (an exponential within 2 steps, a division, and sums of up to
+1024 positive terms over 16 adds per lane and 6 across lanes: below 40 * 2^-24)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import block as B
+
+pytestmark = pytest.mark.gpu
+
+REL = 40 * 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def M():
+    import mixture_experts_ffn_07_amd as M
+    yield M
+    M.moe_set_debug_options(0, 0)
+
+
+def _score(M, name):
+    return M.MOE_SCORE_SOFTMAX if name == "softmax" else M.MOE_SCORE_SIGMOID
+
+
+def _run(M, l, k, bias=None, score="softmax", G=1, tg=1, gt=1, renorm=True, scale=1.0, what=""):
+    T, E = l.shape
+    print(f"[route scored] {what} T={T} E={E} k={k} {score} G={G}/{tg}/{gt} bias={bias is not None} "
+          f"renorm={renorm}", flush=True)
+    idx, w = M.moe_route_scored(l.cuda(), k, bias=None if bias is None else bias.cuda(),
+                                score=_score(M, score), n_groups=G, topk_groups=tg, group_top=gt,
+                                renormalize=renorm, scale=scale)
+    ridx, rw = B.route_scored(l.numpy(), k, None if bias is None else bias.numpy(), score, G, tg, gt,
+                              renorm, scale)
+    assert np.array_equal(idx.cpu().numpy(), ridx)
+    assert np.all(np.abs(w.double().cpu().numpy() - rw) <= np.abs(rw) * REL + 1e-37)
+    return idx, w
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("T,E,k,G,tg,gt", [
+    (1, 8, 2, 1, 1, 1), (5, 3, 3, 1, 1, 1), (33, 64, 6, 8, 3, 2), (65, 100, 7, 10, 4, 1),
+    (17, 384, 8, 8, 4, 2), (9, 1024, 32, 64, 16, 2), (130, 256, 1, 2, 1, 2), (6, 60, 10, 60, 10, 2),
+    (11, 511, 10, 7, 2, 1), (3, 1, 1, 1, 1, 2), (4, 65, 32, 1, 1, 1), (7, 96, 3, 3, 3, 2)])
+def test_route_scored(M, score, bias, renorm, T, E, k, G, tg, gt):
+    g = torch.Generator().manual_seed(T * 31 + E)
+    l = torch.randn(T, E, generator=g) * 2
+    b = 0.2 * torch.randn(E, generator=g) if bias else None
+    _run(M, l, k, b, score, G, tg, gt, renorm, 1.0 if T % 2 else 2.5)
+
+
+def test_route_scored_is_route_topk_without_options(M):
+    l = torch.randn(500, 384, device="cuda")
+    l[::3] = (l[::3] * 2).round() / 2                   # many ties
+    a = M.moe_route_topk(l, 8)
+    b = M.moe_route_scored(l, 8)
+    assert torch.equal(a[0], b[0]) and (a[1] - b[1]).abs().max() <= 4 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("G,tg,gt", [(1, 1, 1), (4, 2, 1), (4, 2, 2)])
+def test_route_scored_ties_take_the_lowest_index(M, score, G, tg, gt):
+    g = torch.Generator().manual_seed(5)
+    l = (torch.randint(-2, 3, (200, 40), generator=g) / 2).float()
+    b = (torch.randint(-1, 2, (40,), generator=g) / 4).float()
+    l[::2][l[::2] == 0] = -0.0
+    _run(M, l, 7, None, score, G, tg, gt, what="ties")
+    _run(M, l, 7, b, score, G, tg, gt, what="ties")
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("G,tg,gt", [(1, 1, 1), (8, 3, 2), (8, 3, 1)])
+def test_route_scored_masks(M, score, bias, renorm, G, tg, gt):
+    g = torch.Generator().manual_seed(6)
+    T, E, k = 64, 64, 6
+    l = torch.randn(T, E, generator=g)
+    u = torch.rand(T, E, generator=g)
+    l[u < 0.5] = -float("inf")
+    l[(u > 0.5) & (u < 0.55)] = float("nan")
+    l[(u > 0.55) & (u < 0.6)] = torch.finfo(torch.float32).min
+    l[(u > 0.6) & (u < 0.65)] = torch.finfo(torch.bfloat16).min
+    l[0] = -float("inf")                                # nothing left
+    l[1] = float("nan")
+    l[2] = torch.finfo(torch.float32).min
+    l[3] = -float("inf")
+    l[3, 40] = 1.5                                      # one expert left
+    l[4] = -float("inf")
+    l[4, 9], l[4, 63] = -80.0, -85.0                    # scores near the end of FP32
+    b = 0.2 * torch.randn(E, generator=g) if bias else None
+    idx, w = _run(M, l, k, b, score, G, tg, gt, renorm, what="masks")
+    assert not w[:3].any()
+    i = idx.cpu().numpy()
+    assert i.min() >= 0 and i.max() < E and all(len(set(r)) == k for r in i)
+
+
+def test_route_scored_extreme_logits(M):
+    l = torch.randn(6, 20)
+    l[0, 3] = float("inf")
+    l[1, 3] = l[1, 4] = float("inf")
+    l[2] = 100 + 0.5 * torch.arange(20)
+    l[3] = -100 - 0.01 * torch.arange(20)               # sigmoid scores of 4e-44: renormalised in FP32
+    l[4, :10] = torch.finfo(torch.float32).max
+    for score in ("softmax", "sigmoid"):
+        for rows in (slice(0, 3), slice(4, 6)):
+            _run(M, l[rows], 4, None, score, renorm=True, what="extremes")
+            _run(M, l[rows], 4, None, score, renorm=False, what="extremes")
+    idx, w = M.moe_route_scored(l.cuda(), 4, score=_score(M, "sigmoid"))
+    assert torch.isfinite(w).all() and idx[3].tolist() == [0, 1, 2, 3]
+
+
+def test_route_scored_near_ties_of_the_biased_choice(M):
+    """Pairs of experts whose c differ by parts in 1e9: FP32 scores would not tell them apart."""
+    g = torch.Generator().manual_seed(8)
+    T, E = 300, 128
+    l = torch.randn(T, E, generator=g)
+    b = 0.1 * torch.randn(E, generator=g)
+    p = torch.sigmoid(l[:, ::2].double())
+    want = p + b[::2].double() - b[1::2].double()       # score that ties the neighbour's c
+    want = want.clamp(0.05, 0.95)
+    l[:, 1::2] = torch.log(want / (1 - want)).float()   # (rounded: c differs in its 8th to 9th digit)
+    _run(M, l, 8, b, "sigmoid", what="near ties")
+
+
+def test_route_scored_empty_batch_and_large(M):
+    idx, w = M.moe_route_scored(torch.empty(0, 8, device="cuda"), 2)
+    assert idx.shape == (0, 2) and w.shape == (0, 2)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    l = torch.randn(70001, 16, generator=g, device="cuda")
+    idx, w = M.moe_route_scored(l, 2, score=_score(M, "sigmoid"), renormalize=False)
+    top = l.topk(2, dim=1)
+    assert torch.equal(idx.long(), top.indices)         # (no ties among these)
+    assert (w - torch.sigmoid(top.values.double())).abs().max() <= REL
+
+
+BACK = [(1, 8, 2), (5, 3, 3), (33, 64, 6), (65, 100, 7), (17, 384, 8), (9, 1024, 32), (130, 256, 1), (6, 511, 10)]
+
+
+def _back(M, l, idx, dw, score, renorm, scale):
+    got = M.moe_route_scored_backward(l.cuda(), idx.cuda(), dw.cuda(), score=_score(M, score),
+                                      renormalize=renorm, scale=scale).double().cpu().numpy()
+    ref = B.route_scored_backward(l.numpy(), idx.numpy(), dw.numpy(), score, renorm, scale)
+    p, _ = B.scores(l.numpy(), score)
+    # size of the terms that are subtracted: p_e (|dw_e| + sum w |dw|), over the scores' sum if renormalised
+    mag = np.zeros_like(ref)
+    for t in range(l.shape[0]):
+        sel = [int(e) for e in idx[t] if 0 <= e < l.shape[1]]
+        a = {}
+        for e, d in zip(idx[t].tolist(), dw[t].tolist()):
+            if 0 <= e < l.shape[1]:
+                a[e] = a.get(e, 0.0) + abs(d)
+        z = sum(p[t, e] for e in sel) if renorm else 1.0
+        mean = sum(p[t, e] * v for e, v in a.items()) / (z if z > 0 else 1.0)
+        for e in (range(l.shape[1]) if score == "softmax" and not renorm else sel):
+            mag[t, e] = abs(scale) * p[t, e] / (z if z > 0 else 1.0) * (a.get(e, 0.0) + mean)
+    assert np.all(np.isfinite(got))
+    # the oracle's own error: p_e (dp_e - sum dp p) in FP64, where for renormalised softmax scores
+    # the sum is 0 but for the rounding of at most 3 * 32 terms, each no larger than the row's mag
+    # summed: below 128 * 2^-53 of that
+    own = mag.sum(axis=1, keepdims=True) * 2.0 ** -46
+    assert np.all(np.abs(got - ref) <= 2 * REL * mag + own + 1e-37)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("T,E,k", BACK)
+def test_route_scored_backward(M, score, renorm, T, E, k):
+    print(f"[route scored backward] T={T} E={E} k={k} {score} renorm={renorm}", flush=True)
+    g = torch.Generator().manual_seed(T + E)
+    l = torch.randn(T, E, generator=g) * 2
+    idx = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).int()
+    _back(M, l, idx, torch.randn(T, k, generator=g), score, renorm, 2.5)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_scored_backward_masks_and_ids(M, score, renorm):
+    g = torch.Generator().manual_seed(3)
+    l = torch.randn(8, 20, generator=g)
+    l[0] = -float("inf")
+    l[1, :15] = -float("inf")
+    l[2, 4] = float("nan")
+    l[3, 1] = torch.finfo(torch.float32).min
+    idx = torch.stack([torch.randperm(20, generator=g)[:5] for _ in range(8)]).int()
+    idx[1] = torch.tensor([0, 1, 15, 16, 17])            # two masked ones among the selected
+    idx[2, 0] = 4
+    idx[3, 2] = 1
+    idx[5, 3] = -1                                       # ids that are no expert
+    idx[6] = torch.tensor([20, -7, 2 ** 31 - 1, 3, 9])
+    _back(M, l, idx, torch.randn(8, 5, generator=g), score, renorm, 1.0)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_scored_gradient_against_differences(M, score, renorm):
+    """<dlogits, v> against the difference of sum(dw w) along v, the selection held fixed."""
+    g = torch.Generator().manual_seed(12)
+    T, E, k = 10, 48, 5
+    l, v, dw = torch.randn(T, E, generator=g), torch.randn(T, E, generator=g), torch.randn(T, k, generator=g)
+    idx, _ = M.moe_route_scored(l.cuda(), k, score=_score(M, score), renormalize=renorm, scale=1.5)
+    d = M.moe_route_scored_backward(l.cuda(), idx, dw.cuda(), score=_score(M, score), renormalize=renorm, scale=1.5)
+    i = idx.long().cpu()
+
+    def f(z):
+        p = torch.softmax(z, 1) if score == "softmax" else torch.sigmoid(z)
+        w = p.gather(1, i)
+        w = w / w.sum(1, keepdim=True) if renorm else w
+        return float((1.5 * w * dw.double()).sum())
+
+    h = 1e-4
+    num = (f(l.double() + h * v.double()) - f(l.double() - h * v.double())) / (2 * h)
+    got = float((d.double().cpu() * v.double()).sum())
+    tol = float((d.double().cpu() * v.double()).abs().sum()) * 1e-5 + 1e-6
+    assert abs(got - num) <= tol
+
+
+def test_route_scored_is_deterministic_and_order_free(M):
+    l = torch.randn(999, 384, device="cuda")
+    b = 0.1 * torch.randn(384, device="cuda")
+    dw = torch.randn(999, 8, device="cuda")
+
+    def call():
+        i, w = M.moe_route_scored(l, 8, bias=b, score=_score(M, "sigmoid"), n_groups=8, topk_groups=4, group_top=2)
+        return i, w, M.moe_route_scored_backward(l, i, dw, score=_score(M, "sigmoid"))
+    ref = call()
+    for seed in range(4):
+        M.moe_set_debug_options(M.MOE_DEBUG_PERMUTE_ORDER if seed else 0, seed)
+        for a, c in zip(ref, call()):
+            assert torch.equal(a.view(torch.int32), c.view(torch.int32))
+    M.moe_set_debug_options(0, 0)
