@@ -419,32 +419,49 @@ def moe_backward_batched_mxfp8(x, w_gate_up, w_gate_up_scales, w_down, w_down_sc
     return dx, dw_gate_up, dw_down, d_topk_w, dlogits
 
 
-class _on:
-    """Device and stream of a call: `with _on(stream, x, ...) as s` checks that the given
-    tensors live on one GPU, makes it the current device for the call (the library launches
-    on the current device) and yields the stream handle - the caller's, or that device's
-    current stream."""
+# The calls below check each tensor once (a 20-microsecond step is a handful of them: the
+# checks and the stream look-up of the calls above cost about 5 us of host time a call,
+# these about 2).
 
-    def __init__(self, stream, *tensors):
-        dev = tensors[0].device
-        for t in tensors:
-            if t is not None and t.device != dev:
-                raise ValueError(f"tensors on {dev} and {t.device}: one call takes one device")
-        if dev.type != "cuda":
-            raise ValueError("tensors passed to the library must live on the GPU")
-        self.stream = stream
-        self.dev = dev
-        self.guard = None
+def _arg(t, name: str, shape, dtypes, dev) -> Optional[int]:
+    """The device pointer of a tensor argument, after checking its element type, shape,
+    device and layout (None stays None: the library names what it requires)."""
+    if t is None:
+        return None
+    if t.dtype is not dtypes and not (isinstance(dtypes, tuple) and t.dtype in dtypes):
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtypes}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} is on {t.device}, the call on {dev}: one call takes one device")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
-    def __enter__(self):
-        if torch.cuda.current_device() != self.dev.index:
-            self.guard = torch.cuda.device(self.dev)
-            self.guard.__enter__()
-        return _stream(self.stream)
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _gpu(t: torch.Tensor, dims: int, name: str):
+    """The GPU that a call runs on: the one of its first tensor."""
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, not {t.dim()}")
+    return t.device
+
+
+def _enqueue(name: str, dev, stream, *args) -> None:
+    """Call the entry point on the given stream (None: the device's current one), with the
+    tensors' device current: the library launches on the current device."""
+    if dev.type != "cuda":
+        raise ValueError("tensors passed to the library must live on the GPU")
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    elif hasattr(stream, "cuda_stream"):
+        stream = stream.cuda_stream
+    if torch.cuda.current_device() == dev.index:
+        status = getattr(lib, name)(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = getattr(lib, name)(*args, stream)
+    if status != MOE_OK:
+        raise MoeError(name, status)
 
 
 def moe_add_rmsnorm(x, weight, eps: float, residual=None, residual_out=None, y=None,
@@ -454,35 +471,32 @@ def moe_add_rmsnorm(x, weight, eps: float, residual=None, residual_out=None, y=N
     qtype MOE_BF16: y (BF16) only; MOE_MXFP8 / MOE_INT8: codes and scales, and y where a
     buffer for it is given.  residual_out is allocated when a residual is given without it,
     and None without a residual."""
-    if x.dim() != 2:
-        raise ValueError("x must be [T, H]")
-    T, H = x.shape
-    dev = x.device
-    _u16(x)
-    _need(weight, "weight", (H,), _BF16)
-    _need(residual, "residual", (T, H), _BF16, optional=True)
+    dev = _gpu(x, 2, "x")
+    shape = T, H = x.shape
+    px = _arg(x, "x", shape, _BF16, dev)
+    pw = _arg(weight, "weight", (H,), _BF16, dev)
+    pr = _arg(residual, "residual", shape, _BF16, dev)
     if residual_out is None and residual is not None:
-        residual_out = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
-    _need(residual_out, "residual_out", (T, H), _BF16, optional=True)
+        residual_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    ps = _arg(residual_out, "residual_out", shape, _BF16, dev)
     if y is None and qtype == MOE_BF16:
-        y = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
-    _need(y, "y", (T, H), _BF16, optional=True)
+        y = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    py = _arg(y, "y", shape, _BF16, dev)
+    pc = pq = None
     if qtype == MOE_BF16:
         codes = scales = None
     else:
-        mx = qtype == MOE_MXFP8
-        cdt, sdt = (torch.uint8, torch.uint8) if mx else (torch.int8, torch.float32)
-        sshape = (T, H // 32) if mx else (T,)
+        if qtype == MOE_MXFP8:
+            cdt, sdt, sshape = torch.uint8, torch.uint8, (T, H // 32)
+        else:
+            cdt, sdt, sshape = torch.int8, torch.float32, (T,)
         if codes is None:
-            codes = torch.empty(T, H, dtype=cdt, device=dev)
+            codes = torch.empty(shape, dtype=cdt, device=dev)
         if scales is None:
             scales = torch.empty(sshape, dtype=sdt, device=dev)
-        _need(codes, "codes", (T, H), cdt)
-        _need(scales, "scales", sshape, sdt)
-    with _on(stream, x, weight, residual, residual_out, y, codes, scales) as s:
-        _check("moe_add_rmsnorm", lib.moe_add_rmsnorm(
-            _ptr(x), _ptr(residual), _ptr(weight), T, H, eps, _ptr(residual_out), _ptr(y), qtype,
-            _ptr(codes), _ptr(scales), s))
+        pc = _arg(codes, "codes", shape, cdt, dev)
+        pq = _arg(scales, "scales", sshape, sdt, dev)
+    _enqueue("moe_add_rmsnorm", dev, stream, px, pr, pw, T, H, eps, ps, py, qtype, pc, pq)
     return residual_out, y, codes, scales
 
 
@@ -490,32 +504,30 @@ def moe_add_rmsnorm_backward_workspace_bytes(T: int, H: int) -> int:
     return int(lib.moe_add_rmsnorm_backward_workspace_bytes(T, H))
 
 
+def _ws_arg(ws, nbytes: int, dev):
+    """(pointer, bytes) of the workspace: the caller's, or a new one of nbytes."""
+    if ws is None:
+        ws = workspace(nbytes, dev)
+    _need_ws(ws, nbytes)
+    return _arg(ws, "workspace", ws.shape, torch.uint8, dev), ws.numel()
+
+
 def moe_add_rmsnorm_backward(s, weight, dy, eps: float, ds=None, dx=None, dweight=None, ws=None,
                              stream=None):
     """Gradients of moe_add_rmsnorm from its residual sum s (x without a residual); ds is the
     gradient that reaches s from elsewhere.  Returns (dx, dweight); dx is the gradient of x
     and of the residual."""
-    if s.dim() != 2:
-        raise ValueError("s must be [T, H]")
-    T, H = s.shape
-    _u16(s)
-    _need(weight, "weight", (H,), _BF16)
-    _need(dy, "dy", (T, H), _BF16)
-    _need(ds, "ds", (T, H), _BF16, optional=True)
+    dev = _gpu(s, 2, "s")
+    shape = T, H = s.shape
     if dx is None:
-        dx = torch.empty(T, H, dtype=torch.bfloat16, device=s.device)
+        dx = torch.empty(shape, dtype=torch.bfloat16, device=dev)
     if dweight is None:
-        dweight = torch.empty(H, dtype=torch.bfloat16, device=s.device)
-    _need(dx, "dx", (T, H), _BF16)
-    _need(dweight, "dweight", (H,), _BF16)
-    need = moe_add_rmsnorm_backward_workspace_bytes(T, H)
-    if ws is None:
-        ws = workspace(need, s.device)
-    _need_ws(ws, need)
-    with _on(stream, s, weight, dy, ds, dx, dweight, ws) as st:
-        _check("moe_add_rmsnorm_backward", lib.moe_add_rmsnorm_backward(
-            _ptr(s), _ptr(weight), _ptr(dy), _ptr(ds), T, H, eps, _ptr(dx), _ptr(dweight), _ptr(ws),
-            ws.numel(), st))
+        dweight = torch.empty(H, dtype=torch.bfloat16, device=dev)
+    ptrs = (_arg(s, "s", shape, _BF16, dev), _arg(weight, "weight", (H,), _BF16, dev),
+            _arg(dy, "dy", shape, _BF16, dev), _arg(ds, "ds", shape, _BF16, dev))
+    outs = _arg(dx, "dx", shape, _BF16, dev), _arg(dweight, "dweight", (H,), _BF16, dev)
+    pws, n = _ws_arg(ws, moe_add_rmsnorm_backward_workspace_bytes(T, H), dev)
+    _enqueue("moe_add_rmsnorm_backward", dev, stream, *ptrs, T, H, eps, *outs, pws, n)
     return dx, dweight
 
 
@@ -524,21 +536,18 @@ def moe_route_scored(logits, k: int, bias=None, score: int = MOE_SCORE_SOFTMAX, 
                      scale: float = 1.0, topk_idx=None, topk_w=None, stream=None):
     """logits [T, E] float32 (-inf masks an expert), bias [E] float32 or None ->
     (topk_idx [T, k] int32, topk_w [T, k] float32)."""
-    if logits.dim() != 2:
-        raise ValueError("logits must be [T, E]")
+    dev = _gpu(logits, 2, "logits")
     T, E = logits.shape
-    _need(logits, "logits", (T, E), torch.float32)
-    _need(bias, "bias", (E,), torch.float32, optional=True)
+    shape = (T, max(k, 0))
     if topk_idx is None:
-        topk_idx = torch.empty(T, max(k, 0), dtype=torch.int32, device=logits.device)
+        topk_idx = torch.empty(shape, dtype=torch.int32, device=dev)
     if topk_w is None:
-        topk_w = torch.empty(T, max(k, 0), dtype=torch.float32, device=logits.device)
-    _need(topk_idx, "topk_idx", (T, k), torch.int32)
-    _need(topk_w, "topk_w", (T, k), torch.float32)
-    with _on(stream, logits, bias, topk_idx, topk_w) as s:
-        _check("moe_route_scored", lib.moe_route_scored(
-            _ptr(logits), _ptr(bias), T, E, k, n_groups, topk_groups, group_top, score,
-            1 if renormalize else 0, scale, _ptr(topk_idx), _ptr(topk_w), s))
+        topk_w = torch.empty(shape, dtype=torch.float32, device=dev)
+    _enqueue("moe_route_scored", dev, stream, _arg(logits, "logits", (T, E), torch.float32, dev),
+             _arg(bias, "bias", (E,), torch.float32, dev), T, E, k, n_groups, topk_groups, group_top,
+             score, 1 if renormalize else 0, scale,
+             _arg(topk_idx, "topk_idx", shape, torch.int32, dev),
+             _arg(topk_w, "topk_w", shape, torch.float32, dev))
     return topk_idx, topk_w
 
 
@@ -546,38 +555,31 @@ def moe_route_scored_backward(logits, topk_idx, d_topk_w, score: int = MOE_SCORE
                               renormalize: bool = True, scale: float = 1.0, dlogits=None,
                               stream=None):
     """Gradient of moe_route_scored's weights (selection held fixed) -> dlogits [T, E] float32."""
-    if logits.dim() != 2 or topk_idx.dim() != 2:
-        raise ValueError("logits must be [T, E] and topk_idx [T, k]")
+    dev = _gpu(logits, 2, "logits")
+    _gpu(topk_idx, 2, "topk_idx")
     T, E = logits.shape
     k = topk_idx.shape[1]
-    _need(logits, "logits", (T, E), torch.float32)
-    _need(topk_idx, "topk_idx", (T, k), torch.int32)
-    _need(d_topk_w, "d_topk_w", (T, k), torch.float32)
     if dlogits is None:
-        dlogits = torch.empty(T, E, dtype=torch.float32, device=logits.device)
-    _need(dlogits, "dlogits", (T, E), torch.float32)
-    with _on(stream, logits, topk_idx, d_topk_w, dlogits) as s:
-        _check("moe_route_scored_backward", lib.moe_route_scored_backward(
-            _ptr(logits), _ptr(topk_idx), _ptr(d_topk_w), T, E, k, score, 1 if renormalize else 0,
-            scale, _ptr(dlogits), s))
+        dlogits = torch.empty((T, E), dtype=torch.float32, device=dev)
+    _enqueue("moe_route_scored_backward", dev, stream,
+             _arg(logits, "logits", (T, E), torch.float32, dev),
+             _arg(topk_idx, "topk_idx", (T, k), torch.int32, dev),
+             _arg(d_topk_w, "d_topk_w", (T, k), torch.float32, dev), T, E, k, score,
+             1 if renormalize else 0, scale, _arg(dlogits, "dlogits", (T, E), torch.float32, dev))
     return dlogits
 
 
 def moe_quantize_int8(src, codes=None, scales=None, stream=None):
     """src [rows, K] BF16 -> (codes [rows, K] int8, scales [rows] float32)."""
-    if src.dim() != 2:
-        raise ValueError("src must be [rows, K]")
+    dev = _gpu(src, 2, "src")
     rows, K = src.shape
-    _u16(src)
     if codes is None:
-        codes = torch.empty(rows, K, dtype=torch.int8, device=src.device)
+        codes = torch.empty((rows, K), dtype=torch.int8, device=dev)
     if scales is None:
-        scales = torch.empty(rows, dtype=torch.float32, device=src.device)
-    _need(codes, "codes", (rows, K), torch.int8)
-    _need(scales, "scales", (rows,), torch.float32)
-    with _on(stream, src, codes, scales) as s:
-        _check("moe_quantize_int8", lib.moe_quantize_int8(_ptr(src), rows, K, _ptr(codes),
-                                                          _ptr(scales), s))
+        scales = torch.empty(rows, dtype=torch.float32, device=dev)
+    _enqueue("moe_quantize_int8", dev, stream, _arg(src, "src", (rows, K), _BF16, dev), rows, K,
+             _arg(codes, "codes", (rows, K), torch.int8, dev),
+             _arg(scales, "scales", (rows,), torch.float32, dev))
     return codes, scales
 
 
@@ -589,33 +591,26 @@ def moe_experts_int8(x, x_scales, w_gate_up, w_gate_up_scales, w_down, w_down_sc
                      topk_w, out=None, ws=None, stream=None):
     """The routed experts' FFN in INT8 (codes with per-token and per-channel scales) -> out
     [T, H] BF16.  Slots whose expert id lies outside [0, E) add nothing."""
-    if x.dim() != 2 or w_gate_up.dim() != 3 or topk_idx.dim() != 2:
-        raise ValueError("x must be [T, H], w_gate_up [E, 2I, H], topk_idx [T, k]")
+    dev = _gpu(x, 2, "x")
+    _gpu(w_gate_up, 3, "w_gate_up")
+    _gpu(topk_idx, 2, "topk_idx")
     T, H = x.shape
     E, I2, _ = w_gate_up.shape
     I = I2 // 2
     k = topk_idx.shape[1]
-    _need(x, "x", (T, H), torch.int8)
-    _need(x_scales, "x_scales", (T,), torch.float32)
-    _need(w_gate_up, "w_gate_up", (E, 2 * I, H), torch.int8)
-    _need(w_gate_up_scales, "w_gate_up_scales", (E, 2 * I), torch.float32)
-    _need(w_down, "w_down", (E, H, I), torch.int8)
-    _need(w_down_scales, "w_down_scales", (E, H), torch.float32)
-    _need(topk_idx, "topk_idx", (T, k), torch.int32)
-    _need(topk_w, "topk_w", (T, k), torch.float32)
     if out is None:
-        out = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
-    _need(out, "out", (T, H), _BF16)
-    need = moe_experts_int8_workspace_bytes(T, H, I, E, k)
-    if ws is None:
-        ws = workspace(need, x.device)
-    _need_ws(ws, need)
-    with _on(stream, x, x_scales, w_gate_up, w_gate_up_scales, w_down, w_down_scales, topk_idx,
-             topk_w, out, ws) as s:
-        _check("moe_experts_int8", lib.moe_experts_int8(
-            _ptr(x), _ptr(x_scales), _ptr(w_gate_up), _ptr(w_gate_up_scales), _ptr(w_down),
-            _ptr(w_down_scales), _ptr(topk_idx), _ptr(topk_w), T, H, I, E, k, _ptr(out), _ptr(ws),
-            ws.numel(), s))
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    i8, f32 = torch.int8, torch.float32
+    ptrs = (_arg(x, "x", (T, H), i8, dev), _arg(x_scales, "x_scales", (T,), f32, dev),
+            _arg(w_gate_up, "w_gate_up", (E, 2 * I, H), i8, dev),
+            _arg(w_gate_up_scales, "w_gate_up_scales", (E, 2 * I), f32, dev),
+            _arg(w_down, "w_down", (E, H, I), i8, dev),
+            _arg(w_down_scales, "w_down_scales", (E, H), f32, dev),
+            _arg(topk_idx, "topk_idx", (T, k), torch.int32, dev),
+            _arg(topk_w, "topk_w", (T, k), f32, dev))
+    pout = _arg(out, "out", (T, H), _BF16, dev)
+    pws, n = _ws_arg(ws, moe_experts_int8_workspace_bytes(T, H, I, E, k), dev)
+    _enqueue("moe_experts_int8", dev, stream, *ptrs, T, H, I, E, k, pout, pws, n)
     return out
 
 
