@@ -15,6 +15,7 @@
 // product, and the slot sum.  A pair whose expert id lies outside [0, E) has no
 // row: it adds nothing to its token.
 #include "common.h"
+#include "gemm_large.h"
 #include "internal.h"
 #include "tiles.h"
 
@@ -41,7 +42,7 @@ constexpr int kI8CH = kI8C / 16;                   // 16-byte code chunks per ro
 Int8Ws int8_ws_layout(int T, int H, int I, int E, int k) {
   Int8Ws L{};
   const size_t P = static_cast<size_t>(T) * k;
-  L.bm = kBM8;
+  L.bm = P >= static_cast<size_t>(kLargeBM) * E ? kLargeBM : kBM8;
   L.max_tiles = static_cast<int>(E + (P + L.bm - 1) / L.bm);
   size_t o = 0;
   L.n_tiles = o;   o += 256;
@@ -55,6 +56,8 @@ Int8Ws int8_ws_layout(int T, int H, int I, int E, int k) {
   L.scales = o;    o = align256(o + sizeof(float) * P);
   L.y = o;
   if (k > 1) o = align256(o + sizeof(float) * P * H);
+  L.partial = o;
+  if (L.bm == kLargeBM) o = align256(o + sizeof(int) * kLargeMaxSlices * kLargeBM * 256);
   L.total = o;
   return L;
 }
@@ -213,6 +216,305 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4, 8)))
   }
 }
 
+// ---------------------------------------------------------------------------
+// Large groups (256 routed rows per expert and more on average): the products are
+// bound by the matrix cores, and run as an LDS-tiled GEMM.  Workgroup tile 256 rows
+// x 256 weight rows (gate_up: 128 gate + 128 up rows of one expert, so that the
+// epilogue finds g and u in one lane), K in stages of 128 codes; 4 waves of 128 x
+// 128 with v_mfma_i32_32x32x32_i8, accumulators in AGPRs; both tiles staged in LDS
+// (2 stages x 2 x 32 KB, 16-byte chunks XOR-swizzled by row), global loads one
+// stage ahead of the LDS writes, which run one stage ahead of the fragment reads.
+// Lane (l32, hi) takes 16-byte chunk 2 ks + hi of its row at K step ks, of both
+// operands.
+namespace {
+constexpr int k8BK = 128;                                // K per stage
+constexpr int k8Tile = kLargeBM * k8BK;                  // bytes per operand stage
+constexpr size_t k8Lds = 2 * 2 * k8Tile;                 // 128 KB
+typedef int i32x16 __attribute__((__vector_size__(16 * sizeof(int))));
+
+__device__ __forceinline__ i32x16 mfma32_i8(i32x4 a, i32x4 b, i32x16 c) {
+  return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
+}
+
+struct Large8 {                                          // what the tile's epilogue writes with
+  const int* perm;
+  const float* acts;
+  const float* wts;                                      // the expert's weight scales
+  const float* w;
+  int H, I, k;
+  float* y;
+  uint16_t* out;
+};
+
+// Four consecutive outputs (n .. n + 3) of tile row r: acc sums -> FP32 values.
+__device__ __forceinline__ f32x4 scaled4(i32x4 v, float sx, const float* __restrict__ ws) {
+  const f32x4 s = *reinterpret_cast<const f32x4*>(ws);
+  f32x4 o;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) o[t] = static_cast<float>(v[t]) * sx * s[t];
+  return o;
+}
+template <int KIND>
+__device__ __forceinline__ void store4(const Large8& p, int grow, int pr, int n, i32x4 a, i32x4 u,
+                                       float sx) {
+  if (KIND == kGateUp8) {
+    const f32x4 g = scaled4(a, sx, p.wts + n), h = scaled4(u, sx, p.wts + p.I + n);
+    f32x4 o;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) o[t] = swiglu(g[t], h[t]);
+    *reinterpret_cast<f32x4*>(p.y + static_cast<size_t>(grow) * p.I + n) = o;
+  } else {
+    const f32x4 o = scaled4(a, sx, p.wts + n);
+    if (KIND == kDownFused8) {
+      const float wt = p.w[pr];                          // k = 1: pair id == token
+      *reinterpret_cast<uint2*>(p.out + static_cast<size_t>(pr) * p.H + n) =
+          make_uint2(pack_bf16x2(wt * o[0], wt * o[1]), pack_bf16x2(wt * o[2], wt * o[3]));
+    } else {
+      *reinterpret_cast<f32x4*>(p.y + static_cast<size_t>(grow) * p.H + n) = o;
+    }
+  }
+}
+template <int KIND>
+__device__ __forceinline__ float row_scale(const Large8& p, int grow, int pr) {
+  return KIND == kGateUp8 ? p.acts[pr / p.k] : p.acts[grow];
+}
+}  // namespace
+
+template <int KIND>
+__global__ __launch_bounds__(256) void gemm_large_i8(
+    const uint8_t* __restrict__ act, const float* __restrict__ acts,
+    const uint8_t* __restrict__ wt, const float* __restrict__ wts, const int* __restrict__ perm,
+    const int2* __restrict__ tiles, const int* __restrict__ n_tiles,
+    const int* __restrict__ counts, const int* __restrict__ offsets, const float* __restrict__ w,
+    int H, int I, int k, float* __restrict__ y, uint16_t* __restrict__ out,
+    int* __restrict__ partial, int ncu, uint32_t okey) {
+  extern __shared__ __align__(16) uint8_t lds8[];        // [stage][A, B][256 x 128]
+  constexpr bool GU = KIND == kGateUp8;
+  const int K = GU ? H : I;
+  const int nblk = GU ? I / 128 : H / 256;
+  const int nk = K / k8BK;
+  const int L = blockIdx.x;
+  int item, kb = 0, ke = nk, slot = -1;
+  {
+    const int n_real = nblk * *n_tiles;
+    const TailPlan plan = tail_plan(n_real, ncu, nk);
+    if (plan.S > 1 && L < plan.full) {
+      item = permute_item(round_item(L, plan.full, ncu), plan.full, okey);
+    } else if (plan.S > 1) {
+      const int t0 = L - plan.full;
+      if (t0 >= plan.rem * plan.S) return;
+      const int t = permute_item(t0, plan.rem * plan.S, okey);
+      item = plan.full + t % plan.rem;
+      const int sl = t / plan.rem;
+      kb = sl * nk / plan.S;
+      ke = (sl + 1) * nk / plan.S;
+      slot = t;
+    } else {
+      item = round_real_item(L, nblk, *n_tiles, ncu);
+      if (item < 0) return;
+      item = permute_item(item, n_real, okey);
+    }
+  }
+  int tile, nb;
+  large_coords(item, nblk, *n_tiles, tile, nb);
+  const int2 te = tiles[tile];
+  const int e = te.x, m0 = te.y;
+  const int mcount = min(kLargeBM, counts[e] - m0);
+  const int rbase = offsets[e] + m0;
+  const int tid = threadIdx.x, wv = tid >> 6, ln = tid & 63, l32 = ln & 31, hi = ln >> 5;
+  const int wm = wv & 1, wn = wv >> 1;
+
+  // loader: thread covers tile rows wv*64 + 8j + (ln >> 3), j = 0..7, of both operands,
+  // 16-byte chunk ln & 7 of each 128-byte row segment
+  const int lrow = ln >> 3, lc = ln & 7;
+  const size_t wrows = GU ? 2 * static_cast<size_t>(I) : static_cast<size_t>(H);
+  const uint8_t* __restrict__ abase = wt + static_cast<size_t>(e) * wrows * K;
+  const int n0 = nb * 128;
+  const int arow = GU ? (wv < 2 ? n0 + wv * 64 : I + n0 + (wv - 2) * 64) : nb * 256 + wv * 64;
+  const uint32_t ao = static_cast<uint32_t>((arow + lrow) * K + lc * 16);
+  uint32_t bo[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int r = wv * 64 + 8 * j + lrow;
+    const int rr = r < mcount ? r : 0;
+    bo[j] = static_cast<uint32_t>((GU ? perm[rbase + rr] / k : rbase + rr) * K + lc * 16);
+  }
+  // LDS: row r, chunk c at r*128 + ((c ^ (r & 7)) * 16); here r & 7 == lrow
+  const int lw = (wv * 64 + lrow) * k8BK + ((lc ^ lrow) * 16);
+  int fa[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    fa[i] = ((GU ? (i >> 1) * 128 + wn * 64 + (i & 1) * 32 : wn * 128 + 32 * i) + l32) * k8BK;
+  const int fb = (wm * 128 + l32) * k8BK;
+  const int swz = l32 & 7;
+
+  i32x4 stg[16];   // [0..7] weight rows, [8..15] activation rows
+#define GLOAD(Q, KT) do {                                                               \
+    const uint32_t kk_ = static_cast<uint32_t>(min((KT), ke - 1) * k8BK);               \
+    if ((Q) < 8) stg[Q] = ld16(abase + ao + static_cast<uint32_t>((Q) * 8) * K + kk_);  \
+    else stg[Q] = ld16(act + bo[(Q) - 8] + kk_);                                        \
+  } while (0)
+#define LWRITE(Q, KT) do {                                                              \
+    uint8_t* st_ = lds8 + ((KT) & 1) * 2 * k8Tile + ((Q) < 8 ? 0 : k8Tile);             \
+    *reinterpret_cast<i32x4*>(&st_[lw + ((Q) & 7) * 8 * k8BK]) = stg[Q];                \
+  } while (0)
+#define RDF(PTR) (*reinterpret_cast<const i32x4*>(PTR))
+  // One MFMA K step on fragments (A, B): 8 groups of 2 MFMAs; groups 0..3 then read
+  // fragments A g and B g of the next K step (stage RKT, step RKS) and write staged
+  // chunk Q0+g of stage WKT to LDS and reload it from stage WKT+1.  sched_barrier
+  // keeps this order.
+#define PHASE(A, B, NA, NB, RKT, RKS, WKT, Q0) do {                                     \
+    const uint8_t* at_ = lds8 + ((RKT) & 1) * 2 * k8Tile;                               \
+    const uint8_t* bt_ = at_ + k8Tile;                                                  \
+    const int so_ = (((2 * (RKS) + hi) ^ swz) * 16);                                    \
+    _Pragma("unroll") for (int g = 0; g < 8; ++g) {                                     \
+      const int i_ = g >> 1, j0_ = (g & 1) * 2;                                         \
+      acc[i_][j0_] = mfma32_i8(A[i_], B[j0_], acc[i_][j0_]);                            \
+      acc[i_][j0_ + 1] = mfma32_i8(A[i_], B[j0_ + 1], acc[i_][j0_ + 1]);                \
+      __builtin_amdgcn_sched_barrier(0);                                                \
+      if (g < 4) {                                                                      \
+        NA[g] = RDF(&at_[fa[g] + so_]);                                                 \
+        NB[g] = RDF(&bt_[fb + 32 * g * k8BK + so_]);                                    \
+        LWRITE((Q0) + g, WKT);                                                          \
+        GLOAD((Q0) + g, (WKT) + 1);                                                     \
+      }                                                                                 \
+      __builtin_amdgcn_sched_barrier(0);                                                \
+    }                                                                                   \
+  } while (0)
+
+  i32x16 acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
+  // The LDS writes of stage s+1 are spread over the four K steps that may write its
+  // buffer: the last step of stage s-1 (chunks 12..15, after the barrier that ends
+  // the reads of stage s-1) and the first three of stage s (chunks 0..11, before the
+  // barrier that publishes stage s+1).
+#pragma unroll
+  for (int q = 0; q < 16; ++q) GLOAD(q, kb);
+#pragma unroll
+  for (int q = 0; q < 16; ++q) LWRITE(q, kb);
+#pragma unroll
+  for (int q = 0; q < 16; ++q) GLOAD(q, kb + 1);
+#pragma unroll
+  for (int q = 12; q < 16; ++q) { LWRITE(q, kb + 1); GLOAD(q, kb + 2); }
+  __syncthreads();
+  i32x4 a0[4], b0[4], a1[4], b1[4];
+  {
+    const uint8_t* at = lds8 + (kb & 1) * 2 * k8Tile;
+    const int so = (hi ^ swz) * 16;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) a0[g] = RDF(&at[fa[g] + so]);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) b0[g] = RDF(&at[k8Tile + fb + 32 * g * k8BK + so]);
+  }
+  for (int kt = kb; kt < ke; ++kt) {
+    PHASE(a0, b0, a1, b1, kt, 1, kt + 1, 0);
+    PHASE(a1, b1, a0, b0, kt, 2, kt + 1, 4);
+    PHASE(a0, b0, a1, b1, kt, 3, kt + 1, 8);
+    // stage kt+1 is in LDS for every wave, and every wave is done reading stage kt
+    wait_lgkm0();
+    __builtin_amdgcn_s_barrier();
+    PHASE(a1, b1, a0, b0, kt + 1, 0, kt + 2, 12);
+  }
+#undef GLOAD
+#undef LWRITE
+#undef RDF
+#undef PHASE
+  if (slot >= 0) {
+    // tail slice: INT32 partial tile in register order, [64 x i32x4][256 threads]
+    i32x4* pp = reinterpret_cast<i32x4*>(partial) + static_cast<size_t>(slot) * 64 * 256 + tid;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          pp[((i * 4 + j) * 4 + q) * 256] =
+              i32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    return;
+  }
+  // lane (l32, hi), register 4q + t of block (i, j): weight row 8q + 4hi + t, tile row l32
+  const Large8 p{perm, acts, wts + static_cast<size_t>(e) * wrows, w, H, I, k, y, out};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = wm * 128 + 32 * j + l32;
+    if (r >= mcount) continue;
+    const int pr = perm[rbase + r];
+    const float sx = row_scale<KIND>(p, rbase + r, pr);
+#pragma unroll
+    for (int i = 0; i < (GU ? 2 : 4); ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int n = (GU ? n0 + wn * 64 : nb * 256 + wn * 128) + 32 * i + 8 * q + 4 * hi;
+        const int iu = GU ? i + 2 : i;
+        store4<KIND>(p, rbase + r, pr, n,
+                     i32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]},
+                     i32x4{acc[iu][j][4 * q], acc[iu][j][4 * q + 1], acc[iu][j][4 * q + 2], acc[iu][j][4 * q + 3]}, sx);
+      }
+  }
+}
+
+// Tail fix-up, element-parallel: thread g of the grid takes one i32x4 of the partial
+// tile of tail item full + g / per_item (register order of the GEMM's thread), adds it
+// over the S slices and applies that piece of the epilogue.
+template <int KIND>
+__global__ __launch_bounds__(256) void gemm_large_i8_fixup(
+    const float* __restrict__ acts, const float* __restrict__ wts, const int* __restrict__ perm,
+    const int2* __restrict__ tiles, const int* __restrict__ n_tiles,
+    const int* __restrict__ counts, const int* __restrict__ offsets, const float* __restrict__ w,
+    int H, int I, int k, float* __restrict__ y, uint16_t* __restrict__ out,
+    const int* __restrict__ partial, int ncu, uint32_t okey) {
+  constexpr bool GU = KIND == kGateUp8;
+  constexpr int kPerItem = GU ? 32 * 256 : 64 * 256;     // threads per tail item
+  const int nblk = GU ? I / 128 : H / 256;
+  const TailPlan plan = tail_plan(nblk * *n_tiles, ncu, (GU ? H : I) / k8BK);
+  const int g = permute_item(blockIdx.x, gridDim.x, okey) * 256 + threadIdx.x;
+  const int b = g / kPerItem;
+  if (plan.S == 1 || b >= plan.rem) return;
+  const int f = g - b * kPerItem;                        // i32x4 index within the tile
+  const int tid = f & 255, ijq = f >> 8;
+  const int i = ijq >> 4, j = (ijq >> 2) & 3, q = ijq & 3;
+  int tile, nb;
+  large_coords(plan.full + b, nblk, *n_tiles, tile, nb);
+  const int2 te = tiles[tile];
+  const int e = te.x, m0 = te.y;
+  const int mcount = min(kLargeBM, counts[e] - m0);
+  const int rbase = offsets[e] + m0;
+  const int wv = tid >> 6, ln = tid & 63, l32 = ln & 31, hi = ln >> 5;
+  const int wm = wv & 1, wn = wv >> 1;
+  const int r = wm * 128 + 32 * j + l32;
+  if (r >= mcount) return;
+  const i32x4* pp = reinterpret_cast<const i32x4*>(partial) + f;
+  i32x4 a = {0, 0, 0, 0}, u = {0, 0, 0, 0};
+  for (int sl = 0; sl < plan.S; ++sl) {
+    const size_t base = static_cast<size_t>(sl * plan.rem + b) * 64 * 256;
+    a += pp[base];
+    if (GU) u += pp[base + 2 * 16 * 256];                // up block i + 2
+  }
+  const size_t wrows = GU ? 2 * static_cast<size_t>(I) : static_cast<size_t>(H);
+  const Large8 p{perm, acts, wts + static_cast<size_t>(e) * wrows, w, H, I, k, y, out};
+  const int pr = perm[rbase + r];
+  const int n = (GU ? nb * 128 + wn * 64 : nb * 256 + wn * 128) + 32 * i + 8 * q + 4 * hi;
+  store4<KIND>(p, rbase + r, pr, n, a, u, row_scale<KIND>(p, rbase + r, pr));
+}
+
+hipError_t int8_set_attributes() {
+  const int bytes = static_cast<int>(k8Lds);
+  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(gemm_large_i8<kGateUp8>),
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess)
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(gemm_large_i8<kDown8>),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == hipSuccess)
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(gemm_large_i8<kDownFused8>),
+                            hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  return e;
+}
+
 // Codes and scales of the FP32 activations, one grouped row per workgroup (I a
 // multiple of 256, at most 16384).  With k = 1 a pair without a row (expert id out
 // of range) gets its output row cleared here, as no down tile will write it.
@@ -270,21 +572,33 @@ hipError_t launch_experts_int8(const int8_t* x, const float* xs, const int8_t* w
   const uint8_t* x8 = reinterpret_cast<const uint8_t*>(x);
   const uint8_t* wgu8 = reinterpret_cast<const uint8_t*>(wgu);
   const uint8_t* wd8 = reinterpret_cast<const uint8_t*>(wd);
+  int* partial = reinterpret_cast<int*>(b + L.partial);
+  const bool large = L.bm == kLargeBM;
+  // grid of the large tiles: every item whole, plus room for the tail slices (rem * S - rem < ncu)
+  auto large_grid = [&](int nblk) { return dim3(round_up(nblk * L.max_tiles + num_cus, kXcds)); };
+#define ARGS perm, tiles, n_tiles, counts, offsets, w, H, I, k
+#define LARGE8(KD, A, AS, W, WS, Y, O, NBLK, PER)                                              \
+  hipLaunchKernelGGL(gemm_large_i8<KD>, large_grid(NBLK), dim3(256), k8Lds, s, A, AS, W, WS,  \
+                     ARGS, Y, O, partial, num_cus, order_key());                              \
+  hipLaunchKernelGGL(gemm_large_i8_fixup<KD>, dim3(num_cus / 2 * PER), dim3(256), 0, s, AS, WS, \
+                     ARGS, Y, O, partial, num_cus, order_key())
+#define STREAM8(KD, A, AS, W, WS, Y, O, NBLK)                                                 \
+  hipLaunchKernelGGL((gemm_i8s<KD, 8>), dim3(round_up((NBLK) * L.max_tiles, kXcds)), dim3(512), \
+                     0, s, A, AS, W, WS, ARGS, Y, O, order_key())
   prof_begin(kInt8GateUp, s);
-  hipLaunchKernelGGL((gemm_i8s<kGateUp8, 8>), dim3(round_up((I / 128) * L.max_tiles, kXcds)), dim3(512),
-                     0, s, x8, xs, wgu8, wgus, perm, tiles, n_tiles, counts, offsets, nullptr, H, I, k,
-                     act, nullptr, order_key());
+  if (large) { LARGE8(kGateUp8, x8, xs, wgu8, wgus, act, nullptr, I / 128, 32); }
+  else STREAM8(kGateUp8, x8, xs, wgu8, wgus, act, nullptr, I / 128);
   prof_end(kInt8GateUp, s);
   hipLaunchKernelGGL(quant_act_rows, dim3(P), dim3(256), 0, s, act, offsets, E, row_of, P, H, I, codes,
                      scales, k == 1 ? out : nullptr, order_key());
   prof_begin(kInt8Down, s);
-  const dim3 grid(round_up((H / 256) * L.max_tiles, kXcds));
-  if (k == 1)
-    hipLaunchKernelGGL((gemm_i8s<kDownFused8, 8>), grid, dim3(512), 0, s, codes, scales, wd8, wds, perm,
-                       tiles, n_tiles, counts, offsets, w, H, I, k, nullptr, out, order_key());
-  else
-    hipLaunchKernelGGL((gemm_i8s<kDown8, 8>), grid, dim3(512), 0, s, codes, scales, wd8, wds, perm,
-                       tiles, n_tiles, counts, offsets, w, H, I, k, y, nullptr, order_key());
+  if (large && k == 1) { LARGE8(kDownFused8, codes, scales, wd8, wds, nullptr, out, H / 256, 64); }
+  else if (large) { LARGE8(kDown8, codes, scales, wd8, wds, y, nullptr, H / 256, 64); }
+  else if (k == 1) STREAM8(kDownFused8, codes, scales, wd8, wds, nullptr, out, H / 256);
+  else STREAM8(kDown8, codes, scales, wd8, wds, y, nullptr, H / 256);
+#undef ARGS
+#undef LARGE8
+#undef STREAM8
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && k > 1)
     e = launch_combine_slots(y, row_of, w, T, H, k, out, 0, H, H, s, num_cus);
