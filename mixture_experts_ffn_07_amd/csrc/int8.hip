@@ -236,47 +236,14 @@ __device__ __forceinline__ i32x16 mfma32_i8(i32x4 a, i32x4 b, i32x16 c) {
   return __builtin_amdgcn_mfma_i32_32x32x32_i8(a, b, c, 0, 0, 0);
 }
 
-struct Large8 {                                          // what the tile's epilogue writes with
-  const int* perm;
-  const float* acts;
-  const float* wts;                                      // the expert's weight scales
-  const float* w;
-  int H, I, k;
-  float* y;
-  uint16_t* out;
-};
-
-// Four consecutive outputs (n .. n + 3) of tile row r: acc sums -> FP32 values.
-__device__ __forceinline__ f32x4 scaled4(i32x4 v, float sx, const float* __restrict__ ws) {
-  const f32x4 s = *reinterpret_cast<const f32x4*>(ws);
-  f32x4 o;
-#pragma unroll
-  for (int t = 0; t < 4; ++t) o[t] = static_cast<float>(v[t]) * sx * s[t];
-  return o;
-}
-template <int KIND>
-__device__ __forceinline__ void store4(const Large8& p, int grow, int pr, int n, i32x4 a, i32x4 u,
-                                       float sx) {
-  if (KIND == kGateUp8) {
-    const f32x4 g = scaled4(a, sx, p.wts + n), h = scaled4(u, sx, p.wts + p.I + n);
-    f32x4 o;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) o[t] = swiglu(g[t], h[t]);
-    *reinterpret_cast<f32x4*>(p.y + static_cast<size_t>(grow) * p.I + n) = o;
-  } else {
-    const f32x4 o = scaled4(a, sx, p.wts + n);
-    if (KIND == kDownFused8) {
-      const float wt = p.w[pr];                          // k = 1: pair id == token
-      *reinterpret_cast<uint2*>(p.out + static_cast<size_t>(pr) * p.H + n) =
-          make_uint2(pack_bf16x2(wt * o[0], wt * o[1]), pack_bf16x2(wt * o[2], wt * o[3]));
-    } else {
-      *reinterpret_cast<f32x4*>(p.y + static_cast<size_t>(grow) * p.H + n) = o;
-    }
-  }
-}
-template <int KIND>
-__device__ __forceinline__ float row_scale(const Large8& p, int grow, int pr) {
-  return KIND == kGateUp8 ? p.acts[pr / p.k] : p.acts[grow];
+// Two lanes that hold neighbouring columns (even, odd) and the values of two rows
+// (v0, v1) exchange one value each: the even lane returns both columns of the first
+// row, the odd lane both of the second, as two BF16 (the lower column in the low half).
+__device__ __forceinline__ uint32_t pair_rows_bf16(float v0, float v1, int odd) {
+  const float give = odd ? v0 : v1;
+  const float got = __int_as_float(__builtin_amdgcn_update_dpp(
+      0, __float_as_int(give), 0xB1, 0xF, 0xF, true));            // quad_perm [1,0,3,2]
+  return odd ? pack_bf16x2(got, v1) : pack_bf16x2(v0, got);
 }
 }  // namespace
 
@@ -324,6 +291,11 @@ __global__ __launch_bounds__(256) void gemm_large_i8(
   const int tid = threadIdx.x, wv = tid >> 6, ln = tid & 63, l32 = ln & 31, hi = ln >> 5;
   const int wm = wv & 1, wn = wv >> 1;
 
+  // the epilogue's data of tile row tid, loaded here: its latency passes during the products
+  const int my_pr = perm[rbase + min(tid, mcount - 1)];
+  const float my_sx = GU ? acts[my_pr / k] : acts[rbase + min(tid, mcount - 1)];
+  const float my_w = KIND == kDownFused8 ? w[my_pr] : 0.f;  // k = 1: pair id == token
+
   // loader: thread covers tile rows wv*64 + 8j + (ln >> 3), j = 0..7, of both operands,
   // 16-byte chunk ln & 7 of each 128-byte row segment
   const int lrow = ln >> 3, lc = ln & 7;
@@ -369,8 +341,8 @@ __global__ __launch_bounds__(256) void gemm_large_i8(
     const int so_ = (((2 * (RKS) + hi) ^ swz) * 16);                                    \
     _Pragma("unroll") for (int g = 0; g < 8; ++g) {                                     \
       const int i_ = g >> 1, j0_ = (g & 1) * 2;                                         \
-      acc[i_][j0_] = mfma32_i8(A[i_], B[j0_], acc[i_][j0_]);                            \
-      acc[i_][j0_ + 1] = mfma32_i8(A[i_], B[j0_ + 1], acc[i_][j0_ + 1]);                \
+      acc[i_][j0_] = mfma32_i8(B[j0_], A[i_], acc[i_][j0_]);                            \
+      acc[i_][j0_ + 1] = mfma32_i8(B[j0_ + 1], A[i_], acc[i_][j0_ + 1]);                \
       __builtin_amdgcn_sched_barrier(0);                                                \
       if (g < 4) {                                                                      \
         NA[g] = RDF(&at_[fa[g] + so_]);                                                 \
@@ -437,25 +409,63 @@ __global__ __launch_bounds__(256) void gemm_large_i8(
               i32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
     return;
   }
-  // lane (l32, hi), register 4q + t of block (i, j): weight row 8q + 4hi + t, tile row l32
-  const Large8 p{perm, acts, wts + static_cast<size_t>(e) * wrows, w, H, I, k, y, out};
+  // Lane (l32, hi), register 4q + t of block (i, j): output column l32 of weight block
+  // i, tile row 8q + 4hi + t of row block j - a store instruction writes 128
+  // consecutive bytes of two rows (FP32), or 64 of four (BF16, columns paired over
+  // lanes).  The rows' scales, pair ids and weights go through LDS, four rows a read.
+  const float* wse = wts + static_cast<size_t>(e) * wrows;
+  float* s_sx = reinterpret_cast<float*>(lds8);
+  int* s_pr = reinterpret_cast<int*>(lds8) + kLargeBM;
+  float* s_w = reinterpret_cast<float*>(lds8) + 2 * kLargeBM;
+  __syncthreads();                                       // every wave is done with the K stages
+  s_sx[tid] = my_sx;
+  s_pr[tid] = my_pr;
+  s_w[tid] = my_w;
+  __syncthreads();
+  float ws[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = wm * 128 + 32 * j + l32;
-    if (r >= mcount) continue;
-    const int pr = perm[rbase + r];
-    const float sx = row_scale<KIND>(p, rbase + r, pr);
+  for (int i = 0; i < 4; ++i)
+    ws[i] = wse[GU ? (i >> 1) * I + n0 + wn * 64 + (i & 1) * 32 + l32 : nb * 256 + wn * 128 + 32 * i + l32];
 #pragma unroll
-    for (int i = 0; i < (GU ? 2 : 4); ++i)
+  for (int j = 0; j < 4; ++j)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int n = (GU ? n0 + wn * 64 : nb * 256 + wn * 128) + 32 * i + 8 * q + 4 * hi;
-        const int iu = GU ? i + 2 : i;
-        store4<KIND>(p, rbase + r, pr, n,
-                     i32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]},
-                     i32x4{acc[iu][j][4 * q], acc[iu][j][4 * q + 1], acc[iu][j][4 * q + 2], acc[iu][j][4 * q + 3]}, sx);
+    for (int q = 0; q < 4; ++q) {
+      const int r0 = wm * 128 + 32 * j + 8 * q + 4 * hi;
+      if (r0 >= mcount) continue;
+      const f32x4 sx = *reinterpret_cast<const f32x4*>(s_sx + r0);
+      if (KIND == kDownFused8) {
+        const i32x4 pr = *reinterpret_cast<const i32x4*>(s_pr + r0);
+        const f32x4 wt4 = *reinterpret_cast<const f32x4*>(s_w + r0);
+        const int odd = l32 & 1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float v[4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+            v[t] = wt4[t] * (static_cast<float>(acc[i][j][4 * q + t]) * sx[t] * ws[i]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t o = pair_rows_bf16(v[2 * h], v[2 * h + 1], odd);
+            const int t = 2 * h + odd;
+            if (r0 + t < mcount)
+              *reinterpret_cast<uint32_t*>(out + static_cast<size_t>(odd ? pr[2 * h + 1] : pr[2 * h]) * H +
+                                           nb * 256 + wn * 128 + 32 * i + l32 - odd) = o;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          if (r0 + t >= mcount) continue;
+          float* yr = y + static_cast<size_t>(rbase + r0 + t) * (GU ? I : H) +
+                      (GU ? n0 + wn * 64 : nb * 256 + wn * 128) + l32;
+#pragma unroll
+          for (int i = 0; i < (GU ? 2 : 4); ++i) {
+            const float v = static_cast<float>(acc[i][j][4 * q + t]) * sx[t] * ws[i];
+            yr[32 * i] = GU ? swiglu(v, static_cast<float>(acc[(i + 2) & 3][j][4 * q + t]) * sx[t] * ws[(i + 2) & 3]) : v;
+          }
+        }
       }
-  }
+    }
 }
 
 // Tail fix-up, element-parallel: thread g of the grid takes one i32x4 of the partial
@@ -486,8 +496,8 @@ __global__ __launch_bounds__(256) void gemm_large_i8_fixup(
   const int rbase = offsets[e] + m0;
   const int wv = tid >> 6, ln = tid & 63, l32 = ln & 31, hi = ln >> 5;
   const int wm = wv & 1, wn = wv >> 1;
-  const int r = wm * 128 + 32 * j + l32;
-  if (r >= mcount) return;
+  const int r0 = wm * 128 + 32 * j + 8 * q + 4 * hi;      // rows r0 .. r0 + 3, one column
+  if (r0 >= mcount) return;
   const i32x4* pp = reinterpret_cast<const i32x4*>(partial) + f;
   i32x4 a = {0, 0, 0, 0}, u = {0, 0, 0, 0};
   for (int sl = 0; sl < plan.S; ++sl) {
@@ -495,11 +505,17 @@ __global__ __launch_bounds__(256) void gemm_large_i8_fixup(
     a += pp[base];
     if (GU) u += pp[base + 2 * 16 * 256];                // up block i + 2
   }
-  const size_t wrows = GU ? 2 * static_cast<size_t>(I) : static_cast<size_t>(H);
-  const Large8 p{perm, acts, wts + static_cast<size_t>(e) * wrows, w, H, I, k, y, out};
-  const int pr = perm[rbase + r];
-  const int n = (GU ? nb * 128 + wn * 64 : nb * 256 + wn * 128) + 32 * i + 8 * q + 4 * hi;
-  store4<KIND>(p, rbase + r, pr, n, a, u, row_scale<KIND>(p, rbase + r, pr));
+  const int n = (GU ? nb * 128 + wn * 64 : nb * 256 + wn * 128) + 32 * i + l32;
+  const float* wse = wts + static_cast<size_t>(e) * (GU ? 2 * static_cast<size_t>(I) : static_cast<size_t>(H));
+  const float wa = wse[n], wu = GU ? wse[I + n] : 0.f;
+  for (int t = 0; t < 4 && r0 + t < mcount; ++t) {
+    const int row = rbase + r0 + t, pr = perm[row];
+    const float sx = GU ? acts[pr / k] : acts[row];
+    const float v = static_cast<float>(a[t]) * sx * wa;
+    if (GU) y[static_cast<size_t>(row) * I + n] = swiglu(v, static_cast<float>(u[t]) * sx * wu);
+    else if (KIND == kDownFused8) out[static_cast<size_t>(pr) * H + n] = static_cast<uint16_t>(f32_to_bf16_rne(w[pr] * v));
+    else y[static_cast<size_t>(row) * H + n] = v;
+  }
 }
 
 hipError_t int8_set_attributes() {
