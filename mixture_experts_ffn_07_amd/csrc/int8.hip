@@ -566,6 +566,157 @@ __global__ __launch_bounds__(256) void quant_act_rows(const float* __restrict__ 
   if (threadIdx.x == 0) scales[b] = int8_scale(amax);
 }
 
+// ---------------------------------------------------------------------------
+// Few pairs (a decode step): two launches, every routed pair on its own, its weights
+// straight from HBM into v_dot4 operands.  A wave reads 8 weight rows x 128
+// contiguous bytes a load, lane (row ln >> 3, 16-byte chunk ln & 7), and keeps up to
+// 16 such loads in flight: the step is bound by the latency of its two dependent
+// passes over memory, not by arithmetic, and needs no grouping.  Pairs that share an
+// expert read its weights from the L2 the second time.
+namespace {
+// Dot product of 16 codes with 16 codes, added to c.
+__device__ __forceinline__ int dot16(i32x4 a, i32x4 b, int c) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) c = __builtin_amdgcn_sdot4(a[i], b[i], c, false);
+  return c;
+}
+// Sum over the 8 lanes of a row (ln & 7), on each of them.
+__device__ __forceinline__ int sum8(int v) {
+#pragma unroll
+  for (int m = 1; m < 8; m <<= 1) v += __shfl_xor(v, m, kWave);
+  return v;
+}
+// Dot products of 8 weight rows (lane (ln >> 3, ln & 7): wrow = its row + 16 (ln & 7))
+// with the codes at x + 16 (ln & 7), K a multiple of 128: U loads of each in flight.
+template <int U>
+__device__ __forceinline__ int rows_dot(const uint8_t* wrow, const uint8_t* x, int K) {
+  int acc = 0;
+  for (int k0 = 0; k0 < K; k0 += 128 * U) {
+    i32x4 a[U], b[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k0 + 128 * u < K) a[u] = ld16_stream(wrow + k0 + 128 * u);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k0 + 128 * u < K) b[u] = *reinterpret_cast<const i32x4*>(x + k0 + 128 * u);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k0 + 128 * u < K) acc = dot16(a[u], b[u], acc);
+  }
+  return sum8(acc);
+}
+constexpr int kPairsMax = 64;                            // pairs up to which this form is taken
+constexpr size_t kPairsLds = 64 << 10;                   // LDS that a kernel may use without an attribute
+constexpr int kPairCols = 8;                             // output columns per workgroup of the down pass
+constexpr int kPairWaves = 8;
+inline size_t pairs_lds(int P, int I) {
+  return static_cast<size_t>(kPairWaves) * I + sizeof(float) * kPairCols * P;
+}
+}  // namespace
+
+// Gate/up and SwiGLU: workgroup (pair, 16 neurons); waves 0, 1 the gate rows, 2, 3 the
+// up rows.  a[pair][I] FP32.
+__global__ __launch_bounds__(256) void pairs_gate_up(
+    const uint8_t* __restrict__ x, const float* __restrict__ xs, const uint8_t* __restrict__ wgu,
+    const float* __restrict__ wgus, const int32_t* __restrict__ idx, int H, int I, int E, int k,
+    int P, float* __restrict__ a, uint32_t okey) {
+  __shared__ int s_dot[32];
+  const int nblk = I / 16;
+  const int item = permute_item(blockIdx.x, nblk * P, okey);
+  const int p = item / nblk, n0 = (item - p * nblk) * 16;
+  const int e = idx[p];
+  if (static_cast<unsigned>(e) >= static_cast<unsigned>(E)) return;
+  const int t = p / k, ln = lane_id(), wv = wave_id();
+  const int row = (wv >> 1) * I + n0 + (wv & 1) * 8 + (ln >> 3);
+  const int d = rows_dot<16>(wgu + static_cast<size_t>(e) * 2 * I * H + static_cast<uint32_t>(row) * H + 16 * (ln & 7),
+                             x + static_cast<size_t>(t) * H + 16 * (ln & 7), H);
+  if ((ln & 7) == 0) s_dot[wv * 8 + (ln >> 3)] = d;
+  __syncthreads();
+  const int c = threadIdx.x;
+  if (c < 16) {
+    const float sx = xs[t];
+    const float* ws = wgus + static_cast<size_t>(e) * 2 * I + n0 + c;
+    const float g = static_cast<float>(s_dot[c]) * sx * ws[0];
+    const float u = static_cast<float>(s_dot[16 + c]) * sx * ws[I];
+    a[static_cast<size_t>(p) * I + n0 + c] = swiglu(g, u);
+  }
+}
+
+// Down and the weighted sum: workgroup = 8 output columns, a wave per pair in turn (its
+// activations' codes in the wave's I bytes of LDS, made from a[pair] by the wave
+// itself); then out[t] from the pairs' values in slot order.
+__global__ __launch_bounds__(kPairWaves * kWave) void pairs_down(
+    const float* __restrict__ a, const uint8_t* __restrict__ wd, const float* __restrict__ wds,
+    const int32_t* __restrict__ idx, const float* __restrict__ w, int H, int I, int E, int k, int P,
+    uint16_t* __restrict__ out, uint32_t okey) {
+  extern __shared__ __align__(16) uint8_t lds8[];        // [wave][I] codes, then [P][8] values
+  float* val = reinterpret_cast<float*>(lds8 + kPairWaves * I);
+  const int ln = lane_id(), wv = wave_id();
+  const int n0 = permute_item(blockIdx.x, gridDim.x, okey) * kPairCols;
+  uint8_t* codes = lds8 + wv * I;
+  for (int p = wv; p < P; p += kPairWaves) {
+    const int e = idx[p];
+    if (static_cast<unsigned>(e) >= static_cast<unsigned>(E)) continue;
+    const float* row = a + static_cast<size_t>(p) * I;
+    const uint8_t* wrow = wd + static_cast<size_t>(e) * H * I + static_cast<uint32_t>(n0 + (ln >> 3)) * I + 16 * (ln & 7);
+    // the first 16 loads of the weights, in flight while the codes are made
+    i32x4 wr[16];
+#pragma unroll
+    for (int u = 0; u < 16; ++u)
+      if (128 * u < I) wr[u] = ld16_stream(wrow + 128 * u);
+    f32x4 v[8];                                          // the first 2048 activations
+    float amax = 0.f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int c = 4 * (u * kWave + ln);
+      v[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (c < I) v[u] = *reinterpret_cast<const f32x4*>(row + c);
+      amax = fmaxf(fmaxf(fmaxf(amax, fabsf(v[u][0])), fabsf(v[u][1])), fmaxf(fabsf(v[u][2]), fabsf(v[u][3])));
+    }
+    for (int c = 2048 + 4 * ln; c < I; c += 4 * kWave) {
+      const f32x4 z = *reinterpret_cast<const f32x4*>(row + c);
+      amax = fmaxf(fmaxf(fmaxf(amax, fabsf(z[0])), fabsf(z[1])), fmaxf(fabsf(z[2]), fabsf(z[3])));
+    }
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor(amax, m, kWave));
+    const float inv = int8_inverse(amax);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int c = 4 * (u * kWave + ln);
+      if (c < I) *reinterpret_cast<uint32_t*>(codes + c) = int8_codes4(v[u][0], v[u][1], v[u][2], v[u][3], inv);
+    }
+    for (int c = 2048 + 4 * ln; c < I; c += 4 * kWave) {
+      const f32x4 z = *reinterpret_cast<const f32x4*>(row + c);
+      *reinterpret_cast<uint32_t*>(codes + c) = int8_codes4(z[0], z[1], z[2], z[3], inv);
+    }
+    // the wave's own codes: its LDS operations complete in order
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    int acc = 0;
+#pragma unroll
+    for (int u = 0; u < 16; ++u)
+      if (128 * u < I) acc = dot16(wr[u], *reinterpret_cast<const i32x4*>(codes + 128 * u + 16 * (ln & 7)), acc);
+    acc = sum8(acc);
+    if (I > 2048) acc += rows_dot<16>(wrow + 2048, codes + 2048 + 16 * (ln & 7), I - 2048);
+    if ((ln & 7) == 0) {
+      const int c = ln >> 3;
+      val[p * kPairCols + c] = static_cast<float>(acc) * int8_scale(amax) * wds[static_cast<size_t>(e) * H + n0 + c];
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  __syncthreads();
+  const int T = P / k;
+  for (int i = threadIdx.x; i < T * kPairCols; i += blockDim.x) {
+    const int t = i / kPairCols, c = i % kPairCols;
+    float o = 0.f;
+    for (int j = 0; j < k; ++j) {
+      const int p = t * k + j;
+      if (static_cast<unsigned>(idx[p]) < static_cast<unsigned>(E)) o = fmaf(w[p], val[p * kPairCols + c], o);
+    }
+    out[static_cast<size_t>(t) * H + n0 + c] = static_cast<uint16_t>(f32_to_bf16_rne(o));
+  }
+}
+
 hipError_t launch_experts_int8(const int8_t* x, const float* xs, const int8_t* wgu,
                                const float* wgus, const int8_t* wd, const float* wds,
                                const int32_t* idx, const float* w, int T, int H, int I, int E,
@@ -583,11 +734,22 @@ hipError_t launch_experts_int8(const int8_t* x, const float* xs, const int8_t* w
   uint8_t* codes = reinterpret_cast<uint8_t*>(b + L.codes);
   float* scales = reinterpret_cast<float*>(b + L.scales);
   float* y = reinterpret_cast<float*>(b + L.y);
-  if (const hipError_t e = launch_group_experts(idx, P, E, L.bm, counts, offsets, tiles, n_tiles,
-                                                perm, row_of, s); e != hipSuccess) return e;
   const uint8_t* x8 = reinterpret_cast<const uint8_t*>(x);
   const uint8_t* wgu8 = reinterpret_cast<const uint8_t*>(wgu);
   const uint8_t* wd8 = reinterpret_cast<const uint8_t*>(wd);
+  if (P <= kPairsMax && pairs_lds(P, I) <= kPairsLds) {
+    prof_begin(kInt8GateUp, s);
+    hipLaunchKernelGGL(pairs_gate_up, dim3(I / 16 * P), dim3(256), 0, s, x8, xs, wgu8, wgus, idx, H, I, E,
+                       k, P, act, order_key());
+    prof_end(kInt8GateUp, s);
+    prof_begin(kInt8Down, s);
+    hipLaunchKernelGGL(pairs_down, dim3(H / kPairCols), dim3(kPairWaves * kWave), pairs_lds(P, I), s, act,
+                       wd8, wds, idx, w, H, I, E, k, P, out, order_key());
+    prof_end(kInt8Down, s);
+    return hipGetLastError();
+  }
+  if (const hipError_t e = launch_group_experts(idx, P, E, L.bm, counts, offsets, tiles, n_tiles,
+                                                perm, row_of, s); e != hipSuccess) return e;
   int* partial = reinterpret_cast<int*>(b + L.partial);
   const bool large = L.bm == kLargeBM;
   // grid of the large tiles: every item whole, plus room for the tail slices (rem * S - rem < ncu)
