@@ -24,6 +24,7 @@ namespace moe {
 namespace {
 
 constexpr int kBM8 = 64;                           // rows (routed pairs) per M-tile
+constexpr int kTall8 = 128;                        // experts averaging 40 rows and more
 inline size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 inline int round_up(int v, int m) { return (v + m - 1) / m * m; }
 
@@ -33,16 +34,13 @@ __device__ __forceinline__ i32x4 mfma_i8(i32x4 a, i32x4 b, i32x4 c) {
 
 enum { kGateUp8 = 0, kDown8 = 1, kDownFused8 = 2 };
 
-constexpr int kI8C = 256;                          // K stage of the staged codes (two chunks)
-constexpr int kI8RS = kI8C + 16;                   // padded LDS row stride (bytes)
-constexpr int kI8CH = kI8C / 16;                   // 16-byte code chunks per row per stage
-
 }  // namespace
 
 Int8Ws int8_ws_layout(int T, int H, int I, int E, int k) {
   Int8Ws L{};
   const size_t P = static_cast<size_t>(T) * k;
-  L.bm = P >= static_cast<size_t>(kLargeBM) * E ? kLargeBM : kBM8;
+  L.bm = P >= static_cast<size_t>(kLargeBM) * E ? kLargeBM
+         : P >= 40 * static_cast<size_t>(E) ? kTall8 : kBM8;
   L.max_tiles = static_cast<int>(E + (P + L.bm - 1) / L.bm);
   size_t o = 0;
   L.n_tiles = o;   o += 256;
@@ -62,19 +60,19 @@ Int8Ws int8_ws_layout(int T, int H, int I, int E, int k) {
   return L;
 }
 
-// Batched INT8 projections with a whole-line weight stream: workgroup = (M-tile of
-// 64 routed rows, NW waves), each wave owning two groups of 16 weight rows
-// (gate_up: 16 neurons' gate and up rows; down: 32 output channels).  A
-// 128-position chunk of a row is 128 bytes: the wave reads its 32 rows as four
-// loads of 8 rows x 128 contiguous bytes (non-temporal), passes them through a
-// wave-private 2 KB LDS tile (16-byte chunks XOR-swizzled by row) and reads back
-// two 16-byte operands of the 16x16x64 MFMA: lane (r, g) takes chunks g and 4 + g
-// of row r, of the weights and of the activations alike.  The activation codes
-// are staged in LDS in 256-position stages, double-buffered and shared by the
-// waves.  Rows past the tile's end load the tile's first row; their columns are
-// computed and discarded.
-template <int KIND, int NW>
-__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4, 8))) void gemm_i8s(
+// Batched INT8 projections with a whole-line weight stream: workgroup = (M-tile of BM
+// routed rows, NW waves), each wave owning two groups of 16 weight rows (gate_up: 16
+// neurons' gate and up rows; down: 32 output channels).  A 128-position chunk of a row
+// is 128 bytes: the wave reads its 32 rows as four loads of 8 rows x 128 contiguous
+// bytes (non-temporal), passes them through a wave-private 2 KB LDS tile (16-byte
+// chunks XOR-swizzled by row) and reads back two 16-byte operands of the 16x16x64
+// MFMA: lane (r, g) takes chunks g and 4 + g of row r, of the weights and of the
+// activations alike.  The activation codes are staged in LDS in stages of C chunks,
+// double-buffered and shared by the waves; the next chunk's weights are in flight
+// while one multiplies.  Rows past the tile's end load the tile's first row; their
+// columns are computed and discarded.
+template <int KIND, int NW, int BM, int C>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == 64 ? 4 : 2, 8))) void gemm_i8s(
     const uint8_t* __restrict__ act, const float* __restrict__ acts,
     const uint8_t* __restrict__ wt, const float* __restrict__ wts,
     const int* __restrict__ perm, const int2* __restrict__ tiles, const int* __restrict__ n_tiles,
@@ -83,8 +81,12 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4, 8)))
   constexpr int NT = NW * 64;
   constexpr bool GU = KIND == kGateUp8;
   constexpr int RPW = GU ? 16 : 32;                       // outputs per wave
-  constexpr int LPT = kBM8 * kI8CH / NT;                  // 16-byte code loads per thread
-  __shared__ __align__(16) uint8_t xl[2][kBM8 * kI8RS];
+  constexpr int G = BM / 16;                              // 16-row groups of the tile
+  constexpr int SB = 128 * C;                             // bytes of a row per stage
+  constexpr int RS = SB + 16;                             // padded LDS row stride
+  constexpr int CH = SB / 16;                             // 16-byte pieces of a row per stage
+  constexpr int LPT = BM * CH / NT;                       // 16-byte code loads per thread
+  __shared__ __align__(16) uint8_t xl[2][BM * RS];
   __shared__ __align__(16) i32x4 wtl[NW][16 * 8];         // per wave: [16 rows][8 chunks]
   const int K = GU ? H : I;                               // reduction length
   const int N = GU ? I : H;                               // outputs
@@ -95,7 +97,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4, 8)))
   const int tile = item / nblk, nb_i = item - tile * nblk;
   const int2 te = tiles[tile];
   const int e = te.x, m0 = te.y;
-  const int mcount = min(kBM8, counts[e] - m0);
+  const int mcount = min(BM, counts[e] - m0);
   const int rbase = offsets[e] + m0;
   const int tid = threadIdx.x, ln = tid & 63, col = ln & 15, grp = ln >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -119,10 +121,10 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4, 8)))
   int lrow[LPT];
 #pragma unroll
   for (int i = 0; i < LPT; ++i) {
-    const int c = tid + i * NT, r = c / kI8CH, rr = r < mcount ? r : 0;
-    lrow[i] = r * kI8RS + (c % kI8CH) * 16;
+    const int c = tid + i * NT, r = c / CH, rr = r < mcount ? r : 0;
+    lrow[i] = r * RS + (c % CH) * 16;
     const int arow = GU ? perm[rbase + rr] / k : rbase + rr;
-    oxl[i] = static_cast<uint32_t>(arow * K + (c % kI8CH) * 16);
+    oxl[i] = static_cast<uint32_t>(arow * K + (c % CH) * 16);
   }
   i32x4 xr[LPT];
 #pragma unroll
@@ -130,62 +132,83 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4, 8)))
 #pragma unroll
   for (int i = 0; i < LPT; ++i) *reinterpret_cast<i32x4*>(&xl[0][lrow[i]]) = xr[i];
 
-  i32x4 acc0[4], acc1[4];
+  i32x4 acc0[G], acc1[G];
 #pragma unroll
-  for (int g = 0; g < 4; ++g) acc0[g] = acc1[g] = i32x4{0, 0, 0, 0};
-  const int nchunk = K / 128, nstage = K / kI8C;
+  for (int g = 0; g < G; ++g) acc0[g] = acc1[g] = i32x4{0, 0, 0, 0};
+  const int nchunk = K / 128, nstage = nchunk / C;        // (both even: K is a multiple of 256)
   i32x4 wA[4], wB[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) wA[i] = ld16_stream(wb + ow[i]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) wB[i] = ld16_stream(wb + ow[i] + 128);
   __syncthreads();
 
-  auto chunk = [&](const i32x4 (&W)[4], int buf, int cc) {
-    const uint8_t* xcur = &xl[buf][col * kI8RS + cc * 128 + 16 * grp];
+  // One chunk: the weights through the wave's LDS tile into operands (both row groups
+  // before the products, so that each activation operand is read once), the chunk
+  // after next on its way into the registers they left, then the products.
+  auto chunk = [&](i32x4 (&W)[4], int buf, int cc, int next) {
+    const uint8_t* xcur = &xl[buf][col * RS + cc * 128 + 16 * grp];
+    i32x4 a[4];
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {                         // row group 0, then 1
+    for (int m = 0; m < 2; ++m) {
       wdst[0] = W[2 * m];
       wdst[64] = W[2 * m + 1];
       __builtin_amdgcn_wave_barrier();
-      const i32x4 a0 = asrc[grp ^ sw], a1 = asrc[(4 + grp) ^ sw];
+      a[2 * m] = asrc[grp ^ sw];
+      a[2 * m + 1] = asrc[(4 + grp) ^ sw];
       __builtin_amdgcn_wave_barrier();
+    }
+    const uint32_t ko = static_cast<uint32_t>(min(next, nchunk - 1) * 128);   // (a harmless repeat past the end)
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const uint8_t* p = xcur + (16 * g) * kI8RS;
-        const i32x4 b0 = *reinterpret_cast<const i32x4*>(p), b1 = *reinterpret_cast<const i32x4*>(p + 64);
-        if (m == 0) acc0[g] = mfma_i8(a1, b1, mfma_i8(a0, b0, acc0[g]));
-        else acc1[g] = mfma_i8(a1, b1, mfma_i8(a0, b0, acc1[g]));
+    for (int i = 0; i < 4; ++i) W[i] = ld16_stream(wb + ow[i] + ko);
+    __builtin_amdgcn_sched_barrier(0);                    // (the compiler would sink the loads behind the products)
+    i32x4 b[2][2];                                        // the next row group's operand is read a group ahead
+    b[0][0] = *reinterpret_cast<const i32x4*>(xcur);
+    b[0][1] = *reinterpret_cast<const i32x4*>(xcur + 64);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      if (g + 1 < G) {
+        const uint8_t* p = xcur + (16 * (g + 1)) * RS;
+        b[(g + 1) & 1][0] = *reinterpret_cast<const i32x4*>(p);
+        b[(g + 1) & 1][1] = *reinterpret_cast<const i32x4*>(p + 64);
       }
+      acc0[g] = mfma_i8(a[0], b[g & 1][0], acc0[g]);
+      acc1[g] = mfma_i8(a[2], b[g & 1][0], acc1[g]);
+      acc0[g] = mfma_i8(a[1], b[g & 1][1], acc0[g]);
+      acc1[g] = mfma_i8(a[3], b[g & 1][1], acc1[g]);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
-  for (int st = 0; st < nstage; ++st) {
-    const int buf = st & 1;
-    const bool more = st + 1 < nstage;
-    if (more) {
+  // activations of stage st + 1, on their way while stage st multiplies
+  auto fetch = [&](int st) {
+    if (st < nstage) {
 #pragma unroll
-      for (int i = 0; i < LPT; ++i) xr[i] = ld16(act + oxl[i] + (st + 1) * kI8C);
+      for (int i = 0; i < LPT; ++i) xr[i] = ld16(act + oxl[i] + st * SB);
     }
-    // chunks 2st (weights in wA) and 2st+1 (wB); the chunk after each is loaded
-    // first (clamped to the last chunk, a harmless repeat: fixed load count)
-    const uint32_t k1 = static_cast<uint32_t>((2 * st + 1) * 128);
-    const uint32_t k2 = static_cast<uint32_t>(min(2 * st + 2, nchunk - 1) * 128);
+  };
+  auto publish = [&](int st) {
+    if (st < nstage) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) wB[i] = ld16_stream(wb + ow[i] + k1);
-    chunk(wA, buf, 0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) wA[i] = ld16_stream(wb + ow[i] + k2);
-    chunk(wB, buf, 1);
-    if (more) {
-#pragma unroll
-      for (int i = 0; i < LPT; ++i) *reinterpret_cast<i32x4*>(&xl[buf ^ 1][lrow[i]]) = xr[i];
+      for (int i = 0; i < LPT; ++i) *reinterpret_cast<i32x4*>(&xl[st & 1][lrow[i]]) = xr[i];
     }
     __syncthreads();
+  };
+  for (int c2 = 0; c2 < nchunk; c2 += 2) {                // two chunks a turn, weights in wA and wB
+    fetch(C == 2 ? c2 / 2 + 1 : c2 + 1);
+    chunk(wA, C == 2 ? (c2 / 2) & 1 : 0, 0, c2 + 2);
+    if (C == 1) {
+      publish(c2 + 1);
+      fetch(c2 + 2);
+    }
+    chunk(wB, C == 2 ? (c2 / 2) & 1 : 1, C == 2 ? 1 : 0, c2 + 3);
+    publish(C == 2 ? c2 / 2 + 1 : c2 + 2);
   }
   // lane: outputs row0 + 4grp + i (group 0) and row1 + 4grp + i (group 1) of tile row 16g + col
   const float* ws_e = wts + static_cast<size_t>(e) * wrows;
   const f32x4 s0 = *reinterpret_cast<const f32x4*>(ws_e + row0 + 4 * grp);
   const f32x4 s1 = *reinterpret_cast<const f32x4*>(ws_e + row1 + 4 * grp);
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
+  for (int g = 0; g < G; ++g) {
     const int r = 16 * g + col;
     if (r >= mcount) continue;
     const int pr = perm[rbase + r];
@@ -605,12 +628,25 @@ __device__ __forceinline__ int rows_dot(const uint8_t* wrow, const uint8_t* x, i
   }
   return sum8(acc);
 }
-constexpr int kPairsMax = 64;                            // pairs up to which this form is taken
+constexpr int kPairsMax = 128;                           // pairs up to which this form may be taken
 constexpr size_t kPairsLds = 64 << 10;                   // LDS that a kernel may use without an attribute
 constexpr int kPairCols = 8;                             // output columns per workgroup of the down pass
 constexpr int kPairWaves = 8;
 inline size_t pairs_lds(int P, int I) {
   return static_cast<size_t>(kPairWaves) * I + sizeof(float) * kPairCols * P;
+}
+// Taken while the weights that it reads more than once (pairs that share an expert;
+// expected number of distinct experts E (1 - (1 - k/E)^T)) stay below 120 MB: about
+// the 20 us that grouping and its launches cost the other form.  Measured, us (this /
+// grouped): H 2048 I 768 E 128 k 8, T 1 13.5 / 38, T 8 60 / 68, T 12 85 / 78; H 7168 I
+// 2048 E 32 k 4, T 2 71 / 92, T 4 124 / 119; H 2048 I 1024 E 8 k 2, T 12 25 / 38.
+inline bool use_pairs(int T, int H, int I, int E, int k) {
+  const int64_t P = static_cast<int64_t>(T) * k;
+  if (P > kPairsMax || pairs_lds(static_cast<int>(P), I) > kPairsLds) return false;
+  double miss = 1.0;                                     // (1 - k/E)^T
+  for (int t = 0; t < T; ++t) miss *= 1.0 - static_cast<double>(k) / E;
+  const double again = static_cast<double>(P) - E * (1.0 - miss);
+  return again * 3.0 * H * I <= 120e6;
 }
 }  // namespace
 
@@ -737,7 +773,7 @@ hipError_t launch_experts_int8(const int8_t* x, const float* xs, const int8_t* w
   const uint8_t* x8 = reinterpret_cast<const uint8_t*>(x);
   const uint8_t* wgu8 = reinterpret_cast<const uint8_t*>(wgu);
   const uint8_t* wd8 = reinterpret_cast<const uint8_t*>(wd);
-  if (P <= kPairsMax && pairs_lds(P, I) <= kPairsLds) {
+  if (use_pairs(T, H, I, E, k)) {
     prof_begin(kInt8GateUp, s);
     hipLaunchKernelGGL(pairs_gate_up, dim3(I / 16 * P), dim3(256), 0, s, x8, xs, wgu8, wgus, idx, H, I, E,
                        k, P, act, order_key());
@@ -761,8 +797,15 @@ hipError_t launch_experts_int8(const int8_t* x, const float* xs, const int8_t* w
   hipLaunchKernelGGL(gemm_large_i8_fixup<KD>, dim3(num_cus / 2 * PER), dim3(256), 0, s, AS, WS, \
                      ARGS, Y, O, partial, num_cus, order_key())
 #define STREAM8(KD, A, AS, W, WS, Y, O, NBLK)                                                 \
-  hipLaunchKernelGGL((gemm_i8s<KD, 8>), dim3(round_up((NBLK) * L.max_tiles, kXcds)), dim3(512), \
-                     0, s, A, AS, W, WS, ARGS, Y, O, order_key())
+  do {                                                                                        \
+    const dim3 grid_(round_up((NBLK) * L.max_tiles, kXcds));                                  \
+    if (L.bm == kTall8)                                                                       \
+      hipLaunchKernelGGL((gemm_i8s<KD, 8, kTall8, 1>), grid_, dim3(512), 0, s, A, AS, W, WS,  \
+                         ARGS, Y, O, order_key());                                            \
+    else                                                                                      \
+      hipLaunchKernelGGL((gemm_i8s<KD, 8, kBM8, 2>), grid_, dim3(512), 0, s, A, AS, W, WS,    \
+                         ARGS, Y, O, order_key());                                            \
+  } while (0)
   prof_begin(kInt8GateUp, s);
   if (large) { LARGE8(kGateUp8, x8, xs, wgu8, wgus, act, nullptr, I / 128, 32); }
   else STREAM8(kGateUp8, x8, xs, wgu8, wgus, act, nullptr, I / 128);
