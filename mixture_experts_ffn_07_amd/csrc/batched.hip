@@ -390,13 +390,25 @@ __global__ __launch_bounds__(256) void combine_slots(const float* __restrict__ y
   const int c4 = cols / 4, c_lo = blockIdx.y * c4 / gridDim.y, c_hi = (blockIdx.y + 1) * c4 / gridDim.y;
   for (int c = c_lo + threadIdx.x; c < c_hi; c += blockDim.x) {
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    for (int j = 0; j < k; ++j) {
-      const int row = row_of[t * k + j];
-      if (static_cast<unsigned>(row) >= static_cast<unsigned>(P)) continue;
-      const float wj = w[t * k + j];
-      const f32x4 v = *reinterpret_cast<const f32x4*>(y + static_cast<size_t>(row) * ldy + 4 * c);
+    for (int j0 = 0; j0 < k; j0 += 8) {                   // eight slots' loads in flight, then their sum in order
+      f32x4 v[8];
+      float wj[8];
+      bool in[8];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i] = fmaf(wj, v[i], acc[i]);
+      for (int j = 0; j < 8; ++j) {
+        const int row = j0 + j < k ? row_of[t * k + j0 + j] : P;
+        in[j] = static_cast<unsigned>(row) < static_cast<unsigned>(P);
+        if (in[j]) {
+          wj[j] = w[t * k + j0 + j];
+          v[j] = *reinterpret_cast<const f32x4*>(y + static_cast<size_t>(row) * ldy + 4 * c);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (in[j]) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[i] = fmaf(wj[j], v[j][i], acc[i]);
+        }
     }
     uint2 o;
     o.x = pack_bf16x2(acc[0], acc[1]);

@@ -39,8 +39,16 @@ enum { kGateUp8 = 0, kDown8 = 1, kDownFused8 = 2 };
 Int8Ws int8_ws_layout(int T, int H, int I, int E, int k) {
   Int8Ws L{};
   const size_t P = static_cast<size_t>(T) * k;
-  L.bm = P >= static_cast<size_t>(kLargeBM) * E ? kLargeBM
-         : P >= 40 * static_cast<size_t>(E) ? kTall8 : kBM8;
+  // 256-row tiles where the products are bound by the matrix cores: 320 rows an expert
+  // and reductions long enough to pay for a tile's start and end.  Measured, us (256-row
+  // / 128-row tiles): H 7168 I 2048 E 6 k 1, 260 rows an expert 178 / 158, 384 228 / 246,
+  // 2000 747 / 1007; H 4096 I 1024 E 32 k 6, 260 349 / 315, 384 382 / 397, 2000 1673 /
+  // 1828; H 2048 I 768 E 64 k 8, 384 390 / 368, 2000 1734 / 1703.
+  // 128-row tiles from 40 rows an expert, where about half the experts would need two of
+  // 64 rows (their weights streamed twice): H 4096 I 1024 E 64 k 6, 37 rows 200 / 200,
+  // 73 rows 262 / 319 (128-row / 64-row).
+  const bool mfma_bound = P >= 320 * static_cast<size_t>(E) && static_cast<size_t>(H) * I >= (size_t(1) << 22);
+  L.bm = mfma_bound ? kLargeBM : P >= 40 * static_cast<size_t>(E) ? kTall8 : kBM8;
   L.max_tiles = static_cast<int>(E + (P + L.bm - 1) / L.bm);
   size_t o = 0;
   L.n_tiles = o;   o += 256;
@@ -67,11 +75,11 @@ Int8Ws int8_ws_layout(int T, int H, int I, int E, int k) {
 // bytes (non-temporal), passes them through a wave-private 2 KB LDS tile (16-byte
 // chunks XOR-swizzled by row) and reads back two 16-byte operands of the 16x16x64
 // MFMA: lane (r, g) takes chunks g and 4 + g of row r, of the weights and of the
-// activations alike.  The activation codes are staged in LDS in stages of C chunks,
-// double-buffered and shared by the waves; the next chunk's weights are in flight
-// while one multiplies.  Rows past the tile's end load the tile's first row; their
+// activations alike.  The activation codes are staged in LDS in stages of two chunks,
+// double-buffered and shared by the waves; the weights of the next two chunks are in
+// flight while one multiplies.  Rows past the tile's end load the tile's first row; their
 // columns are computed and discarded.
-template <int KIND, int NW, int BM, int C>
+template <int KIND, int NW, int BM>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == 64 ? 4 : 2, 8))) void gemm_i8s(
     const uint8_t* __restrict__ act, const float* __restrict__ acts,
     const uint8_t* __restrict__ wt, const float* __restrict__ wts,
@@ -82,7 +90,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == 6
   constexpr bool GU = KIND == kGateUp8;
   constexpr int RPW = GU ? 16 : 32;                       // outputs per wave
   constexpr int G = BM / 16;                              // 16-row groups of the tile
-  constexpr int SB = 128 * C;                             // bytes of a row per stage
+  constexpr int SB = 256;                                 // bytes of a row per stage (two chunks)
   constexpr int RS = SB + 16;                             // padded LDS row stride
   constexpr int CH = SB / 16;                             // 16-byte pieces of a row per stage
   constexpr int LPT = BM * CH / NT;                       // 16-byte code loads per thread
@@ -135,7 +143,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == 6
   i32x4 acc0[G], acc1[G];
 #pragma unroll
   for (int g = 0; g < G; ++g) acc0[g] = acc1[g] = i32x4{0, 0, 0, 0};
-  const int nchunk = K / 128, nstage = nchunk / C;        // (both even: K is a multiple of 256)
+  const int nchunk = K / 128, nstage = nchunk / 2;
   i32x4 wA[4], wB[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) wA[i] = ld16_stream(wb + ow[i]);
@@ -193,15 +201,11 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == 6
     }
     __syncthreads();
   };
-  for (int c2 = 0; c2 < nchunk; c2 += 2) {                // two chunks a turn, weights in wA and wB
-    fetch(C == 2 ? c2 / 2 + 1 : c2 + 1);
-    chunk(wA, C == 2 ? (c2 / 2) & 1 : 0, 0, c2 + 2);
-    if (C == 1) {
-      publish(c2 + 1);
-      fetch(c2 + 2);
-    }
-    chunk(wB, C == 2 ? (c2 / 2) & 1 : 1, C == 2 ? 1 : 0, c2 + 3);
-    publish(C == 2 ? c2 / 2 + 1 : c2 + 2);
+  for (int st = 0; st < nstage; ++st) {                   // weights in wA and wB
+    fetch(st + 1);
+    chunk(wA, st & 1, 0, 2 * st + 2);
+    chunk(wB, st & 1, 1, 2 * st + 3);
+    publish(st + 1);
   }
   // lane: outputs row0 + 4grp + i (group 0) and row1 + 4grp + i (group 1) of tile row 16g + col
   const float* ws_e = wts + static_cast<size_t>(e) * wrows;
@@ -800,10 +804,10 @@ hipError_t launch_experts_int8(const int8_t* x, const float* xs, const int8_t* w
   do {                                                                                        \
     const dim3 grid_(round_up((NBLK) * L.max_tiles, kXcds));                                  \
     if (L.bm == kTall8)                                                                       \
-      hipLaunchKernelGGL((gemm_i8s<KD, 8, kTall8, 1>), grid_, dim3(512), 0, s, A, AS, W, WS,  \
+      hipLaunchKernelGGL((gemm_i8s<KD, 8, kTall8>), grid_, dim3(512), 0, s, A, AS, W, WS,  \
                          ARGS, Y, O, order_key());                                            \
     else                                                                                      \
-      hipLaunchKernelGGL((gemm_i8s<KD, 8, kBM8, 2>), grid_, dim3(512), 0, s, A, AS, W, WS,    \
+      hipLaunchKernelGGL((gemm_i8s<KD, 8, kBM8>), grid_, dim3(512), 0, s, A, AS, W, WS,    \
                          ARGS, Y, O, order_key());                                            \
   } while (0)
   prof_begin(kInt8GateUp, s);

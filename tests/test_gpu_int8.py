@@ -51,7 +51,9 @@ def check(M, d, out, tokens=None):
     (1, 256, 256, 1, 1), (1, 512, 256, 8, 2), (1, 2048, 768, 128, 8), (2, 256, 512, 4, 4), (8, 512, 256, 16, 3),
     (17, 768, 512, 4, 2), (33, 512, 768, 6, 1), (64, 1024, 256, 32, 8), (65, 512, 256, 5, 2), (130, 256, 256, 2, 2),
     (300, 512, 512, 3, 1), (777, 256, 512, 16, 6), (600, 512, 256, 1, 1), (513, 768, 256, 2, 2),
-    (1025, 1024, 512, 4, 1)])
+    (1025, 1024, 512, 4, 1),
+    # 256-row tiles: one ragged expert, several with tail slices along K, k = 1 and more
+    (700, 4096, 1024, 1, 1), (1300, 2048, 2048, 2, 1), (900, 4096, 1024, 4, 2), (1500, 4096, 1024, 9, 2)])
 def test_experts_int8(M, T, H, I, E, k):
     print(f"[int8] T={T} H={H} I={I} E={E} k={k}", flush=True)
     d = make(T, H, I, E, k, seed=T)
@@ -65,16 +67,18 @@ def test_experts_int8_skewed(M, T):
     check(M, d, call(M, d))
 
 
-@pytest.mark.parametrize("T,E,k", [(6, 4, 2), (50, 8, 3), (200, 8, 3), (9, 4, 1), (300, 4, 1), (900, 3, 1), (1200, 3, 2)])
-def test_experts_int8_ids_out_of_range(M, T, E, k):
-    print(f"[int8] ids out of range T={T} E={E} k={k}", flush=True)
-    d = make(T, 512, 256, E, k, seed=2)
+@pytest.mark.parametrize("T,E,k,H,I", [
+    (6, 4, 2, 512, 256), (50, 8, 3, 512, 256), (200, 8, 3, 512, 256), (9, 4, 1, 512, 256), (300, 4, 1, 512, 256),
+    (900, 3, 1, 512, 256), (1200, 3, 2, 512, 256), (1100, 3, 1, 2048, 2048), (600, 3, 2, 4096, 1024)])
+def test_experts_int8_ids_out_of_range(M, T, E, k, H, I):
+    print(f"[int8] ids out of range T={T} E={E} k={k} H={H}", flush=True)
+    d = make(T, H, I, E, k, seed=2)
     g = torch.Generator().manual_seed(7)
     off = torch.rand(T, k, generator=g) < 0.4
     off[1] = True                                          # a token without an expert
     bad = torch.tensor([-1, E, 2 ** 31 - 1, -2 ** 31])[torch.randint(0, 4, (T, k), generator=g)].int()
     d["idx"] = torch.where(off, bad, d["idx"].cpu()).int().cuda()
-    out = torch.full((T, 512), float("nan"), dtype=torch.bfloat16, device="cuda")
+    out = torch.full((T, H), float("nan"), dtype=torch.bfloat16, device="cuda")
     call(M, d, out=out)
     assert not out[1].any()
     check(M, d, out)
@@ -117,16 +121,17 @@ def test_experts_int8_extreme_codes(M):
 def test_experts_int8_rows_do_not_depend_on_the_batch(M):
     """A token's bits are the same alone, in a decode batch and in a large batch (exact sums,
     one order of the slots), on any form of the kernels."""
-    d = make(2100, 512, 256, 4, 2, seed=8)
+    d = make(2100, 4096, 1024, 4, 2, seed=8)
     full = call(M, d)
-    for rows in (slice(0, 1), slice(5, 12), slice(0, 64), slice(100, 190), slice(0, 400)):
+    for rows in (slice(0, 1), slice(5, 12), slice(0, 64), slice(100, 190), slice(0, 400), slice(1400, 2099)):
         part = {n: (t[rows].clone() if n in ("x", "xs", "idx", "w") else t) for n, t in d.items()}
         assert torch.equal(call(M, part), full[rows]), rows
 
 
-@pytest.mark.parametrize("T,E,k", [(1, 8, 2), (40, 8, 2), (500, 8, 2), (900, 2, 1)])
-def test_experts_int8_deterministic_and_order_free(M, T, E, k):
-    d = make(T, 512, 512, E, k, seed=9)
+@pytest.mark.parametrize("T,E,k,H,I", [(1, 8, 2, 512, 512), (40, 8, 2, 512, 512), (500, 8, 2, 512, 512),
+                                       (900, 2, 1, 2048, 2048), (700, 2, 2, 4096, 1024)])
+def test_experts_int8_deterministic_and_order_free(M, T, E, k, H, I):
+    d = make(T, H, I, E, k, seed=9)
     ref = call(M, d)
     for seed in range(4):
         M.moe_set_debug_options(M.MOE_DEBUG_PERMUTE_ORDER if seed else 0, seed)
@@ -135,9 +140,10 @@ def test_experts_int8_deterministic_and_order_free(M, T, E, k):
 
 
 def test_experts_int8_workspace_contents_do_not_matter(M):
-    for T, E, k in ((2, 8, 2), (70, 8, 2), (600, 2, 1)):
-        d = make(T, 512, 256, E, k, seed=10)
-        ws = M.workspace(M.moe_experts_int8_workspace_bytes(T, 512, 256, E, k))
+    for T, E, k, H, I in ((2, 8, 2, 512, 256), (70, 8, 2, 512, 256), (300, 8, 2, 512, 256), (700, 2, 1, 4096, 1024),
+                          (500, 2, 2, 4096, 1024)):
+        d = make(T, H, I, E, k, seed=10)
+        ws = M.workspace(M.moe_experts_int8_workspace_bytes(T, H, I, E, k))
         ws.zero_()
         a = call(M, d, ws=ws)
         ws.fill_(255)
@@ -158,15 +164,16 @@ def test_experts_int8_large_offsets(M):
     assert E * 2 * I * H > 2 ** 31
 
 
-@pytest.mark.parametrize("T,E,k", [(1, 16, 4), (32, 16, 4), (300, 8, 2), (900, 2, 1)])
-def test_experts_int8_graph_replays(M, T, E, k):
+@pytest.mark.parametrize("T,E,k,H,I", [(1, 16, 4, 512, 256), (60, 16, 4, 512, 256), (300, 8, 2, 512, 256),
+                                       (900, 2, 1, 2048, 2048), (700, 2, 2, 4096, 1024)])
+def test_experts_int8_graph_replays(M, T, E, k, H, I):
     """Captured and replayed, with eager work of the program's own between the replays; two
     graphs that share one workspace, replayed in turn."""
     print(f"[int8 graph] T={T} E={E} k={k}", flush=True)
-    ds = [make(T, 512, 256, E, k, seed=20 + j) for j in range(2)]
+    ds = [make(T, H, I, E, k, seed=20 + j) for j in range(2)]
     ref = [call(M, d) for d in ds]
-    ws = M.workspace(M.moe_experts_int8_workspace_bytes(T, 512, 256, E, k))
-    outs = [torch.empty(T, 512, dtype=torch.bfloat16, device="cuda") for _ in ds]
+    ws = M.workspace(M.moe_experts_int8_workspace_bytes(T, H, I, E, k))
+    outs = [torch.empty(T, H, dtype=torch.bfloat16, device="cuda") for _ in ds]
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
