@@ -508,7 +508,7 @@ int moe_route_scored(const float* logits, const float* bias, int T, int E, int k
   const moe::ScoredRoute p{E, k, n_groups, topk_groups, group_top, score == MOE_SCORE_SIGMOID,
                            renormalize != 0, scale};
   return hip_status(moe::launch_route_scored(logits, bias, T, p, topk_idx, topk_w,
-                                             static_cast<hipStream_t>(stream)),
+                                             static_cast<hipStream_t>(stream), cus),
                     "moe_route_scored launch");
 }
 

@@ -92,7 +92,7 @@ struct ScoredRoute {
   float scale;
 };
 hipError_t launch_route_scored(const float* logits, const float* bias, int T, const ScoredRoute& p,
-                               int32_t* idx, float* w, hipStream_t s);
+                               int32_t* idx, float* w, hipStream_t s, int num_cus);
 hipError_t launch_route_scored_backward(const float* logits, const int32_t* idx, const float* dw,
                                         int T, const ScoredRoute& p, float* dlogits, hipStream_t s);
 

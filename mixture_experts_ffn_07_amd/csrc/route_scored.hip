@@ -7,11 +7,14 @@
 //   with the largest score take part; slots = the k largest c among their experts,
 //   (c descending, index ascending); w_j = scale * p_j / (sum of the selected p)
 //
-// The choice is exact: without a bias the scores' order is that of the FP32
-// logits, compared as they are; sums p + b and group scores are formed in FP64
-// (two experts 1e-7 apart are then still told apart as the formula tells them;
-// FP32 scores would swap about one token in three thousand at 384 experts).
-// FP64 vector operations run at the rate of unpacked FP32 ones here.
+// The choice is exact: without a bias the scores' order is that of the FP32 logits,
+// compared as they are; sums p + b and group scores are compared as in FP64 (scores
+// 1e-7 apart are then still told apart as the formula tells them; plain FP32 scores
+// would swap about one token in three thousand at 384 experts).  They are formed in
+// FP32 first: where neighbours in the resulting order lie further apart than FP32 can
+// be wrong, the order is certain; only a token with a closer pair (or an exact tie)
+// is done again in FP64, by its wave alone.  16384 x 384, sigmoid, bias, 8 groups:
+// FP64 throughout 51 us, this form ROUTE_US us.
 #include "common.h"
 #include "internal.h"
 #include "route.h"
@@ -34,9 +37,7 @@ __device__ __forceinline__ double wave_sum64(double v) {
   return v;
 }
 __device__ __forceinline__ float wave_max_f32(float v) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v = fmaxf(v, __shfl_xor(v, m, kWave));
-  return v;
+  return key_to_float(wave_max_u32(ordered_key(v)));     // (-inf and finite values)
 }
 
 // Monotone map of an FP64 value to 64 bits (-0 folded onto +0); finite values map
@@ -46,31 +47,11 @@ __device__ __forceinline__ uint64_t ordered_key64(double d) {
   if ((u << 1) == 0) u = 0;
   return (u >> 63) ? ~u : (u | 0x8000000000000000ull);
 }
-
-// The k largest keys of a wave, lane l holding candidates l + 64 i in key[i]:
-// returns in lane j < k the index of slot j (key descending, index ascending).
-template <int R>
-__device__ __forceinline__ int select_topk(uint64_t (&key)[R], int k) {
-  const int lane = lane_id();
-  int mine = 0;
-  for (int r = 0; r < k; ++r) {
-    uint64_t best = key[0];
-#pragma unroll
-    for (int i = 1; i < R; ++i) best = key[i] > best ? key[i] : best;
-    const uint32_t hi = wave_max_u32(static_cast<uint32_t>(best >> 32));
-    const uint32_t lo = wave_max_u32(static_cast<uint32_t>(best >> 32) == hi ? static_cast<uint32_t>(best) : 0u);
-    best = (static_cast<uint64_t>(hi) << 32) | lo;
-    int sel = 0;
-#pragma unroll
-    for (int i = R - 1; i >= 0; --i) {
-      const uint64_t b = __ballot(key[i] == best);
-      sel = b ? kWave * i + __builtin_ctzll(b) : sel;
-    }
-#pragma unroll
-    for (int i = 0; i < R; ++i) key[i] = (lane + kWave * i == sel) ? 0u : key[i];
-    if (lane == r) mine = sel;
-  }
-  return mine;
+__device__ __forceinline__ uint32_t wave_max_key(uint32_t v) { return wave_max_u32(v); }
+__device__ __forceinline__ uint64_t wave_max_key(uint64_t v) {
+  const uint32_t hi = wave_max_u32(static_cast<uint32_t>(v >> 32));
+  const uint32_t lo = wave_max_u32(static_cast<uint32_t>(v >> 32) == hi ? static_cast<uint32_t>(v) : 0u);
+  return (static_cast<uint64_t>(hi) << 32) | lo;
 }
 
 struct RouteArgs {
@@ -81,127 +62,238 @@ struct RouteArgs {
   float scale;
 };
 
+// Where a wave's candidates live: lane l holds experts first + step * i, i < count.
+// Without groups 64 experts a row; with groups, span lanes per group hold its members.
+struct Place {
+  int first, step, count, span;
+};
+__device__ __forceinline__ Place place(const RouteArgs& a) {
+  const int lane = lane_id();
+  if (a.groups == 1) return Place{lane, kWave, lane < a.E ? (a.E - lane + kWave - 1) / kWave : 0, kWave};
+  int span = 1;
+  while (2 * span * a.groups <= kWave) span *= 2;
+  const int size = a.E / a.groups, g = lane / span, m = lane & (span - 1);
+  return Place{g * size + m, span, g < a.groups && m < size ? (size - m + span - 1) / span : 0, span};
+}
+
+// Whether the group that this lane's candidates belong to takes part (C float or
+// double).  `close`: set where the FP32 scores do not decide it.
+template <int R, typename C>
+__device__ __forceinline__ bool group_taken(const RouteArgs& a, const Place& pl, const C (&c)[R],
+                                            const bool (&on)[R], float tol, bool& close) {
+  const int g = lane_id() / pl.span;
+  C b1 = -INFINITY, b2 = -INFINITY;                      // largest, second largest
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const C x = on[i] ? c[i] : static_cast<C>(-INFINITY);
+    b2 = max(b2, min(b1, x));
+    b1 = max(b1, x);
+  }
+  for (int s = 1; s < pl.span; s *= 2) {
+    const C o1 = __shfl_xor(b1, s, kWave), o2 = __shfl_xor(b2, s, kWave);
+    b2 = max(max(b2, o2), min(b1, o1));
+    b1 = max(b1, o1);
+  }
+  // a group with one expert that takes part scores that expert's c alone
+  C gs = a.group_top > 1 && b2 != -INFINITY ? b1 + b2 : b1;
+  gs += static_cast<C>(0);                               // -0 and +0 tie
+  int rank = 0;
+  for (int o = 0; o < a.groups; ++o) {
+    const C os = __shfl(gs, o * pl.span, kWave);
+    rank += os > gs || (os == gs && o < g) ? 1 : 0;
+  }
+  const bool taken = g < a.groups && rank < a.topk_groups;
+  if (sizeof(C) == 4) {                                  // the last group in against the first one out
+    const float in = -wave_max_f32(taken ? -static_cast<float>(gs) : -INFINITY);
+    const float out = wave_max_f32(taken || g >= a.groups ? -INFINITY : static_cast<float>(gs));
+    if (out != -INFINITY && in - out < 2.f * tol + 4.8e-7f * (fabsf(in) + fabsf(out))) close = true;
+  }
+  return taken;
+}
+
+// The k largest keys of a wave in order (key descending, expert ascending): lane j < k
+// gets slot j's expert and logit.  Key 0: no candidate, 1: masked.  kFloat: the keys are
+// FP32 values' (ordered_key); `close` is set where two neighbours among the first k + 1
+// lie within the error of those.
+template <int R, bool kFloat, typename K>
+__device__ __forceinline__ void select_topk(const RouteArgs& a, const Place& pl, K (&key)[R],
+                                            const float (&v)[R], float tol, bool& close, int& sel_e,
+                                            float& sel_l) {
+  const int lane = lane_id();
+  sel_e = 0;
+  sel_l = 0.f;
+  K head = 0;                                            // the lane's largest key and its expert
+  int he = 0;
+  float hv = 0.f;
+  auto refresh = [&]() {
+    head = key[0];
+    he = pl.first;
+    hv = v[0];
+#pragma unroll
+    for (int i = 1; i < R; ++i) {
+      const bool gt = key[i] > head;
+      head = gt ? key[i] : head;
+      he = gt ? pl.first + pl.step * i : he;
+      hv = gt ? v[i] : hv;
+    }
+  };
+  refresh();
+  float prev = INFINITY;
+  const int rounds = kFloat ? a.k + 1 : a.k;
+  for (int r = 0; r < rounds; ++r) {
+    const K best = wave_max_key(head);
+    if (kFloat) {
+      if (best <= 1) {                                   // only masked ones are left: exact
+        prev = INFINITY;
+        if (r == a.k) break;
+      } else {
+        const float cur = key_to_float(static_cast<uint32_t>(best));
+        if (prev - cur < tol + 2.4e-7f * (fabsf(prev) + fabsf(cur))) close = true;
+        prev = cur;
+        if (r == a.k || close) break;
+      }
+    }
+    const uint64_t who = __ballot(head == best);
+    int win = __builtin_ctzll(who);
+    if (__popcll(who) > 1) {                             // a tie between lanes: the lowest expert
+      const uint32_t low = wave_max_u32(head == best ? ~static_cast<uint32_t>(he) : 0u);
+      win = __builtin_ctzll(__ballot(head == best && ~static_cast<uint32_t>(he) == low));
+    }
+    const int e = __builtin_amdgcn_readlane(he, win);
+    const float l = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(hv), win));
+    sel_e = lane == r ? e : sel_e;
+    sel_l = lane == r ? l : sel_l;
+    if (lane == win) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) key[i] = pl.first + pl.step * i == e ? static_cast<K>(0) : key[i];
+      refresh();
+    }
+  }
+}
+
 }  // namespace
 
-// One wave per token, lane l holding experts l + 64 i.  kChoice: a bias or groups
-// are given (FP64 scores); otherwise the order is the logits'.
+// One wave per token, tokens gridDim.x * 4 apart.  kChoice: a bias or groups are given;
+// otherwise the order is the logits'.
 template <int R, bool kChoice>
 __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs a, int32_t* __restrict__ idx,
                                                            float* __restrict__ w, uint32_t okey) {
-  extern __shared__ __align__(16) double lds_c[];        // kChoice with groups: [wave][E]
-  const int t0 = blockIdx.x * (blockDim.x / kWave) + wave_id();
-  if (t0 >= a.T) return;                                 // (whole waves; no barrier below)
-  const int t = permute_item(t0, a.T, okey);
   const int lane = lane_id(), E = a.E, k = a.k;
-  const float* lrow = a.logits + static_cast<size_t>(t) * E;
-  float v[R];
-  bool on[R];
-  float top = -INFINITY;                                 // largest logit that takes part
+  const Place pl = place(a);
+  float bias[R];
+  if (kChoice && a.bias) {
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int e = lane + kWave * i;
-    const float l = e < E ? lrow[e] : -INFINITY;
-    on[i] = takes_part(l);
-    v[i] = on[i] ? finite_logit(l) : 0.f;
-    if (on[i]) top = fmaxf(top, v[i]);
+    for (int i = 0; i < R; ++i) bias[i] = i < pl.count ? a.bias[pl.first + pl.step * i] : 0.f;
   }
-  const bool need_top = !a.sigmoid && (kChoice || !a.renorm);
-  if (need_top) top = wave_max_f32(top);
-  uint64_t key[R];
-  if (!kChoice) {
+  // FP32's error of a score: sigmoid below 2.5e-7 (the exponential's argument and result,
+  // the reciprocal), softmax below 2.5e-6 (its sum's relative error, |l - max| up to ln E
+  // on average); a bound for the two that a comparison takes, and twice that
+  const float tol = a.sigmoid ? 1e-6f : 1e-5f;
+  const int step = gridDim.x * (blockDim.x / kWave);
+  for (int t0 = blockIdx.x * (blockDim.x / kWave) + wave_id(); t0 < a.T; t0 += step) {
+    const int t = permute_item(t0, a.T, okey);
+    const float* lrow = a.logits + static_cast<size_t>(t) * E;
+    float v[R];
+    bool on[R];
+    float top = -INFINITY;                               // largest logit that takes part
 #pragma unroll
-    for (int i = 0; i < R; ++i)
-      key[i] = lane + kWave * i >= E ? 0ull
-               : on[i] ? (static_cast<uint64_t>(ordered_key(v[i])) << 32) | 2u : 1ull;
-  } else {
-    double c[R];
-    double z = 1.0;
-    if (!a.sigmoid) {
-      z = 0.0;
+    for (int i = 0; i < R; ++i) {
+      const float l = i < pl.count ? lrow[pl.first + pl.step * i] : -INFINITY;
+      on[i] = takes_part(l);
+      v[i] = on[i] ? finite_logit(l) : -INFINITY;
+      top = fmaxf(top, v[i]);
+    }
+    if (!a.sigmoid && (kChoice || !a.renorm)) top = wave_max_f32(top);
+    int sel;
+    float l;
+    bool close = false;
+    uint32_t key[R];
+    if (kChoice) {
+      float c[R];
+      float z = 0.f;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        c[i] = on[i] ? exp(static_cast<double>(v[i]) - static_cast<double>(top)) : 0.0;
+        if (a.sigmoid) c[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-v[i]));
+        else c[i] = on[i] ? __expf(v[i] - top) : 0.f;
         z += c[i];
       }
-      z = wave_sum64(z);
-    }
+      if (!a.sigmoid) {
+        z = __builtin_amdgcn_rcpf(wave_sum(z));
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int e = lane + kWave * i;
-      c[i] = a.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(v[i]))) : c[i] / z;
-      if (a.bias && on[i]) c[i] += static_cast<double>(a.bias[e]);
-    }
-    uint64_t taken = ~0ull;                              // bit group * span: the group takes part
-    int span = 0, size = E;
-    if (a.groups > 1) {
-      // span lanes per group: each takes the two largest of its members, then the
-      // lanes of a group merge theirs
-      double* cw = lds_c + static_cast<size_t>(wave_id()) * E;
-      size = E / a.groups;
+        for (int i = 0; i < R; ++i) c[i] *= z;
+      }
+      if (a.bias) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) c[i] += bias[i];
+      }
+      bool in = true;
+      if (a.groups > 1) in = group_taken<R>(a, pl, c, on, tol, close);
 #pragma unroll
       for (int i = 0; i < R; ++i)
-        if (lane + kWave * i < E) cw[lane + kWave * i] = on[i] ? c[i] : -INFINITY;
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      span = 1;
-      while (2 * span * a.groups <= kWave) span *= 2;
-      const int g = lane / span, m = lane & (span - 1);
-      double b1 = -INFINITY, b2 = -INFINITY;             // largest, second largest
-      if (g < a.groups)
-        for (int j = m; j < size; j += span) {
-          const double x = cw[g * size + j];
-          b2 = fmax(b2, fmin(b1, x));
-          b1 = fmax(b1, x);
+        key[i] = i >= pl.count || !in ? 0u : !on[i] ? 1u : ordered_key(a.bias ? c[i] : v[i]);
+      if (!close) {
+        if (a.bias) select_topk<R, true>(a, pl, key, v, tol, close, sel, l);
+        else select_topk<R, false>(a, pl, key, v, tol, close, sel, l);
+      }
+      if (close) {                                       // the same in FP64
+        double d[R];
+        double zd = 0.0;
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          d[i] = 0.0;
+          if (on[i]) d[i] = a.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(v[i])))
+                                      : exp(static_cast<double>(v[i]) - static_cast<double>(top));
+          zd += d[i];
         }
-      for (int s = 1; s < span; s *= 2) {
-        const double o1 = __shfl_xor(b1, s, kWave), o2 = __shfl_xor(b2, s, kWave);
-        b2 = fmax(fmax(b2, o2), fmin(b1, o1));
-        b1 = fmax(b1, o1);
-      }
-      // a group with one expert that takes part scores that expert's c alone
-      const double gs = a.group_top > 1 && b2 != -INFINITY ? b1 + b2 : b1;
-      const uint64_t gk = ordered_key64(gs);
-      int rank = 0;
-      for (int o = 0; o < a.groups; ++o) {
-        const uint64_t ok = __shfl(gk, o * span, kWave);
-        rank += ok > gk || (ok == gk && o < g) ? 1 : 0;
-      }
-      taken = __ballot(m == 0 && g < a.groups && rank < a.topk_groups);
-    }
+        if (!a.sigmoid) {
+          zd = wave_sum64(zd);
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const int e = lane + kWave * i;
-      const bool in = e < E && ((taken >> ((e < E ? e / size : 0) * span)) & 1);
-      key[i] = !in ? 0ull : !on[i] ? 1ull
-               : a.bias ? ordered_key64(c[i])
-                        : (static_cast<uint64_t>(ordered_key(v[i])) << 32) | 2u;   // the logits' order
-    }
-  }
-  const int sel = select_topk<R>(key, k);
-  // weights of the selected, FP32: lane j < k holds slot j
-  float l = lane < k ? lrow[sel] : -INFINITY;
-  const bool use = takes_part(l);
-  l = use ? finite_logit(l) : 0.f;
-  float p;
-  if (a.sigmoid) {
-    p = use ? 1.0f / (1.0f + expf(-l)) : 0.f;
-  } else if (a.renorm) {
-    const float m = wave_max_f32(use ? l : -INFINITY);
-    p = use ? expf(l - m) : 0.f;
-  } else {
-    float z = 0.f;
+          for (int i = 0; i < R; ++i) d[i] /= zd;
+        }
+        if (a.bias) {
 #pragma unroll
-    for (int i = 0; i < R; ++i) z += on[i] ? expf(v[i] - top) : 0.f;
-    z = wave_sum(z);
-    p = use ? expf(l - top) / z : 0.f;
-  }
-  if (a.renorm) {
-    const float den = wave_sum(p);
-    p = den > 0.f ? p / den : 0.f;
-  }
-  if (lane < k) {
-    idx[static_cast<size_t>(t) * k + lane] = sel;
-    w[static_cast<size_t>(t) * k + lane] = a.scale * p;
+          for (int i = 0; i < R; ++i) d[i] += static_cast<double>(bias[i]);
+        }
+        bool none = false;
+        in = true;
+        if (a.groups > 1) in = group_taken<R>(a, pl, d, on, 0.f, none);
+        uint64_t key64[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          key64[i] = i >= pl.count || !in ? 0ull : !on[i] ? 1ull
+                     : a.bias ? ordered_key64(d[i])
+                              : static_cast<uint64_t>(ordered_key(v[i])) << 32;   // the logits' order
+        select_topk<R, false>(a, pl, key64, v, 0.f, none, sel, l);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < R; ++i) key[i] = i >= pl.count ? 0u : !on[i] ? 1u : ordered_key(v[i]);
+      select_topk<R, false>(a, pl, key, v, tol, close, sel, l);
+    }
+    // weights of the selected, FP32: lane j < k holds slot j
+    const bool use = lane < k && takes_part(l);
+    l = use ? l : 0.f;
+    float p;
+    if (a.sigmoid) {
+      p = use ? 1.0f / (1.0f + expf(-l)) : 0.f;
+    } else if (a.renorm) {
+      const float m = wave_max_f32(use ? l : -INFINITY);
+      p = use ? expf(l - m) : 0.f;
+    } else {
+      float z = 0.f;
+#pragma unroll
+      for (int i = 0; i < R; ++i) z += on[i] ? expf(v[i] - top) : 0.f;
+      z = wave_sum(z);
+      p = use ? expf(l - top) / z : 0.f;
+    }
+    if (a.renorm) {
+      const float den = wave_sum(p);
+      p = den > 0.f ? p / den : 0.f;
+    }
+    if (lane < k) {
+      idx[static_cast<size_t>(t) * k + lane] = sel;
+      w[static_cast<size_t>(t) * k + lane] = a.scale * p;
+    }
   }
 }
 
@@ -297,22 +389,31 @@ RouteArgs route_args(const float* logits, const float* bias, int T, const Scored
 }  // namespace
 
 hipError_t launch_route_scored(const float* logits, const float* bias, int T, const ScoredRoute& p,
-                               int32_t* idx, float* w, hipStream_t s) {
+                               int32_t* idx, float* w, hipStream_t s, int num_cus) {
   const RouteArgs a = route_args(logits, bias, T, p);
-  const dim3 grid((T + kPerBlock - 1) / kPerBlock), block(kPerBlock * kWave);
+  // 8192 waves at most (a bias is read once by each)
+  const int blocks = (T + kPerBlock - 1) / kPerBlock;
+  const dim3 grid(blocks < 8 * num_cus ? blocks : 8 * num_cus), block(kPerBlock * kWave);
   const bool choice = bias != nullptr || p.groups > 1;
-  const size_t lds = p.groups > 1 ? kPerBlock * sizeof(double) * p.E : 0;   // at most 32 KB
+  int cand = (p.E + kWave - 1) / kWave;                    // candidates per lane
+  if (p.groups > 1) {
+    int span = 1;
+    while (2 * span * p.groups <= kWave) span *= 2;
+    cand = (p.E / p.groups + span - 1) / span;             // (at most 31: 33 groups of 31)
+  }
   prof_begin(kRoute, s);
 #define ROUTE(R)                                                                              \
   do {                                                                                        \
-    if (choice) hipLaunchKernelGGL((route_scored_kernel<R, true>), grid, block, lds, s, a, idx, w, order_key()); \
-    else hipLaunchKernelGGL((route_scored_kernel<R, false>), grid, block, 0, s, a, idx, w, order_key());         \
+    if (choice) hipLaunchKernelGGL((route_scored_kernel<R, true>), grid, block, 0, s, a, idx, w, order_key()); \
+    else hipLaunchKernelGGL((route_scored_kernel<R, false>), grid, block, 0, s, a, idx, w, order_key());       \
   } while (0)
-  if (p.E <= 64) ROUTE(1);
-  else if (p.E <= 128) ROUTE(2);
-  else if (p.E <= 256) ROUTE(4);
-  else if (p.E <= 512) ROUTE(8);
-  else ROUTE(16);
+  if (cand <= 1) ROUTE(1);
+  else if (cand <= 2) ROUTE(2);
+  else if (cand <= 4) ROUTE(4);
+  else if (cand <= 6) ROUTE(6);
+  else if (cand <= 8) ROUTE(8);
+  else if (cand <= 16) ROUTE(16);
+  else ROUTE(32);
 #undef ROUTE
   prof_end(kRoute, s);
   return hipGetLastError();
