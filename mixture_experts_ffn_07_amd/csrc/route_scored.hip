@@ -36,9 +36,61 @@ __device__ __forceinline__ double wave_sum64(double v) {
   for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, kWave);
   return v;
 }
-__device__ __forceinline__ float wave_max_f32(float v) {
-  return key_to_float(wave_max_u32(ordered_key(v)));     // (-inf and finite values)
+// One DPP step: the value of the lane that CTRL names (quad_perm [1,0,3,2] and [2,3,0,1],
+// row_half_mirror, row_mirror: partners 1, 2, 4 and 8 lanes away in a reduction).
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
 }
+template <int CTRL>
+__device__ __forceinline__ int dpp(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
+}
+__device__ __forceinline__ float lane_of(float v, int l) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
+}
+// Wave-wide maximum and sum, on every lane: within rows of 16 lanes, then over the rows.
+__device__ __forceinline__ float wave_max_f32(float v) {
+  v = fmaxf(v, dpp<0xB1>(v));
+  v = fmaxf(v, dpp<0x4E>(v));
+  v = fmaxf(v, dpp<0x141>(v));
+  v = fmaxf(v, dpp<0x140>(v));
+  return fmaxf(fmaxf(lane_of(v, 0), lane_of(v, 16)), fmaxf(lane_of(v, 32), lane_of(v, 48)));
+}
+__device__ __forceinline__ float wave_sum_f32(float v) {
+  v += dpp<0xB1>(v);
+  v += dpp<0x4E>(v);
+  v += dpp<0x141>(v);
+  v += dpp<0x140>(v);
+  return (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
+}
+
+// Wave-wide maximum of an integer, uniform.
+__device__ __forceinline__ int wave_max_i32(int v) {
+  v = max(v, dpp<0xB1>(v));
+  v = max(v, dpp<0x4E>(v));
+  v = max(v, dpp<0x141>(v));
+  v = max(v, dpp<0x140>(v));
+  return max(max(__builtin_amdgcn_readlane(v, 0), __builtin_amdgcn_readlane(v, 16)),
+             max(__builtin_amdgcn_readlane(v, 32), __builtin_amdgcn_readlane(v, 48)));
+}
+
+// exp(x), x <= 0, within about 1.5 units in the last place: 2^(x log2 e) with the
+// product's rounding error put back (the hardware's 2^h is good to one unit).
+__device__ __forceinline__ float exp_close(float x) {
+  x = fmaxf(x, -200.0f);                                 // (0 from there on; keeps the products finite)
+  constexpr float kL = 1.44269502162933349609375f, kLLow = 1.92596299112661746887e-8f;
+  const float h = x * kL;
+  const float l = fmaf(x, kL, -h) + x * kLLow;
+  return __builtin_amdgcn_exp2f(h) * fmaf(l, 0.693147180559945f, 1.0f);
+}
+
+// FP32 values as integers of the same order, and back.
+__device__ __forceinline__ int order_of(float f) {
+  const int b = __float_as_int(f);
+  return b ^ ((b >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float float_of(int o) { return __int_as_float(o ^ ((o >> 31) & 0x7FFFFFFF)); }
 
 // Monotone map of an FP64 value to 64 bits (-0 folded onto +0); finite values map
 // above 2^52, so 0 (taken, or not in a selected group) and 1 (masked) lie below.
@@ -76,6 +128,15 @@ __device__ __forceinline__ Place place(const RouteArgs& a) {
   return Place{g * size + m, span, g < a.groups && m < size ? (size - m + span - 1) / span : 0, span};
 }
 
+// Integer keys (order_of): candidates lie above kOffKey, masked experts and places
+// without a candidate at the bottom of the range.
+constexpr int kOffKey = -0x7F7F0000;                     // order_of(-3.3895e38), the mask's own value
+constexpr int kMaskedKey = -0x7FC00000;
+constexpr int kNone = -0x7FFFFFFF - 1;
+
+__device__ __forceinline__ float lane_value(float v, int l) { return lane_of(v, l); }
+__device__ __forceinline__ double lane_value(double v, int l) { return __shfl(v, l, kWave); }
+
 // Whether the group that this lane's candidates belong to takes part (C float or
 // double).  `close`: set where the FP32 scores do not decide it.
 template <int R, typename C>
@@ -83,23 +144,44 @@ __device__ __forceinline__ bool group_taken(const RouteArgs& a, const Place& pl,
                                             const bool (&on)[R], float tol, bool& close) {
   const int g = lane_id() / pl.span;
   C b1 = -INFINITY, b2 = -INFINITY;                      // largest, second largest
+  if constexpr (sizeof(C) == 4) {
+    int k1 = kNone, k2 = kNone;
+    auto take = [&](int x) {
+      k2 = max(k2, min(k1, x));
+      k1 = max(k1, x);
+    };
+    auto merge = [&](int o1, int o2) {
+      k2 = max(max(k2, o2), min(k1, o1));
+      k1 = max(k1, o1);
+    };
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const C x = on[i] ? c[i] : static_cast<C>(-INFINITY);
-    b2 = max(b2, min(b1, x));
-    b1 = max(b1, x);
-  }
-  for (int s = 1; s < pl.span; s *= 2) {
-    const C o1 = __shfl_xor(b1, s, kWave), o2 = __shfl_xor(b2, s, kWave);
-    b2 = max(max(b2, o2), min(b1, o1));
-    b1 = max(b1, o1);
+    for (int i = 0; i < R; ++i) take(on[i] ? order_of(c[i]) : kNone);
+    if (pl.span >= 2) merge(dpp<0xB1>(k1), dpp<0xB1>(k2));
+    if (pl.span >= 4) merge(dpp<0x4E>(k1), dpp<0x4E>(k2));
+    if (pl.span >= 8) merge(dpp<0x141>(k1), dpp<0x141>(k2));
+    if (pl.span >= 16) merge(dpp<0x140>(k1), dpp<0x140>(k2));
+    if (pl.span >= 32) merge(__shfl_xor(k1, 16, kWave), __shfl_xor(k2, 16, kWave));
+    b1 = k1 == kNone ? -INFINITY : float_of(k1);
+    b2 = k2 == kNone ? -INFINITY : float_of(k2);
+  } else {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const C x = on[i] ? c[i] : static_cast<C>(-INFINITY);
+      b2 = max(b2, min(b1, x));
+      b1 = max(b1, x);
+    }
+    for (int s = 1; s < pl.span; s *= 2) {
+      const C o1 = __shfl_xor(b1, s, kWave), o2 = __shfl_xor(b2, s, kWave);
+      b2 = max(max(b2, o2), min(b1, o1));
+      b1 = max(b1, o1);
+    }
   }
   // a group with one expert that takes part scores that expert's c alone
   C gs = a.group_top > 1 && b2 != -INFINITY ? b1 + b2 : b1;
   gs += static_cast<C>(0);                               // -0 and +0 tie
   int rank = 0;
   for (int o = 0; o < a.groups; ++o) {
-    const C os = __shfl(gs, o * pl.span, kWave);
+    const C os = lane_value(gs, o * pl.span);
     rank += os > gs || (os == gs && o < g) ? 1 : 0;
   }
   const bool taken = g < a.groups && rank < a.topk_groups;
@@ -112,63 +194,76 @@ __device__ __forceinline__ bool group_taken(const RouteArgs& a, const Place& pl,
 }
 
 // The k largest keys of a wave in order (key descending, expert ascending): lane j < k
-// gets slot j's expert and logit.  Key 0: no candidate, 1: masked.  kFloat: the keys are
-// FP32 values' (ordered_key); `close` is set where two neighbours among the first k + 1
-// lie within the error of those.
-template <int R, bool kFloat, typename K>
-__device__ __forceinline__ void select_topk(const RouteArgs& a, const Place& pl, K (&key)[R],
-                                            const float (&v)[R], float tol, bool& close, int& sel_e,
-                                            float& sel_l) {
+// gets slot j's expert.  Key 0: no candidate, 1: masked.
+template <int R, typename K>
+__device__ __forceinline__ int select_exact(const RouteArgs& a, const Place& pl, K (&key)[R]) {
   const int lane = lane_id();
-  sel_e = 0;
-  sel_l = 0.f;
-  K head = 0;                                            // the lane's largest key and its expert
-  int he = 0;
-  float hv = 0.f;
-  auto refresh = [&]() {
-    head = key[0];
-    he = pl.first;
-    hv = v[0];
+  int sel = 0;
+  for (int r = 0; r < a.k; ++r) {
+    K head = key[0];                                     // the lane's largest key and its expert
+    int he = pl.first;
 #pragma unroll
     for (int i = 1; i < R; ++i) {
       const bool gt = key[i] > head;
       head = gt ? key[i] : head;
       he = gt ? pl.first + pl.step * i : he;
-      hv = gt ? v[i] : hv;
     }
-  };
-  refresh();
-  float prev = INFINITY;
-  const int rounds = kFloat ? a.k + 1 : a.k;
-  for (int r = 0; r < rounds; ++r) {
     const K best = wave_max_key(head);
-    if (kFloat) {
-      if (best <= 1) {                                   // only masked ones are left: exact
-        prev = INFINITY;
-        if (r == a.k) break;
-      } else {
-        const float cur = key_to_float(static_cast<uint32_t>(best));
-        if (prev - cur < tol + 2.4e-7f * (fabsf(prev) + fabsf(cur))) close = true;
-        prev = cur;
-        if (r == a.k || close) break;
-      }
-    }
-    const uint64_t who = __ballot(head == best);
-    int win = __builtin_ctzll(who);
-    if (__popcll(who) > 1) {                             // a tie between lanes: the lowest expert
-      const uint32_t low = wave_max_u32(head == best ? ~static_cast<uint32_t>(he) : 0u);
-      win = __builtin_ctzll(__ballot(head == best && ~static_cast<uint32_t>(he) == low));
-    }
-    const int e = __builtin_amdgcn_readlane(he, win);
-    const float l = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(hv), win));
-    sel_e = lane == r ? e : sel_e;
-    sel_l = lane == r ? l : sel_l;
+    const uint32_t low = wave_max_u32(head == best ? ~static_cast<uint32_t>(he) : 0u);   // a tie: the lowest expert
+    const int e = static_cast<int>(~low);
+    sel = lane == r ? e : sel;
+#pragma unroll
+    for (int i = 0; i < R; ++i) key[i] = pl.first + pl.step * i == e ? static_cast<K>(0) : key[i];
+  }
+  return sel;
+}
+
+// The same from FP32 values (as integer keys) that may be off by `tol`: each key's low
+// bits make room for its place i in the lane, the lane's keys are sorted
+// (compare-exchanges of one maximum and one minimum), and each round takes the wave's
+// largest head and moves that lane's list up.  Returns false where that does not settle
+// the order: two neighbours among the first k + 1 within the keys' error, or a masked
+// expert among the k.
+template <int R>
+__device__ __forceinline__ bool select_fast(const RouteArgs& a, const Place& pl, int (&c)[R], float tol,
+                                            int& sel) {
+  constexpr int kBits = R <= 8 ? 3 : R <= 16 ? 4 : 5;
+  constexpr int kLow = (1 << kBits) - 1;
+  const int lane = lane_id();
+#pragma unroll
+  for (int i = 0; i < R; ++i) c[i] = (c[i] & ~kLow) | i;
+#pragma unroll
+  for (int p = 1; p < R; p *= 2)                         // odd-even merge sort, largest first
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+      for (int j = q % p; j + q < R; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (i + j + q < R && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const int hi = max(c[i + j], c[i + j + q]), lo = min(c[i + j], c[i + j + q]);
+            c[i + j] = hi;
+            c[i + j + q] = lo;
+          }
+  int mine = kNone;                                      // lane r: the r-th largest key
+  sel = 0;
+  for (int r = 0; r <= a.k; ++r) {
+    const int best = wave_max_i32(c[0]);
+    const int win = __builtin_ctzll(__ballot(c[0] == best));   // (equal heads: not settled below)
+    const int e = __builtin_amdgcn_readlane(pl.first, win) + pl.step * (best & kLow);
+    sel = lane == r ? e : sel;
+    mine = lane == r ? best : mine;
     if (lane == win) {
 #pragma unroll
-      for (int i = 0; i < R; ++i) key[i] = pl.first + pl.step * i == e ? static_cast<K>(0) : key[i];
-      refresh();
+      for (int j = 0; j + 1 < R; ++j) c[j] = c[j + 1];
+      c[R - 1] = kNone;
     }
   }
+  const int next = __shfl_down(mine, 1, kWave);
+  const float fm = float_of(mine), fn = float_of(next);
+  const float err = tol + (fabsf(fm) + fabsf(fn)) * (static_cast<float>(1 << kBits) * 1.1920929e-7f + 2.4e-7f);
+  const bool bad = lane < a.k && (mine < kOffKey || (next >= kOffKey && !(fm - fn >= err)));
+  return __ballot(bad) == 0;
 }
 
 }  // namespace
@@ -205,9 +300,8 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs a, int32_t*
     }
     if (!a.sigmoid && (kChoice || !a.renorm)) top = wave_max_f32(top);
     int sel;
-    float l;
-    bool close = false;
-    uint32_t key[R];
+    bool close = false, in = true;
+    int ck[R];
     if (kChoice) {
       float c[R];
       float z = 0.f;
@@ -218,7 +312,7 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs a, int32_t*
         z += c[i];
       }
       if (!a.sigmoid) {
-        z = __builtin_amdgcn_rcpf(wave_sum(z));
+        z = __builtin_amdgcn_rcpf(wave_sum_f32(z));
 #pragma unroll
         for (int i = 0; i < R; ++i) c[i] *= z;
       }
@@ -226,17 +320,19 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs a, int32_t*
 #pragma unroll
         for (int i = 0; i < R; ++i) c[i] += bias[i];
       }
-      bool in = true;
       if (a.groups > 1) in = group_taken<R>(a, pl, c, on, tol, close);
 #pragma unroll
-      for (int i = 0; i < R; ++i)
-        key[i] = i >= pl.count || !in ? 0u : !on[i] ? 1u : ordered_key(a.bias ? c[i] : v[i]);
-      if (!close) {
-        if (a.bias) select_topk<R, true>(a, pl, key, v, tol, close, sel, l);
-        else select_topk<R, false>(a, pl, key, v, tol, close, sel, l);
-      }
-      if (close) {                                       // the same in FP64
-        double d[R];
+      for (int i = 0; i < R; ++i) ck[i] = order_of(a.bias ? c[i] : v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < R; ++i) ck[i] = order_of(v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < R; ++i) ck[i] = i >= pl.count || !in ? kNone : on[i] ? ck[i] : kMaskedKey;
+    if (close || !select_fast<R>(a, pl, ck, kChoice && a.bias ? tol : 0.f, sel)) {
+      // exactly: on the logits, or on scores and sums in FP64
+      double d[R];
+      if (kChoice) {
         double zd = 0.0;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
@@ -257,38 +353,43 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs a, int32_t*
         bool none = false;
         in = true;
         if (a.groups > 1) in = group_taken<R>(a, pl, d, on, 0.f, none);
-        uint64_t key64[R];
+      }
+      if (kChoice && a.bias) {
+        uint64_t key[R];
 #pragma unroll
         for (int i = 0; i < R; ++i)
-          key64[i] = i >= pl.count || !in ? 0ull : !on[i] ? 1ull
-                     : a.bias ? ordered_key64(d[i])
-                              : static_cast<uint64_t>(ordered_key(v[i])) << 32;   // the logits' order
-        select_topk<R, false>(a, pl, key64, v, 0.f, none, sel, l);
-      }
-    } else {
+          key[i] = i >= pl.count || !in ? 0ull : !on[i] ? 1ull : ordered_key64(d[i]);
+        sel = select_exact<R>(a, pl, key);
+      } else {
+        uint32_t key[R];
 #pragma unroll
-      for (int i = 0; i < R; ++i) key[i] = i >= pl.count ? 0u : !on[i] ? 1u : ordered_key(v[i]);
-      select_topk<R, false>(a, pl, key, v, tol, close, sel, l);
+        for (int i = 0; i < R; ++i) key[i] = i >= pl.count || !in ? 0u : !on[i] ? 1u : ordered_key(v[i]);
+        sel = select_exact<R>(a, pl, key);
+      }
     }
     // weights of the selected, FP32: lane j < k holds slot j
-    const bool use = lane < k && takes_part(l);
-    l = use ? l : 0.f;
+    float l = lane < k ? lrow[sel] : -INFINITY;
+    const bool use = takes_part(l);
+    l = use ? finite_logit(l) : 0.f;
     float p;
-    if (a.sigmoid) {
-      p = use ? 1.0f / (1.0f + expf(-l)) : 0.f;
-    } else if (a.renorm) {
+    if (a.renorm) {
+      // relative to the largest: sigmoid(l) = exp(min(l, 0)) / (1 + exp(-|l|)), and the
+      // first factor over that of the largest does not vanish however low the logits are
       const float m = wave_max_f32(use ? l : -INFINITY);
-      p = use ? expf(l - m) : 0.f;
+      if (a.sigmoid) p = exp_close(fminf(l, 0.f) - fminf(m, 0.f)) * __builtin_amdgcn_rcpf(1.0f + exp_close(-fabsf(l)));
+      else p = exp_close(l - m);
+      p = use ? p : 0.f;
+      const float den = wave_sum_f32(p);
+      p = den > 0.f ? p / den : 0.f;
+    } else if (a.sigmoid) {
+      const float en = exp_close(-fabsf(l));
+      p = use ? (l < 0.f ? en : 1.0f) / (1.0f + en) : 0.f;
     } else {
       float z = 0.f;
 #pragma unroll
-      for (int i = 0; i < R; ++i) z += on[i] ? expf(v[i] - top) : 0.f;
-      z = wave_sum(z);
-      p = use ? expf(l - top) / z : 0.f;
-    }
-    if (a.renorm) {
-      const float den = wave_sum(p);
-      p = den > 0.f ? p / den : 0.f;
+      for (int i = 0; i < R; ++i) z += on[i] ? exp_close(v[i] - top) : 0.f;
+      z = wave_sum_f32(z);
+      p = use ? exp_close(l - top) / z : 0.f;
     }
     if (lane < k) {
       idx[static_cast<size_t>(t) * k + lane] = sel;
@@ -298,7 +399,7 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs a, int32_t*
 }
 
 // Gradient of the weights with the selection held fixed: one wave per token.
-//   sigmoid, renormalised:  dl_j = scale p_j (1 - p_j) (dw_j - sum w' dw) / sum p
+//   sigmoid, renormalised:  dl_j = scale w'_j (1 - p_j) (dw_j - sum w' dw)
 //   sigmoid:                dl_j = scale p_j (1 - p_j) dw_j
 //   softmax, renormalised:  dl_j = scale w'_j (dw_j - sum w' dw)
 //   softmax:                dl_e = scale p_e (dw_e [selected] - sum p dw)   for every e
@@ -329,22 +430,24 @@ __global__ __launch_bounds__(256) void route_scored_backward_kernel(
   for (int i = 0; i < R; ++i) g[i] = 0.f;
   float val;                                             // slot j's own term
   if (a.sigmoid) {
-    const float p = use ? 1.0f / (1.0f + expf(-l)) : 0.f;
-    const float q = use ? 1.0f / (1.0f + expf(l)) : 0.f;    // 1 - p without cancellation
-    if (a.renorm) {
-      const float z = wave_sum(p);
-      const float mean = wave_sum(p * d) / z;
-      val = z > 0.f ? p * q * (d - mean) / z : 0.f;
+    const float en = exp_close(-fabsf(l)), r = 1.0f / (1.0f + en);
+    const float q = (l < 0.f ? 1.0f : en) * r;             // 1 - p without cancellation
+    if (a.renorm) {                                        // (the forward's weights)
+      const float m = wave_max_f32(use ? l : -INFINITY);
+      const float x = use ? exp_close(fminf(l, 0.f) - fminf(m, 0.f)) * r : 0.f;
+      const float z = wave_sum_f32(x);
+      const float p = z > 0.f ? x / z : 0.f;
+      val = p * q * (d - wave_sum_f32(p * d));
     } else {
-      val = p * q * d;
+      val = (l < 0.f ? en : 1.0f) * r * q * d;
     }
     val *= a.scale;
   } else if (a.renorm) {
     const float m = wave_max_f32(use ? l : -INFINITY);
-    const float x = use ? expf(l - m) : 0.f;
-    const float z = wave_sum(x);
+    const float x = use ? exp_close(l - m) : 0.f;
+    const float z = wave_sum_f32(x);
     const float p = z > 0.f ? x / z : 0.f;
-    val = a.scale * p * (d - wave_sum(p * d));
+    val = a.scale * p * (d - wave_sum_f32(p * d));
   } else {
     float v[R], top = -INFINITY;
 #pragma unroll
@@ -358,13 +461,13 @@ __global__ __launch_bounds__(256) void route_scored_backward_kernel(
     float z = 0.f;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      g[i] = v[i] > -INFINITY ? expf(v[i] - top) : 0.f;
+      g[i] = v[i] > -INFINITY ? exp_close(v[i] - top) : 0.f;
       z += g[i];
     }
-    z = wave_sum(z);
+    z = wave_sum_f32(z);
     const float inv = z > 0.f ? 1.0f / z : 0.f;
-    const float p = use ? expf(l - top) * inv : 0.f;
-    const float mean = wave_sum(p * d);
+    const float p = use ? exp_close(l - top) * inv : 0.f;
+    const float mean = wave_sum_f32(p * d);
 #pragma unroll
     for (int i = 0; i < R; ++i) g[i] *= -a.scale * inv * mean;
     val = a.scale * p * d;
