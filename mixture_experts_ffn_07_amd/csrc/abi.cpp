@@ -451,7 +451,7 @@ int moe_add_rmsnorm(const uint16_t* x, const uint16_t* residual, const uint16_t*
 
 size_t moe_add_rmsnorm_backward_workspace_bytes(int T, int H) {
   if (T < 0 || H <= 0) return 0;
-  const size_t rows = static_cast<size_t>(moe::norm_backward_rows(T));
+  const size_t rows = static_cast<size_t>(moe::norm_backward_rows(T, H));
   return (rows > 0 ? rows : 1) * static_cast<size_t>(H) * sizeof(float);
 }
 

@@ -98,8 +98,7 @@ hipError_t launch_route_scored_backward(const float* logits, const int32_t* idx,
 
 // Residual sum + RMS norm (norm.hip).  qtype: MOE_BF16 (no 8-bit output), MOE_MXFP8, MOE_INT8.
 constexpr int kNormMaxH = 16384;           // a row is held in one workgroup's registers
-constexpr int kNormBackwardGrid = 512;     // workgroups (rows of partial weight gradients)
-int norm_backward_rows(int T);
+int norm_backward_rows(int T, int H);      // workgroups (rows of partial weight gradients)
 hipError_t launch_add_rmsnorm(const uint16_t* x, const uint16_t* r, const uint16_t* w, int T, int H,
                               float eps, uint16_t* sum, uint16_t* y, int qtype, uint8_t* codes,
                               void* scales, hipStream_t s, int num_cus);

@@ -186,14 +186,15 @@ __global__ __launch_bounds__(1024) void quant_int8_rows(const uint16_t* __restri
 
 // Backward.  With n = s q (the normed row before the weight),
 //   dx = q (w dy - n mean(n w dy)) + ds      dw = sum over rows of n dy
-// Workgroup b takes rows b, b + gridDim.x, ...: each lane keeps its columns'
-// share of dw in registers and writes it once, into row b of `partial`;
-// norm_dweight adds the gridDim.x rows in order.
+// Workgroup b takes rows b, b + gridDim.x, ...: each lane keeps its columns' share of
+// dw in registers and writes it once, into row b of `partial`; norm_dweight adds the
+// gridDim.x rows in a fixed order.  The next row is on its way while one is worked on,
+// and the two sums of a row share one barrier.
 template <int NV>
 __global__ __launch_bounds__(1024) void add_rmsnorm_backward_kernel(
     const uint16_t* s, const uint16_t* __restrict__ w, const uint16_t* dy, const uint16_t* ds,
     int T, int H, float eps, uint16_t* dx, float* __restrict__ partial, uint32_t okey) {
-  __shared__ float red[2][2][16];                  // [row parity][sum][wave]
+  __shared__ float2 red[2][16];                    // [row parity][wave]
   const int nvec = H / kVec;
   float acc[NV][kVec];
   i32x4 wr[NV];
@@ -206,10 +207,9 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_backward_kernel(
     for (int i = 0; i < kVec; ++i) acc[v][i] = 0.f;
   }
   const int b = permute_item(blockIdx.x, gridDim.x, okey);
-  int par = 0;
-  for (int t = b; t < T; t += gridDim.x, par ^= 1) {
+  i32x4 sr[NV], dr[NV], er[NV];
+  auto fetch = [&](int t) {
     const int64_t row = static_cast<int64_t>(t) * H;
-    i32x4 sr[NV], dr[NV], er[NV];
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = v * blockDim.x + threadIdx.x;
@@ -220,31 +220,58 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_backward_kernel(
         if (ds) er[v] = ld16(ds + row + c * kVec);
       }
     }
-    float ss = 0.f, sd = 0.f;                      // sum s^2, sum s w dy
+  };
+  if (b < T) fetch(b);
+  int par = 0;
+  for (int t = b; t < T; t += gridDim.x, par ^= 1) {
+    i32x4 s0[NV], d0[NV], e0[NV];
+    float2 sum = {0.f, 0.f};                       // sum s^2, sum s w dy
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      s0[v] = sr[v];
+      d0[v] = dr[v];
+      e0[v] = er[v];
+    }
+    // a later row of this workgroup: dx written in place does not reach it
+    if (t + static_cast<int>(gridDim.x) < T) fetch(t + gridDim.x);
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       float a[kVec], d[kVec], g[kVec];
-      unpack8(sr[v], a);
-      unpack8(dr[v], d);
+      unpack8(s0[v], a);
+      unpack8(d0[v], d);
       unpack8(wr[v], g);
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
-        ss = fmaf(a[i], a[i], ss);
-        sd = fmaf(a[i], g[i] * d[i], sd);
+        sum.x = fmaf(a[i], a[i], sum.x);
+        sum.y = fmaf(a[i], g[i] * d[i], sum.y);
       }
     }
-    ss = block_sum(ss, red[par][0]);
-    sd = block_sum(sd, red[par][1]);
-    const float q = 1.0f / sqrtf(ss / static_cast<float>(H) + eps);
-    const float m = sd * q / static_cast<float>(H);   // mean(n w dy)
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) {
+      sum.x += __shfl_xor(sum.x, m, kWave);
+      sum.y += __shfl_xor(sum.y, m, kWave);
+    }
+    const int nw = blockDim.x / kWave;
+    if (nw > 1) {
+      if (lane_id() == 0) red[par][wave_id()] = sum;
+      __syncthreads();
+      sum = red[par][0];
+      for (int i = 1; i < nw; ++i) {
+        sum.x += red[par][i].x;
+        sum.y += red[par][i].y;
+      }
+    }
+    const float q = 1.0f / sqrtf(sum.x / static_cast<float>(H) + eps);
+    const float m = sum.y * q / static_cast<float>(H);   // mean(n w dy)
+    const int64_t row = static_cast<int64_t>(t) * H;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int c = v * blockDim.x + threadIdx.x;
       float a[kVec], d[kVec], g[kVec], e[kVec];
-      unpack8(sr[v], a);
-      unpack8(dr[v], d);
+      unpack8(s0[v], a);
+      unpack8(d0[v], d);
       unpack8(wr[v], g);
-      unpack8(er[v], e);
+      unpack8(e0[v], e);
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
         const float n = a[i] * q;
@@ -265,21 +292,32 @@ __global__ __launch_bounds__(1024) void add_rmsnorm_backward_kernel(
   }
 }
 
-// dweight[c] = bf16(sum of `rows` partial rows): 64 columns per workgroup, wave i
-// of 16 adding rows i, i + 16, ... in order, then the waves' sums in wave order.
-__global__ __launch_bounds__(1024) void norm_dweight(const float* __restrict__ partial, int rows,
-                                                     int H, uint16_t* __restrict__ dweight) {
-  __shared__ float red[16][kWave];
-  const int c = blockIdx.x * kWave + lane_id();
-  float a = 0.f;
-  if (c < H)
-    for (int i = wave_id(); i < rows; i += 16) a += partial[static_cast<int64_t>(i) * H + c];
-  red[wave_id()][lane_id()] = a;
+// dweight[c] = bf16(sum of `rows` partial rows): 32 columns per workgroup, thread (row
+// lane i, four columns) adding rows i, i + 32, ... in order, eight of them in flight,
+// then the 32 row lanes' sums in order.
+__global__ __launch_bounds__(256) void norm_dweight(const float* __restrict__ partial, int rows,
+                                                    int H, uint16_t* __restrict__ dweight) {
+  __shared__ f32x4 red[32][8];
+  const int quad = threadIdx.x & 7, i0 = threadIdx.x >> 3;
+  const float* p = partial + blockIdx.x * 32 + quad * 4;
+  f32x4 a = {0.f, 0.f, 0.f, 0.f};
+  for (int i = i0; i < rows; i += 32 * 8) {
+    f32x4 v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      v[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (i + 32 * u < rows) v[u] = *reinterpret_cast<const f32x4*>(p + static_cast<int64_t>(i + 32 * u) * H);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) a += v[u];
+  }
+  red[i0][quad] = a;
   __syncthreads();
-  if (wave_id() == 0 && c < H) {
-    float s = red[0][lane_id()];
-    for (int i = 1; i < 16; ++i) s += red[i][lane_id()];
-    dweight[c] = static_cast<uint16_t>(f32_to_bf16_rne(s));
+  if (threadIdx.x < 32) {
+    const float* r = reinterpret_cast<const float*>(&red[0][0]) + threadIdx.x;
+    float s = r[0];
+    for (int i = 1; i < 32; ++i) s += r[32 * i];
+    dweight[blockIdx.x * 32 + threadIdx.x] = static_cast<uint16_t>(f32_to_bf16_rne(s));
   }
 }
 
@@ -333,13 +371,21 @@ hipError_t launch_quant_int8(const uint16_t* src, int64_t rows, int K, uint8_t* 
   return hipGetLastError();
 }
 
-int norm_backward_rows(int T) { return T < kNormBackwardGrid ? T : kNormBackwardGrid; }
+// Workgroups of the backward pass: as many as fill 256 CUs with 16 waves each, 1024 at
+// most (every workgroup writes a row of partial weight gradients).  Measured, us (256 /
+// 512 / 1024 workgroups): 2048 x 7168 25.9 / 31.0 / 36.1; 8192 x 4096 49.6 / 46.6 / 51.3;
+// 16384 x 2048 71.6 / 50.0 / 46.5; 16000 x 512 49.2 / 31.4 / 22.0.
+int norm_backward_rows(int T, int H) {
+  const int waves = row_shape(H / kVec, true).threads / kWave;
+  const int grid = waves > 8 ? 256 : waves > 4 ? 512 : 1024;
+  return T < grid ? T : grid;
+}
 
 hipError_t launch_add_rmsnorm_backward(const uint16_t* sum, const uint16_t* w, const uint16_t* dy,
                                        const uint16_t* ds, int T, int H, float eps, uint16_t* dx,
                                        uint16_t* dweight, float* partial, hipStream_t s) {
   const RowShape rs = row_shape(H / kVec, true);
-  const int rows = norm_backward_rows(T);
+  const int rows = norm_backward_rows(T, H);
   prof_begin(kNormBackward, s);
   if (rows > 0) {
     if (rs.nv == 1)
@@ -349,7 +395,7 @@ hipError_t launch_add_rmsnorm_backward(const uint16_t* sum, const uint16_t* w, c
       hipLaunchKernelGGL(add_rmsnorm_backward_kernel<2>, dim3(rows), dim3(rs.threads), 0, s, sum, w, dy,
                          ds, T, H, eps, dx, partial, order_key());
   }
-  hipLaunchKernelGGL(norm_dweight, dim3((H + kWave - 1) / kWave), dim3(1024), 0, s, partial, rows, H,
+  hipLaunchKernelGGL(norm_dweight, dim3(H / 32), dim3(256), 0, s, partial, rows, H,
                      dweight);
   prof_end(kNormBackward, s);
   return hipGetLastError();

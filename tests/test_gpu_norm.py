@@ -176,8 +176,9 @@ def test_norm_backward(M, T, H, res):
     m_abs = np.abs(n * w64 * dy64).mean(axis=1, keepdims=True)
     terms = q * (np.abs(w64 * dy64) + 2 * np.abs(n) * m_abs) + (np.abs(_f64(ds)) if res else 0)
     _check_bf16(dx, rdx, slack=terms * F32)
-    # the sum over rows: at most T / 512 + 1 terms per lane, 32 + 16 partial sums
-    count = T / 512 + 1 + 48
+    # the sum over rows: at most T / 256 + 1 terms per lane, then up to 1024 partial rows in 32
+    # sums of 32 and a sum of those
+    count = T / 256 + 1 + 64
     _check_bf16(dw, rdw, slack=np.abs(dy64 * n).sum(axis=0) * (count * 2.0 ** -24 + F32))
 
 
