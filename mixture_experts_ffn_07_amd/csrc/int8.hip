@@ -338,14 +338,17 @@ __global__ __launch_bounds__(256) void gemm_large_i8(
     const int rr = r < mcount ? r : 0;
     bo[j] = static_cast<uint32_t>((GU ? perm[rbase + rr] / k : rbase + rr) * K + lc * 16);
   }
-  // LDS: row r, chunk c at r*128 + ((c ^ (r & 7)) * 16); here r & 7 == lrow
-  const int lw = (wv * 64 + lrow) * k8BK + ((lc ^ lrow) * 16);
+  // LDS: row r, chunk c at r*128 + ((c ^ ((r >> 1) & 7)) * 16): the 16 rows that a read
+  // serves at once then lie in 64 different banks (two rows span them all, so rows r and
+  // r + 2 must differ); of a thread's rows 8j + lrow the odd j's chunk is c ^ 4
+  const int lw0 = (wv * 64 + lrow) * k8BK + ((lc ^ (lrow >> 1)) * 16);
+  const int lw1 = lw0 ^ 64;
   int fa[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     fa[i] = ((GU ? (i >> 1) * 128 + wn * 64 + (i & 1) * 32 : wn * 128 + 32 * i) + l32) * k8BK;
   const int fb = (wm * 128 + l32) * k8BK;
-  const int swz = l32 & 7;
+  const int swz = (l32 >> 1) & 7;
 
   i32x4 stg[16];   // [0..7] weight rows, [8..15] activation rows
 #define GLOAD(Q, KT) do {                                                               \
@@ -355,7 +358,7 @@ __global__ __launch_bounds__(256) void gemm_large_i8(
   } while (0)
 #define LWRITE(Q, KT) do {                                                              \
     uint8_t* st_ = lds8 + ((KT) & 1) * 2 * k8Tile + ((Q) < 8 ? 0 : k8Tile);             \
-    *reinterpret_cast<i32x4*>(&st_[lw + ((Q) & 7) * 8 * k8BK]) = stg[Q];                \
+    *reinterpret_cast<i32x4*>(&st_[((Q) & 1 ? lw1 : lw0) + ((Q) & 7) * 8 * k8BK]) = stg[Q]; \
   } while (0)
 #define RDF(PTR) (*reinterpret_cast<const i32x4*>(PTR))
   // One MFMA K step on fragments (A, B): 8 groups of 2 MFMAs; groups 0..3 then read
