@@ -68,27 +68,58 @@ BatchedWs batched_ws_layout(int T, int H, int I, int E, int k, int dtype) {
 
 // ---------------------------------------------------------------------------
 // Expert grouping.  Workgroup e builds the full expert histogram in LDS
-// (integer atomics: the totals do not depend on their order), takes its own
-// offset and tile offset from the counts of experts < e, then walks the pairs
-// in order and compacts those routed to e with wave ballots, so the order
-// inside an expert is ascending pair id (= ascending token).  Pairs whose id
-// is out of range get row_of = P (ignored downstream) from workgroup 0.
+// (integer atomics: the totals do not depend on their order; with 8 experts or
+// fewer, wave ballots, since a wave's lanes would queue at the same few
+// counters), takes its own offset and tile offset from the counts of experts
+// < e, then compacts the pairs routed to e: each wave owns a contiguous run of
+// pairs, so its count alone gives the waves' places, and order inside an expert
+// is ascending pair id (= ascending token).  A wave's first kGroupKeep * 64 ids
+// stay in registers between the two passes.  Pairs whose id is out of range get
+// row_of = P (ignored downstream) from workgroup 0.
+constexpr int kGroupKeep = 16;
 __global__ __launch_bounds__(1024) void group_experts(
     const int32_t* __restrict__ idx, int P, int E, int BM, int* __restrict__ counts,
     int* __restrict__ offsets, int2* __restrict__ tiles, int* __restrict__ n_tiles,
     int* __restrict__ perm, int* __restrict__ row_of, uint32_t okey) {
   __shared__ int hist[1024];
-  __shared__ int s_red[2][16];
-  __shared__ int s_wcnt[16];
+  __shared__ int s_red[3][16];
   const int tid = threadIdx.x, wv = wave_id(), lane = lane_id();
   const int e = permute_item(blockIdx.x, gridDim.x, okey);
+  const int nw = blockDim.x / kWave;
   for (int i = tid; i < E; i += blockDim.x) hist[i] = 0;
   __syncthreads();
-  for (int i = tid; i < P; i += blockDim.x) {
-    const unsigned v = static_cast<unsigned>(idx[i]);
-    if (v < static_cast<unsigned>(E)) atomicAdd(&hist[v], 1);
-    else if (e == 0) row_of[i] = P;
+  const int per = (P + nw * kWave - 1) / (nw * kWave);    // 64-pair steps per wave
+  const int i0 = wv * per * kWave;
+  int keep[kGroupKeep];
+  int mine = 0;                                           // this wave's pairs of expert e
+  int small = 0;                                          // lane j < E <= 8: this wave's pairs of expert j
+  auto tally = [&](int i, int v) {
+    const bool in = static_cast<unsigned>(v) < static_cast<unsigned>(E);
+    if (i < P && !in && e == 0) row_of[i] = P;
+    mine += __popcll(__ballot(v == e));
+    if (E <= 8) {
+      for (int j = 0; j < E; ++j) {
+        const int c = __popcll(__ballot(v == j));
+        small += lane == j ? c : 0;
+      }
+    } else if (in) {
+      atomicAdd(&hist[v], 1);
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < kGroupKeep; ++s) {
+    const int i = i0 + s * kWave + lane;
+    keep[s] = s < per && i < P ? idx[i] : -1;
   }
+#pragma unroll
+  for (int s = 0; s < kGroupKeep; ++s)
+    if (s < per) tally(i0 + s * kWave + lane, keep[s]);
+  for (int s = kGroupKeep; s < per; ++s) {
+    const int i = i0 + s * kWave + lane;
+    tally(i, i < P ? idx[i] : -1);
+  }
+  if (E <= 8 && lane < E && small) atomicAdd(&hist[lane], small);
+  if (lane == 0) s_red[2][wv] = mine;
   __syncthreads();
   // offsets of expert e: sum of counts and of tile counts over experts < e
   int c_sum = 0, t_sum = 0;
@@ -105,11 +136,11 @@ __global__ __launch_bounds__(1024) void group_experts(
     s_red[1][wv] = t_sum;
   }
   __syncthreads();
-  int off = 0, toff = 0;
-  const int nw = blockDim.x / kWave;
+  int off = 0, toff = 0, pos = 0;
   for (int w = 0; w < nw; ++w) {
     off += s_red[0][w];
     toff += s_red[1][w];
+    pos += w < wv ? s_red[2][w] : 0;
   }
   const int cnt = hist[e];
   const int ntile = (cnt + BM - 1) / BM;
@@ -122,27 +153,23 @@ __global__ __launch_bounds__(1024) void group_experts(
     }
   }
   for (int q = tid; q < ntile; q += blockDim.x) tiles[toff + q] = make_int2(e, q * BM);
-  // ordered compaction of the pairs routed to e
-  int running = 0;
-  for (int base = 0; base < P; base += blockDim.x) {
-    const int i = base + tid;
-    const bool match = i < P && idx[i] == e;
-    const uint64_t b = __ballot(match);
-    if (lane == 0) s_wcnt[wv] = __popcll(b);
-    __syncthreads();
-    int before = 0, total = 0;
-    for (int w = 0; w < nw; ++w) {
-      const int c = s_wcnt[w];
-      before += w < wv ? c : 0;
-      total += c;
+  // ordered compaction of the wave's pairs routed to e
+  pos += off;
+  auto place = [&](int i, int v) {
+    const uint64_t b = __ballot(v == e);
+    if (v == e) {
+      const int p = pos + __popcll(b & ((1ull << lane) - 1));
+      perm[p] = i;
+      row_of[i] = p;
     }
-    if (match) {
-      const int pos = off + running + before + __popcll(b & ((1ull << lane) - 1));
-      perm[pos] = i;
-      row_of[i] = pos;
-    }
-    running += total;
-    __syncthreads();
+    pos += __popcll(b);
+  };
+#pragma unroll
+  for (int s = 0; s < kGroupKeep; ++s)
+    if (s < per) place(i0 + s * kWave + lane, keep[s]);
+  for (int s = kGroupKeep; s < per; ++s) {
+    const int i = i0 + s * kWave + lane;
+    place(i, i < P ? idx[i] : -1);
   }
 }
 

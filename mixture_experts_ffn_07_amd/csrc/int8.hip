@@ -14,6 +14,8 @@
 // gate/up product with SwiGLU into FP32 a, the rows' codes and scales, the down
 // product, and the slot sum.  A pair whose expert id lies outside [0, E) has no
 // row: it adds nothing to its token.
+#include <type_traits>
+
 #include "common.h"
 #include "gemm_large.h"
 #include "internal.h"
@@ -33,6 +35,13 @@ __device__ __forceinline__ i32x4 mfma_i8(i32x4 a, i32x4 b, i32x4 c) {
 }
 
 enum { kGateUp8 = 0, kDown8 = 1, kDownFused8 = 2 };
+
+// silu(g) u on the hardware's reciprocal (one unit in the last place): an exact division
+// takes ten instructions more, and the 256-row tiles' epilogue is bound by them.  Every
+// form uses this one, so a pair's activations have the same bits in all of them.
+__device__ __forceinline__ float swiglu8(float g, float u) {
+  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
+}
 
 }  // namespace
 
@@ -226,7 +235,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == 6
     if (GU) {
       f32x4 o;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = swiglu(v0[i], v1[i]);
+      for (int i = 0; i < 4; ++i) o[i] = swiglu8(v0[i], v1[i]);
       st16_stream(y + static_cast<size_t>(rbase + r) * I + nb + 4 * grp, o);
     } else if (KIND == kDownFused8) {
       const float wt_ = w[pr];                            // k = 1: pair id == token
@@ -456,46 +465,51 @@ __global__ __launch_bounds__(256) void gemm_large_i8(
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     ws[i] = wse[GU ? (i >> 1) * I + n0 + wn * 64 + (i & 1) * 32 + l32 : nb * 256 + wn * 128 + 32 * i + l32];
+  // whole tiles (the most of them) without the checks of each row
+  auto store = [&](auto whole) {
+    constexpr bool kWhole = decltype(whole)::value;
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 4; ++j)
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int r0 = wm * 128 + 32 * j + 8 * q + 4 * hi;
-      if (r0 >= mcount) continue;
-      const f32x4 sx = *reinterpret_cast<const f32x4*>(s_sx + r0);
-      if (KIND == kDownFused8) {
-        const i32x4 pr = *reinterpret_cast<const i32x4*>(s_pr + r0);
-        const f32x4 wt4 = *reinterpret_cast<const f32x4*>(s_w + r0);
-        const int odd = l32 & 1;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float v[4];
-#pragma unroll
-          for (int t = 0; t < 4; ++t)
-            v[t] = wt4[t] * (static_cast<float>(acc[i][j][4 * q + t]) * sx[t] * ws[i]);
+      for (int q = 0; q < 4; ++q) {
+        __builtin_amdgcn_sched_barrier(0);               // (one group of rows at a time: fewer registers live)
+        const int r0 = wm * 128 + 32 * j + 8 * q + 4 * hi;
+        if (!kWhole && r0 >= mcount) continue;
+        const f32x4 sx = *reinterpret_cast<const f32x4*>(s_sx + r0);
+        if (KIND == kDownFused8) {
+          const i32x4 pr = *reinterpret_cast<const i32x4*>(s_pr + r0);
+          const f32x4 wt4 = *reinterpret_cast<const f32x4*>(s_w + r0);
+          const int odd = l32 & 1;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t o = pair_rows_bf16(v[2 * h], v[2 * h + 1], odd);
-            const int t = 2 * h + odd;
-            if (r0 + t < mcount)
-              *reinterpret_cast<uint32_t*>(out + static_cast<size_t>(odd ? pr[2 * h + 1] : pr[2 * h]) * H +
-                                           nb * 256 + wn * 128 + 32 * i + l32 - odd) = o;
+            uint16_t* orow = out + static_cast<size_t>(odd ? pr[2 * h + 1] : pr[2 * h]) * H + nb * 256 + wn * 128 + l32 - odd;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float v[2];
+#pragma unroll
+              for (int t = 0; t < 2; ++t)
+                v[t] = wt4[2 * h + t] * (static_cast<float>(acc[i][j][4 * q + 2 * h + t]) * sx[2 * h + t] * ws[i]);
+              const uint32_t o = pair_rows_bf16(v[0], v[1], odd);   // (both lanes of a pair take part)
+              if (kWhole || r0 + 2 * h + odd < mcount) *reinterpret_cast<uint32_t*>(orow + 32 * i) = o;
+            }
           }
-        }
-      } else {
+        } else {
 #pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          if (r0 + t >= mcount) continue;
-          float* yr = y + static_cast<size_t>(rbase + r0 + t) * (GU ? I : H) +
-                      (GU ? n0 + wn * 64 : nb * 256 + wn * 128) + l32;
+          for (int t = 0; t < 4; ++t) {
+            if (!kWhole && r0 + t >= mcount) continue;
+            float* yr = y + static_cast<size_t>(rbase + r0 + t) * (GU ? I : H) +
+                        (GU ? n0 + wn * 64 : nb * 256 + wn * 128) + l32;
 #pragma unroll
-          for (int i = 0; i < (GU ? 2 : 4); ++i) {
-            const float v = static_cast<float>(acc[i][j][4 * q + t]) * sx[t] * ws[i];
-            yr[32 * i] = GU ? swiglu(v, static_cast<float>(acc[(i + 2) & 3][j][4 * q + t]) * sx[t] * ws[(i + 2) & 3]) : v;
+            for (int i = 0; i < (GU ? 2 : 4); ++i) {
+              const float v = static_cast<float>(acc[i][j][4 * q + t]) * sx[t] * ws[i];
+              yr[32 * i] = GU ? swiglu8(v, static_cast<float>(acc[(i + 2) & 3][j][4 * q + t]) * sx[t] * ws[(i + 2) & 3]) : v;
+            }
           }
         }
       }
-    }
+  };
+  if (mcount == kLargeBM) store(std::true_type{});
+  else store(std::false_type{});
 }
 
 // Tail fix-up, element-parallel: thread g of the grid takes one i32x4 of the partial
@@ -542,7 +556,7 @@ __global__ __launch_bounds__(256) void gemm_large_i8_fixup(
     const int row = rbase + r0 + t, pr = perm[row];
     const float sx = GU ? acts[pr / k] : acts[row];
     const float v = static_cast<float>(a[t]) * sx * wa;
-    if (GU) y[static_cast<size_t>(row) * I + n] = swiglu(v, static_cast<float>(u[t]) * sx * wu);
+    if (GU) y[static_cast<size_t>(row) * I + n] = swiglu8(v, static_cast<float>(u[t]) * sx * wu);
     else if (KIND == kDownFused8) out[static_cast<size_t>(pr) * H + n] = static_cast<uint16_t>(f32_to_bf16_rne(w[pr] * v));
     else y[static_cast<size_t>(row) * H + n] = v;
   }
@@ -681,7 +695,7 @@ __global__ __launch_bounds__(256) void pairs_gate_up(
     const float* ws = wgus + static_cast<size_t>(e) * 2 * I + n0 + c;
     const float g = static_cast<float>(s_dot[c]) * sx * ws[0];
     const float u = static_cast<float>(s_dot[16 + c]) * sx * ws[I];
-    a[static_cast<size_t>(p) * I + n0 + c] = swiglu(g, u);
+    a[static_cast<size_t>(p) * I + n0 + c] = swiglu8(g, u);
   }
 }
 
