@@ -116,6 +116,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == 6
   const int e = te.x, m0 = te.y;
   const int mcount = min(BM, counts[e] - m0);
   const int rbase = offsets[e] + m0;
+  const int ng = __builtin_amdgcn_readfirstlane((mcount + 15) / 16);   // 16-row groups that hold rows
   const int tid = threadIdx.x, ln = tid & 63, col = ln & 15, grp = ln >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nb = nb_i * NW * RPW + wv * RPW;              // the wave's first output
@@ -184,6 +185,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == 6
     b[0][1] = *reinterpret_cast<const i32x4*>(xcur + 64);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
+      if (g && g >= ng) break;                            // (uniform: the tile has no rows there)
       if (g + 1 < G) {
         const uint8_t* p = xcur + (16 * (g + 1)) * RS;
         b[(g + 1) & 1][0] = *reinterpret_cast<const i32x4*>(p);
