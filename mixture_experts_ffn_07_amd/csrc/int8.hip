@@ -144,21 +144,27 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == 6
     const int arow = GU ? perm[rbase + rr] / k : rbase + rr;
     oxl[i] = static_cast<uint32_t>(arow * K + (c % CH) * 16);
   }
-  i32x4 xr[LPT];
+  const int nchunk = K / 128, nstage = nchunk / 2;
+  i32x4 xr[LPT], wA[4], wB[4];
 #pragma unroll
   for (int i = 0; i < LPT; ++i) xr[i] = ld16(act + oxl[i]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) wA[i] = ld16_stream(wb + ow[i]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) wB[i] = ld16_stream(wb + ow[i] + 128);
+  // the epilogue's data (tile row tid's pair and scale, output tid's weight scale): its
+  // latency passes during the products, and it goes through LDS after them
+  const float* ws_e = wts + static_cast<size_t>(e) * wrows;
+  const int my_pr = perm[rbase + (tid < mcount ? tid : 0)];
+  const float my_sx = GU ? acts[my_pr / k] : acts[rbase + (tid < mcount ? tid : 0)];
+  const int my_n = nb_i * NW * RPW;
+  const float my_ws = tid < 32 * NW ? ws_e[GU && tid >= 16 * NW ? I + my_n + tid - 16 * NW : my_n + tid] : 0.f;
 #pragma unroll
   for (int i = 0; i < LPT; ++i) *reinterpret_cast<i32x4*>(&xl[0][lrow[i]]) = xr[i];
 
   i32x4 acc0[G], acc1[G];
 #pragma unroll
   for (int g = 0; g < G; ++g) acc0[g] = acc1[g] = i32x4{0, 0, 0, 0};
-  const int nchunk = K / 128, nstage = nchunk / 2;
-  i32x4 wA[4], wB[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) wA[i] = ld16_stream(wb + ow[i]);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) wB[i] = ld16_stream(wb + ow[i] + 128);
   __syncthreads();
 
   // One chunk: the weights through the wave's LDS tile into operands (both row groups
@@ -219,15 +225,24 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == 6
     publish(st + 1);
   }
   // lane: outputs row0 + 4grp + i (group 0) and row1 + 4grp + i (group 1) of tile row 16g + col
-  const float* ws_e = wts + static_cast<size_t>(e) * wrows;
-  const f32x4 s0 = *reinterpret_cast<const f32x4*>(ws_e + row0 + 4 * grp);
-  const f32x4 s1 = *reinterpret_cast<const f32x4*>(ws_e + row1 + 4 * grp);
+  int* s_pr = reinterpret_cast<int*>(xl[0]);              // (every wave is done with the stages)
+  float* s_sx = reinterpret_cast<float*>(xl[0]) + BM;
+  float* s_ws = reinterpret_cast<float*>(xl[0]) + 2 * BM;
+  if (tid < BM) {
+    s_pr[tid] = my_pr;
+    s_sx[tid] = my_sx;
+  }
+  if (tid < 32 * NW) s_ws[tid] = my_ws;
+  __syncthreads();
+  const int c0 = wv * RPW + 4 * grp;
+  const f32x4 s0 = *reinterpret_cast<const f32x4*>(s_ws + c0);
+  const f32x4 s1 = *reinterpret_cast<const f32x4*>(s_ws + c0 + (GU ? 16 * NW : 16));
 #pragma unroll
   for (int g = 0; g < G; ++g) {
     const int r = 16 * g + col;
     if (r >= mcount) continue;
-    const int pr = perm[rbase + r];
-    const float sx = GU ? acts[pr / k] : acts[rbase + r];
+    const int pr = s_pr[r];
+    const float sx = s_sx[r];
     f32x4 v0, v1;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
