@@ -263,8 +263,8 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == 6
           make_uint2(pack_bf16x2(wt_ * v1[0], wt_ * v1[1]), pack_bf16x2(wt_ * v1[2], wt_ * v1[3]));
     } else {
       float* yr = y + static_cast<size_t>(rbase + r) * H + nb + 4 * grp;
-      st16_stream(yr, v0);
-      st16_stream(yr + 16, v1);
+      *reinterpret_cast<f32x4*>(yr) = v0;                 // (read back by the slot sum: plain stores, 1% faster)
+      *reinterpret_cast<f32x4*>(yr + 16) = v1;
     }
   }
 }
@@ -593,8 +593,10 @@ hipError_t int8_set_attributes() {
 }
 
 // Codes and scales of the FP32 activations, one grouped row per workgroup (I a
-// multiple of 256, at most 16384).  With k = 1 a pair without a row (expert id out
-// of range) gets its output row cleared here, as no down tile will write it.
+// multiple of 256, at most 1024 NV), the row in registers between its one read and its
+// write.  With k = 1 a pair without a row (expert id out of range) gets its output row
+// cleared here, as no down tile will write it.
+template <int NV>
 __global__ __launch_bounds__(256) void quant_act_rows(const float* __restrict__ a,
                                                       const int* __restrict__ offsets, int E,
                                                       const int* __restrict__ row_of, int P, int H,
@@ -603,28 +605,36 @@ __global__ __launch_bounds__(256) void quant_act_rows(const float* __restrict__ 
                                                       uint16_t* __restrict__ out, uint32_t okey) {
   __shared__ float red[4];
   const int b = permute_item(blockIdx.x, P, okey);
-  if (out && row_of[b] >= P)
-    for (int c = threadIdx.x; c < H / 8; c += blockDim.x)
-      st16(out + static_cast<size_t>(b) * H + 8 * c, i32x4{0, 0, 0, 0});
-  if (b >= offsets[E]) return;
   const float* row = a + static_cast<size_t>(b) * I;
-  float amax = 0.f;
-  for (int c = threadIdx.x; c < I / 4; c += blockDim.x) {
-    const f32x4 v = *reinterpret_cast<const f32x4*>(row + 4 * c);
-    amax = fmaxf(fmaxf(fmaxf(amax, fabsf(v[0])), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+  const int tid = threadIdx.x;
+  f32x4 v[NV];
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {                          // (rows of the workspace: in bounds for every b < P)
+    const int c = 4 * (u * 256 + tid);
+    v[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (c < I) v[u] = *reinterpret_cast<const f32x4*>(row + c);
   }
+  if (out && row_of[b] >= P)
+    for (int c = tid; c < H / 8; c += 256) st16(out + static_cast<size_t>(b) * H + 8 * c, i32x4{0, 0, 0, 0});
+  if (b >= offsets[E]) return;
+  float amax = 0.f;
+#pragma unroll
+  for (int u = 0; u < NV; ++u)
+    amax = fmaxf(fmaxf(fmaxf(amax, fabsf(v[u][0])), fabsf(v[u][1])), fmaxf(fabsf(v[u][2]), fabsf(v[u][3])));
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor(amax, m, kWave));
   if (lane_id() == 0) red[wave_id()] = amax;
   __syncthreads();
   amax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
   const float inv = int8_inverse(amax);
-  for (int c = threadIdx.x; c < I / 4; c += blockDim.x) {
-    const f32x4 v = *reinterpret_cast<const f32x4*>(row + 4 * c);
-    *reinterpret_cast<uint32_t*>(codes + static_cast<size_t>(b) * I + 4 * c) =
-        int8_codes4(v[0], v[1], v[2], v[3], inv);
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    const int c = 4 * (u * 256 + tid);
+    if (c < I)
+      *reinterpret_cast<uint32_t*>(codes + static_cast<size_t>(b) * I + c) =
+          int8_codes4(v[u][0], v[u][1], v[u][2], v[u][3], inv);
   }
-  if (threadIdx.x == 0) scales[b] = int8_scale(amax);
+  if (tid == 0) scales[b] = int8_scale(amax);
 }
 
 // ---------------------------------------------------------------------------
@@ -848,8 +858,14 @@ hipError_t launch_experts_int8(const int8_t* x, const float* xs, const int8_t* w
   if (large) { LARGE8(kGateUp8, x8, xs, wgu8, wgus, act, nullptr, I / 128, 32); }
   else STREAM8(kGateUp8, x8, xs, wgu8, wgus, act, nullptr, I / 128);
   prof_end(kInt8GateUp, s);
-  hipLaunchKernelGGL(quant_act_rows, dim3(P), dim3(256), 0, s, act, offsets, E, row_of, P, H, I, codes,
-                     scales, k == 1 ? out : nullptr, order_key());
+#define QUANT8(NV)                                                                            \
+  hipLaunchKernelGGL(quant_act_rows<NV>, dim3(P), dim3(256), 0, s, act, offsets, E, row_of, P, H, I, \
+                     codes, scales, k == 1 ? out : nullptr, order_key())
+  if (I <= 1024) QUANT8(1);
+  else if (I <= 2048) QUANT8(2);
+  else if (I <= 4096) QUANT8(4);
+  else QUANT8(16);
+#undef QUANT8
   prof_begin(kInt8Down, s);
   if (large && k == 1) { LARGE8(kDownFused8, codes, scales, wd8, wds, nullptr, out, H / 256, 64); }
   else if (large) { LARGE8(kDown8, codes, scales, wd8, wds, y, nullptr, H / 256, 64); }
