@@ -14,7 +14,7 @@
 // FP32 first: where neighbours in the resulting order lie further apart than FP32 can
 // be wrong, the order is certain; only a token with a closer pair (or an exact tie)
 // is done again in FP64, by its wave alone.  16384 x 384, sigmoid, bias, 8 groups:
-// FP64 throughout 51 us, this form ROUTE_US us.
+// FP64 throughout 51 us, this form 25 us (5 us of traffic; bound by its instructions).
 #include "common.h"
 #include "internal.h"
 #include "route.h"
@@ -65,14 +65,17 @@ __device__ __forceinline__ float wave_sum_f32(float v) {
   return (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
 }
 
-// Wave-wide maximum of an integer, uniform.
+// Wave-wide maximum of an integer, uniform: rows of 16 lanes, then rows 0 into 1 and 2
+// into 3, then 1 into 3 (row_bcast:15 and :31); lane 63 has seen all.
 __device__ __forceinline__ int wave_max_i32(int v) {
+  constexpr int kLeast = -0x7FFFFFFF - 1;
   v = max(v, dpp<0xB1>(v));
   v = max(v, dpp<0x4E>(v));
   v = max(v, dpp<0x141>(v));
   v = max(v, dpp<0x140>(v));
-  return max(max(__builtin_amdgcn_readlane(v, 0), __builtin_amdgcn_readlane(v, 16)),
-             max(__builtin_amdgcn_readlane(v, 32), __builtin_amdgcn_readlane(v, 48)));
+  v = max(v, __builtin_amdgcn_update_dpp(kLeast, v, 0x142, 0xA, 0xF, false));
+  v = max(v, __builtin_amdgcn_update_dpp(kLeast, v, 0x143, 0xC, 0xF, false));
+  return __builtin_amdgcn_readlane(v, 63);
 }
 
 // exp(x), x <= 0, within about 1.5 units in the last place: 2^(x log2 e) with the
@@ -245,20 +248,19 @@ __device__ __forceinline__ bool select_fast(const RouteArgs& a, const Place& pl,
             c[i + j] = hi;
             c[i + j + q] = lo;
           }
-  int mine = kNone;                                      // lane r: the r-th largest key
-  sel = 0;
+  int mine = kNone, from = 0;                            // lane r: the r-th largest key and its lane
   for (int r = 0; r <= a.k; ++r) {
     const int best = wave_max_i32(c[0]);
     const int win = __builtin_ctzll(__ballot(c[0] == best));   // (equal heads: not settled below)
-    const int e = __builtin_amdgcn_readlane(pl.first, win) + pl.step * (best & kLow);
-    sel = lane == r ? e : sel;
     mine = lane == r ? best : mine;
-    if (lane == win) {
+    from = lane == r ? win : from;
+    if (lane == win) {                                   // (as selects of c[j + 1] or c[j] it would be indexed)
 #pragma unroll
       for (int j = 0; j + 1 < R; ++j) c[j] = c[j + 1];
       c[R - 1] = kNone;
     }
   }
+  sel = __shfl(pl.first, from, kWave) + pl.step * (mine & kLow);
   const int next = __shfl_down(mine, 1, kWave);
   const float fm = float_of(mine), fn = float_of(next);
   const float err = tol + (fabsf(fm) + fabsf(fn)) * (static_cast<float>(1 << kBits) * 1.1920929e-7f + 2.4e-7f);
@@ -271,7 +273,7 @@ __device__ __forceinline__ bool select_fast(const RouteArgs& a, const Place& pl,
 // One wave per token, tokens gridDim.x * 4 apart.  kChoice: a bias or groups are given;
 // otherwise the order is the logits'.
 template <int R, bool kChoice>
-__global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs a, int32_t* __restrict__ idx,
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(R <= 8 ? 5 : R <= 16 ? 3 : 1))) void route_scored_kernel(RouteArgs a, int32_t* __restrict__ idx,
                                                            float* __restrict__ w, uint32_t okey) {
   const int lane = lane_id(), E = a.E, k = a.k;
   const Place pl = place(a);
@@ -285,7 +287,8 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs a, int32_t*
   // on average); a bound for the two that a comparison takes, and twice that
   const float tol = a.sigmoid ? 1e-6f : 1e-5f;
   const int step = gridDim.x * (blockDim.x / kWave);
-  for (int t0 = blockIdx.x * (blockDim.x / kWave) + wave_id(); t0 < a.T; t0 += step) {
+  // (wave-uniform, said so: the row's address then lives in scalar registers)
+  for (int t0 = blockIdx.x * (blockDim.x / kWave) + __builtin_amdgcn_readfirstlane(wave_id()); t0 < a.T; t0 += step) {
     const int t = permute_item(t0, a.T, okey);
     const float* lrow = a.logits + static_cast<size_t>(t) * E;
     float v[R];
@@ -299,6 +302,12 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs a, int32_t*
       top = fmaxf(top, v[i]);
     }
     if (!a.sigmoid && (kChoice || !a.renorm)) top = wave_max_f32(top);
+    float zsum = 0.f;                                    // softmax's sum, where the weights need it
+    if (!a.sigmoid && !a.renorm) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) zsum += on[i] ? exp_close(v[i] - top) : 0.f;
+      zsum = wave_sum_f32(zsum);
+    }
     int sel;
     bool close = false, in = true;
     int ck[R];
@@ -330,16 +339,31 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs a, int32_t*
 #pragma unroll
     for (int i = 0; i < R; ++i) ck[i] = i >= pl.count || !in ? kNone : on[i] ? ck[i] : kMaskedKey;
     if (close || !select_fast<R>(a, pl, ck, kChoice && a.bias ? tol : 0.f, sel)) {
-      // exactly: on the logits, or on scores and sums in FP64
+      // exactly: on the logits, or on scores and sums in FP64.  The logits and the bias
+      // are read again (from the caches): held across this rare path they would cost the
+      // common one its registers.
+      int again = 0;
+      asm volatile("" : "+v"(again));
+      const float* lr = lrow + again;
+      const float* br = a.bias + again;
+      float u[R];
+      bool part[R];
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const float x = i < pl.count ? lr[pl.first + pl.step * i] : -INFINITY;
+        part[i] = takes_part(x);
+        u[i] = part[i] ? finite_logit(x) : -INFINITY;
+      }
       double d[R];
       if (kChoice) {
         double zd = 0.0;
 #pragma unroll
         for (int i = 0; i < R; ++i) {
           d[i] = 0.0;
-          if (on[i]) d[i] = a.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(v[i])))
-                                      : exp(static_cast<double>(v[i]) - static_cast<double>(top));
+          if (part[i]) d[i] = a.sigmoid ? 1.0 / (1.0 + exp(-static_cast<double>(u[i])))
+                                        : exp(static_cast<double>(u[i]) - static_cast<double>(top));
           zd += d[i];
+          __builtin_amdgcn_sched_barrier(0);             // (one exponential's registers at a time)
         }
         if (!a.sigmoid) {
           zd = wave_sum64(zd);
@@ -348,22 +372,23 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs a, int32_t*
         }
         if (a.bias) {
 #pragma unroll
-          for (int i = 0; i < R; ++i) d[i] += static_cast<double>(bias[i]);
+          for (int i = 0; i < R; ++i)
+            if (i < pl.count) d[i] += static_cast<double>(br[pl.first + pl.step * i]);
         }
         bool none = false;
         in = true;
-        if (a.groups > 1) in = group_taken<R>(a, pl, d, on, 0.f, none);
+        if (a.groups > 1) in = group_taken<R>(a, pl, d, part, 0.f, none);
       }
       if (kChoice && a.bias) {
         uint64_t key[R];
 #pragma unroll
         for (int i = 0; i < R; ++i)
-          key[i] = i >= pl.count || !in ? 0ull : !on[i] ? 1ull : ordered_key64(d[i]);
+          key[i] = i >= pl.count || !in ? 0ull : !part[i] ? 1ull : ordered_key64(d[i]);
         sel = select_exact<R>(a, pl, key);
       } else {
         uint32_t key[R];
 #pragma unroll
-        for (int i = 0; i < R; ++i) key[i] = i >= pl.count || !in ? 0u : !on[i] ? 1u : ordered_key(v[i]);
+        for (int i = 0; i < R; ++i) key[i] = i >= pl.count || !in ? 0u : !part[i] ? 1u : ordered_key(u[i]);
         sel = select_exact<R>(a, pl, key);
       }
     }
@@ -379,17 +404,13 @@ __global__ __launch_bounds__(256) void route_scored_kernel(RouteArgs a, int32_t*
       if (a.sigmoid) p = exp_close(fminf(l, 0.f) - fminf(m, 0.f)) * __builtin_amdgcn_rcpf(1.0f + exp_close(-fabsf(l)));
       else p = exp_close(l - m);
       p = use ? p : 0.f;
-      const float den = wave_sum_f32(p);
-      p = den > 0.f ? p / den : 0.f;
+      const float den = wave_sum_f32(p);                 // (at least 0.5 where any expert takes part)
+      p = den > 0.f ? p * __builtin_amdgcn_rcpf(den) : 0.f;
     } else if (a.sigmoid) {
       const float en = exp_close(-fabsf(l));
-      p = use ? (l < 0.f ? en : 1.0f) / (1.0f + en) : 0.f;
+      p = use ? (l < 0.f ? en : 1.0f) * __builtin_amdgcn_rcpf(1.0f + en) : 0.f;
     } else {
-      float z = 0.f;
-#pragma unroll
-      for (int i = 0; i < R; ++i) z += on[i] ? exp_close(v[i] - top) : 0.f;
-      z = wave_sum_f32(z);
-      p = use ? exp_close(l - top) / z : 0.f;
+      p = use ? exp_close(l - top) / zsum : 0.f;
     }
     if (lane < k) {
       idx[static_cast<size_t>(t) * k + lane] = sel;
@@ -408,7 +429,7 @@ template <int R>
 __global__ __launch_bounds__(256) void route_scored_backward_kernel(
     RouteArgs a, const int32_t* __restrict__ idx, const float* __restrict__ dw,
     float* __restrict__ dlogits, uint32_t okey) {
-  const int t0 = blockIdx.x * (blockDim.x / kWave) + wave_id();
+  const int t0 = blockIdx.x * (blockDim.x / kWave) + __builtin_amdgcn_readfirstlane(wave_id());
   if (t0 >= a.T) return;
   const int t = permute_item(t0, a.T, okey);
   const int lane = lane_id(), E = a.E, k = a.k;
@@ -494,7 +515,7 @@ RouteArgs route_args(const float* logits, const float* bias, int T, const Scored
 hipError_t launch_route_scored(const float* logits, const float* bias, int T, const ScoredRoute& p,
                                int32_t* idx, float* w, hipStream_t s, int num_cus) {
   const RouteArgs a = route_args(logits, bias, T, p);
-  // 8192 waves at most (a bias is read once by each)
+  // 8192 waves at most: what a wave sets up once, and its bias, serve several tokens
   const int blocks = (T + kPerBlock - 1) / kPerBlock;
   const dim3 grid(blocks < 8 * num_cus ? blocks : 8 * num_cus), block(kPerBlock * kWave);
   const bool choice = bias != nullptr || p.groups > 1;
