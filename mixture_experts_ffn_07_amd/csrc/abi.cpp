@@ -10,6 +10,7 @@
 #include <string>
 
 #include "../../include/moe_mi355x.h"
+#include "block.h"
 #include "internal.h"
 
 namespace moe {
@@ -33,7 +34,8 @@ static_assert(MOE_STATIC_SCRATCH_BYTES == moe::kStaticScratchBytes,
               "the header's scratch size must match the array's");
 static_assert(MOE_DEBUG_PERMUTE_ORDER == moe::kDebugPermute &&
               MOE_DEBUG_DECODE_FUSED == moe::kDebugDecodeFused, "debug option bits");
-static_assert(MOE_KERNEL_COUNT == moe::kKernelCount, "kernel ids");
+static_assert(MOE_KERNEL_COUNT == moe::kAllKernelCount &&
+              MOE_KERNEL_NORM == moe::kNorm && MOE_KERNEL_INT8_DOWN == moe::kInt8Down, "kernel ids");
 
 namespace {
 
@@ -141,7 +143,7 @@ const char* moe_status_string(int status) {
 const char* moe_last_error(void) { return g_last_error.c_str(); }
 
 int moe_profile_kernel(int kernel, void* start_event, void* stop_event) {
-  if (kernel < 0 || kernel >= moe::kKernelCount)
+  if (kernel < 0 || kernel >= moe::kAllKernelCount)
     return fail(MOE_ERR_SHAPE, "unknown kernel id %d", kernel);
   moe::ProfileHook& h = moe::profile_hook();
   h.kernel = (start_event && stop_event) ? kernel : 0;

@@ -22,6 +22,7 @@
 // the gathered activation rows come from L2.  Work items are ordered so that
 // the items sharing one expert's activation rows run on the same XCD (same
 // L2): workgroups are dispatched to the 8 XCDs round-robin by linear id.
+#include "block.h"
 #include "common.h"
 #include "internal.h"
 #include "tiles.h"

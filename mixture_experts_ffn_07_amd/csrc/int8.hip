@@ -16,9 +16,10 @@
 // row: it adds nothing to its token.
 #include <type_traits>
 
+#include "block.h"
 #include "common.h"
 #include "gemm_large.h"
-#include "internal.h"
+#include "int8.h"
 #include "tiles.h"
 
 namespace moe {

@@ -62,9 +62,8 @@ inline int column_parts(size_t rows, int cols, int cw, int max_tiles, int min_it
 enum KernelId { kRoute = 1, kDecGateUp = 2, kDecDown = 3, kGroup = 4, kQuant = 5,
                 kGemmGateUp = 6, kGemmDown = 7, kCombine = 8, kBwdGateUp = 9, kBwdDown = 10,
                 kBwdInput = 11, kBwdWDown = 12, kBwdWGateUp = 13, kDecFused = 14,
-                kBwdRequant = 15, kNorm = 16, kNormBackward = 17, kRouteBackward = 18,
-                kInt8GateUp = 19, kInt8Down = 20,
-                kKernelCount = 21 };
+                kBwdRequant = 15,
+                kKernelCount = 16 };
 
 // Library-owned device scratch (scratch.hip): kStaticScratchBytes per GPU for
 // the entry points that allocate nothing.  static_scratch(dev) gives its device
@@ -84,45 +83,6 @@ DecodeWs decode_ws_layout(int T, int H, int I, int E, int k);
 
 hipError_t launch_route_topk(const float* logits, int T, int E, int k, int32_t* idx, float* w,
                              hipStream_t s);
-
-// Routing by scores (route_scored.hip).
-struct ScoredRoute {
-  int E, k, groups, topk_groups, group_top;
-  bool sigmoid, renorm;
-  float scale;
-};
-hipError_t launch_route_scored(const float* logits, const float* bias, int T, const ScoredRoute& p,
-                               int32_t* idx, float* w, hipStream_t s, int num_cus);
-hipError_t launch_route_scored_backward(const float* logits, const int32_t* idx, const float* dw,
-                                        int T, const ScoredRoute& p, float* dlogits, hipStream_t s);
-
-// Residual sum + RMS norm (norm.hip).  qtype: MOE_BF16 (no 8-bit output), MOE_MXFP8, MOE_INT8.
-constexpr int kNormMaxH = 16384;           // a row is held in one workgroup's registers
-int norm_backward_rows(int T, int H);      // workgroups (rows of partial weight gradients)
-hipError_t launch_add_rmsnorm(const uint16_t* x, const uint16_t* r, const uint16_t* w, int T, int H,
-                              float eps, uint16_t* sum, uint16_t* y, int qtype, uint8_t* codes,
-                              void* scales, hipStream_t s, int num_cus);
-hipError_t launch_add_rmsnorm_backward(const uint16_t* sum, const uint16_t* w, const uint16_t* dy,
-                                       const uint16_t* ds, int T, int H, float eps, uint16_t* dx,
-                                       uint16_t* dweight, float* partial, hipStream_t s);
-hipError_t launch_quant_int8(const uint16_t* src, int64_t rows, int K, uint8_t* codes, float* scales,
-                             hipStream_t s, int num_cus);
-
-// INT8 experts (int8.hip): byte layout of the workspace, and the whole layer.
-struct Int8Ws {
-  size_t n_tiles, counts, offsets, tiles, perm, row_of, act, codes, scales, y, partial, total;
-  int max_tiles, bm;
-};
-Int8Ws int8_ws_layout(int T, int H, int I, int E, int k);
-hipError_t launch_experts_int8(const int8_t* x, const float* xs, const int8_t* wgu,
-                               const float* wgus, const int8_t* wd, const float* wds,
-                               const int32_t* idx, const float* w, int T, int H, int I, int E,
-                               int k, uint16_t* out, void* ws, hipStream_t s, int num_cus);
-
-// combine_slots over the columns [col0, col0 + cols) (batched.hip).
-hipError_t launch_combine_slots(const float* y, const int* row_of, const float* w, int T, int H,
-                                int k, uint16_t* out, int col0, int cols, int ldy, hipStream_t s,
-                                int num_cus);
 
 hipError_t launch_decode(const uint16_t* x, const float* logits, const uint16_t* wgu,
                          const uint16_t* wd, int T, int H, int I, int E, int k, uint16_t* out,

@@ -8,8 +8,9 @@
 // is that of the rounded s, so the backward pass, which reads s back, is the
 // gradient of exactly what the forward computed.  y is not rounded on its way
 // to the 8-bit codes.
+#include "block.h"
 #include "common.h"
-#include "internal.h"
+#include "int8.h"
 #include "tiles.h"
 
 namespace moe {

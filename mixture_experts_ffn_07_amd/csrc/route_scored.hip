@@ -15,8 +15,8 @@
 // be wrong, the order is certain; only a token with a closer pair (or an exact tie)
 // is done again in FP64, by its wave alone.  16384 x 384, sigmoid, bias, 8 groups:
 // FP64 throughout 51 us, this form 25 us (5 us of traffic; bound by its instructions).
+#include "block.h"
 #include "common.h"
-#include "internal.h"
 #include "route.h"
 #include "tiles.h"
 
