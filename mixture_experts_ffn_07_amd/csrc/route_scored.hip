@@ -263,7 +263,8 @@ __device__ __forceinline__ bool select_fast(const RouteArgs& a, const Place& pl,
   sel = __shfl(pl.first, from, kWave) + pl.step * (mine & kLow);
   const int next = __shfl_down(mine, 1, kWave);
   const float fm = float_of(mine), fn = float_of(next);
-  const float err = tol + (fabsf(fm) + fabsf(fn)) * (static_cast<float>(1 << kBits) * 1.1920929e-7f + 2.4e-7f);
+  // (1e-30: keys of 0 and next to it, where the low bits alone set the order)
+  const float err = tol + 1e-30f + (fabsf(fm) + fabsf(fn)) * (static_cast<float>(1 << kBits) * 1.1920929e-7f + 2.4e-7f);
   const bool bad = lane < a.k && (mine < kOffKey || (next >= kOffKey && !(fm - fn >= err)));
   return __ballot(bad) == 0;
 }

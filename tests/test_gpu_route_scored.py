@@ -72,6 +72,31 @@ def test_route_scored_ties_take_the_lowest_index(M, score, G, tg, gt):
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("E,k,G,tg", [(256, 8, 1, 1), (384, 8, 8, 4), (130, 5, 1, 1), (1024, 32, 1, 1)])
+def test_route_scored_equal_logits_across_a_lane(M, score, bias, E, k, G, tg):
+    """Ties among experts that one lane holds (several per lane), of value 0, near 0 and not 0."""
+    l = torch.zeros(7, E)
+    l[1] = 0.75
+    l[2] = -2.5
+    l[3, ::3] = 1e-40                                  # below FP32's normal range, above 0
+    l[4, 1::2] = -0.0
+    l[5, 5:] = -1e-39
+    l[6, ::2] = 2.0 ** -126
+    _run(M, l, k, torch.zeros(E) if bias else None, score, G, tg, 2, what="equal logits")
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("T,E,k,G,tg,gt", [(9, 1023, 16, 33, 7, 2), (6, 1020, 9, 17, 3, 2), (5, 1017, 9, 9, 2, 1),
+                                           (8, 64, 2, 64, 5, 2), (4, 1024, 32, 2, 1, 2)])
+def test_route_scored_odd_groups(M, score, bias, T, E, k, G, tg, gt):
+    g = torch.Generator().manual_seed(E + G)
+    l = torch.randn(T, E, generator=g) * 2
+    _run(M, l, k, 0.2 * torch.randn(E, generator=g) if bias else None, score, G, tg, gt, True, 1.0)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias", [False, True])
 @pytest.mark.parametrize("renorm", [False, True])
 @pytest.mark.parametrize("G,tg,gt", [(1, 1, 1), (8, 3, 2), (8, 3, 1)])
 def test_route_scored_masks(M, score, bias, renorm, G, tg, gt):
