@@ -38,7 +38,7 @@ hipError_t launch_quant_int8(const uint16_t* src, int64_t rows, int K, uint8_t* 
 // INT8 experts (int8.hip): byte layout of the workspace, and the whole layer.
 struct Int8Ws {
   size_t n_tiles, counts, offsets, tiles, perm, row_of, act, codes, scales, y, partial, total;
-  int max_tiles, bm;
+  int max_tiles, bm, slices_gu, slices_down;   // slices of the two reductions
 };
 Int8Ws int8_ws_layout(int T, int H, int I, int E, int k);
 hipError_t launch_experts_int8(const int8_t* x, const float* xs, const int8_t* wgu,

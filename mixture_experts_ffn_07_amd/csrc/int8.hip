@@ -44,6 +44,22 @@ __device__ __forceinline__ float swiglu8(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
 
+// Slices of a streaming product's reduction: where its tiles (nblk column blocks each)
+// leave half the CUs or more without a workgroup, as many as those have room for, of at
+// least three 256-code stages.  The slices' INT32 sums are exact and are added by the
+// kernel that reads them next.  Measured, us (split / whole): T 100 H 7168 I 2048 E 4 k 2
+// 64 / 87; T 40 H 4096 I 1024 E 6 k 4 37 / 47; T 14 H 2560 I 1792 E 5 k 5 41 / 45.  Room
+// for half as many again: T 128 H 3584 I 1024 E 8 k 8 57 against 59, but T 809 H 3840 I 512
+// E 4 k 2 68 against 55.  Slices of one stage: T 2000 H 1024 I 512 E 4 k 1 55 against 36
+// whole; of two: T 40 H 4096 40 against 37 of three.
+constexpr int kSplitGroups = 256, kSplitStages = 3;
+inline int slices(size_t P, int E, int bm, int nblk, int nstage) {
+  const size_t tiles = (P < static_cast<size_t>(E) ? P : E) + P / bm;   // (about; each expert ends one early)
+  const size_t room = tiles ? kSplitGroups / (tiles * nblk) : 1, most = nstage / kSplitStages;
+  const size_t s = room < most ? room : most;
+  return s < 2 ? 1 : static_cast<int>(s);
+}
+
 }  // namespace
 
 Int8Ws int8_ws_layout(int T, int H, int I, int E, int k) {
@@ -60,6 +76,9 @@ Int8Ws int8_ws_layout(int T, int H, int I, int E, int k) {
   const bool mfma_bound = P >= 320 * static_cast<size_t>(E) && static_cast<size_t>(H) * I >= (size_t(1) << 22);
   L.bm = mfma_bound ? kLargeBM : P >= 40 * static_cast<size_t>(E) ? kTall8 : kBM8;
   L.max_tiles = static_cast<int>(E + (P + L.bm - 1) / L.bm);
+  const bool split = L.bm != kLargeBM;
+  L.slices_gu = split ? slices(P, E, L.bm, I / 128, H / 256) : 1;
+  L.slices_down = split ? slices(P, E, L.bm, H / 256, I / 256) : 1;
   size_t o = 0;
   L.n_tiles = o;   o += 256;
   L.counts = o;    o = align256(o + sizeof(int) * E);
@@ -74,6 +93,9 @@ Int8Ws int8_ws_layout(int T, int H, int I, int E, int k) {
   if (k > 1) o = align256(o + sizeof(float) * P * H);
   L.partial = o;
   if (L.bm == kLargeBM) o = align256(o + sizeof(int) * kLargeMaxSlices * kLargeBM * 256);
+  const size_t gu = L.slices_gu > 1 ? sizeof(int) * L.slices_gu * P * 2 * I : 0;
+  const size_t down = L.slices_down > 1 ? sizeof(int) * L.slices_down * P * H : 0;
+  o = align256(o + (gu > down ? gu : down));
   L.total = o;
   return L;
 }
@@ -88,14 +110,16 @@ Int8Ws int8_ws_layout(int T, int H, int I, int E, int k) {
 // activations alike.  The activation codes are staged in LDS in stages of two chunks,
 // double-buffered and shared by the waves; the weights of the next two chunks are in
 // flight while one multiplies.  Rows past the tile's end load the tile's first row; their
-// columns are computed and discarded.
-template <int KIND, int NW, int BM>
+// columns are computed and discarded.  PART: the workgroup takes one of S slices of the
+// reduction and stores its INT32 sums in part[S][P][weight rows of an expert].
+template <int KIND, int NW, int BM, bool PART>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == 64 ? 4 : 2, 8))) void gemm_i8s(
     const uint8_t* __restrict__ act, const float* __restrict__ acts,
     const uint8_t* __restrict__ wt, const float* __restrict__ wts,
     const int* __restrict__ perm, const int2* __restrict__ tiles, const int* __restrict__ n_tiles,
     const int* __restrict__ counts, const int* __restrict__ offsets, const float* __restrict__ w,
-    int H, int I, int k, float* __restrict__ y, uint16_t* __restrict__ out, uint32_t okey) {
+    int H, int I, int k, float* __restrict__ y, uint16_t* __restrict__ out, int P,
+    int S, int* __restrict__ part, uint32_t okey) {
   constexpr int NT = NW * 64;
   constexpr bool GU = KIND == kGateUp8;
   constexpr int RPW = GU ? 16 : 32;                       // outputs per wave
@@ -108,11 +132,15 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == 6
   __shared__ __align__(16) i32x4 wtl[NW][16 * 8];         // per wave: [16 rows][8 chunks]
   const int K = GU ? H : I;                               // reduction length
   const int N = GU ? I : H;                               // outputs
-  const int nblk = N / (NW * RPW);
-  const int item0 = real_item(blockIdx.x, nblk, *n_tiles);
+  const int nblk = N / (NW * RPW), nitem = PART ? nblk * S : nblk;
+  const int item0 = real_item(blockIdx.x, nitem, *n_tiles);
   if (item0 < 0) return;
-  const int item = permute_item(item0, nblk * *n_tiles, okey);
-  const int tile = item / nblk, nb_i = item - tile * nblk;
+  const int item = permute_item(item0, nitem * *n_tiles, okey);
+  const int tile = item / nitem, in_tile = item - tile * nitem;
+  const int slice = PART ? in_tile / nblk : 0, nb_i = in_tile - slice * nblk;
+  // the stages [st0, st0 + nstage) of the reduction
+  const int st0 = PART ? slice * (K / SB) / S : 0;
+  const int nstage = PART ? (slice + 1) * (K / SB) / S - st0 : K / SB, nchunk = 2 * nstage;
   const int2 te = tiles[tile];
   const int e = te.x, m0 = te.y;
   const int mcount = min(BM, counts[e] - m0);
@@ -130,7 +158,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == 6
   uint32_t ow[4];                                         // group 0 rows 0-7, 8-15, group 1 rows 0-7, 8-15
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    ow[i] = static_cast<uint32_t>(((i < 2 ? row0 : row1) + 8 * (i & 1) + lr) * K + lc * 16);
+    ow[i] = static_cast<uint32_t>(((i < 2 ? row0 : row1) + 8 * (i & 1) + lr) * K + lc * 16 + st0 * SB);
   i32x4* tw = wtl[wv];
   i32x4* wdst = tw + lr * 8 + (lc ^ lr);                  // + 64 for rows 8-15
   const i32x4* asrc = tw + col * 8;
@@ -143,9 +171,8 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == 6
     const int c = tid + i * NT, r = c / CH, rr = r < mcount ? r : 0;
     lrow[i] = r * RS + (c % CH) * 16;
     const int arow = GU ? perm[rbase + rr] / k : rbase + rr;
-    oxl[i] = static_cast<uint32_t>(arow * K + (c % CH) * 16);
+    oxl[i] = static_cast<uint32_t>(arow * K + (c % CH) * 16 + st0 * SB);
   }
-  const int nchunk = K / 128, nstage = nchunk / 2;
   i32x4 xr[LPT], wA[4], wB[4];
 #pragma unroll
   for (int i = 0; i < LPT; ++i) xr[i] = ld16(act + oxl[i]);
@@ -156,10 +183,10 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == 6
   // the epilogue's data (tile row tid's pair and scale, output tid's weight scale): its
   // latency passes during the products, and it goes through LDS after them
   const float* ws_e = wts + static_cast<size_t>(e) * wrows;
-  const int my_pr = perm[rbase + (tid < mcount ? tid : 0)];
-  const float my_sx = GU ? acts[my_pr / k] : acts[rbase + (tid < mcount ? tid : 0)];
+  const int my_pr = PART ? 0 : perm[rbase + (tid < mcount ? tid : 0)];
+  const float my_sx = PART ? 0.f : GU ? acts[my_pr / k] : acts[rbase + (tid < mcount ? tid : 0)];
   const int my_n = nb_i * NW * RPW;
-  const float my_ws = tid < 32 * NW ? ws_e[GU && tid >= 16 * NW ? I + my_n + tid - 16 * NW : my_n + tid] : 0.f;
+  const float my_ws = !PART && tid < 32 * NW ? ws_e[GU && tid >= 16 * NW ? I + my_n + tid - 16 * NW : my_n + tid] : 0.f;
 #pragma unroll
   for (int i = 0; i < LPT; ++i) *reinterpret_cast<i32x4*>(&xl[0][lrow[i]]) = xr[i];
 
@@ -226,6 +253,17 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == 6
     publish(st + 1);
   }
   // lane: outputs row0 + 4grp + i (group 0) and row1 + 4grp + i (group 1) of tile row 16g + col
+  if (PART) {
+    int* pt = part + (static_cast<size_t>(slice) * P + rbase + col) * wrows + 4 * grp;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      if (16 * g + col >= mcount) continue;
+      int* pr = pt + static_cast<size_t>(16 * g) * wrows;
+      *reinterpret_cast<i32x4*>(pr + row0) = acc0[g];
+      *reinterpret_cast<i32x4*>(pr + row1) = acc1[g];
+    }
+    return;
+  }
   int* s_pr = reinterpret_cast<int*>(xl[0]);              // (every wave is done with the stages)
   float* s_sx = reinterpret_cast<float*>(xl[0]) + BM;
   float* s_ws = reinterpret_cast<float*>(xl[0]) + 2 * BM;
@@ -593,12 +631,22 @@ hipError_t int8_set_attributes() {
   return e;
 }
 
+// What joins the slices of a product: part[S][P][N] INT32 and the scales of both operands.
+struct Int8Parts {
+  const int* part;
+  int S, k;
+  const int* perm;
+  const int32_t* idx;
+  const float *acts, *wts;
+};
+
 // Codes and scales of the FP32 activations, one grouped row per workgroup (I a
 // multiple of 256, at most 1024 NV), the row in registers between its one read and its
-// write.  With k = 1 a pair without a row (expert id out of range) gets its output row
+// write (PART: made here from the slices of a split gate/up product).  With k = 1 a pair without a row (expert id out of range) gets its output row
 // cleared here, as no down tile will write it.
-template <int NV>
+template <int NV, bool PART>
 __global__ __launch_bounds__(256) void quant_act_rows(const float* __restrict__ a,
+                                                      const Int8Parts sum,
                                                       const int* __restrict__ offsets, int E,
                                                       const int* __restrict__ row_of, int P, int H,
                                                       int I, uint8_t* __restrict__ codes,
@@ -613,11 +661,32 @@ __global__ __launch_bounds__(256) void quant_act_rows(const float* __restrict__ 
   for (int u = 0; u < NV; ++u) {                          // (rows of the workspace: in bounds for every b < P)
     const int c = 4 * (u * 256 + tid);
     v[u] = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (c < I) v[u] = *reinterpret_cast<const f32x4*>(row + c);
+    if (!PART && c < I) v[u] = *reinterpret_cast<const f32x4*>(row + c);
   }
   if (out && row_of[b] >= P)
     for (int c = tid; c < H / 8; c += 256) st16(out + static_cast<size_t>(b) * H + 8 * c, i32x4{0, 0, 0, 0});
   if (b >= offsets[E]) return;
+  if (PART) {
+    const int pr = sum.perm[b];
+    const float sx = sum.acts[pr / sum.k];
+    const float* ws = sum.wts + static_cast<size_t>(sum.idx[pr]) * 2 * I;
+#pragma unroll
+    for (int u = 0; u < NV; ++u) {
+      const int c = 4 * (u * 256 + tid);
+      if (c >= I) continue;
+      const f32x4 sg = *reinterpret_cast<const f32x4*>(ws + c), su = *reinterpret_cast<const f32x4*>(ws + I + c);
+      i32x4 g = {0, 0, 0, 0}, up = {0, 0, 0, 0};
+      const int* p = sum.part + static_cast<size_t>(b) * 2 * I + c;
+#pragma unroll 4
+      for (int sl = 0; sl < sum.S; ++sl, p += static_cast<size_t>(P) * 2 * I) {
+        g += *reinterpret_cast<const i32x4*>(p);
+        up += *reinterpret_cast<const i32x4*>(p + I);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[u][i] = swiglu8(static_cast<float>(g[i]) * sx * sg[i], static_cast<float>(up[i]) * sx * su[i]);
+    }
+  }
   float amax = 0.f;
 #pragma unroll
   for (int u = 0; u < NV; ++u)
@@ -636,6 +705,54 @@ __global__ __launch_bounds__(256) void quant_act_rows(const float* __restrict__ 
           int8_codes4(v[u][0], v[u][1], v[u][2], v[u][3], inv);
   }
   if (tid == 0) scales[b] = int8_scale(amax);
+}
+
+// Slot sum over the slices of a split down product: the same values and the same order as
+// one product and combine_slots (with k = 1 the weighted value itself, its sign included).
+__global__ __launch_bounds__(256) void combine_parts(const Int8Parts sum, const int* __restrict__ row_of,
+                                                     const float* __restrict__ w, int T, int H,
+                                                     uint16_t* __restrict__ out, uint32_t okey) {
+  const int t = permute_item(blockIdx.x, gridDim.x, okey);
+  const int k = sum.k, P = T * k;
+  const int c = blockIdx.y * 1024 + 4 * threadIdx.x;
+  if (c >= H) return;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  for (int j0 = 0; j0 < k; j0 += 8) {                     // eight slots' loads in flight, then their sum in order
+    i32x4 v[8];
+    float wj[8], sh[8];
+    f32x4 sd[8];
+    const int* p[8];
+    bool in[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int row = j0 + j < k ? row_of[t * k + j0 + j] : P;
+      in[j] = static_cast<unsigned>(row) < static_cast<unsigned>(P);
+      v[j] = i32x4{0, 0, 0, 0};
+      if (in[j]) {
+        wj[j] = w[t * k + j0 + j];
+        sh[j] = sum.acts[row];
+        sd[j] = *reinterpret_cast<const f32x4*>(sum.wts + static_cast<size_t>(sum.idx[t * k + j0 + j]) * H + c);
+        p[j] = sum.part + static_cast<size_t>(row) * H + c;
+      }
+    }
+    for (int sl = 0; sl < sum.S; ++sl)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (in[j]) v[j] += *reinterpret_cast<const i32x4*>(p[j] + static_cast<size_t>(sl) * P * H);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (in[j]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float y = static_cast<float>(v[j][i]) * sh[j] * sd[j][i];
+          acc[i] = k == 1 ? wj[j] * y : fmaf(wj[j], y, acc[i]);
+        }
+      }
+  }
+  uint2 o;
+  o.x = pack_bf16x2(acc[0], acc[1]);
+  o.y = pack_bf16x2(acc[2], acc[3]);
+  *reinterpret_cast<uint2*>(out + static_cast<size_t>(t) * H + c) = o;
 }
 
 // ---------------------------------------------------------------------------
@@ -845,23 +962,33 @@ hipError_t launch_experts_int8(const int8_t* x, const float* xs, const int8_t* w
                      ARGS, Y, O, partial, num_cus, order_key());                              \
   hipLaunchKernelGGL(gemm_large_i8_fixup<KD>, dim3(num_cus / 2 * PER), dim3(256), 0, s, AS, WS, \
                      ARGS, Y, O, partial, num_cus, order_key())
-#define STREAM8(KD, A, AS, W, WS, Y, O, NBLK)                                                 \
+#define STREAM8(KD, PART, A, AS, W, WS, Y, O, NBLK, S)                                        \
   do {                                                                                        \
-    const dim3 grid_(round_up((NBLK) * L.max_tiles, kXcds));                                  \
+    const dim3 grid_(round_up((NBLK) * (S) * L.max_tiles, kXcds));                            \
     if (L.bm == kTall8)                                                                       \
-      hipLaunchKernelGGL((gemm_i8s<KD, 8, kTall8>), grid_, dim3(512), 0, s, A, AS, W, WS,  \
-                         ARGS, Y, O, order_key());                                            \
+      hipLaunchKernelGGL((gemm_i8s<KD, 8, kTall8, PART>), grid_, dim3(512), 0, s, A, AS, W, WS, \
+                         ARGS, Y, O, P, S, partial, order_key());                             \
     else                                                                                      \
-      hipLaunchKernelGGL((gemm_i8s<KD, 8, kBM8>), grid_, dim3(512), 0, s, A, AS, W, WS,    \
-                         ARGS, Y, O, order_key());                                            \
+      hipLaunchKernelGGL((gemm_i8s<KD, 8, kBM8, PART>), grid_, dim3(512), 0, s, A, AS, W, WS, \
+                         ARGS, Y, O, P, S, partial, order_key());                             \
   } while (0)
   prof_begin(kInt8GateUp, s);
   if (large) { LARGE8(kGateUp8, x8, xs, wgu8, wgus, act, nullptr, I / 128, 32); }
-  else STREAM8(kGateUp8, x8, xs, wgu8, wgus, act, nullptr, I / 128);
+  else if (L.slices_gu > 1) STREAM8(kGateUp8, true, x8, xs, wgu8, wgus, nullptr, nullptr, I / 128, L.slices_gu);
+  else STREAM8(kGateUp8, false, x8, xs, wgu8, wgus, act, nullptr, I / 128, 1);
   prof_end(kInt8GateUp, s);
+  const Int8Parts gu{partial, L.slices_gu, k, perm, idx, xs, wgus};
+  const Int8Parts down{partial, L.slices_down, k, perm, idx, scales, wds};
+  uint16_t* const clear = k == 1 && L.slices_down == 1 ? out : nullptr;
 #define QUANT8(NV)                                                                            \
-  hipLaunchKernelGGL(quant_act_rows<NV>, dim3(P), dim3(256), 0, s, act, offsets, E, row_of, P, H, I, \
-                     codes, scales, k == 1 ? out : nullptr, order_key())
+  do {                                                                                        \
+    if (L.slices_gu > 1)                                                                      \
+      hipLaunchKernelGGL((quant_act_rows<NV, true>), dim3(P), dim3(256), 0, s, nullptr, gu, offsets, E, \
+                         row_of, P, H, I, codes, scales, clear, order_key());                 \
+    else                                                                                      \
+      hipLaunchKernelGGL((quant_act_rows<NV, false>), dim3(P), dim3(256), 0, s, act, gu, offsets, E, \
+                         row_of, P, H, I, codes, scales, clear, order_key());                 \
+  } while (0)
   if (I <= 1024) QUANT8(1);
   else if (I <= 2048) QUANT8(2);
   else if (I <= 4096) QUANT8(4);
@@ -870,13 +997,17 @@ hipError_t launch_experts_int8(const int8_t* x, const float* xs, const int8_t* w
   prof_begin(kInt8Down, s);
   if (large && k == 1) { LARGE8(kDownFused8, codes, scales, wd8, wds, nullptr, out, H / 256, 64); }
   else if (large) { LARGE8(kDown8, codes, scales, wd8, wds, y, nullptr, H / 256, 64); }
-  else if (k == 1) STREAM8(kDownFused8, codes, scales, wd8, wds, nullptr, out, H / 256);
-  else STREAM8(kDown8, codes, scales, wd8, wds, y, nullptr, H / 256);
+  else if (L.slices_down > 1) STREAM8(kDown8, true, codes, scales, wd8, wds, nullptr, nullptr, H / 256, L.slices_down);
+  else if (k == 1) STREAM8(kDownFused8, false, codes, scales, wd8, wds, nullptr, out, H / 256, 1);
+  else STREAM8(kDown8, false, codes, scales, wd8, wds, y, nullptr, H / 256, 1);
 #undef ARGS
 #undef LARGE8
 #undef STREAM8
+  if (L.slices_down > 1)
+    hipLaunchKernelGGL(combine_parts, dim3(T, (H + 1023) / 1024), dim3(256), 0, s, down, row_of, w, T, H, out,
+                       order_key());
   hipError_t e = hipGetLastError();
-  if (e == hipSuccess && k > 1)
+  if (e == hipSuccess && k > 1 && L.slices_down == 1)
     e = launch_combine_slots(y, row_of, w, T, H, k, out, 0, H, H, s, num_cus);
   prof_end(kInt8Down, s);
   return e;

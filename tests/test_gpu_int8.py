@@ -87,6 +87,31 @@ def test_experts_int8_ids_out_of_range(M, T, E, k, H, I):
     assert not call(M, d, out=out).any()
 
 
+@pytest.mark.parametrize("T,H,I,E,k", [
+    (14, 2560, 1792, 5, 5), (100, 4096, 1024, 4, 2), (300, 4096, 1024, 4, 1), (40, 4096, 256, 3, 3), (60, 512, 2048, 4, 4),
+    (90, 1536, 1792, 2, 1), (20, 512, 4096, 16, 12), (131, 7168, 256, 1, 1)])
+def test_experts_int8_split_reductions(M, T, H, I, E, k):
+    """Few rows and few experts: reductions in slices, on either or both projections."""
+    print(f"[int8] split T={T} H={H} I={I} E={E} k={k}", flush=True)
+    d = make(T, H, I, E, k, seed=12)
+    ws = M.workspace(M.moe_experts_int8_workspace_bytes(T, H, I, E, k))
+    ws.fill_(255)
+    ref = call(M, d, ws=ws)
+    check(M, d, ref)
+    one = {n: (t[3:4].clone() if n in ("x", "xs", "idx", "w") else t) for n, t in d.items()}
+    assert torch.equal(call(M, one), ref[3:4])              # exact sums: the bits of an unsplit form
+    for seed in (1, 2, 3):
+        M.moe_set_debug_options(M.MOE_DEBUG_PERMUTE_ORDER, seed)
+        assert torch.equal(call(M, d), ref)
+    M.moe_set_debug_options(0, 0)
+    d["idx"][1] = E                                         # a token without an expert, a slot without one
+    d["idx"][2, 0] = -1
+    out = torch.full((T, H), float("nan"), dtype=torch.bfloat16, device="cuda")
+    call(M, d, out=out)
+    assert not out[1].any()
+    check(M, d, out)
+
+
 def test_experts_int8_same_expert_twice(M):
     d = make(40, 512, 256, 6, 3, seed=3)
     d["idx"][:, 2] = d["idx"][:, 0]
