@@ -65,15 +65,19 @@ inline int slices(size_t P, int E, int bm, int nblk, int nstage) {
 Int8Ws int8_ws_layout(int T, int H, int I, int E, int k) {
   Int8Ws L{};
   const size_t P = static_cast<size_t>(T) * k;
-  // 256-row tiles where the products are bound by the matrix cores: 320 rows an expert
-  // and reductions long enough to pay for a tile's start and end.  Measured, us (256-row
-  // / 128-row tiles): H 7168 I 2048 E 6 k 1, 260 rows an expert 178 / 158, 384 228 / 246,
-  // 2000 747 / 1007; H 4096 I 1024 E 32 k 6, 260 349 / 315, 384 382 / 397, 2000 1673 /
-  // 1828; H 2048 I 768 E 64 k 8, 384 390 / 368, 2000 1734 / 1703.
+  // 256-row tiles where the products are bound by the matrix cores: 360 rows an expert,
+  // tiles for half of the CUs, and reductions long enough to pay for a tile's start and
+  // end.  Measured, us (256-row / 128-row tiles):
+  //   H 7168 I 2048 E 6 k 1: 320 rows an expert 198 / 201, 400 208 / 239, 1500 532 / 713
+  //   H 4096 I 1024 E 32 k 6: 320 rows 301 / 292, 400 326 / 378, 1500 1087 / 1312
+  //   H 2048 I 768 E 64 k 8: 320 rows 279 / 261, 400 307 / 328, 1500 1070 / 1148
+  //   H 1024 I 512 E 16 k 4: 400 rows 95 / 51, 1500 180 / 134
+  //   H 4096 I 1024 E 4 k 2: 400 rows (50 tiles of gate/up) 99 / 68, 600 (75) 96 / 92, 1500 (187) 152 / 184
   // 128-row tiles from 40 rows an expert, where about half the experts would need two of
   // 64 rows (their weights streamed twice): H 4096 I 1024 E 64 k 6, 37 rows 200 / 200,
   // 73 rows 262 / 319 (128-row / 64-row).
-  const bool mfma_bound = P >= 320 * static_cast<size_t>(E) && static_cast<size_t>(H) * I >= (size_t(1) << 22);
+  const bool mfma_bound = P >= 360 * static_cast<size_t>(E) && P / kLargeBM * (I / 128) >= 128 &&
+                          static_cast<size_t>(H) * I >= (size_t(3) << 19);
   L.bm = mfma_bound ? kLargeBM : P >= 40 * static_cast<size_t>(E) ? kTall8 : kBM8;
   L.max_tiles = static_cast<int>(E + (P + L.bm - 1) / L.bm);
   const bool split = L.bm != kLargeBM;
@@ -321,7 +325,8 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == 6
 namespace {
 constexpr int k8BK = 128;                                // K per stage
 constexpr int k8Tile = kLargeBM * k8BK;                  // bytes per operand stage
-constexpr size_t k8Lds = 2 * 2 * k8Tile;                 // 128 KB
+constexpr int k8Stages = 2 * 2 * k8Tile;                 // 128 KB
+constexpr size_t k8Lds = k8Stages + 3 * 4 * kLargeBM;    // and the rows' scales, pair ids and weights
 typedef int i32x16 __attribute__((__vector_size__(16 * sizeof(int))));
 
 __device__ __forceinline__ i32x16 mfma32_i8(i32x4 a, i32x4 b, i32x16 c) {
@@ -352,48 +357,39 @@ __global__ __launch_bounds__(256) void gemm_large_i8(
   const int K = GU ? H : I;
   const int nblk = GU ? I / 128 : H / 256;
   const int nk = K / k8BK;
+  const int nt = *n_tiles;
+  const TailPlan plan = tail_plan(nblk * nt, ncu, nk);
   const int L = blockIdx.x;
-  int item, kb = 0, ke = nk, slot = -1;
-  {
-    const int n_real = nblk * *n_tiles;
-    const TailPlan plan = tail_plan(n_real, ncu, nk);
-    if (plan.S > 1 && L < plan.full) {
-      item = permute_item(round_item(L, plan.full, ncu), plan.full, okey);
-    } else if (plan.S > 1) {
-      const int t0 = L - plan.full;
-      if (t0 >= plan.rem * plan.S) return;
-      const int t = permute_item(t0, plan.rem * plan.S, okey);
-      item = plan.full + t % plan.rem;
-      const int sl = t / plan.rem;
-      kb = sl * nk / plan.S;
-      ke = (sl + 1) * nk / plan.S;
-      slot = t;
-    } else {
-      item = round_real_item(L, nblk, *n_tiles, ncu);
-      if (item < 0) return;
-      item = permute_item(item, n_real, okey);
-    }
+  const int tid = threadIdx.x, wv = tid >> 6, ln = tid & 63, l32 = ln & 31, hi = ln >> 5;
+  const int wm = wv & 1, wn = wv >> 1;
+  int item, kb = 0, ke = nk, slot = -1;                  // slot >= 0: a slice of a tile of the last round
+  if (plan.S > 1 && L < plan.full) {
+    item = permute_item(round_item(L, plan.full, ncu), plan.full, okey);
+  } else if (plan.S > 1) {
+    if (L - plan.full >= plan.rem * plan.S) return;
+    slot = permute_item(L - plan.full, plan.rem * plan.S, okey);
+    item = plan.full + slot % plan.rem;
+    const int sl = slot / plan.rem;
+    kb = sl * nk / plan.S;
+    ke = (sl + 1) * nk / plan.S;
+  } else {
+    item = round_real_item(L, nblk, nt, ncu);
+    if (item < 0) return;
+    item = permute_item(item, nblk * nt, okey);
   }
   int tile, nb;
-  large_coords(item, nblk, *n_tiles, tile, nb);
+  large_coords(item, nblk, nt, tile, nb);
   const int2 te = tiles[tile];
   const int e = te.x, m0 = te.y;
   const int mcount = min(kLargeBM, counts[e] - m0);
   const int rbase = offsets[e] + m0;
-  const int tid = threadIdx.x, wv = tid >> 6, ln = tid & 63, l32 = ln & 31, hi = ln >> 5;
-  const int wm = wv & 1, wn = wv >> 1;
-
-  // the epilogue's data of tile row tid, loaded here: its latency passes during the products
-  const int my_pr = perm[rbase + min(tid, mcount - 1)];
-  const float my_sx = GU ? acts[my_pr / k] : acts[rbase + min(tid, mcount - 1)];
-  const float my_w = KIND == kDownFused8 ? w[my_pr] : 0.f;  // k = 1: pair id == token
+  const int n0 = nb * 128;
 
   // loader: thread covers tile rows wv*64 + 8j + (ln >> 3), j = 0..7, of both operands,
   // 16-byte chunk ln & 7 of each 128-byte row segment
   const int lrow = ln >> 3, lc = ln & 7;
   const size_t wrows = GU ? 2 * static_cast<size_t>(I) : static_cast<size_t>(H);
   const uint8_t* __restrict__ abase = wt + static_cast<size_t>(e) * wrows * K;
-  const int n0 = nb * 128;
   const int arow = GU ? (wv < 2 ? n0 + wv * 64 : I + n0 + (wv - 2) * 64) : nb * 256 + wv * 64;
   const uint32_t ao = static_cast<uint32_t>((arow + lrow) * K + lc * 16);
   uint32_t bo[8];
@@ -416,6 +412,7 @@ __global__ __launch_bounds__(256) void gemm_large_i8(
   const int swz = (l32 >> 1) & 7;
 
   i32x4 stg[16];   // [0..7] weight rows, [8..15] activation rows
+  // (past the end the last stage again)
 #define GLOAD(Q, KT) do {                                                               \
     const uint32_t kk_ = static_cast<uint32_t>(min((KT), ke - 1) * k8BK);               \
     if ((Q) < 8) stg[Q] = ld16(abase + ao + static_cast<uint32_t>((Q) * 8) * K + kk_);  \
@@ -449,13 +446,6 @@ __global__ __launch_bounds__(256) void gemm_large_i8(
     }                                                                                   \
   } while (0)
 
-  i32x16 acc[4][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
   // The LDS writes of stage s+1 are spread over the four K steps that may write its
   // buffer: the last step of stage s-1 (chunks 12..15, after the barrier that ends
   // the reads of stage s-1) and the first three of stage s (chunks 0..11, before the
@@ -478,6 +468,23 @@ __global__ __launch_bounds__(256) void gemm_large_i8(
 #pragma unroll
     for (int g = 0; g < 4; ++g) b0[g] = RDF(&at[k8Tile + fb + 32 * g * k8BK + so]);
   }
+  // the epilogue's data (tile row tid's scale, pair and weight; the columns' scales),
+  // requested here: its latency passes during the products
+  const int my_row = rbase + min(tid, mcount - 1);
+  const int my_pr = perm[my_row];
+  float my_sx = 0.f, my_w = 0.f;
+  float ws[4];
+  const float* wse = wts + static_cast<size_t>(e) * wrows;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    ws[i] = wse[GU ? (i >> 1) * I + n0 + wn * 64 + (i & 1) * 32 + l32 : nb * 256 + wn * 128 + 32 * i + l32];
+  i32x16 acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0;
   for (int kt = kb; kt < ke; ++kt) {
     PHASE(a0, b0, a1, b1, kt, 1, kt + 1, 0);
     PHASE(a1, b1, a0, b0, kt, 2, kt + 1, 4);
@@ -485,42 +492,41 @@ __global__ __launch_bounds__(256) void gemm_large_i8(
     // stage kt+1 is in LDS for every wave, and every wave is done reading stage kt
     wait_lgkm0();
     __builtin_amdgcn_s_barrier();
+    // In the loop on purpose: a loop of one basic block keeps a copy of the accumulators
+    // outside the AGPRs for the code after it, made again every stage (16384 rows, 6
+    // experts 929 us instead of 848).
+    if (kt == kb) {
+      my_sx = GU ? acts[my_pr / k] : acts[my_row];
+      if (KIND == kDownFused8) my_w = w[my_pr];          // k = 1: pair id == token
+    }
     PHASE(a1, b1, a0, b0, kt + 1, 0, kt + 2, 12);
   }
-#undef GLOAD
-#undef LWRITE
-#undef RDF
-#undef PHASE
   if (slot >= 0) {
     // tail slice: INT32 partial tile in register order, [64 x i32x4][256 threads]
     i32x4* pp = reinterpret_cast<i32x4*>(partial) + static_cast<size_t>(slot) * 64 * 256 + tid;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 4; ++j) {
+        asm volatile("" : "+a"(acc[i][j]));
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           pp[((i * 4 + j) * 4 + q) * 256] =
               i32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+      }
     return;
   }
   // Lane (l32, hi), register 4q + t of block (i, j): output column l32 of weight block
   // i, tile row 8q + 4hi + t of row block j - a store instruction writes 128
   // consecutive bytes of two rows (FP32), or 64 of four (BF16, columns paired over
   // lanes).  The rows' scales, pair ids and weights go through LDS, four rows a read.
-  const float* wse = wts + static_cast<size_t>(e) * wrows;
-  float* s_sx = reinterpret_cast<float*>(lds8);
-  int* s_pr = reinterpret_cast<int*>(lds8) + kLargeBM;
-  float* s_w = reinterpret_cast<float*>(lds8) + 2 * kLargeBM;
-  __syncthreads();                                       // every wave is done with the K stages
+  float* s_sx = reinterpret_cast<float*>(lds8 + k8Stages);
+  int* s_pr = reinterpret_cast<int*>(lds8 + k8Stages) + kLargeBM;
+  float* s_w = reinterpret_cast<float*>(lds8 + k8Stages) + 2 * kLargeBM;
   s_sx[tid] = my_sx;
   s_pr[tid] = my_pr;
   s_w[tid] = my_w;
   __syncthreads();
-  float ws[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    ws[i] = wse[GU ? (i >> 1) * I + n0 + wn * 64 + (i & 1) * 32 + l32 : nb * 256 + wn * 128 + 32 * i + l32];
   // whole tiles (the most of them) without the checks of each row
   auto store = [&](auto whole) {
     constexpr bool kWhole = decltype(whole)::value;
@@ -528,6 +534,9 @@ __global__ __launch_bounds__(256) void gemm_large_i8(
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
+        if (q == 0)                                      // (read from the AGPRs here, not all at once: 876 -> 848 us)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) asm volatile("" : "+a"(acc[i][j]));
         __builtin_amdgcn_sched_barrier(0);               // (one group of rows at a time: fewer registers live)
         const int r0 = wm * 128 + 32 * j + 8 * q + 4 * hi;
         if (!kWhole && r0 >= mcount) continue;
@@ -566,6 +575,10 @@ __global__ __launch_bounds__(256) void gemm_large_i8(
   };
   if (mcount == kLargeBM) store(std::true_type{});
   else store(std::false_type{});
+#undef GLOAD
+#undef LWRITE
+#undef RDF
+#undef PHASE
 }
 
 // Tail fix-up, element-parallel: thread g of the grid takes one i32x4 of the partial

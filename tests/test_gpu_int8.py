@@ -53,7 +53,8 @@ def check(M, d, out, tokens=None):
     (300, 512, 512, 3, 1), (777, 256, 512, 16, 6), (600, 512, 256, 1, 1), (513, 768, 256, 2, 2),
     (1025, 1024, 512, 4, 1),
     # 256-row tiles: one ragged expert, several with tail slices along K, k = 1 and more
-    (700, 4096, 1024, 1, 1), (1300, 2048, 2048, 2, 1), (900, 4096, 1024, 4, 2), (1500, 4096, 1024, 9, 2)])
+    (700, 4096, 1024, 1, 1), (1300, 2048, 2048, 2, 1), (900, 4096, 1024, 4, 2), (1500, 4096, 1024, 9, 2),
+    (2200, 1024, 2048, 3, 1), (1500, 1024, 2048, 4, 2), (2601, 1792, 1792, 2, 1)])
 def test_experts_int8(M, T, H, I, E, k):
     print(f"[int8] T={T} H={H} I={I} E={E} k={k}", flush=True)
     d = make(T, H, I, E, k, seed=T)
@@ -69,7 +70,8 @@ def test_experts_int8_skewed(M, T):
 
 @pytest.mark.parametrize("T,E,k,H,I", [
     (6, 4, 2, 512, 256), (50, 8, 3, 512, 256), (200, 8, 3, 512, 256), (9, 4, 1, 512, 256), (300, 4, 1, 512, 256),
-    (900, 3, 1, 512, 256), (1200, 3, 2, 512, 256), (1100, 3, 1, 2048, 2048), (600, 3, 2, 4096, 1024)])
+    (900, 3, 1, 512, 256), (1200, 3, 2, 512, 256), (1100, 3, 1, 2048, 2048), (600, 3, 2, 4096, 1024),
+    (2200, 3, 1, 1024, 2048), (1100, 3, 2, 1024, 2048)])
 def test_experts_int8_ids_out_of_range(M, T, E, k, H, I):
     print(f"[int8] ids out of range T={T} E={E} k={k} H={H}", flush=True)
     d = make(T, H, I, E, k, seed=2)
@@ -154,7 +156,8 @@ def test_experts_int8_rows_do_not_depend_on_the_batch(M):
 
 
 @pytest.mark.parametrize("T,E,k,H,I", [(1, 8, 2, 512, 512), (40, 8, 2, 512, 512), (500, 8, 2, 512, 512),
-                                       (900, 2, 1, 2048, 2048), (700, 2, 2, 4096, 1024)])
+                                       (900, 2, 1, 2048, 2048), (700, 2, 2, 4096, 1024),
+                                       (2100, 2, 1, 1024, 2048), (1050, 2, 2, 1024, 2048)])
 def test_experts_int8_deterministic_and_order_free(M, T, E, k, H, I):
     d = make(T, H, I, E, k, seed=9)
     ref = call(M, d)
@@ -166,7 +169,7 @@ def test_experts_int8_deterministic_and_order_free(M, T, E, k, H, I):
 
 def test_experts_int8_workspace_contents_do_not_matter(M):
     for T, E, k, H, I in ((2, 8, 2, 512, 256), (70, 8, 2, 512, 256), (300, 8, 2, 512, 256), (700, 2, 1, 4096, 1024),
-                          (500, 2, 2, 4096, 1024)):
+                          (500, 2, 2, 4096, 1024), (2100, 2, 1, 1024, 2048), (1050, 2, 2, 1024, 2048)):
         d = make(T, H, I, E, k, seed=10)
         ws = M.workspace(M.moe_experts_int8_workspace_bytes(T, H, I, E, k))
         ws.zero_()
@@ -190,7 +193,8 @@ def test_experts_int8_large_offsets(M):
 
 
 @pytest.mark.parametrize("T,E,k,H,I", [(1, 16, 4, 512, 256), (60, 16, 4, 512, 256), (300, 8, 2, 512, 256),
-                                       (900, 2, 1, 2048, 2048), (700, 2, 2, 4096, 1024)])
+                                       (900, 2, 1, 2048, 2048), (700, 2, 2, 4096, 1024),
+                                       (2100, 2, 1, 1024, 2048), (1050, 2, 2, 1024, 2048)])
 def test_experts_int8_graph_replays(M, T, E, k, H, I):
     """Captured and replayed, with eager work of the program's own between the replays; two
     graphs that share one workspace, replayed in turn."""
