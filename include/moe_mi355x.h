@@ -400,7 +400,9 @@ size_t moe_add_rmsnorm_backward_workspace_bytes(int T, int H);
  *            score, and it is selected (weight 0, lowest index first) only where
  *            fewer than k experts of the selected groups take part.  A group with
  *            no expert that takes part ranks last.  +inf counts as FLT_MAX.
- *            Weights whose selected scores sum to 0 are 0.
+ *            Where no selected expert takes part the weights are 0.  Renormalised
+ *            weights are ratios to the largest selected score: they hold however
+ *            low the scores are.
  *   bias     [E] float32, or NULL; no NaN or +inf
  *   topk_idx [T, k] int32 out, always within [0, E) and distinct within a row
  *   topk_w   [T, k] float32 out

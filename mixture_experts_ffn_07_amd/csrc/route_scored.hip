@@ -89,6 +89,15 @@ __device__ __forceinline__ float exp_close(float x) {
   return __builtin_amdgcn_exp2f(h) * fmaf(l, 0.693147180559945f, 1.0f);
 }
 
+// exp(a - b), a <= b, as close: the difference's own rounding error (half a step of it,
+// which at a - b = -70 would be 60 steps of the exponential) is put back too.
+__device__ __forceinline__ float exp_diff(float a, float b) {
+  const float d = a - b, bb = d - a;
+  const float err = (a - (d - bb)) - (b + bb);
+  const float p = exp_close(d);
+  return d > -200.0f ? fmaf(p, err, p) : 0.f;
+}
+
 // FP32 values as integers of the same order, and back.
 __device__ __forceinline__ int order_of(float f) {
   const int b = __float_as_int(f);
@@ -403,8 +412,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(R <= 8 ? 5 
       // relative to the largest: sigmoid(l) = exp(min(l, 0)) / (1 + exp(-|l|)), and the
       // first factor over that of the largest does not vanish however low the logits are
       const float m = wave_max_f32(use ? l : -INFINITY);
-      if (a.sigmoid) p = exp_close(fminf(l, 0.f) - fminf(m, 0.f)) * __builtin_amdgcn_rcpf(1.0f + exp_close(-fabsf(l)));
-      else p = exp_close(l - m);
+      if (a.sigmoid) p = exp_diff(fminf(l, 0.f), fminf(m, 0.f)) * __builtin_amdgcn_rcpf(1.0f + exp_close(-fabsf(l)));
+      else p = exp_diff(l, m);
       p = use ? p : 0.f;
       const float den = wave_sum_f32(p);                 // (at least 0.5 where any expert takes part)
       p = den > 0.f ? p * __builtin_amdgcn_rcpf(den) : 0.f;
@@ -412,7 +421,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(R <= 8 ? 5 
       const float en = exp_close(-fabsf(l));
       p = use ? (l < 0.f ? en : 1.0f) * __builtin_amdgcn_rcpf(1.0f + en) : 0.f;
     } else {
-      p = use ? exp_close(l - top) / zsum : 0.f;
+      p = use ? exp_diff(l, top) / zsum : 0.f;
     }
     if (lane < k) {
       idx[static_cast<size_t>(t) * k + lane] = sel;
@@ -459,7 +468,7 @@ __global__ __launch_bounds__(256) void route_scored_backward_kernel(
     const float q = (l < 0.f ? 1.0f : en) * r;             // 1 - p without cancellation
     if (a.renorm) {                                        // (the forward's weights)
       const float m = wave_max_f32(use ? l : -INFINITY);
-      const float x = use ? exp_close(fminf(l, 0.f) - fminf(m, 0.f)) * r : 0.f;
+      const float x = use ? exp_diff(fminf(l, 0.f), fminf(m, 0.f)) * r : 0.f;
       const float z = wave_sum_f32(x);
       const float p = z > 0.f ? x / z : 0.f;
       val = p * q * (d - wave_sum_f32(p * d));
@@ -469,7 +478,7 @@ __global__ __launch_bounds__(256) void route_scored_backward_kernel(
     val *= a.scale;
   } else if (a.renorm) {
     const float m = wave_max_f32(use ? l : -INFINITY);
-    const float x = use ? exp_close(l - m) : 0.f;
+    const float x = use ? exp_diff(l, m) : 0.f;
     const float z = wave_sum_f32(x);
     const float p = z > 0.f ? x / z : 0.f;
     val = a.scale * p * (d - wave_sum_f32(p * d));
@@ -486,12 +495,12 @@ __global__ __launch_bounds__(256) void route_scored_backward_kernel(
     float z = 0.f;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      g[i] = v[i] > -INFINITY ? exp_close(v[i] - top) : 0.f;
+      g[i] = v[i] > -INFINITY ? exp_diff(v[i], top) : 0.f;
       z += g[i];
     }
     z = wave_sum_f32(z);
     const float inv = z > 0.f ? 1.0f / z : 0.f;
-    const float p = use ? exp_close(l - top) * inv : 0.f;
+    const float p = use ? exp_diff(l, top) * inv : 0.f;
     const float mean = wave_sum_f32(p * d);
 #pragma unroll
     for (int i = 0; i < R; ++i) g[i] *= -a.scale * inv * mean;

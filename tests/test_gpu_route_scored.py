@@ -256,3 +256,38 @@ def test_route_scored_is_deterministic_and_order_free(M):
         for a, c in zip(ref, call()):
             assert torch.equal(a.view(torch.int32), c.view(torch.int32))
     M.moe_set_debug_options(0, 0)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_route_scored_weights_of_low_logits(M, score, renorm):
+    """Selected logits tens below the largest (a bias picks them): the difference's rounding
+    alone, half a step of it, would be up to 64 steps of the exponential.  All logits far
+    below 0 and above the masks: sigmoid scores that vanish in FP32 still have their ratio."""
+    g = torch.Generator().manual_seed(3)
+    l = -torch.rand(64, 96, generator=g) * 65
+    l[:, 0] = 6.28125 + torch.rand(64, generator=g)
+    b = torch.zeros(96)
+    b[64:] = 2.0
+    _run(M, l, 32, b, score, renorm=renorm, what="low")
+    _run(M, l, 96 // 3, None, score, renorm=renorm, what="low")
+    idx, w = M.moe_route_scored((l - 600).cuda(), 8, score=_score(M, "sigmoid"), renormalize=True)
+    top = torch.gather((l - 600).double(), 1, idx.cpu().long())
+    ref = torch.softmax(top, 1)
+    assert ((w.cpu().double() - ref).abs() <= ref * REL + 1e-37).all()
+
+
+def test_route_scored_backward_of_low_logits(M):
+    """Softmax, not renormalised: the gradient of experts tens below the largest."""
+    g = torch.Generator().manual_seed(4)
+    l = -torch.rand(32, 96, generator=g) * 65
+    l[:, 0] = 6.28125
+    idx, _ = M.moe_route_scored(l.cuda(), 8, renormalize=False)
+    d = torch.randn(32, 8, generator=g)
+    got = M.moe_route_scored_backward(l.cuda(), idx, d.cuda(), renormalize=False).cpu().double()
+    p = torch.softmax(l.double(), 1)
+    sel = idx.cpu().long()
+    mean = (torch.gather(p, 1, sel) * d).sum(1, keepdim=True)
+    full = torch.zeros(32, 96, dtype=torch.float64).scatter(1, sel, d.double())
+    size = full.abs() + (torch.gather(p, 1, sel) * d.abs()).sum(1, keepdim=True)   # (the terms' magnitudes)
+    assert ((got - p * (full - mean)).abs() <= 2 * REL * p * size + 1e-37).all()
