@@ -119,7 +119,7 @@ def experts_int8(x, x_scales, w_gate_up, w_gate_up_scales, w_down, w_down_scales
     """(out [T, H], slack [T, H]): the INT8 layer, and how far out may move when activations
     that lie within 2.5e-3 codes of a rounding border (FP32's error of a 127 / amax, 2e-5
     relative with the exponential's) are coded the other way: each such code moves y by
-    sh sd |wd| <= 127 sh sd."""
+    sh sd |wd|, |wd| that of its weight (128 for a weight of -128)."""
     x = np.asarray(x, dtype=np.float64)
     T, H = x.shape
     E, I = w_down.shape[0], w_down.shape[2]
@@ -136,11 +136,11 @@ def experts_int8(x, x_scales, w_gate_up, w_gate_up_scales, w_down, w_down_scales
         hq, sh = int8_rows(a)
         amax = np.abs(a).max(axis=1, keepdims=True)
         code = np.abs(a) * np.where(amax > 0, 127.0 / np.where(amax > 0, amax, 1.0), 0.0)
-        near = (np.abs(code - np.floor(code) - 0.5) < 2.5e-3).sum(axis=1)
+        near = (np.abs(code - np.floor(code) - 0.5) < 2.5e-3).astype(np.float64)
         sd = np.asarray(w_down_scales[e], dtype=np.float64)
         y = (hq @ np.asarray(w_down[e], dtype=np.float64).T) * sh[:, None] * sd
         wt = np.asarray(w, dtype=np.float64)[t, j][:, None]
         np.add.at(out, t, wt * y)
-        np.add.at(slack, t, np.abs(wt) * (127.0 * near * sh)[:, None] * sd
+        np.add.at(slack, t, np.abs(wt) * (near @ np.abs(np.asarray(w_down[e], dtype=np.float64)).T) * sh[:, None] * sd
                   + np.abs(wt * y) * 2.0 ** -16)      # FP32: a (2e-5) through sh, the products, the sum
     return out, slack

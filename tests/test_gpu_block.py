@@ -59,7 +59,8 @@ def test_int8_block(M, T):
     assert np.array_equal(idx.cpu().numpy(), ridx)
     n = lambda t: t.cpu().numpy()  # noqa: E731
     ref, slack = B.experts_int8(n(c), n(sc), *(n(t) for t in q), ridx, n(w))
-    assert np.all(np.abs(_f64(out) - ref) <= np.abs(ref) * 2.0 ** -8 + slack)
+    # (out is the BF16 value next to some v with |v - ref| <= slack: half a step of v, 2^-8 |v|, more)
+    assert np.all(np.abs(_f64(out) - ref) <= (np.abs(ref) + slack) * 2.0 ** -8 + slack)
     # against the same block in 64 bits throughout: what 8-bit operands cost.  Each of x, W, a, W_d
     # is off by at most half a code, on average 1/sqrt(12) of one; with codes of up to 127 and rows of
     # Gaussian values (amax near 3.5 sigma) that is about 1% an operand, 4 operands in two products

@@ -41,9 +41,10 @@ def check(M, d, out, tokens=None):
     ref, slack = B.experts_int8(n(d["x"])[rows], n(d["xs"])[rows], n(d["wg"]), n(d["sg"]), n(d["wd"]), n(d["sd"]),
                                 n(d["idx"])[rows], n(d["w"])[rows])
     got = out.double().cpu().numpy()[rows]
-    # half a step of a BF16 result: 2^-8 of it, and 2^-134 below the normal range (steps of 2^-133
-    # there: a weight of 1e-43 times y has no nearer BF16 value)
-    over = np.abs(got - ref) - (np.abs(ref) * 2.0 ** -8 + 2.0 ** -134 + slack)
+    # out is the BF16 value next to some v with |v - ref| <= slack: |out - ref| <= half a step of
+    # v + slack, half a step <= 2^-8 |v| <= 2^-8 (|ref| + slack), and 2^-134 below the normal
+    # range (steps of 2^-133 there: a weight of 1e-43 times y has no nearer BF16 value)
+    over = np.abs(got - ref) - ((np.abs(ref) + slack) * 2.0 ** -8 + 2.0 ** -134 + slack)
     assert np.all(np.isfinite(got)) and np.all(over <= 0), f"{over.max():.3e} over, |ref| {np.abs(ref).max():.3e}"
 
 
