@@ -48,7 +48,7 @@ __device__ __forceinline__ float swiglu8(float g, float u) {
 // leave half the CUs or more without a workgroup, as many as those have room for, of at
 // least three 256-code stages.  The slices' INT32 sums are exact and are added by the
 // kernel that reads them next.  Measured, us (split / whole): T 100 H 7168 I 2048 E 4 k 2
-// 64 / 87; T 40 H 4096 I 1024 E 6 k 4 37 / 47; T 14 H 2560 I 1792 E 5 k 5 41 / 45.  Room
+// 64 / 87; T 40 H 4096 I 1024 E 6 k 4 37 / 47; T 14 H 2560 I 1792 E 5 k 5 39 / 45.  Room
 // for half as many again: T 128 H 3584 I 1024 E 8 k 8 57 against 59, but T 809 H 3840 I 512
 // E 4 k 2 68 against 55.  Slices of one stage: T 2000 H 1024 I 512 E 4 k 1 55 against 36
 // whole; of two: T 40 H 4096 40 against 37 of three.
@@ -740,27 +740,30 @@ __global__ __launch_bounds__(256) void combine_parts(const Int8Parts sum, const 
   if (c >= H) return;
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   for (int j0 = 0; j0 < k; j0 += 8) {                     // eight slots' loads in flight, then their sum in order
-    i32x4 v[8];
+    i32x4 v[8], next[8];
     float wj[8], sh[8];
     f32x4 sd[8];
     const int* p[8];
     bool in[8];
+    // (loads without conditions, which would wait for each: a slot without a row, or past the
+    // last, reads row 0 and is left out below)
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int row = j0 + j < k ? row_of[t * k + j0 + j] : P;
-      in[j] = static_cast<unsigned>(row) < static_cast<unsigned>(P);
-      v[j] = i32x4{0, 0, 0, 0};
-      if (in[j]) {
-        wj[j] = w[t * k + j0 + j];
-        sh[j] = sum.acts[row];
-        sd[j] = *reinterpret_cast<const f32x4*>(sum.wts + static_cast<size_t>(sum.idx[t * k + j0 + j]) * H + c);
-        p[j] = sum.part + static_cast<size_t>(row) * H + c;
-      }
+      const int pr = t * k + min(j0 + j, k - 1), row = row_of[pr], e = sum.idx[pr];
+      const bool any = static_cast<unsigned>(row) < static_cast<unsigned>(P);
+      in[j] = any && j0 + j < k;
+      wj[j] = w[pr];
+      sh[j] = sum.acts[any ? row : 0];
+      sd[j] = *reinterpret_cast<const f32x4*>(sum.wts + static_cast<size_t>(any ? e : 0) * H + c);
+      p[j] = sum.part + static_cast<size_t>(any ? row : 0) * H + c;
+      v[j] = *reinterpret_cast<const i32x4*>(p[j]);
     }
-    for (int sl = 0; sl < sum.S; ++sl)
+    for (int sl = 1; sl < sum.S; ++sl) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (in[j]) v[j] += *reinterpret_cast<const i32x4*>(p[j] + static_cast<size_t>(sl) * P * H);
+      for (int j = 0; j < 8; ++j) next[j] = *reinterpret_cast<const i32x4*>(p[j] + static_cast<size_t>(sl) * P * H);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] += next[j];
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (in[j]) {
