@@ -55,7 +55,8 @@ __device__ __forceinline__ float swiglu8(float g, float u) {
 constexpr int kSplitGroups = 256, kSplitStages = 3;
 inline int slices(size_t P, int E, int bm, int nblk, int nstage) {
   const size_t tiles = (P < static_cast<size_t>(E) ? P : E) + P / bm;   // (about; each expert ends one early)
-  const size_t room = tiles ? kSplitGroups / (tiles * nblk) : 1, most = nstage / kSplitStages;
+  const size_t groups = tiles * nblk;                    // (0 for sizes that the layer refuses)
+  const size_t room = groups ? kSplitGroups / groups : 1, most = nstage / kSplitStages;
   const size_t s = room < most ? room : most;
   return s < 2 ? 1 : static_cast<int>(s);
 }

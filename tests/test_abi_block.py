@@ -121,6 +121,17 @@ def test_experts_int8_refusals(m):
     assert call(T=0, ws=None, x=None, out=None) == m.MOE_OK
 
 
+@pytest.mark.parametrize("T", [-5, 0, 1, 3, 1000, 2 ** 31 - 1])
+@pytest.mark.parametrize("E,k", [(1, 1), (8, 2), (1024, 32), (2 ** 31 - 1, 2 ** 31 - 1), (0, 0), (-1, -1)])
+def test_workspace_queries_answer_for_any_sizes(m, T, E, k):
+    """Sizes that the calls themselves refuse come in through the queries too."""
+    for H in (-256, 0, 1, 64, 255, 256, 4096, 2 ** 31 - 1):
+        assert m.lib.moe_add_rmsnorm_backward_workspace_bytes(T, H) >= 0
+        for I in (-128, 0, 1, 64, 127, 128, 255, 256, 2 ** 31 - 1):
+            n = m.lib.moe_experts_int8_workspace_bytes(T, H, I, E, k)
+            assert n >= 0 and (n == 0 or min(T, H, I, E, k) >= 1)
+
+
 def test_int8_is_not_a_type_of_the_batched_calls(m):
     assert m.lib.moe_workspace_bytes(4, 512, 256, 8, 2, m.MOE_INT8) == 0
     assert m.lib.moe_gate_up_3d_batched(FAKE, None, FAKE, None, FAKE, 4, 512, 256, 8, 2, m.MOE_INT8, FAKE,
