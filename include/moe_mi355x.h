@@ -349,8 +349,8 @@ size_t moe_backward_mxfp8_workspace_bytes(int T, int H, int I, int E, int k);
  * In place: residual_out may be x or residual, and y may be x or residual (the
  * same pointer, not an overlap), but not both the same one; nothing else may
  * overlap.
- * Limits: T >= 0 (0 enqueues nothing), H a multiple of 32, 32 <= H <= 16384, eps
- * finite and above 0.  A row with a non-finite value, or whose squares' sum leaves
+ * Limits: 0 <= T < 2^22 (0 enqueues nothing), H a multiple of 32, 32 <= H <=
+ * 16384, eps finite and above 0.  A row with a non-finite value, or whose squares' sum leaves
  * FP32 (magnitudes of 1e17 and more), has undefined contents; other rows are not
  * affected.
  */
@@ -406,7 +406,7 @@ size_t moe_add_rmsnorm_backward_workspace_bytes(int T, int H);
  *   bias     [E] float32, or NULL; no NaN or +inf
  *   topk_idx [T, k] int32 out, always within [0, E) and distinct within a row
  *   topk_w   [T, k] float32 out
- * Limits: T >= 0 (0 enqueues nothing), E <= 1024, 1 <= k <= 32, n_groups <= 64 and
+ * Limits: 0 <= T < 2^22 (0 enqueues nothing), E <= 1024, 1 <= k <= 32, n_groups <= 64 and
  * a divisor of E, 1 <= topk_groups <= n_groups, k <= topk_groups * (E / n_groups),
  * scale finite.
  */
@@ -432,7 +432,7 @@ int moe_route_scored(const float* logits, const float* bias, int T, int E, int k
  *                      expert gets 0; ids outside [0, E) are ignored)
  *   d_topk_w [T, k] float32
  *   dlogits  [T, E] float32 out, every element
- * Limits: T >= 0 (0 enqueues nothing), E <= 1024, 1 <= k <= min(E, 32), scale finite.
+ * Limits: 0 <= T < 2^22 (0 enqueues nothing), E <= 1024, 1 <= k <= min(E, 32), scale finite.
  */
 int moe_route_scored_backward(const float* logits, const int32_t* topk_idx, const float* d_topk_w,
                               int T, int E, int k, moe_score score, int renormalize, float scale,

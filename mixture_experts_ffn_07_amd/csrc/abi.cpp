@@ -418,7 +418,7 @@ int moe_gate_up_3d_batched_train(const uint16_t* x, const uint16_t* w_gate_up,
 }
 
 static int check_norm(int T, int H, float eps) {
-  if (T < 0) return fail(MOE_ERR_SHAPE, "T=%d < 0", T);
+  if (T < 0 || T >= moe::kMaxRows) return fail(MOE_ERR_SHAPE, "T=%d outside [0, %d)", T, moe::kMaxRows);
   if (H < 32 || H % 32 || H > moe::kNormMaxH)
     return fail(MOE_ERR_SHAPE, "H=%d is not a multiple of 32 in [32, %d]", H, moe::kNormMaxH);
   if (!(eps > 0.0f) || !std::isfinite(eps))
@@ -480,7 +480,7 @@ int moe_add_rmsnorm_backward(const uint16_t* s, const uint16_t* weight, const ui
 }
 
 static int check_scored(int T, int E, int k, moe_score score, float scale) {
-  if (T < 0) return fail(MOE_ERR_SHAPE, "T=%d < 0", T);
+  if (T < 0 || T >= moe::kMaxRows) return fail(MOE_ERR_SHAPE, "T=%d outside [0, %d)", T, moe::kMaxRows);
   if (E < 1 || E > 1024) return fail(MOE_ERR_SHAPE, "E=%d outside [1, 1024]", E);
   if (k < 1 || k > E || k > 32) return fail(MOE_ERR_SHAPE, "k=%d outside [1, min(E=%d, 32)]", k, E);
   if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID)

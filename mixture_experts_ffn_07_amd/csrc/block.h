@@ -12,6 +12,10 @@ namespace moe {
 enum BlockKernelId { kNorm = kKernelCount, kNormBackward, kRouteBackward, kInt8GateUp, kInt8Down,
                      kAllKernelCount };
 
+// Rows of one launch with a workgroup of up to 1024 threads each: a grid holds fewer than
+// 2^32 threads.
+constexpr int kMaxRows = 1 << 22;
+
 // Routing by scores (route_scored.hip).
 struct ScoredRoute {
   int E, k, groups, topk_groups, group_top;

@@ -365,12 +365,16 @@ hipError_t launch_quant_int8(const uint16_t* src, int64_t rows, int K, uint8_t* 
                              hipStream_t s, int num_cus) {
   const RowShape rs = row_shape(K / kVec, rows <= 2 * num_cus);
   prof_begin(kQuant, s);
-  if (rs.nv == 1)
-    hipLaunchKernelGGL(quant_int8_rows<1>, dim3(static_cast<unsigned>(rows)), dim3(rs.threads), 0, s, src,
-                       rows, K, codes, scales, order_key());
-  else
-    hipLaunchKernelGGL(quant_int8_rows<2>, dim3(static_cast<unsigned>(rows)), dim3(rs.threads), 0, s, src,
-                       rows, K, codes, scales, order_key());
+  for (int64_t r0 = 0; r0 < rows; r0 += kMaxRows - 1) {   // (one launch but for millions of rows)
+    const int64_t n = rows - r0 < kMaxRows - 1 ? rows - r0 : kMaxRows - 1;
+    const dim3 grid(static_cast<unsigned>(n)), block(rs.threads);
+    if (rs.nv == 1)
+      hipLaunchKernelGGL(quant_int8_rows<1>, grid, block, 0, s, src + r0 * K, n, K, codes + r0 * K,
+                         scales + r0, order_key());
+    else
+      hipLaunchKernelGGL(quant_int8_rows<2>, grid, block, 0, s, src + r0 * K, n, K, codes + r0 * K,
+                         scales + r0, order_key());
+  }
   prof_end(kQuant, s);
   return hipGetLastError();
 }

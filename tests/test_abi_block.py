@@ -21,7 +21,8 @@ def _norm(m, x=FAKE, r=None, w=FAKE, T=4, H=512, eps=1e-6, ro=None, y=FAKE, q=0,
 
 
 def test_norm_refusals(m):
-    assert _norm(m, T=-1) == m.MOE_ERR_SHAPE
+    for T in (-1, 1 << 22, 2 ** 31 - 1):
+        assert _norm(m, T=T) == m.MOE_ERR_SHAPE, T
     for H in (0, -32, 31, 48, 16384 + 32):
         assert _norm(m, H=H) == m.MOE_ERR_SHAPE, H
     for eps in (0.0, -1e-6, float("nan"), float("inf")):
@@ -48,7 +49,8 @@ def test_norm_backward_refusals(m):
     need = m.lib.moe_add_rmsnorm_backward_workspace_bytes(4, 512)
     assert need >= 4 * 512 * 4
     assert m.lib.moe_add_rmsnorm_backward_workspace_bytes(-1, 512) == 0
-    assert call(T=-1, n=1 << 20) == m.MOE_ERR_SHAPE
+    for T in (-1, 1 << 22, 2 ** 31 - 1):
+        assert call(T=T, n=1 << 40) == m.MOE_ERR_SHAPE, T
     assert call(H=40) == m.MOE_ERR_SHAPE
     assert call(eps=0.0) == m.MOE_ERR_SHAPE
     for bad in (dict(s=None), dict(w=None), dict(dy=None), dict(dx=None), dict(dw=None)):
@@ -64,7 +66,7 @@ def _route(m, l=FAKE, b=None, T=4, E=32, k=4, G=1, tg=1, gt=1, score=0, rn=1, sc
 
 
 def test_route_scored_refusals(m):
-    for bad in (dict(T=-1), dict(E=0), dict(E=1025), dict(k=0), dict(k=33, E=64), dict(k=5, E=4),
+    for bad in (dict(T=-1), dict(T=1 << 22), dict(T=2 ** 31 - 1), dict(E=0), dict(E=1025), dict(k=0), dict(k=33, E=64), dict(k=5, E=4),
                 dict(G=0), dict(G=5), dict(G=128, E=1024), dict(G=4, tg=0), dict(G=4, tg=5),
                 dict(gt=0), dict(gt=3), dict(G=8, tg=1, k=5), dict(score=2), dict(score=-1),
                 dict(sc=float("nan")), dict(sc=float("inf"))):
@@ -79,7 +81,7 @@ def test_route_scored_refusals(m):
 def test_route_scored_backward_refusals(m):
     def call(l=FAKE, i=FAKE, d=FAKE, T=4, E=32, k=4, score=1, sc=1.0, o=FAKE):
         return m.lib.moe_route_scored_backward(l, i, d, T, E, k, score, 1, sc, o, None)
-    for bad in (dict(T=-1), dict(E=1025), dict(k=0), dict(k=33), dict(score=7), dict(sc=float("inf"))):
+    for bad in (dict(T=-1), dict(T=1 << 22), dict(T=2 ** 31 - 1), dict(E=1025), dict(k=0), dict(k=33), dict(score=7), dict(sc=float("inf"))):
         assert call(**bad) == m.MOE_ERR_SHAPE, bad
     for bad in (dict(l=None), dict(i=None), dict(d=None), dict(o=None)):
         assert call(**bad) == m.MOE_ERR_NULL, bad

@@ -248,3 +248,21 @@ def test_norm_on_a_side_stream(M):
     side.synchronize()
     for a, b in zip(ref, got):
         assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
+def test_most_rows(M):
+    """The most rows a call takes (and, for the codes, one launch's worth and more): the last
+    rows, some in the middle and the first as a small call gives them."""
+    T, H = (1 << 22) - 1, 32
+    x = torch.randn(T + 6, H, device="cuda").bfloat16()
+    w = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    c, s = M.moe_quantize_int8(x)
+    y = M.moe_add_rmsnorm(x[:T], w, EPS)[1]
+    for a in (0, 1 << 21, (1 << 22) - 8, T - 2):
+        c1, s1 = M.moe_quantize_int8(x[a:a + 8].clone())
+        assert torch.equal(c[a:a + 8], c1) and torch.equal(s[a:a + 8], s1)
+        a = min(a, T - 8)
+        assert torch.equal(y[a:a + 8], M.moe_add_rmsnorm(x[a:a + 8].clone(), w, EPS)[1])
+    dx = M.moe_add_rmsnorm_backward(x[:T], w, y, EPS)[0]
+    a = T - 8
+    assert torch.equal(dx[a:], M.moe_add_rmsnorm_backward(x[a:T].clone(), w, y[a:].clone(), EPS)[0])

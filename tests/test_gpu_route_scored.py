@@ -291,3 +291,16 @@ def test_route_scored_backward_of_low_logits(M):
     full = torch.zeros(32, 96, dtype=torch.float64).scatter(1, sel, d.double())
     size = full.abs() + (torch.gather(p, 1, sel) * d.abs()).sum(1, keepdim=True)   # (the terms' magnitudes)
     assert ((got - p * (full - mean)).abs() <= 2 * REL * p * size + 1e-37).all()
+
+
+def test_route_scored_most_tokens(M):
+    T, E, k = (1 << 22) - 1, 4, 2
+    l = torch.randn(T, E, device="cuda")
+    idx, w = M.moe_route_scored(l, k)
+    d = torch.randn(T, k, device="cuda")
+    g = M.moe_route_scored_backward(l, idx, d)
+    for a in (0, 1 << 21, T - 9):
+        n = lambda t: t[a:a + 9].clone()  # noqa: E731
+        i1, w1 = M.moe_route_scored(n(l), k)
+        assert torch.equal(n(idx), i1) and torch.equal(n(w), w1)
+        assert torch.equal(n(g), M.moe_route_scored_backward(n(l), i1, n(d)))
