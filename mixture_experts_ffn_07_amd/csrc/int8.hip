@@ -821,7 +821,7 @@ __device__ __forceinline__ int rows_dot(const uint8_t* wrow, const uint8_t* x, i
   }
   return sum8(acc);
 }
-constexpr int kPairsMax = 128;                           // pairs up to which this form may be taken
+constexpr int kPairsMax = 48;                            // pairs up to which this form may be taken
 constexpr size_t kPairsLds = 64 << 10;                   // LDS that a kernel may use without an attribute
 constexpr int kPairCols = 8;                             // output columns per workgroup of the down pass
 constexpr int kPairWaves = 8;
@@ -830,9 +830,12 @@ inline size_t pairs_lds(int P, int I) {
 }
 // Taken while the weights that it reads more than once (pairs that share an expert;
 // expected number of distinct experts E (1 - (1 - k/E)^T)) stay below 120 MB: about
-// the 20 us that grouping and its launches cost the other form.  Measured, us (this /
-// grouped): H 2048 I 768 E 128 k 8, T 1 13.5 / 38, T 8 60 / 68, T 12 85 / 78; H 7168 I
-// 2048 E 32 k 4, T 2 71 / 92, T 4 124 / 119; H 2048 I 1024 E 8 k 2, T 12 25 / 38.
+// the 20 us that grouping and its launches cost the other form; and for 48 pairs at
+// most, which a wave of the down pass takes eight apart, one after the other.  Measured,
+// us (this / grouped): H 2048 I 768 E 128 k 8, T 1 13.8 / 27.4, T 8 (64 pairs) 60 / 61,
+// T 12 86 / 70; H 7168 I 2048 E 32 k 4, T 2 71 / 70, T 4 (122 MB) 124 / 106; H 2048 I 1024
+// E 8 k 2, T 12 (102 MB) 25 / 30; H 1024 I 512 E 8 k 2, T 20 18.5 / 23.5, T 30 (60 pairs)
+// 25.0 / 23.4; H 768 I 512 E 64 k 8, T 12 (96 pairs) 44 / 27.
 inline bool use_pairs(int T, int H, int I, int E, int k) {
   const int64_t P = static_cast<int64_t>(T) * k;
   if (P > kPairsMax || pairs_lds(static_cast<int>(P), I) > kPairsLds) return false;
