@@ -505,11 +505,13 @@ def moe_add_rmsnorm_backward_workspace_bytes(T: int, H: int) -> int:
 
 
 def _ws_arg(ws, nbytes: int, dev):
-    """(pointer, bytes) of the workspace: the caller's, or a new one of nbytes."""
+    """(workspace, pointer, bytes): the caller's workspace, or a new one of nbytes.  Who calls
+    holds the tensor until the kernels are enqueued: dropped before, its memory could be given
+    to work of another thread that is enqueued ahead of them, or be unmapped."""
     if ws is None:
         ws = workspace(nbytes, dev)
     _need_ws(ws, nbytes)
-    return _arg(ws, "workspace", ws.shape, torch.uint8, dev), ws.numel()
+    return ws, _arg(ws, "workspace", ws.shape, torch.uint8, dev), ws.numel()
 
 
 def moe_add_rmsnorm_backward(s, weight, dy, eps: float, ds=None, dx=None, dweight=None, ws=None,
@@ -526,7 +528,7 @@ def moe_add_rmsnorm_backward(s, weight, dy, eps: float, ds=None, dx=None, dweigh
     ptrs = (_arg(s, "s", shape, _BF16, dev), _arg(weight, "weight", (H,), _BF16, dev),
             _arg(dy, "dy", shape, _BF16, dev), _arg(ds, "ds", shape, _BF16, dev))
     outs = _arg(dx, "dx", shape, _BF16, dev), _arg(dweight, "dweight", (H,), _BF16, dev)
-    pws, n = _ws_arg(ws, moe_add_rmsnorm_backward_workspace_bytes(T, H), dev)
+    ws, pws, n = _ws_arg(ws, moe_add_rmsnorm_backward_workspace_bytes(T, H), dev)
     _enqueue("moe_add_rmsnorm_backward", dev, stream, *ptrs, T, H, eps, *outs, pws, n)
     return dx, dweight
 
@@ -609,7 +611,7 @@ def moe_experts_int8(x, x_scales, w_gate_up, w_gate_up_scales, w_down, w_down_sc
             _arg(topk_idx, "topk_idx", (T, k), torch.int32, dev),
             _arg(topk_w, "topk_w", (T, k), f32, dev))
     pout = _arg(out, "out", (T, H), _BF16, dev)
-    pws, n = _ws_arg(ws, moe_experts_int8_workspace_bytes(T, H, I, E, k), dev)
+    ws, pws, n = _ws_arg(ws, moe_experts_int8_workspace_bytes(T, H, I, E, k), dev)
     _enqueue("moe_experts_int8", dev, stream, *ptrs, T, H, I, E, k, pout, pws, n)
     return out
 
