@@ -422,6 +422,11 @@ def moe_backward_batched_mxfp8(x, w_gate_up, w_gate_up_scales, w_down, w_down_sc
 # The calls below check each tensor once (a 20-microsecond step is a handful of them: the
 # checks and the stream look-up of the calls above cost about 5 us of host time a call,
 # these about 2).
+#
+# Streams: a call runs on `stream`, a torch stream or a raw hipStream_t (None: the current
+# one).  What it allocates itself, outputs and workspace, belongs to that stream.  Tensors
+# that it is given stay the caller's matter: they have to be ready on that stream, and to
+# live, or to be recorded on it, until its work has ended.
 
 def _arg(t, name: str, shape, dtypes, dev) -> Optional[int]:
     """The device pointer of a tensor argument, after checking its element type, shape,
@@ -444,6 +449,33 @@ def _gpu(t: torch.Tensor, dims: int, name: str):
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions, not {t.dim()}")
     return t.device
+
+
+def _home(stream, dev):
+    """The stream that owns what a call allocates: None for the current one, else the given
+    one.  (Memory of the current stream could hold a tensor that its pending work still uses
+    when the call's kernels start, and a workspace, once dropped, would go to the current
+    stream's next tensor while they still run.)"""
+    if stream is None or dev.type != "cuda":
+        return None
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+    if handle == torch._C._cuda_getCurrentRawStream(dev.index):
+        return None
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+
+
+def _new(shape, dtype, dev, home) -> torch.Tensor:
+    """Memory for an output.  One that belongs to another stream than the current one is known
+    to the allocator as used on both: the caller may read it here, after the wait that this
+    takes, and drop it."""
+    if home is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(home):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    t.record_stream(torch.cuda.current_stream(dev))
+    return t
 
 
 def _enqueue(name: str, dev, stream, *args) -> None:
@@ -472,15 +504,16 @@ def moe_add_rmsnorm(x, weight, eps: float, residual=None, residual_out=None, y=N
     buffer for it is given.  residual_out is allocated when a residual is given without it,
     and None without a residual."""
     dev = _gpu(x, 2, "x")
+    home = _home(stream, dev)
     shape = T, H = x.shape
     px = _arg(x, "x", shape, _BF16, dev)
     pw = _arg(weight, "weight", (H,), _BF16, dev)
     pr = _arg(residual, "residual", shape, _BF16, dev)
     if residual_out is None and residual is not None:
-        residual_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        residual_out = _new(shape, torch.bfloat16, dev, home)
     ps = _arg(residual_out, "residual_out", shape, _BF16, dev)
     if y is None and qtype == MOE_BF16:
-        y = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        y = _new(shape, torch.bfloat16, dev, home)
     py = _arg(y, "y", shape, _BF16, dev)
     pc = pq = None
     if qtype == MOE_BF16:
@@ -491,9 +524,9 @@ def moe_add_rmsnorm(x, weight, eps: float, residual=None, residual_out=None, y=N
         else:
             cdt, sdt, sshape = torch.int8, torch.float32, (T,)
         if codes is None:
-            codes = torch.empty(shape, dtype=cdt, device=dev)
+            codes = _new(shape, cdt, dev, home)
         if scales is None:
-            scales = torch.empty(sshape, dtype=sdt, device=dev)
+            scales = _new(sshape, sdt, dev, home)
         pc = _arg(codes, "codes", shape, cdt, dev)
         pq = _arg(scales, "scales", sshape, sdt, dev)
     _enqueue("moe_add_rmsnorm", dev, stream, px, pr, pw, T, H, eps, ps, py, qtype, pc, pq)
@@ -504,12 +537,16 @@ def moe_add_rmsnorm_backward_workspace_bytes(T: int, H: int) -> int:
     return int(lib.moe_add_rmsnorm_backward_workspace_bytes(T, H))
 
 
-def _ws_arg(ws, nbytes: int, dev):
+def _ws_arg(ws, nbytes: int, dev, home):
     """(workspace, pointer, bytes): the caller's workspace, or a new one of nbytes.  Who calls
     holds the tensor until the kernels are enqueued: dropped before, its memory could be given
     to work of another thread that is enqueued ahead of them, or be unmapped."""
     if ws is None:
-        ws = workspace(nbytes, dev)
+        if home is None:
+            ws = workspace(nbytes, dev)
+        else:
+            with torch.cuda.stream(home):
+                ws = workspace(nbytes, dev)
     _need_ws(ws, nbytes)
     return ws, _arg(ws, "workspace", ws.shape, torch.uint8, dev), ws.numel()
 
@@ -520,15 +557,16 @@ def moe_add_rmsnorm_backward(s, weight, dy, eps: float, ds=None, dx=None, dweigh
     gradient that reaches s from elsewhere.  Returns (dx, dweight); dx is the gradient of x
     and of the residual."""
     dev = _gpu(s, 2, "s")
+    home = _home(stream, dev)
     shape = T, H = s.shape
     if dx is None:
-        dx = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        dx = _new(shape, torch.bfloat16, dev, home)
     if dweight is None:
-        dweight = torch.empty(H, dtype=torch.bfloat16, device=dev)
+        dweight = _new((H,), torch.bfloat16, dev, home)
     ptrs = (_arg(s, "s", shape, _BF16, dev), _arg(weight, "weight", (H,), _BF16, dev),
             _arg(dy, "dy", shape, _BF16, dev), _arg(ds, "ds", shape, _BF16, dev))
     outs = _arg(dx, "dx", shape, _BF16, dev), _arg(dweight, "dweight", (H,), _BF16, dev)
-    ws, pws, n = _ws_arg(ws, moe_add_rmsnorm_backward_workspace_bytes(T, H), dev)
+    ws, pws, n = _ws_arg(ws, moe_add_rmsnorm_backward_workspace_bytes(T, H), dev, home)
     _enqueue("moe_add_rmsnorm_backward", dev, stream, *ptrs, T, H, eps, *outs, pws, n)
     return dx, dweight
 
@@ -539,12 +577,13 @@ def moe_route_scored(logits, k: int, bias=None, score: int = MOE_SCORE_SOFTMAX, 
     """logits [T, E] float32 (-inf masks an expert), bias [E] float32 or None ->
     (topk_idx [T, k] int32, topk_w [T, k] float32)."""
     dev = _gpu(logits, 2, "logits")
+    home = _home(stream, dev)
     T, E = logits.shape
     shape = (T, max(k, 0))
     if topk_idx is None:
-        topk_idx = torch.empty(shape, dtype=torch.int32, device=dev)
+        topk_idx = _new(shape, torch.int32, dev, home)
     if topk_w is None:
-        topk_w = torch.empty(shape, dtype=torch.float32, device=dev)
+        topk_w = _new(shape, torch.float32, dev, home)
     _enqueue("moe_route_scored", dev, stream, _arg(logits, "logits", (T, E), torch.float32, dev),
              _arg(bias, "bias", (E,), torch.float32, dev), T, E, k, n_groups, topk_groups, group_top,
              score, 1 if renormalize else 0, scale,
@@ -558,11 +597,12 @@ def moe_route_scored_backward(logits, topk_idx, d_topk_w, score: int = MOE_SCORE
                               stream=None):
     """Gradient of moe_route_scored's weights (selection held fixed) -> dlogits [T, E] float32."""
     dev = _gpu(logits, 2, "logits")
+    home = _home(stream, dev)
     _gpu(topk_idx, 2, "topk_idx")
     T, E = logits.shape
     k = topk_idx.shape[1]
     if dlogits is None:
-        dlogits = torch.empty((T, E), dtype=torch.float32, device=dev)
+        dlogits = _new((T, E), torch.float32, dev, home)
     _enqueue("moe_route_scored_backward", dev, stream,
              _arg(logits, "logits", (T, E), torch.float32, dev),
              _arg(topk_idx, "topk_idx", (T, k), torch.int32, dev),
@@ -574,11 +614,12 @@ def moe_route_scored_backward(logits, topk_idx, d_topk_w, score: int = MOE_SCORE
 def moe_quantize_int8(src, codes=None, scales=None, stream=None):
     """src [rows, K] BF16 -> (codes [rows, K] int8, scales [rows] float32)."""
     dev = _gpu(src, 2, "src")
+    home = _home(stream, dev)
     rows, K = src.shape
     if codes is None:
-        codes = torch.empty((rows, K), dtype=torch.int8, device=dev)
+        codes = _new((rows, K), torch.int8, dev, home)
     if scales is None:
-        scales = torch.empty(rows, dtype=torch.float32, device=dev)
+        scales = _new((rows,), torch.float32, dev, home)
     _enqueue("moe_quantize_int8", dev, stream, _arg(src, "src", (rows, K), _BF16, dev), rows, K,
              _arg(codes, "codes", (rows, K), torch.int8, dev),
              _arg(scales, "scales", (rows,), torch.float32, dev))
@@ -594,6 +635,7 @@ def moe_experts_int8(x, x_scales, w_gate_up, w_gate_up_scales, w_down, w_down_sc
     """The routed experts' FFN in INT8 (codes with per-token and per-channel scales) -> out
     [T, H] BF16.  Slots whose expert id lies outside [0, E) add nothing."""
     dev = _gpu(x, 2, "x")
+    home = _home(stream, dev)
     _gpu(w_gate_up, 3, "w_gate_up")
     _gpu(topk_idx, 2, "topk_idx")
     T, H = x.shape
@@ -601,7 +643,7 @@ def moe_experts_int8(x, x_scales, w_gate_up, w_gate_up_scales, w_down, w_down_sc
     I = I2 // 2
     k = topk_idx.shape[1]
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        out = _new((T, H), torch.bfloat16, dev, home)
     i8, f32 = torch.int8, torch.float32
     ptrs = (_arg(x, "x", (T, H), i8, dev), _arg(x_scales, "x_scales", (T,), f32, dev),
             _arg(w_gate_up, "w_gate_up", (E, 2 * I, H), i8, dev),
@@ -611,7 +653,7 @@ def moe_experts_int8(x, x_scales, w_gate_up, w_gate_up_scales, w_down, w_down_sc
             _arg(topk_idx, "topk_idx", (T, k), torch.int32, dev),
             _arg(topk_w, "topk_w", (T, k), f32, dev))
     pout = _arg(out, "out", (T, H), _BF16, dev)
-    ws, pws, n = _ws_arg(ws, moe_experts_int8_workspace_bytes(T, H, I, E, k), dev)
+    ws, pws, n = _ws_arg(ws, moe_experts_int8_workspace_bytes(T, H, I, E, k), dev, home)
     _enqueue("moe_experts_int8", dev, stream, *ptrs, T, H, I, E, k, pout, pws, n)
     return out
 
