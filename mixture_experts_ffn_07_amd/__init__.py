@@ -138,6 +138,55 @@ def _need_ws(ws: torch.Tensor, nbytes: int) -> None:
         raise ValueError(f"workspace holds {ws.numel()} bytes, {nbytes} required")
 
 
+def workspace(nbytes: int, device="cuda") -> torch.Tensor:
+    """A device buffer for the workspace argument (256-byte aligned by torch)."""
+    return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
+
+
+# Streams: a call runs on `stream`, a torch stream or a raw hipStream_t (None: the current
+# one).  What it allocates itself, outputs and workspace, belongs to that stream.  Tensors
+# that it is given stay the caller's matter: they have to be ready on that stream, and to
+# live, or to be recorded on it, until its work has ended.
+def _home(stream, dev):
+    """The stream that owns what a call allocates: None for the current one, else the given
+    one.  (Memory of the current stream could hold a tensor that its pending work still uses
+    when the call's kernels start, and a workspace, once dropped, would go to the current
+    stream's next tensor while they still run.)"""
+    if stream is None or dev.type != "cuda":
+        return None
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+    if handle == torch._C._cuda_getCurrentRawStream(dev.index):
+        return None
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
+
+
+def _make(make, dev, stream) -> torch.Tensor:
+    """make() as memory of a call on `stream`.  A tensor that belongs to another stream than
+    the current one is known to the allocator as used on both: the caller may read it here,
+    after the wait that this takes, and drop it."""
+    home = _home(stream, dev)
+    if home is None:
+        return make()
+    with torch.cuda.stream(home):
+        t = make()
+    t.record_stream(torch.cuda.current_stream(dev))
+    return t
+
+
+def _new(shape, dtype, dev, stream) -> torch.Tensor:
+    """Memory for an output of a call on `stream`."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    return _make(lambda: torch.empty(shape, dtype=dtype, device=dev), dev, stream)
+
+
+def _new_ws(nbytes: int, dev, stream) -> torch.Tensor:
+    """A workspace for a call on `stream` (the gate/up calls return theirs)."""
+    return _make(lambda: workspace(nbytes, dev), dev, stream)
+
+
 def moe_route_topk(logits: torch.Tensor, k: int, topk_idx: torch.Tensor = None,
                    topk_w: torch.Tensor = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """logits [T, E] float32 -> (topk_idx [T, k] int32, topk_w [T, k] float32)."""
@@ -147,9 +196,9 @@ def moe_route_topk(logits: torch.Tensor, k: int, topk_idx: torch.Tensor = None,
     if logits.dtype != torch.float32:
         raise TypeError("logits must be float32")
     if topk_idx is None:
-        topk_idx = torch.empty(T, k, dtype=torch.int32, device=logits.device)
+        topk_idx = _new((T, k), torch.int32, logits.device, stream)
     if topk_w is None:
-        topk_w = torch.empty(T, k, dtype=torch.float32, device=logits.device)
+        topk_w = _new((T, k), torch.float32, logits.device, stream)
     _need(topk_idx, "topk_idx", (T, k), torch.int32)
     _need(topk_w, "topk_w", (T, k), torch.float32)
     _check("moe_route_topk", lib.moe_route_topk(_ptr(logits), T, E, k, _ptr(topk_idx),
@@ -165,11 +214,6 @@ def moe_workspace_bytes(T: int, H: int, I: int, E: int, k: int, dtype: int) -> i
     return int(lib.moe_workspace_bytes(T, H, I, E, k, dtype))
 
 
-def workspace(nbytes: int, device="cuda") -> torch.Tensor:
-    """A device buffer for the workspace argument (256-byte aligned by torch)."""
-    return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
-
-
 def moe_decode_forward(x: torch.Tensor, logits: torch.Tensor, w_gate_up: torch.Tensor,
                        w_down: torch.Tensor, k: int, out: torch.Tensor = None,
                        topk_idx: torch.Tensor = None, topk_w: torch.Tensor = None,
@@ -183,13 +227,13 @@ def moe_decode_forward(x: torch.Tensor, logits: torch.Tensor, w_gate_up: torch.T
     _u16(x), _u16(w_gate_up), _u16(w_down)
     _need(logits, "logits", (T, E), torch.float32)
     if out is None:
-        out = torch.empty(T, H, dtype=torch.bfloat16, device=x.device)
+        out = _new((T, H), torch.bfloat16, x.device, stream)
     _need(out, "out", (T, H), _BF16)
     _need(topk_idx, "topk_idx", (T, k), torch.int32, optional=True)
     _need(topk_w, "topk_w", (T, k), torch.float32, optional=True)
     need = moe_decode_workspace_bytes(T, H, I, E, k)
     if ws is None:
-        ws = workspace(need, x.device)
+        ws = _new_ws(need, x.device, stream)
     _need_ws(ws, need)
     _check("moe_decode_forward", lib.moe_decode_forward(
         _ptr(x), _ptr(logits), _ptr(w_gate_up), _ptr(w_down), T, H, I, E, k, _ptr(out),
@@ -228,9 +272,9 @@ def moe_quantize_mxfp8(src: torch.Tensor, codes: torch.Tensor = None, scales: to
     rows, K = src.shape
     _u16(src)
     if codes is None:
-        codes = torch.empty(rows, K, dtype=torch.uint8, device=src.device)
+        codes = _new((rows, K), torch.uint8, src.device, stream)
     if scales is None:
-        scales = torch.empty(rows, K // 32, dtype=torch.uint8, device=src.device)
+        scales = _new((rows, K // 32), torch.uint8, src.device, stream)
     _need(codes, "codes", (rows, K), torch.uint8)
     _need(scales, "scales", (rows, K // 32), torch.uint8)
     _check("moe_quantize_mxfp8", lib.moe_quantize_mxfp8(_ptr(src), rows, K, _ptr(codes),
@@ -255,16 +299,15 @@ def moe_gate_up_3d_batched(x, w_gate_up, topk_idx, k: int, dtype: int = MOE_BF16
         _need(x_scales, "x_scales", (T, H // 32), torch.uint8)
         _need(w_gate_up_scales, "w_gate_up_scales", (E, I2, H // 32), torch.uint8)
     if h is None:
-        h = torch.empty(T * k, I, dtype=torch.bfloat16 if dtype == MOE_BF16 else torch.uint8,
-                        device=x.device)
+        h = _new((T * k, I), torch.bfloat16 if dtype == MOE_BF16 else torch.uint8, x.device, stream)
     if mx and h_scales is None:
-        h_scales = torch.empty(T * k, I // 32, dtype=torch.uint8, device=x.device)
+        h_scales = _new((T * k, I // 32), torch.uint8, x.device, stream)
     _need(h, "h", (T * k, I), edt)
     if mx:
         _need(h_scales, "h_scales", (T * k, I // 32), torch.uint8)
     need = moe_workspace_bytes(T, H, I, E, k, dtype)
     if ws is None:
-        ws = workspace(need, x.device)
+        ws = _new_ws(need, x.device, stream)
     _need_ws(ws, need)
     _check("moe_gate_up_3d_batched", lib.moe_gate_up_3d_batched(
         _ptr(x), _ptr(x_scales), _ptr(w_gate_up), _ptr(w_gate_up_scales), _ptr(topk_idx),
@@ -287,7 +330,7 @@ def moe_down_3d_batched(h, w_down, topk_idx, topk_w, ws, k: int, dtype: int = MO
         _need(h_scales, "h_scales", (T * k, I // 32), torch.uint8)
         _need(w_down_scales, "w_down_scales", (E, H, I // 32), torch.uint8)
     if out is None:
-        out = torch.empty(T, H, dtype=torch.bfloat16, device=h.device)
+        out = _new((T, H), torch.bfloat16, h.device, stream)
     _need(out, "out", (T, H), _BF16)
     _need_ws(ws, moe_workspace_bytes(T, H, I, E, k, dtype))
     _check("moe_down_3d_batched", lib.moe_down_3d_batched(
@@ -311,14 +354,14 @@ def moe_gate_up_3d_batched_train(x, w_gate_up, topk_idx, k: int, h=None, gu=None
     _need(w_gate_up, "w_gate_up", (E, I2, H), _BF16)
     _need(topk_idx, "topk_idx", (T, k), torch.int32)
     if h is None:
-        h = torch.empty(T * k, I, dtype=torch.bfloat16, device=x.device)
+        h = _new((T * k, I), torch.bfloat16, x.device, stream)
     if gu is None:
-        gu = torch.empty(T * k, I2, dtype=torch.float32, device=x.device)
+        gu = _new((T * k, I2), torch.float32, x.device, stream)
     _need(h, "h", (T * k, I), _BF16)
     _need(gu, "gu", (T * k, I2), torch.float32)
     need = moe_workspace_bytes(T, H, I, E, k, MOE_BF16)
     if ws is None:
-        ws = workspace(need, x.device)
+        ws = _new_ws(need, x.device, stream)
     _need_ws(ws, need)
     _check("moe_gate_up_3d_batched_train", lib.moe_gate_up_3d_batched_train(
         _ptr(x), _ptr(w_gate_up), _ptr(topk_idx), T, H, I, E, k, _ptr(h), _ptr(gu), _ptr(ws),
@@ -342,15 +385,15 @@ def moe_backward_batched(x, w_gate_up, w_down, topk_idx, topk_w, dout, k: int, g
     _need(dout, "dout", (T, H), _BF16)
     _need(gu_saved, "gu_saved", (T * k, I2), torch.float32, optional=True)
     if dx is None:
-        dx = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+        dx = _new((T, H), torch.bfloat16, dev, stream)
     if dw_gate_up is None:
-        dw_gate_up = torch.empty(E, I2, H, dtype=torch.bfloat16, device=dev)
+        dw_gate_up = _new((E, I2, H), torch.bfloat16, dev, stream)
     if dw_down is None:
-        dw_down = torch.empty(E, H, I, dtype=torch.bfloat16, device=dev)
+        dw_down = _new((E, H, I), torch.bfloat16, dev, stream)
     if d_topk_w is None:
-        d_topk_w = torch.empty(T, k, dtype=torch.float32, device=dev)
+        d_topk_w = _new((T, k), torch.float32, dev, stream)
     if dlogits is None:
-        dlogits = torch.empty(T, E, dtype=torch.float32, device=dev)
+        dlogits = _new((T, E), torch.float32, dev, stream)
     _need(dx, "dx", (T, H), _BF16)
     _need(dw_gate_up, "dw_gate_up", (E, I2, H), _BF16)
     _need(dw_down, "dw_down", (E, H, I), _BF16)
@@ -358,7 +401,7 @@ def moe_backward_batched(x, w_gate_up, w_down, topk_idx, topk_w, dout, k: int, g
     _need(dlogits, "dlogits", (T, E), torch.float32)
     need = moe_backward_workspace_bytes(T, H, I, E, k)
     if ws is None:
-        ws = workspace(need, dev)
+        ws = _new_ws(need, dev, stream)
     _need_ws(ws, need)
     _check("moe_backward_batched", lib.moe_backward_batched(
         _ptr(x), _ptr(w_gate_up), _ptr(w_down), _ptr(topk_idx), _ptr(topk_w), _ptr(dout),
@@ -394,15 +437,15 @@ def moe_backward_batched_mxfp8(x, w_gate_up, w_gate_up_scales, w_down, w_down_sc
     _need(topk_w, "topk_w", (T, k), torch.float32)
     _need(dout, "dout", (T, H), _BF16)
     if dx is None:
-        dx = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+        dx = _new((T, H), torch.bfloat16, dev, stream)
     if dw_gate_up is None:
-        dw_gate_up = torch.empty(E, I2, H, dtype=torch.bfloat16, device=dev)
+        dw_gate_up = _new((E, I2, H), torch.bfloat16, dev, stream)
     if dw_down is None:
-        dw_down = torch.empty(E, H, I, dtype=torch.bfloat16, device=dev)
+        dw_down = _new((E, H, I), torch.bfloat16, dev, stream)
     if d_topk_w is None:
-        d_topk_w = torch.empty(T, k, dtype=torch.float32, device=dev)
+        d_topk_w = _new((T, k), torch.float32, dev, stream)
     if dlogits is None:
-        dlogits = torch.empty(T, E, dtype=torch.float32, device=dev)
+        dlogits = _new((T, E), torch.float32, dev, stream)
     _need(dx, "dx", (T, H), _BF16)
     _need(dw_gate_up, "dw_gate_up", (E, I2, H), _BF16)
     _need(dw_down, "dw_down", (E, H, I), _BF16)
@@ -410,7 +453,7 @@ def moe_backward_batched_mxfp8(x, w_gate_up, w_gate_up_scales, w_down, w_down_sc
     _need(dlogits, "dlogits", (T, E), torch.float32)
     need = moe_backward_mxfp8_workspace_bytes(T, H, I, E, k)
     if ws is None:
-        ws = workspace(need, dev)
+        ws = _new_ws(need, dev, stream)
     _need_ws(ws, need)
     _check("moe_backward_batched_mxfp8", lib.moe_backward_batched_mxfp8(
         _ptr(x), _ptr(w_gate_up), _ptr(w_gate_up_scales), _ptr(w_down), _ptr(w_down_scales),
@@ -422,11 +465,6 @@ def moe_backward_batched_mxfp8(x, w_gate_up, w_gate_up_scales, w_down, w_down_sc
 # The calls below check each tensor once (a 20-microsecond step is a handful of them: the
 # checks and the stream look-up of the calls above cost about 5 us of host time a call,
 # these about 2).
-#
-# Streams: a call runs on `stream`, a torch stream or a raw hipStream_t (None: the current
-# one).  What it allocates itself, outputs and workspace, belongs to that stream.  Tensors
-# that it is given stay the caller's matter: they have to be ready on that stream, and to
-# live, or to be recorded on it, until its work has ended.
 
 def _arg(t, name: str, shape, dtypes, dev) -> Optional[int]:
     """The device pointer of a tensor argument, after checking its element type, shape,
@@ -449,33 +487,6 @@ def _gpu(t: torch.Tensor, dims: int, name: str):
     if t.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions, not {t.dim()}")
     return t.device
-
-
-def _home(stream, dev):
-    """The stream that owns what a call allocates: None for the current one, else the given
-    one.  (Memory of the current stream could hold a tensor that its pending work still uses
-    when the call's kernels start, and a workspace, once dropped, would go to the current
-    stream's next tensor while they still run.)"""
-    if stream is None or dev.type != "cuda":
-        return None
-    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
-    if handle == torch._C._cuda_getCurrentRawStream(dev.index):
-        return None
-    if isinstance(stream, torch.cuda.Stream):
-        return stream
-    return torch.cuda.ExternalStream(handle, device=dev) if handle else torch.cuda.default_stream(dev)
-
-
-def _new(shape, dtype, dev, home) -> torch.Tensor:
-    """Memory for an output.  One that belongs to another stream than the current one is known
-    to the allocator as used on both: the caller may read it here, after the wait that this
-    takes, and drop it."""
-    if home is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    with torch.cuda.stream(home):
-        t = torch.empty(shape, dtype=dtype, device=dev)
-    t.record_stream(torch.cuda.current_stream(dev))
-    return t
 
 
 def _enqueue(name: str, dev, stream, *args) -> None:
@@ -504,16 +515,15 @@ def moe_add_rmsnorm(x, weight, eps: float, residual=None, residual_out=None, y=N
     buffer for it is given.  residual_out is allocated when a residual is given without it,
     and None without a residual."""
     dev = _gpu(x, 2, "x")
-    home = _home(stream, dev)
     shape = T, H = x.shape
     px = _arg(x, "x", shape, _BF16, dev)
     pw = _arg(weight, "weight", (H,), _BF16, dev)
     pr = _arg(residual, "residual", shape, _BF16, dev)
     if residual_out is None and residual is not None:
-        residual_out = _new(shape, torch.bfloat16, dev, home)
+        residual_out = _new(shape, torch.bfloat16, dev, stream)
     ps = _arg(residual_out, "residual_out", shape, _BF16, dev)
     if y is None and qtype == MOE_BF16:
-        y = _new(shape, torch.bfloat16, dev, home)
+        y = _new(shape, torch.bfloat16, dev, stream)
     py = _arg(y, "y", shape, _BF16, dev)
     pc = pq = None
     if qtype == MOE_BF16:
@@ -524,9 +534,9 @@ def moe_add_rmsnorm(x, weight, eps: float, residual=None, residual_out=None, y=N
         else:
             cdt, sdt, sshape = torch.int8, torch.float32, (T,)
         if codes is None:
-            codes = _new(shape, cdt, dev, home)
+            codes = _new(shape, cdt, dev, stream)
         if scales is None:
-            scales = _new(sshape, sdt, dev, home)
+            scales = _new(sshape, sdt, dev, stream)
         pc = _arg(codes, "codes", shape, cdt, dev)
         pq = _arg(scales, "scales", sshape, sdt, dev)
     _enqueue("moe_add_rmsnorm", dev, stream, px, pr, pw, T, H, eps, ps, py, qtype, pc, pq)
@@ -537,16 +547,12 @@ def moe_add_rmsnorm_backward_workspace_bytes(T: int, H: int) -> int:
     return int(lib.moe_add_rmsnorm_backward_workspace_bytes(T, H))
 
 
-def _ws_arg(ws, nbytes: int, dev, home):
+def _ws_arg(ws, nbytes: int, dev, stream):
     """(workspace, pointer, bytes): the caller's workspace, or a new one of nbytes.  Who calls
     holds the tensor until the kernels are enqueued: dropped before, its memory could be given
     to work of another thread that is enqueued ahead of them, or be unmapped."""
     if ws is None:
-        if home is None:
-            ws = workspace(nbytes, dev)
-        else:
-            with torch.cuda.stream(home):
-                ws = workspace(nbytes, dev)
+        ws = _new_ws(nbytes, dev, stream)
     _need_ws(ws, nbytes)
     return ws, _arg(ws, "workspace", ws.shape, torch.uint8, dev), ws.numel()
 
@@ -557,16 +563,15 @@ def moe_add_rmsnorm_backward(s, weight, dy, eps: float, ds=None, dx=None, dweigh
     gradient that reaches s from elsewhere.  Returns (dx, dweight); dx is the gradient of x
     and of the residual."""
     dev = _gpu(s, 2, "s")
-    home = _home(stream, dev)
     shape = T, H = s.shape
     if dx is None:
-        dx = _new(shape, torch.bfloat16, dev, home)
+        dx = _new(shape, torch.bfloat16, dev, stream)
     if dweight is None:
-        dweight = _new((H,), torch.bfloat16, dev, home)
+        dweight = _new((H,), torch.bfloat16, dev, stream)
     ptrs = (_arg(s, "s", shape, _BF16, dev), _arg(weight, "weight", (H,), _BF16, dev),
             _arg(dy, "dy", shape, _BF16, dev), _arg(ds, "ds", shape, _BF16, dev))
     outs = _arg(dx, "dx", shape, _BF16, dev), _arg(dweight, "dweight", (H,), _BF16, dev)
-    ws, pws, n = _ws_arg(ws, moe_add_rmsnorm_backward_workspace_bytes(T, H), dev, home)
+    ws, pws, n = _ws_arg(ws, moe_add_rmsnorm_backward_workspace_bytes(T, H), dev, stream)
     _enqueue("moe_add_rmsnorm_backward", dev, stream, *ptrs, T, H, eps, *outs, pws, n)
     return dx, dweight
 
@@ -577,13 +582,12 @@ def moe_route_scored(logits, k: int, bias=None, score: int = MOE_SCORE_SOFTMAX, 
     """logits [T, E] float32 (-inf masks an expert), bias [E] float32 or None ->
     (topk_idx [T, k] int32, topk_w [T, k] float32)."""
     dev = _gpu(logits, 2, "logits")
-    home = _home(stream, dev)
     T, E = logits.shape
     shape = (T, max(k, 0))
     if topk_idx is None:
-        topk_idx = _new(shape, torch.int32, dev, home)
+        topk_idx = _new(shape, torch.int32, dev, stream)
     if topk_w is None:
-        topk_w = _new(shape, torch.float32, dev, home)
+        topk_w = _new(shape, torch.float32, dev, stream)
     _enqueue("moe_route_scored", dev, stream, _arg(logits, "logits", (T, E), torch.float32, dev),
              _arg(bias, "bias", (E,), torch.float32, dev), T, E, k, n_groups, topk_groups, group_top,
              score, 1 if renormalize else 0, scale,
@@ -597,12 +601,11 @@ def moe_route_scored_backward(logits, topk_idx, d_topk_w, score: int = MOE_SCORE
                               stream=None):
     """Gradient of moe_route_scored's weights (selection held fixed) -> dlogits [T, E] float32."""
     dev = _gpu(logits, 2, "logits")
-    home = _home(stream, dev)
     _gpu(topk_idx, 2, "topk_idx")
     T, E = logits.shape
     k = topk_idx.shape[1]
     if dlogits is None:
-        dlogits = _new((T, E), torch.float32, dev, home)
+        dlogits = _new((T, E), torch.float32, dev, stream)
     _enqueue("moe_route_scored_backward", dev, stream,
              _arg(logits, "logits", (T, E), torch.float32, dev),
              _arg(topk_idx, "topk_idx", (T, k), torch.int32, dev),
@@ -614,12 +617,11 @@ def moe_route_scored_backward(logits, topk_idx, d_topk_w, score: int = MOE_SCORE
 def moe_quantize_int8(src, codes=None, scales=None, stream=None):
     """src [rows, K] BF16 -> (codes [rows, K] int8, scales [rows] float32)."""
     dev = _gpu(src, 2, "src")
-    home = _home(stream, dev)
     rows, K = src.shape
     if codes is None:
-        codes = _new((rows, K), torch.int8, dev, home)
+        codes = _new((rows, K), torch.int8, dev, stream)
     if scales is None:
-        scales = _new((rows,), torch.float32, dev, home)
+        scales = _new((rows,), torch.float32, dev, stream)
     _enqueue("moe_quantize_int8", dev, stream, _arg(src, "src", (rows, K), _BF16, dev), rows, K,
              _arg(codes, "codes", (rows, K), torch.int8, dev),
              _arg(scales, "scales", (rows,), torch.float32, dev))
@@ -635,7 +637,6 @@ def moe_experts_int8(x, x_scales, w_gate_up, w_gate_up_scales, w_down, w_down_sc
     """The routed experts' FFN in INT8 (codes with per-token and per-channel scales) -> out
     [T, H] BF16.  Slots whose expert id lies outside [0, E) add nothing."""
     dev = _gpu(x, 2, "x")
-    home = _home(stream, dev)
     _gpu(w_gate_up, 3, "w_gate_up")
     _gpu(topk_idx, 2, "topk_idx")
     T, H = x.shape
@@ -643,7 +644,7 @@ def moe_experts_int8(x, x_scales, w_gate_up, w_gate_up_scales, w_down, w_down_sc
     I = I2 // 2
     k = topk_idx.shape[1]
     if out is None:
-        out = _new((T, H), torch.bfloat16, dev, home)
+        out = _new((T, H), torch.bfloat16, dev, stream)
     i8, f32 = torch.int8, torch.float32
     ptrs = (_arg(x, "x", (T, H), i8, dev), _arg(x_scales, "x_scales", (T,), f32, dev),
             _arg(w_gate_up, "w_gate_up", (E, 2 * I, H), i8, dev),
@@ -653,7 +654,7 @@ def moe_experts_int8(x, x_scales, w_gate_up, w_gate_up_scales, w_down, w_down_sc
             _arg(topk_idx, "topk_idx", (T, k), torch.int32, dev),
             _arg(topk_w, "topk_w", (T, k), f32, dev))
     pout = _arg(out, "out", (T, H), _BF16, dev)
-    ws, pws, n = _ws_arg(ws, moe_experts_int8_workspace_bytes(T, H, I, E, k), dev, home)
+    ws, pws, n = _ws_arg(ws, moe_experts_int8_workspace_bytes(T, H, I, E, k), dev, stream)
     _enqueue("moe_experts_int8", dev, stream, *ptrs, T, H, I, E, k, pout, pws, n)
     return out
 

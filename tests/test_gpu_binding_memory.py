@@ -79,11 +79,67 @@ def _all_calls(M):
         "route": lambda st: M.moe_route_scored(l, 4, stream=st),
         "route backward": lambda st: (M.moe_route_scored_backward(l, idx, tw, stream=st),),
         "quantize int8": lambda st: M.moe_quantize_int8(x, stream=st),
-        "experts int8": lambda st: (M.moe_experts_int8(*i8, stream=st),)}
+        "experts int8": lambda st: (M.moe_experts_int8(*i8, stream=st),), **_layer_calls(M)}
 
 
-NAMES = ["norm", "norm mxfp8", "norm int8", "norm backward", "route", "route backward", "quantize int8",
-         "experts int8"]
+def _layer_calls(M):
+    """The same for the layer's own calls, BF16 and MXFP8."""
+    T, H, I, E, k = 48, 512, 256, 8, 2
+    g = torch.Generator(device="cuda").manual_seed(4)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    x, l, wg, wd, dout = r(T, H), r(T, E).float(), r(E, 2 * I, H) / 16, r(E, H, I) / 16, r(T, H)
+    idx, tw = M.moe_route_topk(l, k)
+    qx, qg, qd = M.moe_quantize_mxfp8(x), M.moe_quantize_mxfp8(wg.view(-1, H)), M.moe_quantize_mxfp8(wd.view(-1, I))
+    qg = qg[0].view(E, 2 * I, H), qg[1].view(E, 2 * I, H // 32)
+    qd = qd[0].view(E, H, I), qd[1].view(E, H, I // 32)
+
+    def batched(st):
+        h, _, ws = M.moe_gate_up_3d_batched(x, wg, idx, k, stream=st)
+        return h, M.moe_down_3d_batched(h, wd, idx, tw, ws, k, stream=st)
+
+    def batched_mx(st):
+        h, hs, ws = M.moe_gate_up_3d_batched(qx[0], qg[0], idx, k, M.MOE_MXFP8, x_scales=qx[1],
+                                             w_gate_up_scales=qg[1], stream=st)
+        return h, hs, M.moe_down_3d_batched(h, qd[0], idx, tw, ws, k, M.MOE_MXFP8, h_scales=hs,
+                                            w_down_scales=qd[1], stream=st)
+    return {
+        "topk": lambda st: M.moe_route_topk(l, k, stream=st),
+        "decode": lambda st: (M.moe_decode_forward(x, l, wg, wd, k, stream=st),),
+        "quantize mxfp8": lambda st: M.moe_quantize_mxfp8(x, stream=st),
+        "batched": batched, "batched mxfp8": batched_mx,
+        "train": lambda st: M.moe_gate_up_3d_batched_train(x, wg, idx, k, stream=st)[:2],
+        "backward": lambda st: M.moe_backward_batched(x, wg, wd, idx, tw, dout, k, stream=st),
+        "backward mxfp8": lambda st: M.moe_backward_batched_mxfp8(x, *qg, *qd, idx, tw, dout, k, stream=st)}
+
+
+NEW = ["norm", "norm mxfp8", "norm int8", "norm backward", "route", "route backward", "quantize int8", "experts int8"]
+LAYER = ["topk", "decode", "quantize mxfp8", "batched", "batched mxfp8", "train", "backward", "backward mxfp8"]
+NAMES = NEW + LAYER
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_what_a_call_makes_for_another_stream_is_not_of_the_current_one(M, monkeypatch, name):
+    """Everything a call on `side` allocates, outputs and workspaces, dropped: tensors of the
+    current stream lie elsewhere.  (Everything has ended by then: only the addresses count.)"""
+    call = _all_calls(M)[name]
+    call(None)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    got, make = [], torch.empty
+
+    def note(*a, **kw):
+        t = make(*a, **kw)
+        got.append((t.data_ptr(), t.numel() * t.element_size()))
+        return t
+    monkeypatch.setattr(torch, "empty", note)
+    call(side)
+    monkeypatch.undo()
+    torch.cuda.synchronize()
+    assert got
+    mine = [torch.empty(n, dtype=torch.uint8, device="cuda") for _, n in got * 3]
+    for p, n in got:
+        assert all(t.data_ptr() + t.numel() <= p or p + n <= t.data_ptr() for t in mine)
 
 
 @pytest.mark.parametrize("name", NAMES)
