@@ -943,7 +943,9 @@ __global__ __launch_bounds__(kPairWaves * kWave) void pairs_down(
     float o = 0.f;
     for (int j = 0; j < k; ++j) {
       const int p = t * k + j;
-      if (static_cast<unsigned>(idx[p]) < static_cast<unsigned>(E)) o = fmaf(w[p], val[p * kPairCols + c], o);
+      // (one slot: the weighted value itself, the sign of a zero included, as in the other forms)
+      if (static_cast<unsigned>(idx[p]) < static_cast<unsigned>(E))
+        o = k == 1 ? w[p] * val[p * kPairCols + c] : fmaf(w[p], val[p * kPairCols + c], o);
     }
     out[static_cast<size_t>(t) * H + n0 + c] = static_cast<uint16_t>(f32_to_bf16_rne(o));
   }

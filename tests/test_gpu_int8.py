@@ -227,3 +227,20 @@ def test_experts_int8_graph_replays(M, T, E, k, H, I):
         call(M, ds[0], ws=ws)
         _ = (outs[0].float() * 2).sum()
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("H,I,E", [(512, 256, 8), (4096, 1024, 4), (2048, 2048, 2)])
+def test_experts_int8_one_slot_zero_and_negative_weights(M, H, I, E):
+    """k = 1: a token's bits, the sign of a zero included, are the same in every form (weight 0
+    is what routing gives a masked expert that fills a slot)."""
+    print(f"[int8] one slot H={H} I={I} E={E}", flush=True)
+    d = make(2100, H, I, E, 1, seed=13)
+    d["w"][::3] = 0
+    d["w"][1::3] *= -1
+    full = call(M, d)
+    check(M, d, full)
+    zero = full[::3].view(torch.int16)
+    assert ((zero == 0) | (zero == -2 ** 15)).all() and (zero == 0).any() and (zero != 0).any()
+    for rows in (slice(0, 1), slice(3, 4), slice(5, 12), slice(0, 20), slice(0, 48), slice(100, 190), slice(0, 400)):
+        part = {n: (t[rows].clone() if n in ("x", "xs", "idx", "w") else t) for n, t in d.items()}
+        assert torch.equal(call(M, part).view(torch.int16), full[rows].view(torch.int16)), rows
