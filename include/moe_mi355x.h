@@ -403,7 +403,10 @@ size_t moe_add_rmsnorm_backward_workspace_bytes(int T, int H);
  *            Where no selected expert takes part the weights are 0.  Renormalised
  *            weights are ratios to the largest selected score: they hold however
  *            low the scores are.
- *   bias     [E] float32, or NULL; no NaN or +inf
+ *   bias     [E] float32, or NULL; no NaN or +inf.  -inf: the expert comes after all
+ *            others that take part and before the masked ones, and a group that
+ *            counts it among its group_top scores -inf, above a group with no expert
+ *            that takes part.
  *   topk_idx [T, k] int32 out, always within [0, E) and distinct within a row
  *   topk_w   [T, k] float32 out
  * Limits: 0 <= T < 2^22 (0 enqueues nothing), E <= 1024, 1 <= k <= 32, n_groups <= 64 and

@@ -147,60 +147,71 @@ constexpr int kOffKey = -0x7F7F0000;                     // order_of(-3.3895e38)
 constexpr int kMaskedKey = -0x7FC00000;
 constexpr int kNone = -0x7FFFFFFF - 1;
 
-__device__ __forceinline__ float lane_value(float v, int l) { return lane_of(v, l); }
-__device__ __forceinline__ double lane_value(double v, int l) { return __shfl(v, l, kWave); }
+__device__ __forceinline__ int lane_value(int v, int l) { return __builtin_amdgcn_readlane(v, l); }
+__device__ __forceinline__ uint64_t lane_value(uint64_t v, int l) { return __shfl(v, l, kWave); }
+
+// Scores as whole numbers of the same order, FP32 and FP64: below them all is kNoScore, the
+// place of an expert that does not take part (-inf is a score like others: a bias gives it).
+template <typename C> struct Ordered;
+template <> struct Ordered<float> {
+  typedef int Key;
+  static constexpr int kNoScore = kNone;
+  static __device__ __forceinline__ int key(float c) { return order_of(c); }
+  static __device__ __forceinline__ float value(int k) { return float_of(k); }
+};
+template <> struct Ordered<double> {
+  typedef uint64_t Key;
+  static constexpr uint64_t kNoScore = 0;
+  static __device__ __forceinline__ uint64_t key(double c) { return ordered_key64(c); }
+  static __device__ __forceinline__ double value(uint64_t k) {
+    return __longlong_as_double(static_cast<long long>(k >> 63 ? k & 0x7FFFFFFFFFFFFFFFull : ~k));
+  }
+};
 
 // Whether the group that this lane's candidates belong to takes part (C float or
 // double).  `close`: set where the FP32 scores do not decide it.
 template <int R, typename C>
 __device__ __forceinline__ bool group_taken(const RouteArgs& a, const Place& pl, const C (&c)[R],
                                             const bool (&on)[R], float tol, bool& close) {
+  typedef Ordered<C> O;
+  typedef typename O::Key Key;
   const int g = lane_id() / pl.span;
-  C b1 = -INFINITY, b2 = -INFINITY;                      // largest, second largest
-  if constexpr (sizeof(C) == 4) {
-    int k1 = kNone, k2 = kNone;
-    auto take = [&](int x) {
-      k2 = max(k2, min(k1, x));
-      k1 = max(k1, x);
-    };
-    auto merge = [&](int o1, int o2) {
-      k2 = max(max(k2, o2), min(k1, o1));
-      k1 = max(k1, o1);
-    };
+  Key k1 = O::kNoScore, k2 = O::kNoScore;                // largest, second largest
+  auto merge = [&](Key o1, Key o2) {
+    k2 = max(max(k2, o2), min(k1, o1));
+    k1 = max(k1, o1);
+  };
 #pragma unroll
-    for (int i = 0; i < R; ++i) take(on[i] ? order_of(c[i]) : kNone);
+  for (int i = 0; i < R; ++i) {
+    const Key x = on[i] ? O::key(c[i]) : O::kNoScore;
+    k2 = max(k2, min(k1, x));
+    k1 = max(k1, x);
+  }
+  if constexpr (sizeof(C) == 4) {
     if (pl.span >= 2) merge(dpp<0xB1>(k1), dpp<0xB1>(k2));
     if (pl.span >= 4) merge(dpp<0x4E>(k1), dpp<0x4E>(k2));
     if (pl.span >= 8) merge(dpp<0x141>(k1), dpp<0x141>(k2));
     if (pl.span >= 16) merge(dpp<0x140>(k1), dpp<0x140>(k2));
     if (pl.span >= 32) merge(__shfl_xor(k1, 16, kWave), __shfl_xor(k2, 16, kWave));
-    b1 = k1 == kNone ? -INFINITY : float_of(k1);
-    b2 = k2 == kNone ? -INFINITY : float_of(k2);
   } else {
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const C x = on[i] ? c[i] : static_cast<C>(-INFINITY);
-      b2 = max(b2, min(b1, x));
-      b1 = max(b1, x);
-    }
-    for (int s = 1; s < pl.span; s *= 2) {
-      const C o1 = __shfl_xor(b1, s, kWave), o2 = __shfl_xor(b2, s, kWave);
-      b2 = max(max(b2, o2), min(b1, o1));
-      b1 = max(b1, o1);
-    }
+    for (int s = 1; s < pl.span; s *= 2) merge(__shfl_xor(k1, s, kWave), __shfl_xor(k2, s, kWave));
   }
-  // a group with one expert that takes part scores that expert's c alone
-  C gs = a.group_top > 1 && b2 != -INFINITY ? b1 + b2 : b1;
+  // a group with one expert that takes part scores that expert's c alone; one without any
+  // comes after all others
+  const bool live = k1 != O::kNoScore;
+  C gs = O::value(k1);
+  if (a.group_top > 1 && k2 != O::kNoScore) gs += O::value(k2);
   gs += static_cast<C>(0);                               // -0 and +0 tie
+  const Key gk = live ? O::key(gs) : O::kNoScore;
   int rank = 0;
   for (int o = 0; o < a.groups; ++o) {
-    const C os = lane_value(gs, o * pl.span);
-    rank += os > gs || (os == gs && o < g) ? 1 : 0;
+    const Key ok = lane_value(gk, o * pl.span);
+    rank += ok > gk || (ok == gk && o < g) ? 1 : 0;
   }
   const bool taken = g < a.groups && rank < a.topk_groups;
   if (sizeof(C) == 4) {                                  // the last group in against the first one out
-    const float in = -wave_max_f32(taken ? -static_cast<float>(gs) : -INFINITY);
-    const float out = wave_max_f32(taken || g >= a.groups ? -INFINITY : static_cast<float>(gs));
+    const float in = -wave_max_f32(taken && live ? -static_cast<float>(gs) : -INFINITY);
+    const float out = wave_max_f32(taken || !live ? -INFINITY : static_cast<float>(gs));
     if (out != -INFINITY && in - out < 2.f * tol + 4.8e-7f * (fabsf(in) + fabsf(out))) close = true;
   }
   return taken;

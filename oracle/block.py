@@ -66,8 +66,8 @@ def route_scored(logits, k: int, bias=None, score: str = "softmax", groups: int 
         value = []
         for g in range(groups):
             mine = sorted((c[e] for e in range(g * size, (g + 1) * size) if on[t, e]), reverse=True)
-            value.append(sum(mine[:group_top]) if mine else -np.inf)
-        best = sorted(range(groups), key=lambda g: (-value[g], g))[:top_groups]
+            value.append((not mine, -sum(mine[:group_top])))   # a group with nothing to offer comes last
+        best = sorted(range(groups), key=lambda g: (value[g], g))[:top_groups]
         pool = [e for e in range(E) if e // size in best]
         # without a bias the order is the logits' own
         order = lambda e: (not on[t, e], (-c[e] if bias is not None else -l[t, e]) if on[t, e] else 0.0, e)  # noqa: E731

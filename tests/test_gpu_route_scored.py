@@ -304,3 +304,27 @@ def test_route_scored_most_tokens(M):
         i1, w1 = M.moe_route_scored(n(l), k)
         assert torch.equal(n(idx), i1) and torch.equal(n(w), w1)
         assert torch.equal(n(g), M.moe_route_scored_backward(n(l), i1, n(d)))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("G,tg,gt", [(1, 1, 1), (2, 1, 2), (8, 3, 1), (8, 3, 2), (32, 9, 2)])
+def test_route_scored_infinite_biases(M, score, G, tg, gt):
+    """A bias of -inf: the expert comes after all others that take part, before the masked
+    ones, and a group that has to count it scores -inf, still above a group without experts."""
+    if G == 2:                                          # one group's second largest is the -inf
+        l = torch.tensor([[0.1, 0.2, -3.0, -3.0]])
+        idx, _ = _run(M, l, 1, torch.tensor([5.0, -float("inf"), 0.0, 0.0]), score, 2, 1, 2, what="-inf")
+        assert idx.tolist() == [[2]]
+    g = torch.Generator().manual_seed(G + gt)
+    T, E, k = 96, 64, 6
+    l = torch.randn(T, E, generator=g)
+    b = 0.2 * torch.randn(E, generator=g)
+    b[torch.rand(E, generator=g) < 0.5] = -float("inf")
+    _run(M, l, k, b, score, G, tg, gt, what="-inf")
+    u = torch.rand(T, E, generator=g)
+    l[u < 0.5] = -float("inf")
+    l[:4] = -float("inf")
+    l[2, 63] = l[3, 3] = 1.0
+    l[8:16, :32] = -float("inf")
+    _run(M, l, k, b, score, G, tg, gt, renorm=False, what="-inf and masks")
+    _run(M, l, k, torch.full((E,), -float("inf")), score, G, tg, gt, what="all -inf and masks")

@@ -139,3 +139,21 @@ def test_experts_int8_against_a_scalar_loop():
             for h in range(H):
                 ref[h] += w[t, j] * top / 127 * sd[e, h] * sum(q[n] * int(wd[e, h, n]) for n in range(I))
         assert np.allclose(got[t], ref, rtol=1e-12, atol=1e-15)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_route_scored_infinite_biases(score):
+    inf = np.inf
+    l = np.array([[0.1, 0.2, -3.0, -3.0]], dtype=np.float32)
+    b = np.array([5.0, -inf, 0.0, 0.0])
+    # c of -inf: the group that counts it scores -inf, the one that counts one expert does not
+    assert B.route_scored(l, 1, b, score, 2, 1, 2)[0].tolist() == [[2]]
+    assert B.route_scored(l, 1, b, score, 2, 1, 1)[0].tolist() == [[0]]
+    assert B.route_scored(l, 4, b, score)[0].tolist() == [[0, 2, 3, 1]]
+    # above masked experts and groups, by index among equals
+    l = np.array([[-inf, -inf, 1.0, 2.0, 0.0, 0.0]], dtype=np.float32)
+    b = np.array([9.0, 9.0, -inf, -inf, -inf, -inf])
+    assert B.route_scored(l, 2, b, score, 3, 1, 2)[0].tolist() == [[2, 3]]
+    assert B.route_scored(l, 6, b, score)[0].tolist() == [[2, 3, 4, 5, 0, 1]]
+    idx, w = B.route_scored(l, 4, b, score, 3, 2, 2)
+    assert idx.tolist() == [[2, 3, 4, 5]] and np.all(w > 0)
