@@ -212,7 +212,10 @@ __device__ __forceinline__ bool group_taken(const RouteArgs& a, const Place& pl,
   if (sizeof(C) == 4) {                                  // the last group in against the first one out
     const float in = -wave_max_f32(taken && live ? -static_cast<float>(gs) : -INFINITY);
     const float out = wave_max_f32(taken || !live ? -INFINITY : static_cast<float>(gs));
-    if (out != -INFINITY && in - out < 2.f * tol + 4.8e-7f * (fabsf(in) + fabsf(out))) close = true;
+    // (a sum past FP32's range is infinite: the difference, or the bound, is then NaN or
+    // infinite, and the comparison does not hold)
+    const bool left = __ballot(live && !taken) != 0;
+    if (left && !(in - out >= 2.f * tol + 4.8e-7f * (fabsf(in) + fabsf(out)))) close = true;
   }
   return taken;
 }

@@ -328,3 +328,25 @@ def test_route_scored_infinite_biases(M, score, G, tg, gt):
     l[8:16, :32] = -float("inf")
     _run(M, l, k, b, score, G, tg, gt, renorm=False, what="-inf and masks")
     _run(M, l, k, torch.full((E,), -float("inf")), score, G, tg, gt, what="all -inf and masks")
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_route_scored_group_sums_past_fp32(M, score, sign):
+    """Two biases whose sum FP32 does not hold: group scores are compared all the same."""
+    g = torch.Generator().manual_seed(10)
+    l = torch.randn(8, 4, generator=g)
+    b = sign * torch.tensor([2e38, 2e38, 3e38, 3e38])
+    idx, _ = _run(M, l, 1, b, score, 2, 1, 2, what="sums past FP32")
+    assert all(i >= 2 for i in idx[:, 0].tolist()) == (sign > 0)
+    _run(M, l, 1, b.flip(0), score, 2, 1, 2, what="sums past FP32")
+    # both groups just past FP32's range, the second by more
+    hi, lo = 1.5 * 2.0 ** 127 + 7 * 2.0 ** 104, 2.0 ** 126 - 2.0 ** 102
+    b = sign * torch.tensor([hi, lo, hi + 2.0 ** 107, lo])
+    idx, _ = _run(M, l, 1, b, score, 2, 1, 2, what="sums just past FP32")
+    assert idx[:, 0].tolist() == ([2] * 8 if sign > 0 else [1] * 8)
+    l = torch.randn(40, 64, generator=g)
+    b = sign * (1.6 + 1.8 * torch.rand(64, generator=g)) * 1e38
+    b[torch.rand(64, generator=g) < 0.3] = 0.5
+    for G, tg in ((4, 2), (16, 5), (32, 7)):
+        _run(M, l, 2, b, score, G, tg, 2, what="sums past FP32")
