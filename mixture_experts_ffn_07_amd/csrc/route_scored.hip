@@ -148,42 +148,33 @@ constexpr int kMaskedKey = -0x7FC00000;
 constexpr int kNone = -0x7FFFFFFF - 1;
 
 __device__ __forceinline__ int lane_value(int v, int l) { return __builtin_amdgcn_readlane(v, l); }
-__device__ __forceinline__ uint64_t lane_value(uint64_t v, int l) { return __shfl(v, l, kWave); }
+__device__ __forceinline__ double lane_value(double v, int l) { return __shfl(v, l, kWave); }
 
-// Scores as whole numbers of the same order, FP32 and FP64: below them all is kNoScore, the
-// place of an expert that does not take part (-inf is a score like others: a bias gives it).
-template <typename C> struct Ordered;
-template <> struct Ordered<float> {
-  typedef int Key;
-  static constexpr int kNoScore = kNone;
-  static __device__ __forceinline__ int key(float c) { return order_of(c); }
-  static __device__ __forceinline__ float value(int k) { return float_of(k); }
-};
-template <> struct Ordered<double> {
-  typedef uint64_t Key;
-  static constexpr uint64_t kNoScore = 0;
-  static __device__ __forceinline__ uint64_t key(double c) { return ordered_key64(c); }
-  static __device__ __forceinline__ double value(uint64_t k) {
-    return __longlong_as_double(static_cast<long long>(k >> 63 ? k & 0x7FFFFFFFFFFFFFFFull : ~k));
-  }
-};
+// Scores as values of the same order, with a place below -inf (a score like others: a bias
+// gives it) for an expert that does not take part: whole numbers for FP32; for FP64, whose
+// scores come from FP32 biases and lie far from its ends, -inf is moved to kLeast64.
+constexpr double kLeast64 = -1e300;
+__device__ __forceinline__ int order_key_of(float c) { return order_of(c); }
+__device__ __forceinline__ double order_key_of(double c) { return max(c, kLeast64); }
+__device__ __forceinline__ double from_order_key(double k) { return k; }
+__device__ __forceinline__ float from_order_key(int k) { return float_of(k); }
 
 // Whether the group that this lane's candidates belong to takes part (C float or
 // double).  `close`: set where the FP32 scores do not decide it.
 template <int R, typename C>
 __device__ __forceinline__ bool group_taken(const RouteArgs& a, const Place& pl, const C (&c)[R],
                                             const bool (&on)[R], float tol, bool& close) {
-  typedef Ordered<C> O;
-  typedef typename O::Key Key;
+  typedef decltype(order_key_of(C())) Key;
+  constexpr Key kOut = sizeof(C) == 4 ? static_cast<Key>(kNone) : static_cast<Key>(-INFINITY);
   const int g = lane_id() / pl.span;
-  Key k1 = O::kNoScore, k2 = O::kNoScore;                // largest, second largest
+  Key k1 = kOut, k2 = kOut;                              // largest, second largest
   auto merge = [&](Key o1, Key o2) {
     k2 = max(max(k2, o2), min(k1, o1));
     k1 = max(k1, o1);
   };
 #pragma unroll
   for (int i = 0; i < R; ++i) {
-    const Key x = on[i] ? O::key(c[i]) : O::kNoScore;
+    const Key x = on[i] ? order_key_of(c[i]) : kOut;
     k2 = max(k2, min(k1, x));
     k1 = max(k1, x);
   }
@@ -198,11 +189,13 @@ __device__ __forceinline__ bool group_taken(const RouteArgs& a, const Place& pl,
   }
   // a group with one expert that takes part scores that expert's c alone; one without any
   // comes after all others
-  const bool live = k1 != O::kNoScore;
-  C gs = O::value(k1);
-  if (a.group_top > 1 && k2 != O::kNoScore) gs += O::value(k2);
+  const bool live = k1 != kOut;
+  C gs = from_order_key(k1);
+  if (a.group_top > 1 && k2 != kOut) gs += from_order_key(k2);
   gs += static_cast<C>(0);                               // -0 and +0 tie
-  const Key gk = live ? O::key(gs) : O::kNoScore;
+  // (a sum with kLeast64 in it is -inf)
+  if constexpr (sizeof(C) == 8) gs = gs < 0.5 * kLeast64 ? kLeast64 : gs;
+  const Key gk = live ? order_key_of(gs) : kOut;
   int rank = 0;
   for (int o = 0; o < a.groups; ++o) {
     const Key ok = lane_value(gk, o * pl.span);
