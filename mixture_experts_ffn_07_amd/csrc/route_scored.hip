@@ -202,13 +202,20 @@ __device__ __forceinline__ bool group_taken(const RouteArgs& a, const Place& pl,
     rank += ok > gk || (ok == gk && o < g) ? 1 : 0;
   }
   const bool taken = g < a.groups && rank < a.topk_groups;
-  if (sizeof(C) == 4) {                                  // the last group in against the first one out
-    const float in = -wave_max_f32(taken && live ? -static_cast<float>(gs) : -INFINITY);
-    const float out = wave_max_f32(taken || !live ? -INFINITY : static_cast<float>(gs));
-    // (a sum past FP32's range is infinite: the difference, or the bound, is then NaN or
-    // infinite, and the comparison does not hold)
-    const bool left = __ballot(live && !taken) != 0;
-    if (left && !(in - out >= 2.f * tol + 4.8e-7f * (fabsf(in) + fabsf(out)))) close = true;
+  if constexpr (sizeof(C) == 4) {
+    // Every group in has to lie above every group out by more than both can be off: the
+    // scores p by less than tol, each c by half a step of itself (p + b is rounded: 2^-24 |c|,
+    // however little of it a sum that cancels leaves), the sum by half a step; twice these
+    // roundings here.  A c of -inf is exact; a sum past FP32's range has infinite bounds.
+    const float c1 = from_order_key(k1), c2 = a.group_top > 1 && k2 != kOut ? from_order_key(k2) : 0.f;
+    const float size = fabsf(c1) + fabsf(c2);
+    const bool exact = c1 == -INFINITY || c2 == -INFINITY;
+    const float err = exact ? 0.f : tol + 2.4e-7f * size;
+    const float lo = exact ? -INFINITY : err < INFINITY ? gs - err : -INFINITY;
+    const float hi = exact ? -INFINITY : err < INFINITY ? gs + err : INFINITY;
+    const float in = -wave_max_f32(taken && live ? -lo : -INFINITY);
+    const float out = wave_max_f32(live && !taken ? hi : -INFINITY);
+    if (__ballot(live && !taken) && !(in > out)) close = true;
   }
   return taken;
 }

@@ -350,3 +350,22 @@ def test_route_scored_group_sums_past_fp32(M, score, sign):
     b[torch.rand(64, generator=g) < 0.3] = 0.5
     for G, tg in ((4, 2), (16, 5), (32, 7)):
         _run(M, l, 2, b, score, G, tg, 2, what="sums past FP32")
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [64.0, 1000.0, 1e5])
+def test_route_scored_group_sums_that_cancel(M, score, size):
+    """Each group's two largest have large biases of opposite sign: the sum keeps the rounding
+    of its terms (2^-24 of the bias), far above that of the sum itself.  Groups apart by
+    about that much."""
+    g = torch.Generator().manual_seed(int(size))
+    T, G = 400, 8
+    l = torch.randn(T, 1, 2, generator=g).expand(T, G, 2) + size * 2.0 ** -22 * torch.randn(T, G, 2, generator=g)
+    b = torch.tensor([size, -size]).repeat(G)
+    _run(M, l.reshape(T, 2 * G).contiguous(), 2, b, score, G, 1, 2, what=f"cancelling {size}")
+    # groups of three, the third masked or far below
+    l3 = torch.full((T, G, 3), -float("inf"))
+    l3[:, :, :2] = l
+    l3[::2, :, 2] = -4.0
+    b3 = torch.tensor([size, -size, -3 * size]).repeat(G)
+    _run(M, l3.reshape(T, 3 * G), 4, b3, score, G, 3, 2, what=f"cancelling {size}")
