@@ -472,7 +472,8 @@ int moe_quantize_int8(const uint16_t* src, int64_t rows, int K, int8_t* codes, f
  *             elsewhere, a padded token) adds nothing; a token without any other
  *             slot gets zeros.
  *   out       [T, H] BF16 out
- *   workspace >= moe_experts_int8_workspace_bytes(T, H, I, E, k), contents ignored
+ *   workspace >= moe_experts_int8_workspace_bytes(T, H, I, E, k), contents ignored; the
+ *             query does not fall as T grows: a workspace for the largest batch serves all
  * Limits: T >= 0 (0 enqueues nothing), H and I multiples of 256 up to 16384, 1 <= k
  * <= min(E, 32), E <= 1024; T*H, T*k*H, T*k*I and 2*I*H each below 2^31.
  */

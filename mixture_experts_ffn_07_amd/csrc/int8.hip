@@ -60,6 +60,16 @@ inline int slices(size_t P, int E, int bm, int nblk, int nstage) {
   const size_t s = room < most ? room : most;
   return s < 2 ? 1 : static_cast<int>(s);
 }
+// Bytes that the slices of T k = P rows or fewer take, `row` bytes of INT32 sums each: at most
+// `most` slices a row, and 2^25 bytes however many rows (slices * tiles * nblk <= 256, P <
+// 128 * tiles, row = 1024 nblk for both products).  It does not fall as P grows, where the
+// slices themselves come and go.
+inline size_t slice_bytes(size_t P, int nstage, size_t row) {
+  const size_t most = nstage / kSplitStages, cap = size_t(1) << 25;
+  if (most < 2) return 0;
+  const size_t rows = most * P;
+  return row && rows > cap / row ? cap : rows * row;
+}
 
 }  // namespace
 
@@ -84,11 +94,14 @@ Int8Ws int8_ws_layout(int T, int H, int I, int E, int k) {
   const bool split = L.bm != kLargeBM;
   L.slices_gu = split ? slices(P, E, L.bm, I / 128, H / 256) : 1;
   L.slices_down = split ? slices(P, E, L.bm, H / 256, I / 256) : 1;
+  // Each part holds what any smaller T takes, so that a workspace for the largest batch serves
+  // every batch (tiles: as many as of the least rows).
+  const size_t tile_room = E + (P + kBM8 - 1) / kBM8;
   size_t o = 0;
   L.n_tiles = o;   o += 256;
   L.counts = o;    o = align256(o + sizeof(int) * E);
   L.offsets = o;   o = align256(o + sizeof(int) * (E + 1));
-  L.tiles = o;     o = align256(o + sizeof(int) * 2 * L.max_tiles);
+  L.tiles = o;     o = align256(o + sizeof(int) * 2 * tile_room);
   L.perm = o;      o = align256(o + sizeof(int) * P);
   L.row_of = o;    o = align256(o + sizeof(int) * P);
   L.act = o;       o = align256(o + sizeof(float) * P * I);
@@ -97,10 +110,9 @@ Int8Ws int8_ws_layout(int T, int H, int I, int E, int k) {
   L.y = o;
   if (k > 1) o = align256(o + sizeof(float) * P * H);
   L.partial = o;
-  if (L.bm == kLargeBM) o = align256(o + sizeof(int) * kLargeMaxSlices * kLargeBM * 256);
-  const size_t gu = L.slices_gu > 1 ? sizeof(int) * L.slices_gu * P * 2 * I : 0;
-  const size_t down = L.slices_down > 1 ? sizeof(int) * L.slices_down * P * H : 0;
-  o = align256(o + (gu > down ? gu : down));
+  const size_t gu = slice_bytes(P, H / 256, sizeof(int) * 2 * I), down = slice_bytes(P, I / 256, sizeof(int) * H);
+  const size_t tail = L.bm == kLargeBM ? sizeof(int) * kLargeMaxSlices * kLargeBM * 256 : 0;
+  o = align256(o + (tail > gu ? tail > down ? tail : down : gu > down ? gu : down));
   L.total = o;
   return L;
 }

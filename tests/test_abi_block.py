@@ -175,3 +175,20 @@ def test_header_names_every_binding(m):
     text = open(os.path.join(root, "include", "moe_mi355x.h")).read()
     for name in m._SIGS:
         assert name + "(" in text, name
+
+
+@pytest.mark.parametrize("H,I,E,k", [
+    (7168, 2048, 6, 1), (7168, 2048, 2, 1), (2048, 768, 128, 8), (4096, 1024, 6, 4), (2560, 1792, 5, 5), (4096, 1024, 64, 6),
+    (512, 256, 8, 2), (16384, 256, 1, 1), (256, 16384, 3, 2), (1536, 4096, 32, 12), (1024, 2048, 3, 1)])
+def test_int8_workspace_for_a_batch_serves_smaller_ones(m, H, I, E, k):
+    q = lambda T: m.lib.moe_experts_int8_workspace_bytes(T, H, I, E, k)  # noqa: E731
+    T = list(range(1, 2500)) + list(range(2500, 40000, 37))
+    n = [q(t) for t in T]
+    worse = [(T[i], n[i], T[i + 1], n[i + 1]) for i in range(len(T) - 1) if n[i + 1] < n[i]]
+    assert not worse, worse[:3]
+
+
+@pytest.mark.parametrize("H", [32, 512, 4096, 7168])
+def test_norm_backward_workspace_for_a_batch_serves_smaller_ones(m, H):
+    n = [m.lib.moe_add_rmsnorm_backward_workspace_bytes(t, H) for t in range(3000)]
+    assert n == sorted(n)

@@ -244,3 +244,17 @@ def test_experts_int8_one_slot_zero_and_negative_weights(M, H, I, E):
     for rows in (slice(0, 1), slice(3, 4), slice(5, 12), slice(0, 20), slice(0, 48), slice(100, 190), slice(0, 400)):
         part = {n: (t[rows].clone() if n in ("x", "xs", "idx", "w") else t) for n, t in d.items()}
         assert torch.equal(call(M, part).view(torch.int16), full[rows].view(torch.int16)), rows
+
+
+@pytest.mark.parametrize("H,I,E,k", [(2560, 1792, 5, 5), (2048, 2048, 2, 1), (4096, 1024, 4, 2)])
+def test_experts_int8_one_workspace_for_all_batches(M, H, I, E, k):
+    """Sized once, for the largest batch: every smaller one is taken, and its outputs are
+    those with a workspace of its own."""
+    print(f"[int8] one workspace H={H} I={I} E={E} k={k}", flush=True)
+    most = 2100
+    d = make(most, H, I, E, k, seed=14)
+    ws = M.workspace(M.moe_experts_int8_workspace_bytes(most, H, I, E, k))
+    ws.fill_(255)
+    for T in (1, 2, 3, 9, 14, 40, 48, 100, 123, 300, 383, 700, 1025, most):
+        part = {n: (t[:T].clone() if n in ("x", "xs", "idx", "w") else t) for n, t in d.items()}
+        assert torch.equal(call(M, part, ws=ws), call(M, part)), T
