@@ -74,11 +74,15 @@ BatchedWs batched_ws_layout(int T, int H, int I, int E, int k, int dtype) {
 // counters), takes its own offset and tile offset from the counts of experts
 // < e, then compacts the pairs routed to e: each wave owns a contiguous run of
 // pairs, so its count alone gives the waves' places, and order inside an expert
-// is ascending pair id (= ascending token).  A wave's first kGroupKeep * 64 ids
-// stay in registers between the two passes.  Pairs whose id is out of range get
-// row_of = P (ignored downstream) from workgroup 0.
-constexpr int kGroupKeep = 16;
-__global__ __launch_bounds__(1024) void group_experts(
+// is ascending pair id (= ascending token).  A wave's first KEEP * 64 ids stay in
+// registers between the two passes.  Pairs whose id is out of range get row_of = P
+// (ignored downstream) from workgroup 0.  At most 64 registers, so that two
+// workgroups fit a CU: with one, more experts than CUs run in two rounds.  KEEP by
+// the steps that P gives a wave; whole gate/up calls, H 256 I 256, us (this / 16 for
+// every P and 68 registers): T 64 E 384 k 8 22 / 26; T 32 E 256 k 8 14.9 / 16.1; T 512
+// E 384 k 8 28 / 31; T 32768 E 384 k 8 331 / 416.
+template <int KEEP>
+__global__ __launch_bounds__(1024, 8) void group_experts(
     const int32_t* __restrict__ idx, int P, int E, int BM, int* __restrict__ counts,
     int* __restrict__ offsets, int2* __restrict__ tiles, int* __restrict__ n_tiles,
     int* __restrict__ perm, int* __restrict__ row_of, uint32_t okey) {
@@ -91,7 +95,7 @@ __global__ __launch_bounds__(1024) void group_experts(
   __syncthreads();
   const int per = (P + nw * kWave - 1) / (nw * kWave);    // 64-pair steps per wave
   const int i0 = wv * per * kWave;
-  int keep[kGroupKeep];
+  int keep[KEEP];
   int mine = 0;                                           // this wave's pairs of expert e
   int small = 0;                                          // lane j < E <= 8: this wave's pairs of expert j
   auto tally = [&](int i, int v) {
@@ -108,14 +112,14 @@ __global__ __launch_bounds__(1024) void group_experts(
     }
   };
 #pragma unroll
-  for (int s = 0; s < kGroupKeep; ++s) {
+  for (int s = 0; s < KEEP; ++s) {
     const int i = i0 + s * kWave + lane;
     keep[s] = s < per && i < P ? idx[i] : -1;
   }
 #pragma unroll
-  for (int s = 0; s < kGroupKeep; ++s)
+  for (int s = 0; s < KEEP; ++s)
     if (s < per) tally(i0 + s * kWave + lane, keep[s]);
-  for (int s = kGroupKeep; s < per; ++s) {
+  for (int s = KEEP; s < per; ++s) {
     const int i = i0 + s * kWave + lane;
     tally(i, i < P ? idx[i] : -1);
   }
@@ -166,9 +170,9 @@ __global__ __launch_bounds__(1024) void group_experts(
     pos += __popcll(b);
   };
 #pragma unroll
-  for (int s = 0; s < kGroupKeep; ++s)
+  for (int s = 0; s < KEEP; ++s)
     if (s < per) place(i0 + s * kWave + lane, keep[s]);
-  for (int s = kGroupKeep; s < per; ++s) {
+  for (int s = KEEP; s < per; ++s) {
     const int i = i0 + s * kWave + lane;
     place(i, i < P ? idx[i] : -1);
   }
@@ -787,10 +791,8 @@ hipError_t launch_gate_up_batched(const void* x, const uint8_t* xs, const void* 
   const BatchedWs L = batched_ws_layout(T, H, I, E, k, dtype);
   const BatchedPtrs p = batched_ptrs(ws, L);
   const int P = T * k;
-  prof_begin(kGroup, s);
-  hipLaunchKernelGGL(group_experts, dim3(E), dim3(1024), 0, s, idx, P, E, L.bm, p.counts,
-                     p.offsets, p.tiles, p.n_tiles, p.perm, p.row_of, order_key());
-  prof_end(kGroup, s);
+  if (const hipError_t e = launch_group_experts(idx, P, E, L.bm, p.counts, p.offsets, p.tiles,
+                                                p.n_tiles, p.perm, p.row_of, s); e != hipSuccess) return e;
   if (L.bm == kLargeBM) {
     prof_begin(kGemmGateUp, s);
     const hipError_t e =
@@ -1013,8 +1015,13 @@ hipError_t launch_mx_gate_up_raw_rows(const uint8_t* x, const uint8_t* xs, const
 hipError_t launch_group_experts(const int32_t* idx, int P, int E, int BM, int* counts, int* offsets,
                                 int2* tiles, int* n_tiles, int* perm, int* row_of, hipStream_t s) {
   prof_begin(kGroup, s);
-  hipLaunchKernelGGL(group_experts, dim3(E), dim3(1024), 0, s, idx, P, E, BM, counts, offsets,
-                     tiles, n_tiles, perm, row_of, order_key());
+#define GROUP(KEEP)                                                                             \
+  hipLaunchKernelGGL(group_experts<KEEP>, dim3(E), dim3(1024), 0, s, idx, P, E, BM, counts, offsets, \
+                     tiles, n_tiles, perm, row_of, order_key())
+  if (P <= 1024) GROUP(1);
+  else if (P <= 4096) GROUP(4);
+  else GROUP(16);
+#undef GROUP
   prof_end(kGroup, s);
   return hipGetLastError();
 }
