@@ -410,7 +410,9 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == 1
 // chain starting from 0), rounded once to BF16.  Workgroup (x, y): token x,
 // column chunk y of gridDim.y (small batches split the columns so that the
 // launch still spreads over the CUs); a launch covers the output columns [col0,
-// col0 + cols), y holding them with row stride ldy from its column 0.
+// col0 + cols), y holding them with row stride ldy from its column 0.  S slots' loads are
+// in flight at a time.
+template <int S>
 __global__ __launch_bounds__(256) void combine_slots(const float* __restrict__ y,
                                                      const int* __restrict__ row_of,
                                                      const float* __restrict__ w, int T, int H,
@@ -422,12 +424,12 @@ __global__ __launch_bounds__(256) void combine_slots(const float* __restrict__ y
   const int c4 = cols / 4, c_lo = blockIdx.y * c4 / gridDim.y, c_hi = (blockIdx.y + 1) * c4 / gridDim.y;
   for (int c = c_lo + threadIdx.x; c < c_hi; c += blockDim.x) {
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    for (int j0 = 0; j0 < k; j0 += 8) {                   // eight slots' loads in flight, then their sum in order
-      f32x4 v[8];
-      float wj[8];
-      bool in[8];
+    for (int j0 = 0; j0 < k; j0 += S) {                   // S slots' loads, then their sum in order
+      f32x4 v[S];
+      float wj[S];
+      bool in[S];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < S; ++j) {
         const int row = j0 + j < k ? row_of[t * k + j0 + j] : P;
         in[j] = static_cast<unsigned>(row) < static_cast<unsigned>(P);
         if (in[j]) {
@@ -436,7 +438,7 @@ __global__ __launch_bounds__(256) void combine_slots(const float* __restrict__ y
         }
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < S; ++j)
         if (in[j]) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[i] = fmaf(wj[j], v[j][i], acc[i]);
@@ -899,9 +901,7 @@ hipError_t launch_down_batched(const void* h, const uint8_t* hs, const void* wd,
                                    p.n_tiles, p.counts, p.offsets, w, H, I, k, p.y, out,
                                    p.partial, L.max_tiles, num_cus, s, T, E, p.sct);
     if (e == hipSuccess && k > 1) {
-      hipLaunchKernelGGL(combine_slots, combine_grid(T, H, num_cus), dim3(256), 0, s, p.y, p.row_of, w, T,
-                         H, k, out, order_key(), 0, H, H);
-      e = hipGetLastError();
+      e = launch_combine_slots(p.y, p.row_of, w, T, H, k, out, 0, H, H, s, num_cus);
     }
     prof_end(kGemmDown, s);
     return e;
@@ -944,9 +944,10 @@ hipError_t launch_down_batched(const void* h, const uint8_t* hs, const void* wd,
     }
 #undef DOWN_ARGS_B
 #undef DOWN_ARGS_M
-    if (k > 1)
-      hipLaunchKernelGGL(combine_slots, combine_grid(T, hq, num_cus), dim3(256), 0, s, p.y, p.row_of, w,
-                         T, H, k, out, order_key(), q * hq, hq, hq);
+    if (k > 1) {
+      const hipError_t e = launch_combine_slots(p.y, p.row_of, w, T, H, k, out, q * hq, hq, hq, s, num_cus);
+      if (e != hipSuccess) return e;
+    }
   }
   prof_end(kGemmDown, s);
   return hipGetLastError();
@@ -1029,8 +1030,13 @@ hipError_t launch_group_experts(const int32_t* idx, int P, int E, int BM, int* c
 hipError_t launch_combine_slots(const float* y, const int* row_of, const float* w, int T, int H,
                                 int k, uint16_t* out, int col0, int cols, int ldy, hipStream_t s,
                                 int num_cus) {
-  hipLaunchKernelGGL(combine_slots, combine_grid(T, cols, num_cus), dim3(256), 0, s, y, row_of, w, T, H,
-                     k, out, order_key(), col0, cols, ldy);
+#define COMBINE(S)                                                                                 \
+  hipLaunchKernelGGL(combine_slots<S>, combine_grid(T, cols, num_cus), dim3(256), 0, s, y, row_of, w, T, H, \
+                     k, out, order_key(), col0, cols, ldy)
+  if (k <= 2) COMBINE(2);
+  else if (k <= 4) COMBINE(4);
+  else COMBINE(8);
+#undef COMBINE
   return hipGetLastError();
 }
 

@@ -41,3 +41,27 @@ def test_rows_by_expert(M, T, k, E, skew):
         ref = gu[:, :I] * torch.sigmoid(gu[:, :I]) * gu[:, I:]
         # half a BF16 step, and FP32's error of silu (an exponential of an argument below 16 and a division)
         assert ((h[rows].float() - ref).abs() <= ref.abs() * (2.0 ** -8 + 32 * 2.0 ** -24)).all(), e
+
+
+@pytest.mark.parametrize("T,H", [(3, 512), (70, 1024), (700, 256)])
+def test_slot_sums_of_any_number_of_slots(M, T, H):
+    """Further slots of weight 0 leave the output's bits as they are, whichever form of the slot
+    sum their number selects."""
+    I, E, most = 256, 256, 13
+    g = torch.Generator(device="cuda").manual_seed(T)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    x, wg, wd = r(T, H).bfloat16(), (r(E, 2 * I, H) / 16).bfloat16(), (r(E, H, I) / 16).bfloat16()
+    idx = r(T, E).topk(most, dim=1).indices.int()
+    w = torch.rand(T, most, generator=g, device="cuda")
+
+    def layer(n, k):
+        i = idx[:, :k].contiguous()
+        wk = w[:, :k].clone()
+        wk[:, n:] = 0
+        h, _, ws = M.moe_gate_up_3d_batched(x, wg, i, k)
+        return M.moe_down_3d_batched(h, wd, i, wk, ws, k)
+    for n in (2, 3, 4, 5, 8, 9):
+        ref = layer(n, n)
+        assert ref.any()
+        for k in range(n + 1, most + 1):
+            assert torch.equal(layer(n, k), ref), (n, k)
