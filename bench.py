@@ -62,18 +62,19 @@ CSRC = os.path.join(ROOT, "mixture_experts_ffn_07_amd", "csrc")
 # Each record holds a fingerprint of the kernel sources it was measured on; when
 # the sources change the figure no longer describes the kernel and is reported
 # as null until the counters are taken again.  (A change that leaves a record's
-# kernels alone - the machine code compared kernel by kernel - keeps its figure:
-# the grouping and the slot sum in batched.hip, and the shared tile order moved from
-# gemm_large.hip into gemm_large.h, since the counters were taken.)
+# kernels alone - the machine code compared kernel by kernel, in
+# profiles/kernel_code_digests.md - keeps its figure: the grouping and the slot sum in
+# batched.hip, and the shared tile order moved from gemm_large.hip into gemm_large.h,
+# since the counters were taken.)
 TRAFFIC = {
     ("gemm_gate_up", "kimi-bf16-T2048"): (
-        23012.2e6, ('batched.hip', 'common.h', 'tiles.h', 'internal.h'), "08a71aad5354ed19",
+        23012.2e6, ('batched.hip', 'common.h', 'tiles.h', 'internal.h'), "492cfd7c02f92106",
         "profiles/gemm_gate_up_kimi-bf16-T2048.md"),
     ("gemm_gate_up", "dsv4-mxfp8-T2048"): (
-        18188.0e6, ('batched.hip', 'common.h', 'tiles.h', 'internal.h'), "08a71aad5354ed19",
+        18188.0e6, ('batched.hip', 'common.h', 'tiles.h', 'internal.h'), "492cfd7c02f92106",
         "profiles/gemm_gate_up_dsv4-mxfp8-T2048.md"),
     ("gemm_gate_up", "glm-bf16-T2048"): (
-        13239.0e6, ('batched.hip', 'common.h', 'tiles.h', 'internal.h'), "08a71aad5354ed19",
+        13239.0e6, ('batched.hip', 'common.h', 'tiles.h', 'internal.h'), "492cfd7c02f92106",
         "profiles/gemm_gate_up_glm-bf16-T2048.md"),
     ("gemm_gate_up", "kimi-bf16-ep64share"): (
         2055.4e6, ('gemm_large.hip', 'gemm_large.h', 'common.h', 'tiles.h', 'internal.h'), "acdbd6a8bca4e25a",
@@ -94,28 +95,28 @@ TRAFFIC = {
         1114.8e6, ('decode.hip', 'common.h', 'internal.h', 'route.h', 'tiles.h'), "fd2144a70db086dc",
         "profiles/decode_gate_up_q35-zipf-T64.md"),
     ("gemm_gate_up", "qwen3-mxfp8-decode-T32"): (
-        378.8e6, ('batched.hip', 'common.h', 'tiles.h', 'internal.h'), "08a71aad5354ed19",
+        378.8e6, ('batched.hip', 'common.h', 'tiles.h', 'internal.h'), "492cfd7c02f92106",
         "profiles/gemm_gate_up_qwen3-mxfp8-decode-T32.md"),
     ("bwd_input", "kimi-bf16-T2048"): (
-        24773.4e6, ('backward.hip', 'batched.hip', 'gemm_large.hip', 'gemm_large.h', 'common.h', 'tiles.h', 'internal.h'), "9ece75ed9c0505e8",
+        24773.4e6, ('backward.hip', 'batched.hip', 'gemm_large.hip', 'gemm_large.h', 'common.h', 'tiles.h', 'internal.h'), "31d122eb0e0fb211",
         "profiles/bwd_kimi-bf16-T2048.md"),
     ("bwd_wgate_up", "kimi-bf16-T2048"): (
-        22916.5e6, ('backward.hip', 'batched.hip', 'gemm_large.hip', 'gemm_large.h', 'common.h', 'tiles.h', 'internal.h'), "9ece75ed9c0505e8",
+        22916.5e6, ('backward.hip', 'batched.hip', 'gemm_large.hip', 'gemm_large.h', 'common.h', 'tiles.h', 'internal.h'), "31d122eb0e0fb211",
         "profiles/bwd_kimi-bf16-T2048.md"),
     ("bwd_input", "kimi-bf16-ep64share"): (
-        2189.0e6, ('backward.hip', 'batched.hip', 'gemm_large.hip', 'gemm_large.h', 'common.h', 'tiles.h', 'internal.h'), "9ece75ed9c0505e8",
+        2189.0e6, ('backward.hip', 'batched.hip', 'gemm_large.hip', 'gemm_large.h', 'common.h', 'tiles.h', 'internal.h'), "31d122eb0e0fb211",
         "profiles/bwd_kimi-bf16-ep64share.md"),
     ("bwd_wgate_up", "kimi-bf16-ep64share"): (
-        2558.1e6, ('backward.hip', 'batched.hip', 'gemm_large.hip', 'gemm_large.h', 'common.h', 'tiles.h', 'internal.h'), "9ece75ed9c0505e8",
+        2558.1e6, ('backward.hip', 'batched.hip', 'gemm_large.hip', 'gemm_large.h', 'common.h', 'tiles.h', 'internal.h'), "31d122eb0e0fb211",
         "profiles/bwd_kimi-bf16-ep64share.md"),
     ("bwd_requant", "dsv4-mxfp8-T2048"): (
-        59007.7e6, ('backward.hip', 'batched.hip', 'gemm_large.hip', 'gemm_large.h', 'common.h', 'tiles.h', 'internal.h'), "9ece75ed9c0505e8",
+        59007.7e6, ('backward.hip', 'batched.hip', 'gemm_large.hip', 'gemm_large.h', 'common.h', 'tiles.h', 'internal.h'), "31d122eb0e0fb211",
         "profiles/bwd_mxfp8_dsv4-mxfp8-T2048.md"),
     ("bwd_wgate_up", "dsv4-mxfp8-T2048"): (
-        56072.7e6, ('backward.hip', 'batched.hip', 'gemm_large.hip', 'gemm_large.h', 'common.h', 'tiles.h', 'internal.h'), "9ece75ed9c0505e8",
+        56072.7e6, ('backward.hip', 'batched.hip', 'gemm_large.hip', 'gemm_large.h', 'common.h', 'tiles.h', 'internal.h'), "31d122eb0e0fb211",
         "profiles/bwd_mxfp8_dsv4-mxfp8-T2048.md"),
     ("bwd_wgate_up", "dsv4-mxfp8-ep64share"): (
-        4018.3e6, ('backward.hip', 'batched.hip', 'gemm_large.hip', 'gemm_large.h', 'common.h', 'tiles.h', 'internal.h'), "9ece75ed9c0505e8",
+        4018.3e6, ('backward.hip', 'batched.hip', 'gemm_large.hip', 'gemm_large.h', 'common.h', 'tiles.h', 'internal.h'), "31d122eb0e0fb211",
         "profiles/bwd_mxfp8_dsv4-mxfp8-ep64share.md"),
 }
 
