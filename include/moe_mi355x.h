@@ -393,7 +393,8 @@ size_t moe_add_rmsnorm_backward_workspace_bytes(int T, int H);
  *
  * The choice is made on exact comparisons: without a bias on the FP32 logits
  * themselves (as moe_route_topk; -0 and +0 tie), with one on c in FP64; group
- * scores are FP64.  The weights are FP32.
+ * scores are FP64.  The weights are computed in FP32, within 40 * 2^-24 of their value
+ * (and 1e-37).
  *
  *   logits   [T, E] float32.  A logit of -3.3895e38 (BF16's lowest finite value) or
  *            less, -inf or NaN masks the expert: p = 0, it adds nothing to a group's

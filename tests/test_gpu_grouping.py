@@ -13,13 +13,13 @@ def M():
     return M
 
 
-@pytest.mark.parametrize("E", [1, 7, 9, 384])
-@pytest.mark.parametrize("T,k", [(1, 1), (65, 1), (1023, 1), (1024, 1), (1025, 1), (512, 2), (4095, 1), (1024, 4), (4097, 1),
-                                 (2731, 6), (16384, 1), (16385, 1), (2100, 8)])
+SIZES = [(1, 1), (65, 1), (1023, 1), (1024, 1), (1025, 1), (512, 2), (4095, 1), (1024, 4), (4097, 1), (2731, 6), (16384, 1),
+         (16385, 1), (2100, 8)]
+
+
+@pytest.mark.parametrize("T,k,E", [(T, k, E) for T, k in SIZES for E in (1, 7, 9, 384) if k <= E])
 @pytest.mark.parametrize("skew", [False, True])
 def test_rows_by_expert(M, T, k, E, skew):
-    if k > E:
-        pytest.skip("fewer experts than slots")
     print(f"[grouping] T={T} k={k} E={E} skew={skew}", flush=True)
     H = I = 256
     g = torch.Generator(device="cuda").manual_seed(T + E)
