@@ -61,6 +61,10 @@ typedef enum {
   MOE_INT8 = 2,   /* INT8 codes with one FP32 scale per row: an output type of
                      moe_add_rmsnorm; the batched calls do not take it
                      (moe_experts_int8 is the INT8 form of the layer)        */
+  MOE_MXFP4 = 3,  /* E2M1 codes, two to a byte (the even element in the low four
+                     bits), with one E8M0 scale per 32 along K: an activation type of
+                     moe_experts_mxfp4, whose weights have it; the batched calls and
+                     the norm do not take it                                   */
   /* not element types: they make the enum span every int, so that an unknown
    * value passed by a caller is a valid value of the type that the library
    * rejects (MOE_ERR_SHAPE) rather than undefined behaviour in C++ */
@@ -487,6 +491,127 @@ int moe_experts_int8(const int8_t* x, const float* x_scales, const int8_t* w_gat
 size_t moe_experts_int8_workspace_bytes(int T, int H, int I, int E, int k);
 
 /*
+ * moe_quantize_mxfp4 -- MX block quantization of a BF16 matrix along its last
+ * dimension to 4 bits, beside moe_quantize_mxfp8 (block rule of OCP Microscaling v1.0).
+ *
+ *   src    [rows, K] BF16
+ *   codes  [rows, K/2] uint8 out: E2M1 codes, element 2i of a row in the low and element
+ *          2i + 1 in the high four bits of its byte i
+ *   scales [rows, K/32] uint8 E8M0 out
+ * Per block of 32: s = floor(log2(max |v|)) - 2 clamped to [-127, 127] (an all-zero
+ * block takes s = -127); code = E2M1 of v / 2^s rounded to nearest even and saturated
+ * to +-6, sign bit copied from v.  A block with a NaN or an infinity has undefined
+ * contents; other blocks are not affected.
+ * Limits: rows >= 0 (0 enqueues nothing), K a positive multiple of 32, rows * K < 2^40.
+ */
+int moe_quantize_mxfp4(const uint16_t* src, int64_t rows, int K, uint8_t* codes, uint8_t* scales,
+                       void* stream);
+
+/*
+ * moe_dequantize_mxfp4 -- the values of MXFP4 rows in BF16, exact: code * 2^(scale - 127)
+ * (past BF16's range, at scales of 253 and 254, an infinity; scale 255 gives NaN).
+ *
+ *   codes  [rows, K/2] uint8,  scales [rows, K/32] uint8, as moe_quantize_mxfp4 writes them
+ *   dst    [rows, K] BF16 out
+ * Limits as for moe_quantize_mxfp4.
+ */
+int moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int K,
+                         uint16_t* dst, void* stream);
+
+/*
+ * moe_experts_mxfp4 -- the layer's expert products with MXFP4 weights, from routed MXFP8
+ * or MXFP4 activations to the weighted sum, for any number of tokens.
+ *
+ *   g, u   = W_gate_up[e] x[t]             a = silu(g) * u   (FP32, not rounded)
+ *   h      = codes and scales of a along I in x's type, by the rule of moe_quantize_mxfp8
+ *            or moe_quantize_mxfp4
+ *   y      = W_down[e] h
+ *   out[t] = sum over slots j = 0..k-1, in that order, of topk_w[t, j] * y[t, j]
+ * Sums in FP32, out rounded once to BF16.  (With MXFP8 activations the matrix instruction
+ * adds its 64 or 128 products with about 16 bits below the largest of them; with MXFP4
+ * ones their sum is exact to FP32.)
+ *
+ *   x         xtype MOE_MXFP8: [T, H] E4M3 codes (moe_quantize_mxfp8, moe_add_rmsnorm);
+ *             MOE_MXFP4: [T, H/2] bytes (moe_quantize_mxfp4)
+ *   x_scales  [T, H/32] E8M0
+ *   w_gate_up [E, 2I, H/2] bytes, rows [0, I) gate and [I, 2I) up;  scales [E, 2I, H/32] E8M0
+ *   w_down    [E, H, I/2] bytes;  scales [E, H, I/32] E8M0
+ *   topk_idx, topk_w [T, k].  A slot whose id lies outside [0, E) (an expert held
+ *             elsewhere, a padded token) adds nothing; a token without any other
+ *             slot gets zeros.
+ *   out       [T, H] BF16 out
+ *   workspace >= moe_experts_mxfp4_workspace_bytes(T, H, I, E, k, xtype), contents ignored;
+ *             the query does not fall as T grows: a workspace for the largest batch serves all
+ * A token whose activations or whose experts' weights hold a NaN code or a scale of 255, or
+ * whose sums leave FP32, has undefined contents; others are not affected.
+ * Limits: T >= 0 (0 enqueues nothing), H and I multiples of 256 up to 16384, 1 <= k
+ * <= min(E, 32), E <= 1024; T*H, T*k*H, T*k*I and 2*I*H each below 2^31.
+ */
+int moe_experts_mxfp4(const uint8_t* x, const uint8_t* x_scales, moe_dtype xtype,
+                      const uint8_t* w_gate_up, const uint8_t* w_gate_up_scales,
+                      const uint8_t* w_down, const uint8_t* w_down_scales,
+                      const int32_t* topk_idx, const float* topk_w, int T, int H, int I, int E,
+                      int k, uint16_t* out, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+size_t moe_experts_mxfp4_workspace_bytes(int T, int H, int I, int E, int k, moe_dtype xtype);
+
+/*
+ * moe_balance_loss -- the auxiliary losses that keep a router's load even, beside
+ * moe_route_topk and moe_route_scored, with the tokens and the mean score of each expert.
+ *
+ * The T tokens are n_seqs consecutive sequences of L = T / n_seqs; a token whose mask byte
+ * is 0 (padding) takes no part.  With the N_s tokens of sequence s that take part:
+ *   p[t, e]  = exp(l_e) / sum exp(l)  (MOE_SCORE_SOFTMAX)  or  sigma(l_e) / sum sigma(l)
+ *              (MOE_SCORE_SIGMOID), over the experts that are not masked
+ *   probs[s, e]  = mean of p[t, e] over them (zeros if there are none)
+ *   counts[s, e] = their slots routed to expert e
+ *   f[s, e]      = E * counts[s, e] / sum over m of counts[s, m]   (0 without any)
+ *   losses[0]    = mean over the n_seqs sequences of sum over e of f[s, e] * probs[s, e]
+ *   losses[1]    = mean over all N = sum N_s tokens of lse_t^2, lse_t = log sum exp(l) (0 if
+ *                  N = 0)
+ * The losses are not scaled: their coefficients go into the gradient's d_losses.
+ *
+ *   logits     [T, E] float32.  A logit of -3.3895e38 (BF16's lowest finite value) or less,
+ *              -inf or NaN masks the expert (p = 0); a token whose experts are all masked
+ *              has p = 0 and lse = 0.  +inf counts as FLT_MAX.
+ *   topk_idx   [T, k] int32; ids outside [0, E) are not counted
+ *   token_mask [T] uint8, or NULL: every token takes part
+ *   losses     [2] float32 out,  counts [n_seqs, E] int32 out,  probs [n_seqs, E] float32 out,
+ *   tokens     [n_seqs] int32 out: N_s
+ *   workspace  >= moe_balance_loss_workspace_bytes(T, E, n_seqs), contents ignored
+ * Scores and sums are FP32 (a few units in the last place; sums over workgroups FP64).
+ * Limits: 0 <= T < 2^22, 1 <= n_seqs <= 4096 and a divisor of T, E <= 1024, 1 <= k <=
+ * min(E, 32).  T = 0 writes zeros.
+ */
+int moe_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* token_mask, int T,
+                     int E, int k, int n_seqs, moe_score score, float* losses, int32_t* counts,
+                     float* probs, int32_t* tokens, void* workspace, size_t workspace_bytes,
+                     void* stream);
+
+size_t moe_balance_loss_workspace_bytes(int T, int E, int n_seqs);
+
+/*
+ * moe_balance_loss_backward -- gradient of d_losses[0] * losses[0] + d_losses[1] * losses[1],
+ * the counts held fixed:
+ *   dlogits[t, e] = d_add[t, e] + d_losses[0] / (n_seqs * N_s) * p_e * (f_e - sum_m p_m f_m) *
+ *                   (MOE_SCORE_SIGMOID: 1 - sigma(l_e)) + d_losses[1] * 2 lse_t / N * exp(l_e - lse_t)
+ * A masked expert and a token that takes no part get d_add alone.
+ *
+ *   logits, token_mask  as given to moe_balance_loss
+ *   counts, tokens      as returned by it, or their sums over several GPUs (the loss of the
+ *                       whole batch; N_s and N are then those of the sums)
+ *   d_losses [2] float32 (on the device)
+ *   d_add    [T, E] float32, or NULL: the gradient that reaches the logits elsewhere
+ *            (moe_route_scored_backward, moe_backward_batched)
+ *   dlogits  [T, E] float32 out, every element; may be d_add (the same pointer)
+ * Limits as for moe_balance_loss (T = 0 enqueues nothing).
+ */
+int moe_balance_loss_backward(const float* logits, const uint8_t* token_mask, const int32_t* counts,
+                              const int32_t* tokens, const float* d_losses, const float* d_add, int T,
+                              int E, int n_seqs, moe_score score, float* dlogits, void* stream);
+
+/*
  * Kernel timing hook for benchmarks and profilers (not on any page).
  * moe_profile_kernel(kernel, start, stop): from now on, the calling thread's
  * launches of `kernel` are bracketed by hipEventRecord(start) and
@@ -501,7 +626,7 @@ typedef enum {
   MOE_KERNEL_DECODE_GATE_UP = 2,
   MOE_KERNEL_DECODE_DOWN = 3,
   MOE_KERNEL_GROUP = 4,          /* expert grouping of the batched path        */
-  MOE_KERNEL_QUANT = 5,          /* moe_quantize_mxfp8, moe_quantize_int8      */
+  MOE_KERNEL_QUANT = 5,          /* moe_quantize_mxfp8, _int8, _mxfp4, moe_dequantize_mxfp4 */
   MOE_KERNEL_GEMM_GATE_UP = 6,
   MOE_KERNEL_GEMM_DOWN = 7,      /* batched down projection and the weighted combine
                                     (which runs interleaved with it in column parts) */
@@ -519,7 +644,11 @@ typedef enum {
   MOE_KERNEL_ROUTE_BACKWARD = 18,/* moe_route_scored_backward (moe_route_scored: ROUTE) */
   MOE_KERNEL_INT8_GATE_UP = 19,  /* moe_experts_int8: gate/up product and SwiGLU */
   MOE_KERNEL_INT8_DOWN = 20,     /* moe_experts_int8: down product and the weighted sum */
-  MOE_KERNEL_COUNT = 21
+  MOE_KERNEL_MXFP4_GATE_UP = 21, /* moe_experts_mxfp4: gate/up product and SwiGLU */
+  MOE_KERNEL_MXFP4_DOWN = 22,    /* moe_experts_mxfp4: down product and the weighted sum */
+  MOE_KERNEL_BALANCE = 23,       /* moe_balance_loss                           */
+  MOE_KERNEL_BALANCE_BACKWARD = 24, /* moe_balance_loss_backward               */
+  MOE_KERNEL_COUNT = 25
 } moe_kernel_id;
 
 int moe_profile_kernel(int kernel, void* start_event, void* stop_event);

@@ -19,13 +19,14 @@ LIB_PATH = os.path.join(_HERE, "lib", "libmoe_mi355x.so")
 
 MOE_OK, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_ALIGN = 0, -1, -2, -3
 MOE_ERR_WORKSPACE, MOE_ERR_UNSUPPORTED, MOE_ERR_HIP = -4, -5, -6
-MOE_BF16, MOE_MXFP8, MOE_INT8 = 0, 1, 2
+MOE_BF16, MOE_MXFP8, MOE_INT8, MOE_MXFP4 = 0, 1, 2, 3
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 KERNELS = {"none": 0, "route": 1, "decode_gate_up": 2, "decode_down": 3, "group": 4,
            "quant": 5, "gemm_gate_up": 6, "gemm_down": 7, "combine": 8, "bwd_gate_up": 9,
            "bwd_down": 10, "bwd_input": 11, "bwd_wdown": 12, "bwd_wgate_up": 13,
            "decode_fused": 14, "bwd_requant": 15, "norm": 16, "norm_backward": 17,
-           "route_backward": 18, "int8_gate_up": 19, "int8_down": 20}
+           "route_backward": 18, "int8_gate_up": 19, "int8_down": 20,
+           "mxfp4_gate_up": 21, "mxfp4_down": 22, "balance": 23, "balance_backward": 24}
 MOE_DEBUG_PERMUTE_ORDER, MOE_DEBUG_DECODE_FUSED = 1, 2
 
 _P = ctypes.c_void_p
@@ -56,6 +57,13 @@ _SIGS = {
     "moe_quantize_int8": (_I, [_P, ctypes.c_int64, _I, _P, _P, _P]),
     "moe_experts_int8": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _SZ, _P]),
     "moe_experts_int8_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "moe_quantize_mxfp4": (_I, [_P, ctypes.c_int64, _I, _P, _P, _P]),
+    "moe_dequantize_mxfp4": (_I, [_P, _P, ctypes.c_int64, _I, _P, _P]),
+    "moe_experts_mxfp4": (_I, [_P, _P, _I, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _SZ, _P]),
+    "moe_experts_mxfp4_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "moe_balance_loss": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _SZ, _P]),
+    "moe_balance_loss_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "moe_balance_loss_backward": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P]),
     "moe_profile_kernel": (_I, [_I, _P, _P]),
     "moe_set_debug_options": (_I, [ctypes.c_uint, ctypes.c_uint32]),
     "moe_status_string": (ctypes.c_char_p, [_I]),
@@ -107,6 +115,7 @@ def _stream(stream) -> Optional[int]:
 
 
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)   # 16-bit patterns read as BF16
+_MASK = (torch.uint8, torch.bool)
 
 
 def _u16(t: torch.Tensor) -> torch.Tensor:
@@ -659,6 +668,116 @@ def moe_experts_int8(x, x_scales, w_gate_up, w_gate_up_scales, w_down, w_down_sc
     return out
 
 
+def moe_quantize_mxfp4(src, codes=None, scales=None, stream=None):
+    """src [rows, K] BF16 -> (E2M1 codes [rows, K/2] uint8, two to a byte with the even element
+    in the low four bits, E8M0 scales [rows, K/32] uint8)."""
+    dev = _gpu(src, 2, "src")
+    rows, K = src.shape
+    if codes is None:
+        codes = _new((rows, K // 2), torch.uint8, dev, stream)
+    if scales is None:
+        scales = _new((rows, K // 32), torch.uint8, dev, stream)
+    _enqueue("moe_quantize_mxfp4", dev, stream, _arg(src, "src", (rows, K), _BF16, dev), rows, K,
+             _arg(codes, "codes", (rows, K // 2), torch.uint8, dev),
+             _arg(scales, "scales", (rows, K // 32), torch.uint8, dev))
+    return codes, scales
+
+
+def moe_dequantize_mxfp4(codes, scales, out=None, stream=None):
+    """MXFP4 rows (codes [rows, K/2] and scales [rows, K/32], uint8) -> their values [rows, K] BF16."""
+    dev = _gpu(codes, 2, "codes")
+    rows, K = codes.shape[0], 2 * codes.shape[1]
+    if out is None:
+        out = _new((rows, K), torch.bfloat16, dev, stream)
+    _enqueue("moe_dequantize_mxfp4", dev, stream, _arg(codes, "codes", (rows, K // 2), torch.uint8, dev),
+             _arg(scales, "scales", (rows, K // 32), torch.uint8, dev), rows, K,
+             _arg(out, "out", (rows, K), _BF16, dev))
+    return out
+
+
+def moe_experts_mxfp4_workspace_bytes(T: int, H: int, I: int, E: int, k: int, xtype: int = MOE_MXFP8) -> int:
+    return int(lib.moe_experts_mxfp4_workspace_bytes(T, H, I, E, k, xtype))
+
+
+def moe_experts_mxfp4(x, x_scales, w_gate_up, w_gate_up_scales, w_down, w_down_scales, topk_idx,
+                      topk_w, xtype: int = MOE_MXFP8, out=None, ws=None, stream=None):
+    """The routed experts' FFN with MXFP4 weights ([E, 2I, H/2] and [E, H, I/2] bytes) -> out
+    [T, H] BF16.  xtype MOE_MXFP8: x [T, H] E4M3 codes; MOE_MXFP4: x [T, H/2] bytes; scales
+    [.., K/32].  Slots whose expert id lies outside [0, E) add nothing."""
+    dev = _gpu(x, 2, "x")
+    _gpu(w_down, 3, "w_down")
+    _gpu(topk_idx, 2, "topk_idx")
+    T, k = topk_idx.shape
+    E, H, I = w_down.shape[0], w_down.shape[1], 2 * w_down.shape[2]
+    if out is None:
+        out = _new((T, H), torch.bfloat16, dev, stream)
+    u8, f32 = torch.uint8, torch.float32
+    ptrs = (_arg(x, "x", (T, H // 2 if xtype == MOE_MXFP4 else H), u8, dev),
+            _arg(x_scales, "x_scales", (T, H // 32), u8, dev), xtype,
+            _arg(w_gate_up, "w_gate_up", (E, 2 * I, H // 2), u8, dev),
+            _arg(w_gate_up_scales, "w_gate_up_scales", (E, 2 * I, H // 32), u8, dev),
+            _arg(w_down, "w_down", (E, H, I // 2), u8, dev),
+            _arg(w_down_scales, "w_down_scales", (E, H, I // 32), u8, dev),
+            _arg(topk_idx, "topk_idx", (T, k), torch.int32, dev),
+            _arg(topk_w, "topk_w", (T, k), f32, dev))
+    pout = _arg(out, "out", (T, H), _BF16, dev)
+    ws, pws, n = _ws_arg(ws, moe_experts_mxfp4_workspace_bytes(T, H, I, E, k, xtype), dev, stream)
+    _enqueue("moe_experts_mxfp4", dev, stream, *ptrs, T, H, I, E, k, pout, pws, n)
+    return out
+
+
+def moe_balance_loss_workspace_bytes(T: int, E: int, n_seqs: int = 1) -> int:
+    return int(lib.moe_balance_loss_workspace_bytes(T, E, n_seqs))
+
+
+def moe_balance_loss(logits, topk_idx, score: int = MOE_SCORE_SOFTMAX, n_seqs: int = 1, token_mask=None,
+                     losses=None, counts=None, probs=None, tokens=None, ws=None, stream=None):
+    """The router's balance loss and z-loss of logits [T, E] float32 and topk_idx [T, k] int32, over
+    n_seqs sequences of T / n_seqs tokens; token_mask [T] uint8 or bool (0: no part) or None.  Returns
+    (losses [2] float32, counts [n_seqs, E] int32, mean scores [n_seqs, E] float32, tokens [n_seqs]
+    int32)."""
+    dev = _gpu(logits, 2, "logits")
+    _gpu(topk_idx, 2, "topk_idx")
+    T, E = logits.shape
+    k, S = topk_idx.shape[1], max(n_seqs, 0)
+    f32, i32 = torch.float32, torch.int32
+    if losses is None:
+        losses = _new((2,), f32, dev, stream)
+    if counts is None:
+        counts = _new((S, E), i32, dev, stream)
+    if probs is None:
+        probs = _new((S, E), f32, dev, stream)
+    if tokens is None:
+        tokens = _new((S,), i32, dev, stream)
+    ptrs = (_arg(logits, "logits", (T, E), f32, dev), _arg(topk_idx, "topk_idx", (T, k), i32, dev),
+            _arg(token_mask, "token_mask", (T,), _MASK, dev))
+    outs = (_arg(losses, "losses", (2,), f32, dev), _arg(counts, "counts", (S, E), i32, dev),
+            _arg(probs, "probs", (S, E), f32, dev), _arg(tokens, "tokens", (S,), i32, dev))
+    ws, pws, n = _ws_arg(ws, moe_balance_loss_workspace_bytes(T, E, n_seqs), dev, stream)
+    _enqueue("moe_balance_loss", dev, stream, *ptrs, T, E, k, n_seqs, score, *outs, pws, n)
+    return losses, counts, probs, tokens
+
+
+def moe_balance_loss_backward(logits, counts, tokens, d_losses, score: int = MOE_SCORE_SOFTMAX,
+                              token_mask=None, d_add=None, dlogits=None, stream=None):
+    """Gradient of d_losses . losses of moe_balance_loss (counts [n_seqs, E] and tokens [n_seqs] as it
+    returned them; d_losses [2] on the GPU), added to d_add [T, E] if given -> dlogits [T, E] float32
+    (which may be d_add)."""
+    dev = _gpu(logits, 2, "logits")
+    _gpu(counts, 2, "counts")
+    T, E = logits.shape
+    S = counts.shape[0]
+    f32, i32 = torch.float32, torch.int32
+    if dlogits is None:
+        dlogits = _new((T, E), f32, dev, stream)
+    _enqueue("moe_balance_loss_backward", dev, stream, _arg(logits, "logits", (T, E), f32, dev),
+             _arg(token_mask, "token_mask", (T,), _MASK, dev), _arg(counts, "counts", (S, E), i32, dev),
+             _arg(tokens, "tokens", (S,), i32, dev), _arg(d_losses, "d_losses", (2,), f32, dev),
+             _arg(d_add, "d_add", (T, E), f32, dev), T, E, S, score,
+             _arg(dlogits, "dlogits", (T, E), f32, dev))
+    return dlogits
+
+
 def moe_profile_kernel(kernel, start_event: Optional[int], stop_event: Optional[int]) -> None:
     """Bracket the named kernel's launches with the given hipEvent_t handles."""
     kid = KERNELS[kernel] if isinstance(kernel, str) else int(kernel)
@@ -677,4 +796,7 @@ __all__ = ["lib", "LIB_PATH", "MoeError", "moe_route_topk", "moe_decode_forward"
            "moe_add_rmsnorm_backward_workspace_bytes", "moe_route_scored",
            "moe_route_scored_backward", "moe_quantize_int8", "moe_experts_int8",
            "moe_experts_int8_workspace_bytes", "MOE_SCORE_SOFTMAX", "MOE_SCORE_SIGMOID",
-           "MOE_BF16", "MOE_MXFP8", "MOE_INT8", "KERNELS"]
+           "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_experts_mxfp4",
+           "moe_experts_mxfp4_workspace_bytes", "moe_balance_loss",
+           "moe_balance_loss_workspace_bytes", "moe_balance_loss_backward",
+           "MOE_BF16", "MOE_MXFP8", "MOE_INT8", "MOE_MXFP4", "KERNELS"]

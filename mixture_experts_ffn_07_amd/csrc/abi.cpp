@@ -35,7 +35,8 @@ static_assert(MOE_STATIC_SCRATCH_BYTES == moe::kStaticScratchBytes,
 static_assert(MOE_DEBUG_PERMUTE_ORDER == moe::kDebugPermute &&
               MOE_DEBUG_DECODE_FUSED == moe::kDebugDecodeFused, "debug option bits");
 static_assert(MOE_KERNEL_COUNT == moe::kAllKernelCount &&
-              MOE_KERNEL_NORM == moe::kNorm && MOE_KERNEL_INT8_DOWN == moe::kInt8Down, "kernel ids");
+              MOE_KERNEL_NORM == moe::kNorm && MOE_KERNEL_INT8_DOWN == moe::kInt8Down &&
+              MOE_KERNEL_BALANCE_BACKWARD == moe::kBalanceBackward, "kernel ids");
 
 namespace {
 
@@ -580,6 +581,131 @@ int moe_experts_int8(const int8_t* x, const float* x_scales, const int8_t* w_gat
                                              w_down_scales, topk_idx, topk_w, T, H, I, E, k, out,
                                              workspace, static_cast<hipStream_t>(stream), cus),
                     "moe_experts_int8 launch");
+}
+
+static int check_mx4_rows(int64_t rows, int K) {
+  if (K <= 0 || K % 32) return fail(MOE_ERR_SHAPE, "K=%d is not a positive multiple of 32", K);
+  if (rows < 0 || rows >= (1LL << 40) / K)
+    return fail(MOE_ERR_SHAPE, "rows=%lld is negative, or rows * K reaches 2^40", static_cast<long long>(rows));
+  return MOE_OK;
+}
+
+int moe_quantize_mxfp4(const uint16_t* src, int64_t rows, int K, uint8_t* codes, uint8_t* scales,
+                       void* stream) {
+  if (int st = check_mx4_rows(rows, K)) return st;
+  if (rows == 0) return ok();
+  if (!src || !codes || !scales) return fail(MOE_ERR_NULL, "src, codes and scales are required");
+  if (!aligned16(src) || !aligned16(codes) || !aligned16(scales))
+    return fail(MOE_ERR_ALIGN, "device pointers must be 16-byte aligned");
+  int cus = 0;
+  if (int st = device_info(&cus)) return st;
+  return hip_status(moe::launch_quant_mx4(src, rows, K, codes, scales, static_cast<hipStream_t>(stream)),
+                    "moe_quantize_mxfp4 launch");
+}
+
+int moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int K, uint16_t* dst,
+                         void* stream) {
+  if (int st = check_mx4_rows(rows, K)) return st;
+  if (rows == 0) return ok();
+  if (!codes || !scales || !dst) return fail(MOE_ERR_NULL, "codes, scales and dst are required");
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(dst))
+    return fail(MOE_ERR_ALIGN, "device pointers must be 16-byte aligned");
+  int cus = 0;
+  if (int st = device_info(&cus)) return st;
+  return hip_status(moe::launch_dequant_mx4(codes, scales, rows, K, dst, static_cast<hipStream_t>(stream)),
+                    "moe_dequantize_mxfp4 launch");
+}
+
+// Sizes that moe_experts_mxfp4 serves (T and k aside, those of its limits).
+static int check_mx4(int T, int H, int I, int E, int k, moe_dtype xtype) {
+  if (int st = check_common(T, H, I, E, k, 256, 256)) return st;
+  if (H > moe::kNormMaxH || I > moe::kNormMaxH)
+    return fail(MOE_ERR_SHAPE, "H=%d or I=%d above %d", H, I, moe::kNormMaxH);
+  if (xtype != MOE_MXFP8 && xtype != MOE_MXFP4) return fail(MOE_ERR_SHAPE, "xtype=%d", xtype);
+  return check_offsets(T, H, I, k);
+}
+
+size_t moe_experts_mxfp4_workspace_bytes(int T, int H, int I, int E, int k, moe_dtype xtype) {
+  if (T < 1 || check_mx4(T, H, I, E, k, xtype) != MOE_OK) return 0;
+  return moe::mx4_ws_layout(T, H, I, E, k, xtype == MOE_MXFP4).total;
+}
+
+int moe_experts_mxfp4(const uint8_t* x, const uint8_t* x_scales, moe_dtype xtype,
+                      const uint8_t* w_gate_up, const uint8_t* w_gate_up_scales,
+                      const uint8_t* w_down, const uint8_t* w_down_scales, const int32_t* topk_idx,
+                      const float* topk_w, int T, int H, int I, int E, int k, uint16_t* out,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+  if (int st = check_mx4(T, H, I, E, k, xtype)) return st;
+  if (T == 0) return ok();
+  if (!x || !x_scales || !w_gate_up || !w_gate_up_scales || !w_down || !w_down_scales || !topk_idx ||
+      !topk_w || !out)
+    return fail(MOE_ERR_NULL, "every input and output pointer is required");
+  if (!workspace) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
+  const size_t need = moe::mx4_ws_layout(T, H, I, E, k, xtype == MOE_MXFP4).total;
+  if (workspace_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "workspace %zu bytes < %zu required", workspace_bytes, need);
+  if (!aligned16(x) || !aligned16(x_scales) || !aligned16(w_gate_up) || !aligned16(w_gate_up_scales) ||
+      !aligned16(w_down) || !aligned16(w_down_scales) || !aligned16(topk_idx) || !aligned16(topk_w) ||
+      !aligned16(out) || !aligned16(workspace))
+    return fail(MOE_ERR_ALIGN, "device pointers must be 16-byte aligned");
+  int cus = 0;
+  if (int st = device_info(&cus)) return st;
+  return hip_status(moe::launch_experts_mx4(x, x_scales, xtype == MOE_MXFP4, w_gate_up, w_gate_up_scales,
+                                            w_down, w_down_scales, topk_idx, topk_w, T, H, I, E, k, out,
+                                            workspace, static_cast<hipStream_t>(stream), cus),
+                    "moe_experts_mxfp4 launch");
+}
+
+static int check_balance(int T, int E, int k, int n_seqs, moe_score score) {
+  if (int st = check_scored(T, E, k, score, 1.0f)) return st;
+  if (n_seqs < 1 || n_seqs > moe::kMaxSeqs || T % n_seqs)
+    return fail(MOE_ERR_SHAPE, "n_seqs=%d is not a divisor of T=%d in [1, %d]", n_seqs, T, moe::kMaxSeqs);
+  return MOE_OK;
+}
+
+size_t moe_balance_loss_workspace_bytes(int T, int E, int n_seqs) {
+  if (T < 0 || T >= moe::kMaxRows || E < 1 || E > 1024 || n_seqs < 1 || n_seqs > moe::kMaxSeqs) return 0;
+  return moe::balance_ws_layout(T, E, n_seqs).total;
+}
+
+int moe_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* token_mask, int T,
+                     int E, int k, int n_seqs, moe_score score, float* losses, int32_t* counts,
+                     float* probs, int32_t* tokens, void* workspace, size_t workspace_bytes,
+                     void* stream) {
+  if (int st = check_balance(T, E, k, n_seqs, score)) return st;
+  if ((T > 0 && (!logits || !topk_idx)) || !losses || !counts || !probs || !tokens)
+    return fail(MOE_ERR_NULL, "logits, topk_idx, losses, counts, probs and tokens are required");
+  if (!workspace) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
+  const size_t need = moe_balance_loss_workspace_bytes(T, E, n_seqs);
+  if (workspace_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "workspace %zu bytes < %zu required", workspace_bytes, need);
+  if (!aligned16(logits) || !aligned16(topk_idx) || !aligned16(token_mask) || !aligned16(losses) ||
+      !aligned16(counts) || !aligned16(probs) || !aligned16(tokens) || !aligned16(workspace))
+    return fail(MOE_ERR_ALIGN, "device pointers must be 16-byte aligned");
+  int cus = 0;
+  if (int st = device_info(&cus)) return st;
+  return hip_status(moe::launch_balance_loss(logits, topk_idx, token_mask, T, E, k, n_seqs,
+                                             score == MOE_SCORE_SIGMOID, losses, counts, probs, tokens,
+                                             workspace, static_cast<hipStream_t>(stream)),
+                    "moe_balance_loss launch");
+}
+
+int moe_balance_loss_backward(const float* logits, const uint8_t* token_mask, const int32_t* counts,
+                              const int32_t* tokens, const float* d_losses, const float* d_add, int T,
+                              int E, int n_seqs, moe_score score, float* dlogits, void* stream) {
+  if (int st = check_balance(T, E, 1, n_seqs, score)) return st;
+  if (T == 0) return ok();
+  if (!logits || !counts || !tokens || !d_losses || !dlogits)
+    return fail(MOE_ERR_NULL, "logits, counts, tokens, d_losses and dlogits are required");
+  if (!aligned16(logits) || !aligned16(token_mask) || !aligned16(counts) || !aligned16(tokens) ||
+      !aligned16(d_losses) || !aligned16(d_add) || !aligned16(dlogits))
+    return fail(MOE_ERR_ALIGN, "device pointers must be 16-byte aligned");
+  int cus = 0;
+  if (int st = device_info(&cus)) return st;
+  return hip_status(moe::launch_balance_loss_backward(logits, token_mask, counts, tokens, d_losses, d_add,
+                                                      T, E, n_seqs, score == MOE_SCORE_SIGMOID, dlogits,
+                                                      static_cast<hipStream_t>(stream)),
+                    "moe_balance_loss_backward launch");
 }
 
 }  // extern "C"

@@ -1,5 +1,6 @@
 // Launch wrappers of the operators around the routed experts (norm.hip,
-// route_scored.hip, int8.hip), between the C ABI (abi.cpp) and their kernels.
+// route_scored.hip, int8.hip, mxfp4.hip, balance.hip), between the C ABI (abi.cpp) and
+// their kernels.
 // Arguments have been validated by the caller; each returns hipGetLastError()
 // after its launches.
 #pragma once
@@ -10,7 +11,7 @@ namespace moe {
 
 // Kernel ids of the timing hook, after internal.h's.
 enum BlockKernelId { kNorm = kKernelCount, kNormBackward, kRouteBackward, kInt8GateUp, kInt8Down,
-                     kAllKernelCount };
+                     kMx4GateUp, kMx4Down, kBalance, kBalanceBackward, kAllKernelCount };
 
 // Rows of one launch with a workgroup of up to 1024 threads each: a grid holds fewer than
 // 2^32 threads.
@@ -49,6 +50,37 @@ hipError_t launch_experts_int8(const int8_t* x, const float* xs, const int8_t* w
                                const float* wgus, const int8_t* wd, const float* wds,
                                const int32_t* idx, const float* w, int T, int H, int I, int E,
                                int k, uint16_t* out, void* ws, hipStream_t s, int num_cus);
+
+// MXFP4 rows, and the experts with MXFP4 weights (mxfp4.hip): byte layout of the workspace,
+// and the whole layer.  a4: MXFP4 activations, else MXFP8.
+hipError_t launch_quant_mx4(const uint16_t* src, int64_t rows, int K, uint8_t* codes, uint8_t* scales,
+                            hipStream_t s);
+hipError_t launch_dequant_mx4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int K,
+                              uint16_t* dst, hipStream_t s);
+struct Mx4Ws {
+  size_t n_tiles, counts, offsets, tiles, perm, row_of, codes, scales, y, total;
+  int max_tiles, bm;
+};
+Mx4Ws mx4_ws_layout(int T, int H, int I, int E, int k, bool a4);
+hipError_t launch_experts_mx4(const uint8_t* x, const uint8_t* xs, bool a4, const uint8_t* wgu,
+                              const uint8_t* wgus, const uint8_t* wd, const uint8_t* wds,
+                              const int32_t* idx, const float* w, int T, int H, int I, int E, int k,
+                              uint16_t* out, void* ws, hipStream_t s, int num_cus);
+
+// The router's balance loss (balance.hip): S sequences of T / S tokens, cut into chunks of
+// `rows` rows, `chunks` to a sequence.
+constexpr int kMaxSeqs = 4096;
+struct BalanceWs {
+  size_t probs, counts, z, tokens, total;
+  int chunks, rows;
+};
+BalanceWs balance_ws_layout(int T, int E, int S);
+hipError_t launch_balance_loss(const float* logits, const int32_t* idx, const uint8_t* mask, int T, int E,
+                               int k, int S, bool sigmoid, float* losses, int32_t* counts, float* probs,
+                               int32_t* tokens, void* ws, hipStream_t s);
+hipError_t launch_balance_loss_backward(const float* logits, const uint8_t* mask, const int32_t* counts,
+                                        const int32_t* tokens, const float* d_losses, const float* d_add,
+                                        int T, int E, int S, bool sigmoid, float* dlogits, hipStream_t s);
 
 // combine_slots over the columns [col0, col0 + cols) (batched.hip).
 hipError_t launch_combine_slots(const float* y, const int* row_of, const float* w, int T, int H,

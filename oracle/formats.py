@@ -13,6 +13,11 @@
   nearest E4M3 value, ties to even, saturating to +-448.  An all-zero block
   gets scale code 0 and all-zero codes.
 
+* FP4 E2M1 (OCP Microscaling v1.0): 1 sign bit, 2 exponent bits (bias 1), 1
+  mantissa bit; the magnitudes 0, 0.5, 1, 1.5, 2, 3, 4, 6, no infinity or NaN.
+  MXFP4 blocks follow the same rule with s = floor(log2(max |v|)) - 2; two codes
+  share a byte, the even element in the low four bits.
+
 Everything is float64 and exact: scaling by powers of two and the rounding
 below introduce no error beyond the format's own rounding.
 """
@@ -119,3 +124,52 @@ def mx_dequantize(codes, scales, block: int = 32) -> np.ndarray:
     K = c.shape[-1]
     s = e8m0_decode(scales)
     return (c.reshape(c.shape[:-1] + (K // block, block)) * s[..., None]).reshape(c.shape)
+
+
+# E2M1 magnitudes by code
+_E2M1_VALUES = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+E2M1_MAX = 6.0
+
+
+def e2m1_decode(codes) -> np.ndarray:
+    """E2M1 codes 0..15 -> float64 (exact)."""
+    c = np.asarray(codes, dtype=np.int64)
+    return np.where(c & 8, -1.0, 1.0) * _E2M1_VALUES[c & 7]
+
+
+def e2m1_encode(v) -> np.ndarray:
+    """float64 -> E2M1 code 0..15 (uint8), round to nearest, ties to the even code, saturating to
+    +-6.  Inputs must be finite.  -0.0 encodes as 8."""
+    v = np.asarray(v, dtype=np.float64)
+    if not np.all(np.isfinite(v)):
+        raise ValueError("e2m1_encode: non-finite input")
+    # the midpoints between neighbours; a tie goes to the lower code if that is even
+    mid = (_E2M1_VALUES[1:] + _E2M1_VALUES[:-1]) / 2
+    a = np.abs(v)
+    code = np.zeros(v.shape, dtype=np.int64)
+    for i, m in enumerate(mid):
+        code += (a > m) if i % 2 == 0 else (a >= m)
+    return (code | (np.signbit(v).astype(np.int64) << 3)).astype(np.uint8)
+
+
+def mxfp4_scale(amax) -> np.ndarray:
+    """The block's scale exponent s."""
+    amax = np.asarray(amax, dtype=np.float64)
+    _, ex = np.frexp(amax)
+    return np.where(amax == 0.0, -127, np.clip(ex.astype(np.int64) - 3, -127, 127))
+
+
+def mxfp4_quantize(v):
+    """Blocks of 32 along the last axis -> (bytes uint8 [..., K/2], scale codes uint8 [..., K/32])."""
+    v = np.asarray(v, dtype=np.float64)
+    blocks = v.reshape(v.shape[:-1] + (v.shape[-1] // 32, 32))
+    s = mxfp4_scale(np.abs(blocks).max(axis=-1))
+    codes = e2m1_encode(blocks / np.exp2(s.astype(np.float64))[..., None]).reshape(v.shape)
+    return codes[..., 0::2] | (codes[..., 1::2] << 4), (s + 127).astype(np.uint8)
+
+
+def mxfp4_dequantize(packed, scales) -> np.ndarray:
+    p = np.asarray(packed, dtype=np.uint8)
+    c = e2m1_decode(np.stack([p & 15, p >> 4], axis=-1).reshape(p.shape[:-1] + (2 * p.shape[-1],)))
+    s = e8m0_decode(scales)
+    return (c.reshape(c.shape[:-1] + (c.shape[-1] // 32, 32)) * s[..., None]).reshape(c.shape)
