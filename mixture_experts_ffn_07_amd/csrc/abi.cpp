@@ -18,6 +18,7 @@ hipError_t decode_set_attributes();
 hipError_t batched_set_attributes();
 hipError_t backward_set_attributes();
 hipError_t int8_set_attributes();
+hipError_t mx4_set_attributes();
 
 ProfileHook& profile_hook() {
   thread_local ProfileHook hook;
@@ -86,6 +87,7 @@ int device_info(int* num_cus, void** scratch = nullptr) {
     if (e == hipSuccess) e = moe::batched_set_attributes();
     if (e == hipSuccess) e = moe::backward_set_attributes();
     if (e == hipSuccess) e = moe::int8_set_attributes();
+    if (e == hipSuccess) e = moe::mx4_set_attributes();
     if (e != hipSuccess) return fail(MOE_ERR_HIP, "hipFuncSetAttribute: %s", hipGetErrorString(e));
     // the device address of this device's scratch array (the device is current)
     e = moe::static_scratch(dev, &d.scratch);

@@ -58,7 +58,7 @@ hipError_t launch_quant_mx4(const uint16_t* src, int64_t rows, int K, uint8_t* c
 hipError_t launch_dequant_mx4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int K,
                               uint16_t* dst, hipStream_t s);
 struct Mx4Ws {
-  size_t n_tiles, counts, offsets, tiles, perm, row_of, codes, scales, y, total;
+  size_t n_tiles, counts, offsets, tiles, perm, row_of, codes, scales, y, partial, wgu_t, wd_t, x_t, total;
   int max_tiles, bm;
 };
 Mx4Ws mx4_ws_layout(int T, int H, int I, int E, int k, bool a4);

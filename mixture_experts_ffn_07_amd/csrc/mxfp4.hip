@@ -8,8 +8,11 @@
 // group_experts (expert-grouped rows, as the other batched forms), the gate/up product with
 // SwiGLU and the encoding in its epilogue, the down product, the slot sum.  A pair whose
 // expert id lies outside [0, E) has no row: it adds nothing to its token.
+#include <type_traits>
+
 #include "block.h"
 #include "common.h"
+#include "gemm_large.h"
 #include "mxfp4.h"
 #include "tiles.h"
 
@@ -91,19 +94,27 @@ __global__ __launch_bounds__(256) void dequant_mx4_rows(const uint32_t* __restri
 Mx4Ws mx4_ws_layout(int T, int H, int I, int E, int k, bool a4) {
   Mx4Ws L{};
   const size_t P = static_cast<size_t>(T) * k;
-  L.bm = kBM4;
+  L.bm = P >= 256 * static_cast<size_t>(E) ? kLargeBM : kBM4;
   L.max_tiles = static_cast<int>(E + (P + L.bm - 1) / L.bm);
+  const size_t tile_room = E + (P + kBM4 - 1) / kBM4;      // (as many as any smaller T takes)
   size_t o = 0;
   L.n_tiles = o;   o += 256;
   L.counts = o;    o = align256(o + sizeof(int) * E);
   L.offsets = o;   o = align256(o + sizeof(int) * (E + 1));
-  L.tiles = o;     o = align256(o + sizeof(int) * 2 * L.max_tiles);
+  L.tiles = o;     o = align256(o + sizeof(int) * 2 * tile_room);
   L.perm = o;      o = align256(o + sizeof(int) * P);
   L.row_of = o;    o = align256(o + sizeof(int) * P);
   L.codes = o;     o = align256(o + P * (a4 ? I / 2 : I));
   L.scales = o;    o = align256(o + P * (I / 32));
   L.y = o;
   if (k > 1) o = align256(o + sizeof(float) * P * H);
+  L.partial = L.wgu_t = L.wd_t = L.x_t = o;
+  if (L.bm == kLargeBM) {
+    o = align256(o + sizeof(float) * kLargeMaxSlices * kLargeBM * 256);
+    L.wgu_t = o;   o = align256(o + static_cast<size_t>(E) * 2 * I * (H / 32));
+    L.wd_t = o;    o = align256(o + static_cast<size_t>(E) * H * (I / 32));
+    L.x_t = o;     o = align256(o + P * (H / 32));
+  }
   L.total = o;
   return L;
 }
@@ -351,6 +362,577 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == 6
   }
 }
 
+// ---------------------------------------------------------------------------
+// Large groups (hundreds of routed rows per expert and more): the products are bound by the
+// matrix cores and by LDS, and run as an LDS-tiled GEMM.  Workgroup tile 256 rows x 256
+// weight rows (gate_up: 128 gate + 128 up rows of one expert, so that the epilogue finds g
+// and u in one lane); 4 waves of 128 x 128 with the block-scaled 32x32x64 MFMA, accumulators
+// in AGPRs; both tiles staged in LDS, two stages, 16-byte pieces XOR-swizzled by row; global
+// loads one stage ahead of the LDS writes, which run one stage ahead of the fragment reads.
+//
+// A step of 256 positions is four MFMA K steps.  MXFP4 activations: one LDS stage of 128
+// bytes of either row; K step ks takes blocks 4 hi + ks in lane half hi, so a lane's four
+// scale bytes are one dword and ks selects its byte.  MXFP8 activations (a stage of 256
+// positions would not fit): two stages of 128 bytes of activation and 64 of weight row; K
+// step ks of stage st takes blocks 2 hi + (ks & 1) of the stage's four, and the scale bytes
+// are stored in the order that makes these a dword too (scale_place).
+//
+// The scales come straight to registers, a dword a row and step, from copies with the step
+// outside and the row inside (mx4_scales_t; the gate/up epilogue writes h's that way): from
+// rows as they are given, a wave's load would touch 32 lines.
+namespace {
+constexpr int kLTile = kLargeBM * 128;                   // bytes of an operand's stage
+
+// Place, within a row's 8 scale bytes of a step, of the byte of block b.
+template <bool A4>
+__host__ __device__ constexpr int scale_place(int b) {
+  return A4 ? b : 4 * (b >> 1 & 1) + 2 * (b >> 2) + (b & 1);
+}
+
+template <bool A4>
+constexpr size_t large4_lds() {
+  return A4 ? 2 * 2 * kLTile : 2 * (kLTile + kLTile / 2);
+}
+constexpr size_t kLSide = 3 * sizeof(int) * kLargeBM;    // (down: the rows' pair ids and weights)
+
+// 32x32x64 with weights w (E2M1) and activations x (E2M1 or E4M3); XW: the activation rows
+// along the result's registers and the weight rows along its lanes, else the other way.
+template <bool A4, bool XW, int SEL>
+__device__ __forceinline__ f32x16 mfma_mx4_32(i32x4 w, i32x8 x, uint32_t sw, uint32_t sx, f32x16 c) {
+  const i32x8 w8 = {w[0], w[1], w[2], w[3], 0, 0, 0, 0};
+  if (XW)
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, w8, c, A4 ? 4 : 0, 4, SEL, static_cast<int>(sx),
+                                                           SEL, static_cast<int>(sw));
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w8, x, c, 4, A4 ? 4 : 0, SEL, static_cast<int>(sw),
+                                                         SEL, static_cast<int>(sx));
+}
+
+// SwiGLU and the MX codes of two 32-neuron blocks of one row: the lanes (l32, hi = 0 / 1) of
+// a row hold neurons 8q + 4hi + t in register 4q + t; each encodes its half of both blocks,
+// and the lanes exchange halves, so that lane hi stores block hi, n + 32 hi on.
+template <bool A4>
+__device__ __forceinline__ void mx4_store_row(const f32x16 (&g)[2], const f32x16 (&u)[2], int r, int mcount,
+                                              int rbase, int n, int hi, int I, int P,
+                                              uint8_t* __restrict__ hq, uint8_t* __restrict__ hs) {
+  uint32_t c[2][4];
+  int sx[2];
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    float v[16], top = 0.f;
+#pragma unroll
+    for (int x = 0; x < 16; ++x) {
+      v[x] = swiglu4(g[b][x], u[b][x]);
+      top = fmaxf(top, fabsf(v[x]));
+    }
+    top = fmaxf(top, __shfl_xor(top, 32, kWave));
+    sx[b] = A4 ? mx4_scale_exp(top) : mx_scale_exp(top);
+    const float inv = exp2_neg(sx[b]);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float a0 = v[4 * q] * inv, a1 = v[4 * q + 1] * inv, a2 = v[4 * q + 2] * inv, a3 = v[4 * q + 3] * inv;
+      c[b][q] = A4 ? f32x4_to_e2m1x4(a0, a1, a2, a3) : f32x4_to_e4m3x4(a0, a1, a2, a3);
+    }
+  }
+  // what the other lane stores goes there; bytes of quad q: those of lane hi = 0, then of 1
+  uint32_t own[4], got[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    own[q] = hi ? c[1][q] : c[0][q];
+    got[q] = hi ? c[0][q] : c[1][q];
+  }
+  if (A4) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const uint32_t o = static_cast<uint32_t>(__shfl_xor(static_cast<int>(got[2 * p] | got[2 * p + 1] << 16), 32, kWave));
+      got[2 * p] = o & 0xFFFFu;
+      got[2 * p + 1] = o >> 16;
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) got[q] = static_cast<uint32_t>(__shfl_xor(static_cast<int>(got[q]), 32, kWave));
+  }
+  if (r >= mcount) return;
+  const int nb = n + 32 * hi;
+  const size_t row = static_cast<size_t>(rbase + r);
+  if (A4) {
+    i32x4 o;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) o[q] = static_cast<int>(hi ? got[q] | own[q] << 16 : own[q] | got[q] << 16);
+    st16(hq + row * (I / 2) + nb / 2, o);
+  } else {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      i32x4 o;
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        o[2 * z] = static_cast<int>(hi ? got[2 * p + z] : own[2 * p + z]);
+        o[2 * z + 1] = static_cast<int>(hi ? own[2 * p + z] : got[2 * p + z]);
+      }
+      st16(hq + row * I + nb + 16 * p, o);
+    }
+  }
+  hs[(static_cast<size_t>(nb / 256) * P + row) * 8 + scale_place<A4>(nb / 32 % 8)] =
+      static_cast<uint8_t>((hi ? sx[1] : sx[0]) + 127);
+}
+
+// Two lanes that hold neighbouring columns (even, odd) and the values of two rows (v0, v1)
+// exchange one value each: the even lane returns both columns of the first row, the odd
+// lane both of the second, as two BF16 (the lower column in the low half).
+__device__ __forceinline__ uint32_t pair_rows_bf16(float v0, float v1, int odd) {
+  const float give = odd ? v0 : v1;
+  const float got = __int_as_float(__builtin_amdgcn_update_dpp(
+      0, __float_as_int(give), 0xB1, 0xF, 0xF, true));              // quad_perm [1,0,3,2]
+  return odd ? pack_bf16x2(got, v1) : pack_bf16x2(v0, got);
+}
+}  // namespace
+
+// act / acts: the activations' codes and their scales [K/256][rows][8] (grouped rows); wt / wts:
+// the weights' codes and their scales [E][K/256][weight rows][8].  See above.
+template <int KIND, bool A4>
+__global__ __launch_bounds__(256) void gemm_large_mx4(
+    const uint8_t* __restrict__ act, const uint32_t* __restrict__ acts,
+    const uint8_t* __restrict__ wt, const uint32_t* __restrict__ wts, const int* __restrict__ perm,
+    const int2* __restrict__ tiles, const int* __restrict__ n_tiles, const int* __restrict__ counts,
+    const int* __restrict__ offsets, const float* __restrict__ w, int H, int I, int k, int P,
+    uint8_t* __restrict__ hq, uint8_t* __restrict__ hs, float* __restrict__ y,
+    uint16_t* __restrict__ out, float* __restrict__ partial, int ncu, uint32_t okey) {
+  extern __shared__ __align__(16) uint8_t ldl[];         // [stage][weights, activations]
+  constexpr bool GU = KIND == kGateUp4;
+  constexpr int WB = A4 ? 128 : 64;                      // bytes of a weight row per stage
+  constexpr int kWTile = kLargeBM * WB, kStage = kWTile + kLTile;
+  constexpr int NW = WB / 16, NS = NW + 8;               // 16-byte loads per thread and stage: weights, all
+  constexpr int KS = A4 ? 4 : 2;                         // MFMA K steps per stage
+  constexpr int PER = NS / KS;                           // loads and LDS writes per K step
+  const int K = GU ? H : I;
+  const int RB = K / 2, AB = A4 ? K / 2 : K;             // bytes of a row: weights, activations
+  const int nblk = GU ? I / 128 : H / 256;
+  const int nk = K / 256;
+  const int nt = *n_tiles;
+  const TailPlan plan = tail_plan(nblk * nt, ncu, nk);
+  const int L = blockIdx.x;
+  const int tid = threadIdx.x, wv = tid >> 6, ln = tid & 63, l32 = ln & 31, hi = ln >> 5;
+  const int wm = wv & 1, wn = wv >> 1;
+  int item, kb = 0, ke = nk, slot = -1;                  // slot >= 0: a slice of a tile of the last round
+  if (plan.S > 1 && L < plan.full) {
+    item = permute_item(round_item(L, plan.full, ncu), plan.full, okey);
+  } else if (plan.S > 1) {
+    if (L - plan.full >= plan.rem * plan.S) return;
+    slot = permute_item(L - plan.full, plan.rem * plan.S, okey);
+    item = plan.full + slot % plan.rem;
+    const int sl = slot / plan.rem;
+    kb = sl * nk / plan.S;
+    ke = (sl + 1) * nk / plan.S;
+  } else {
+    item = round_real_item(L, nblk, nt, ncu);
+    if (item < 0) return;
+    item = permute_item(item, nblk * nt, okey);
+  }
+  int tile, nb;
+  large_coords(item, nblk, nt, tile, nb);
+  const int2 te = tiles[tile];
+  const int e = te.x, m0 = te.y;
+  const int mcount = min(kLargeBM, counts[e] - m0);
+  const int rbase = offsets[e] + m0;
+  const int n0 = nb * 128;
+
+  // loaders.  Activations (and weights of 128 bytes a stage): rows wv*64 + 8j + (ln >> 3), piece
+  // ln & 7; weights of 64 bytes: rows wv*64 + 16j + (ln >> 2), piece ln & 3
+  const int lrow = ln >> 3, lc = ln & 7;
+  const int wrow = A4 ? lrow : ln >> 2, wc = A4 ? lc : ln & 3;
+  const size_t wrows = GU ? 2 * static_cast<size_t>(I) : static_cast<size_t>(H);
+  const uint8_t* __restrict__ abase = wt + static_cast<size_t>(e) * wrows * RB;
+  const int arow = GU ? (wv < 2 ? n0 + wv * 64 : I + n0 + (wv - 2) * 64) : nb * 256 + wv * 64;
+  const uint32_t ao = static_cast<uint32_t>((arow + wrow) * RB + wc * 16);
+  uint32_t bo[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const int r = wv * 64 + 8 * j + lrow, rr = r < mcount ? r : 0;
+    bo[j] = static_cast<uint32_t>((GU ? perm[rbase + rr] / k : rbase + rr) * AB + lc * 16);
+  }
+  // LDS: piece c of row r of 128 bytes at c ^ (r >> 1 & 7), of 64 bytes at c ^ (r >> 2 & 3): the
+  // 16 rows that a read serves at once lie in 64 different banks
+  const int lx0 = (wv * 64 + lrow) * 128 + ((lc ^ (lrow >> 1)) * 16);      // even j; odd j: the piece ^ 4
+  const int lx1 = lx0 ^ 64;
+  const int lw0 = A4 ? lx0 : (wv * 64 + wrow) * 64 + ((wc ^ (wrow >> 2 & 3)) * 16);
+  int fa[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    fa[i] = (GU ? (i >> 1) * 128 + wn * 64 + (i & 1) * 32 : wn * 128 + 32 * i) + l32;
+  const int fb = wm * 128 + l32;
+  const int swx = l32 >> 1 & 7, sww = A4 ? swx : l32 >> 2 & 3;
+  // scales: dword hi of row fa[i] of the weight tile, of row fb + 32 j of the activations
+  uint32_t osa[4], osb[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    osa[i] = static_cast<uint32_t>(GU ? (i >> 1) * I + n0 + wn * 64 + (i & 1) * 32 + l32 : nb * 256 + fa[i]) * 2 + hi;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) osb[j] = static_cast<uint32_t>(rbase + min(fb + 32 * j, mcount - 1)) * 2 + hi;
+  const uint32_t* __restrict__ sab = wts + static_cast<size_t>(e) * nk * wrows * 2;
+
+  i32x4 stg[NS];   // [0, NW) weight rows, [NW, NS) activation rows
+  // stage s covers step s / 2 (MXFP8) or s (MXFP4); past the end the last one again
+  const int s_end = A4 ? ke : 2 * ke;
+  auto gload = [&](int q, int s) {
+    const int ss = min(s, s_end - 1);
+    if (q < NW) stg[q] = ld16(abase + ao + static_cast<uint32_t>(q * (A4 ? 8 : 16)) * RB + static_cast<uint32_t>(ss * WB));
+    else stg[q] = ld16(act + bo[(q - NW) & 7] + static_cast<uint32_t>(ss * 128));
+  };
+  auto lwrite = [&](int q, int s) {
+    uint8_t* st = ldl + (s & 1) * kStage;
+    if (q < NW) *reinterpret_cast<i32x4*>(st + (A4 ? (q & 1 ? lx1 : lx0) + q * 8 * 128 : lw0 + q * 16 * 64)) = stg[q];
+    else *reinterpret_cast<i32x4*>(st + kWTile + (q & 1 ? lx1 : lx0) + ((q - NW) & 7) * 8 * 128) = stg[q];
+  };
+  struct Frag {
+    i32x4 a[4];
+    i32x8 b[4];
+  };
+  // fragment g (0..3) of both operands, K step ks of stage s
+  auto rda = [&](Frag& f, int g, int s, int ks) {
+    const uint8_t* st = ldl + (s & 1) * kStage;
+    f.a[g] = *reinterpret_cast<const i32x4*>(st + fa[g] * WB + (((A4 ? 4 * hi + ks : 2 * hi + ks) ^ sww) * 16));
+  };
+  auto rdb = [&](Frag& f, int g, int s, int ks) {
+    const uint8_t* st = ldl + (s & 1) * kStage + kWTile + (fb + 32 * g) * 128;
+    if (A4) {
+      f.b[g] = cat8(*reinterpret_cast<const i32x4*>(st + ((4 * hi + ks) ^ swx) * 16), i32x4{0, 0, 0, 0});
+    } else {
+      f.b[g] = cat8(*reinterpret_cast<const i32x4*>(st + ((2 * ks + hi) ^ swx) * 16),
+                    *reinterpret_cast<const i32x4*>(st + ((4 + 2 * ks + hi) ^ swx) * 16));
+    }
+  };
+  uint32_t sa[4], sb[4], na[4], nbs[4];
+  auto sload = [&](int kt) {
+    const uint32_t kk = static_cast<uint32_t>(min(kt, ke - 1));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) na[i] = sab[kk * static_cast<uint32_t>(2 * wrows) + osa[i]];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) nbs[j] = acts[static_cast<size_t>(kk) * (2 * static_cast<size_t>(P)) + osb[j]];
+  };
+  f32x16 acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
+  // One MFMA K step on fragments f (scale byte SEL): 8 groups of 2 MFMAs; the first groups read the
+  // fragments of K step rks of stage rs into n, and write PER staged pieces of stage ws to LDS and
+  // reload them from stage ws + 1.  sched_barrier keeps this order.
+  auto phase = [&](auto sel, Frag& f, Frag& n, int rs, int rks, int ws, int q0) {
+    constexpr int SEL = decltype(sel)::value;
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      const int i = g >> 1, j = (g & 1) * 2;
+#pragma unroll
+      for (int z = 0; z < 2; ++z)
+        acc[i][j + z] = mfma_mx4_32<A4, !GU, SEL>(f.a[i], f.b[j + z], sa[i], sb[j + z], acc[i][j + z]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (g < 4) {
+        rda(n, g, rs, rks);
+        rdb(n, g, rs, rks);
+      }
+      if (g < PER) {
+        lwrite(q0 + g, ws);
+        gload(q0 + g, ws + 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // The LDS writes of stage s + 1 are spread over the K steps that may write its buffer: the last
+  // one of stage s - 1 (the last PER pieces, after the barrier that ends the reads of stage s - 1)
+  // and all but the last of stage s (before the barrier that publishes stage s + 1).
+  const int s0 = A4 ? kb : 2 * kb;
+  sload(kb);
+#pragma unroll
+  for (int q = 0; q < NS; ++q) gload(q, s0);
+#pragma unroll
+  for (int q = 0; q < NS; ++q) lwrite(q, s0);
+#pragma unroll
+  for (int q = 0; q < NS; ++q) gload(q, s0 + 1);
+#pragma unroll
+  for (int q = NS - PER; q < NS; ++q) {
+    lwrite(q, s0 + 1);
+    gload(q, s0 + 2);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    sa[i] = na[i];
+    sb[i] = nbs[i];
+  }
+  __syncthreads();
+  Frag f0, f1;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    rda(f0, g, s0, 0);
+    rdb(f0, g, s0, 0);
+  }
+  // the epilogue's data (tile row tid's pair and weight)
+  const int my_pr = GU ? 0 : perm[rbase + min(tid, mcount - 1)];
+  float my_w = 0.f;
+  auto publish = [&]() {
+    wait_lgkm0();
+    __builtin_amdgcn_s_barrier();
+  };
+  using std::integral_constant;
+  for (int kt = kb; kt < ke; ++kt) {
+    sload(kt + 1);
+    if (A4) {
+      phase(integral_constant<int, 0>{}, f0, f1, kt, 1, kt + 1, 0);
+      phase(integral_constant<int, 1>{}, f1, f0, kt, 2, kt + 1, PER);
+      phase(integral_constant<int, 2>{}, f0, f1, kt, 3, kt + 1, 2 * PER);
+      publish();
+      // In the loop on purpose: a loop of one basic block would keep a copy of the accumulators
+      // outside the AGPRs for the code after it.
+      if (KIND == kDownFused4 && kt == kb) my_w = w[my_pr];          // k = 1: pair id == token
+      phase(integral_constant<int, 3>{}, f1, f0, kt + 1, 0, kt + 2, 3 * PER);
+    } else {
+      phase(integral_constant<int, 0>{}, f0, f1, 2 * kt, 1, 2 * kt + 1, 0);
+      publish();
+      phase(integral_constant<int, 1>{}, f1, f0, 2 * kt + 1, 0, 2 * kt + 2, PER);
+      if (KIND == kDownFused4 && kt == kb) my_w = w[my_pr];
+      phase(integral_constant<int, 2>{}, f0, f1, 2 * kt + 1, 1, 2 * kt + 2, 0);
+      publish();
+      phase(integral_constant<int, 3>{}, f1, f0, 2 * kt + 2, 0, 2 * kt + 3, PER);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sa[i] = na[i];
+      sb[i] = nbs[i];
+    }
+  }
+  if (slot >= 0) {
+    // tail slice: FP32 partial tile in register order, [64 x f32x4][256 threads]
+    f32x4* pp = reinterpret_cast<f32x4*>(partial) + static_cast<size_t>(slot) * 64 * 256 + tid;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        asm volatile("" : "+a"(acc[i][j]));
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          pp[((i * 4 + j) * 4 + q) * 256] =
+              f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+      }
+    return;
+  }
+  if (GU) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) asm volatile("" : "+a"(acc[i][j]));
+      const f32x16 g[2] = {acc[0][j], acc[1][j]}, u[2] = {acc[2][j], acc[3][j]};
+      mx4_store_row<A4>(g, u, wm * 128 + 32 * j + l32, mcount, rbase, n0 + wn * 64, hi, I, P, hq, hs);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    return;
+  }
+  // Lane (l32, hi), register 4q + t of block (i, j): output column l32 of weight block i, tile row
+  // 8q + 4hi + t of row block j: a store instruction writes 128 consecutive bytes of two rows (FP32),
+  // or 64 of four (BF16, columns paired over lanes).
+  int* s_pr = reinterpret_cast<int*>(ldl + large4_lds<A4>());
+  float* s_w = reinterpret_cast<float*>(ldl + large4_lds<A4>()) + kLargeBM;
+  s_pr[tid] = my_pr;
+  s_w[tid] = my_w;
+  __syncthreads();
+  auto store = [&](auto whole) {
+    constexpr bool kWhole = decltype(whole)::value;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (q == 0)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) asm volatile("" : "+a"(acc[i][j]));
+        __builtin_amdgcn_sched_barrier(0);
+        const int r0 = wm * 128 + 32 * j + 8 * q + 4 * hi;
+        if (!kWhole && r0 >= mcount) continue;
+        if (KIND == kDownFused4) {
+          const i32x4 pr = *reinterpret_cast<const i32x4*>(s_pr + r0);
+          const f32x4 wt4 = *reinterpret_cast<const f32x4*>(s_w + r0);
+          const int odd = l32 & 1;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint16_t* orow = out + static_cast<size_t>(odd ? pr[2 * h + 1] : pr[2 * h]) * H + nb * 256 + wn * 128 + l32 - odd;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t o = pair_rows_bf16(wt4[2 * h] * acc[i][j][4 * q + 2 * h],
+                                                wt4[2 * h + 1] * acc[i][j][4 * q + 2 * h + 1], odd);
+              if (kWhole || r0 + 2 * h + odd < mcount) *reinterpret_cast<uint32_t*>(orow + 32 * i) = o;
+            }
+          }
+        } else {
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            if (!kWhole && r0 + t >= mcount) continue;
+            float* yr = y + static_cast<size_t>(rbase + r0 + t) * H + nb * 256 + wn * 128 + l32;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) yr[32 * i] = acc[i][j][4 * q + t];
+          }
+        }
+      }
+  };
+  if (mcount == kLargeBM) store(std::true_type{});
+  else store(std::false_type{});
+}
+
+// Tail fix-up: the slices of a tile of the last round, added in slice order, and the epilogue.
+// gate_up: workgroup (tail item, row block j), a GEMM thread's blocks of that j each; down:
+// element-parallel, an f32x4 of the partial tile to a thread.
+template <bool A4>
+__global__ __launch_bounds__(256) void gemm_large_mx4_fixup_gate_up(
+    const int2* __restrict__ tiles, const int* __restrict__ n_tiles, const int* __restrict__ counts,
+    const int* __restrict__ offsets, int H, int I, int P, uint8_t* __restrict__ hq,
+    uint8_t* __restrict__ hs, const float* __restrict__ partial, int ncu, uint32_t okey) {
+  const int nblk = I / 128;
+  const TailPlan plan = tail_plan(nblk * *n_tiles, ncu, H / 256);
+  const int g = permute_item(blockIdx.x, gridDim.x, okey);
+  const int b = g >> 2, j = g & 3;
+  if (plan.S == 1 || b >= plan.rem) return;
+  int tile, nb;
+  large_coords(plan.full + b, nblk, *n_tiles, tile, nb);
+  const int2 te = tiles[tile];
+  const int e = te.x, m0 = te.y;
+  const int mcount = min(kLargeBM, counts[e] - m0);
+  const int rbase = offsets[e] + m0;
+  const int tid = threadIdx.x, wv = tid >> 6, ln = tid & 63, l32 = ln & 31, hi = ln >> 5;
+  const int wm = wv & 1, wn = wv >> 1;
+  if (wm * 128 + 32 * j >= mcount) return;               // (uniform in the wave)
+  f32x16 acc[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int q = 0; q < 16; ++q) acc[i][q] = 0.f;
+  for (int sl = 0; sl < plan.S; ++sl) {
+    const f32x4* pp = reinterpret_cast<const f32x4*>(partial) + static_cast<size_t>(sl * plan.rem + b) * 64 * 256 + tid;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const f32x4 v = pp[((i * 4 + j) * 4 + q) * 256];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) acc[i][4 * q + t] += v[t];
+      }
+  }
+  const f32x16 gg[2] = {acc[0], acc[1]}, uu[2] = {acc[2], acc[3]};
+  mx4_store_row<A4>(gg, uu, wm * 128 + 32 * j + l32, mcount, rbase, nb * 128 + wn * 64, hi, I, P, hq, hs);
+}
+
+template <int KIND>
+__global__ __launch_bounds__(256) void gemm_large_mx4_fixup_down(
+    const int* __restrict__ perm, const int2* __restrict__ tiles, const int* __restrict__ n_tiles,
+    const int* __restrict__ counts, const int* __restrict__ offsets, const float* __restrict__ w, int H,
+    int I, float* __restrict__ y, uint16_t* __restrict__ out, const float* __restrict__ partial, int ncu,
+    uint32_t okey) {
+  const int nblk = H / 256;
+  const TailPlan plan = tail_plan(nblk * *n_tiles, ncu, I / 256);
+  const int g = permute_item(blockIdx.x, gridDim.x, okey) * 256 + threadIdx.x;
+  const int b = g >> 14;                                  // 64 x 256 threads per tail item
+  if (plan.S == 1 || b >= plan.rem) return;
+  const int f = g & 16383;                                // f32x4 index within the tile
+  const int tid = f & 255, ijq = f >> 8;
+  const int i = ijq >> 4, j = (ijq >> 2) & 3, q = ijq & 3;
+  int tile, nb;
+  large_coords(plan.full + b, nblk, *n_tiles, tile, nb);
+  const int2 te = tiles[tile];
+  const int e = te.x, m0 = te.y;
+  const int mcount = min(kLargeBM, counts[e] - m0);
+  const int rbase = offsets[e] + m0;
+  const int wv = tid >> 6, ln = tid & 63, l32 = ln & 31, hi = ln >> 5;
+  const int wm = wv & 1, wn = wv >> 1;
+  const int r0 = wm * 128 + 32 * j + 8 * q + 4 * hi;      // rows r0 .. r0 + 3, one column
+  if (r0 >= mcount) return;
+  const f32x4* pp = reinterpret_cast<const f32x4*>(partial) + f;
+  f32x4 a = {0.f, 0.f, 0.f, 0.f};
+  for (int sl = 0; sl < plan.S; ++sl) a += pp[static_cast<size_t>(sl * plan.rem + b) * 64 * 256];
+  const int n = nb * 256 + wn * 128 + 32 * i + l32;
+  for (int t = 0; t < 4 && r0 + t < mcount; ++t) {
+    const int row = rbase + r0 + t;
+    if (KIND == kDownFused4) {
+      const int pr = perm[row];
+      out[static_cast<size_t>(pr) * H + n] = static_cast<uint16_t>(f32_to_bf16_rne(w[pr] * a[t]));
+    } else {
+      y[static_cast<size_t>(row) * H + n] = a[t];
+    }
+  }
+}
+
+// Scales with the step of 256 positions outside and the row inside, 8 bytes each in the order of
+// scale_place, of both weights and of the routed activations (gathered into grouped order):
+// workgroup = 64 rows x 32 steps through LDS, reads and writes along their own rows.  With one
+// slot, output rows of pairs without an expert are cleared here.
+template <bool A4>
+__global__ __launch_bounds__(256) void mx4_scales_t(
+    const uint2* __restrict__ wgus, const uint2* __restrict__ wds, const uint2* __restrict__ xs,
+    const int* __restrict__ perm, const int* __restrict__ row_of, const int* __restrict__ offsets, int H,
+    int I, int E, int k, int P, uint2* __restrict__ wgu_t, uint2* __restrict__ wd_t, uint2* __restrict__ x_t,
+    uint16_t* __restrict__ out, uint32_t okey) {
+  __shared__ uint2 tile[32][65];
+  const int tid = threadIdx.x;
+  if (out)
+    for (int b = blockIdx.x; b < P; b += gridDim.x)
+      if (row_of[b] >= P)
+        for (int c = tid; c < H / 8; c += 256) st16(out + static_cast<size_t>(b) * H + 8 * c, i32x4{0, 0, 0, 0});
+  const int nh = H / 256, ni = I / 256;                   // steps of a row
+  const int ch = (nh + 31) / 32, ci = (ni + 31) / 32;     // blocks of 32 steps
+  const int gu = 2 * I / 64, dn = H / 64;                 // blocks of 64 rows (H and I multiples of 256)
+  int b = permute_item(blockIdx.x, gridDim.x, okey);
+  const uint2* src;
+  uint2* dst;
+  int rows, steps, r0, s0, limit;
+  bool gather = false;
+  if (b < E * gu * ch) {
+    const int e = b / (gu * ch), m = b - e * gu * ch;
+    rows = 2 * I, steps = nh, r0 = m / ch * 64, s0 = m % ch * 32, limit = rows;
+    src = wgus + static_cast<size_t>(e) * rows * steps;
+    dst = wgu_t + static_cast<size_t>(e) * rows * steps;
+  } else if ((b -= E * gu * ch) < E * dn * ci) {
+    const int e = b / (dn * ci), m = b - e * dn * ci;
+    rows = H, steps = ni, r0 = m / ci * 64, s0 = m % ci * 32, limit = rows;
+    src = wds + static_cast<size_t>(e) * rows * steps;
+    dst = wd_t + static_cast<size_t>(e) * rows * steps;
+  } else {
+    b -= E * dn * ci;
+    rows = P, steps = nh, r0 = b / ch * 64, s0 = b % ch * 32, limit = offsets[E];
+    src = xs;
+    dst = x_t;
+    gather = true;
+  }
+  if (r0 >= limit) return;
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const int r = u * 8 + (tid >> 5), s = tid & 31;
+    if (r0 + r < limit && s0 + s < steps) {
+      const size_t row = gather ? perm[r0 + r] / k : r0 + r;
+      uint2 v = src[row * steps + s0 + s];
+      if (!A4)                                            // blocks 0, 1, 4, 5 and 2, 3, 6, 7 (scale_place)
+        v = make_uint2((v.x & 0xFFFFu) | v.y << 16, v.x >> 16 | (v.y & 0xFFFF0000u));
+      tile[s][r] = v;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < 8; ++u) {
+    const int s = u * 4 + (tid >> 6), r = tid & 63;
+    if (r0 + r < limit && s0 + s < steps) dst[static_cast<size_t>(s0 + s) * rows + r0 + r] = tile[s][r];
+  }
+}
+
+hipError_t mx4_set_attributes() {
+  hipError_t e = hipSuccess;
+#define LDS(F, A4)                                                                              \
+  if (e == hipSuccess)                                                                          \
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(F), hipFuncAttributeMaxDynamicSharedMemorySize, \
+                            static_cast<int>(large4_lds<A4>() + kLSide))
+  LDS((gemm_large_mx4<kGateUp4, true>), true);
+  LDS((gemm_large_mx4<kDown4, true>), true);
+  LDS((gemm_large_mx4<kDownFused4, true>), true);
+  LDS((gemm_large_mx4<kGateUp4, false>), false);
+  LDS((gemm_large_mx4<kDown4, false>), false);
+  LDS((gemm_large_mx4<kDownFused4, false>), false);
+#undef LDS
+  return e;
+}
+
 // The MX rows' launches: grids of fewer than 2^32 threads.
 constexpr int64_t kMx4Launch = int64_t(1) << 31;
 
@@ -398,6 +980,44 @@ hipError_t launch_experts_mx4(const uint8_t* x, const uint8_t* xs, bool a4, cons
   float* y = reinterpret_cast<float*>(b + L.y);
   if (const hipError_t e = launch_group_experts(idx, P, E, L.bm, counts, offsets, tiles, n_tiles, perm, row_of, s);
       e != hipSuccess) return e;
+  if (L.bm == kLargeBM) {
+    float* partial = reinterpret_cast<float*>(b + L.partial);
+    uint8_t *wgu_t = reinterpret_cast<uint8_t*>(b + L.wgu_t), *wd_t = reinterpret_cast<uint8_t*>(b + L.wd_t),
+            *x_t = reinterpret_cast<uint8_t*>(b + L.x_t);
+    // grid: every item whole, plus room for the tail slices (rem * S - rem < ncu)
+    auto grid = [&](int nblk) { return dim3(round_up(nblk * L.max_tiles + num_cus, kXcds)); };
+    const int ch = (H / 256 + 31) / 32, ci = (I / 256 + 31) / 32;
+    const dim3 tgrid(E * (2 * I / 64) * ch + E * (H / 64) * ci + (P + 63) / 64 * ch);
+#define LARGE4(A4, KD, A, AS, W, WS, Y, O, NBLK)                                                  \
+  hipLaunchKernelGGL((gemm_large_mx4<KD, A4>), grid(NBLK), dim3(256), large4_lds<A4>() + kLSide, s, A, \
+                     reinterpret_cast<const uint32_t*>(AS), W, reinterpret_cast<const uint32_t*>(WS), perm, \
+                     tiles, n_tiles, counts, offsets, w, H, I, k, P, hq, hs, Y, O, partial, num_cus, order_key())
+#define LAYER4(A4)                                                                                \
+  do {                                                                                            \
+    prof_begin(kMx4GateUp, s);                                                                    \
+    hipLaunchKernelGGL(mx4_scales_t<A4>, tgrid, dim3(256), 0, s, reinterpret_cast<const uint2*>(wgus), \
+                       reinterpret_cast<const uint2*>(wds), reinterpret_cast<const uint2*>(xs), perm, row_of, \
+                       offsets, H, I, E, k, P, reinterpret_cast<uint2*>(wgu_t), reinterpret_cast<uint2*>(wd_t), \
+                       reinterpret_cast<uint2*>(x_t), k == 1 ? out : nullptr, order_key());       \
+    LARGE4(A4, kGateUp4, x, x_t, wgu, wgu_t, nullptr, nullptr, I / 128);                          \
+    hipLaunchKernelGGL(gemm_large_mx4_fixup_gate_up<A4>, dim3(num_cus / 2 * 4), dim3(256), 0, s, tiles, n_tiles, \
+                       counts, offsets, H, I, P, hq, hs, partial, num_cus, order_key());          \
+    prof_end(kMx4GateUp, s);                                                                      \
+    prof_begin(kMx4Down, s);                                                                      \
+    if (k == 1) LARGE4(A4, kDownFused4, hq, hs, wd, wd_t, nullptr, out, H / 256);                 \
+    else LARGE4(A4, kDown4, hq, hs, wd, wd_t, y, nullptr, H / 256);                               \
+  } while (0)
+    if (a4) LAYER4(true);
+    else LAYER4(false);
+#undef LAYER4
+#undef LARGE4
+#define FIXUP4(KD)                                                                                \
+  hipLaunchKernelGGL(gemm_large_mx4_fixup_down<KD>, dim3(num_cus / 2 * 64), dim3(256), 0, s, perm, tiles, n_tiles, \
+                     counts, offsets, w, H, I, y, out, partial, num_cus, order_key())
+    if (k == 1) FIXUP4(kDownFused4);
+    else FIXUP4(kDown4);
+#undef FIXUP4
+  } else {
 #define STREAM4(KD, A, AS, W, WS, Y, O, NBLK)                                                    \
   do {                                                                                           \
     const dim3 grid_(round_up((NBLK) * L.max_tiles, kXcds));                                     \
@@ -408,13 +1028,14 @@ hipError_t launch_experts_mx4(const uint8_t* x, const uint8_t* xs, bool a4, cons
       hipLaunchKernelGGL((gemm_mx4s<KD, 8, kBM4, false>), grid_, dim3(512), 0, s, A, AS, W, WS, perm, tiles, \
                          n_tiles, counts, offsets, row_of, w, H, I, k, P, hq, hs, Y, O, order_key()); \
   } while (0)
-  prof_begin(kMx4GateUp, s);
-  STREAM4(kGateUp4, x, xs, wgu, wgus, nullptr, k == 1 ? out : nullptr, I / 128);
-  prof_end(kMx4GateUp, s);
-  prof_begin(kMx4Down, s);
-  if (k == 1) STREAM4(kDownFused4, hq, hs, wd, wds, nullptr, out, H / 256);
-  else STREAM4(kDown4, hq, hs, wd, wds, y, nullptr, H / 256);
+    prof_begin(kMx4GateUp, s);
+    STREAM4(kGateUp4, x, xs, wgu, wgus, nullptr, k == 1 ? out : nullptr, I / 128);
+    prof_end(kMx4GateUp, s);
+    prof_begin(kMx4Down, s);
+    if (k == 1) STREAM4(kDownFused4, hq, hs, wd, wds, nullptr, out, H / 256);
+    else STREAM4(kDown4, hq, hs, wd, wds, y, nullptr, H / 256);
 #undef STREAM4
+  }
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && k > 1) e = launch_combine_slots(y, row_of, w, T, H, k, out, 0, H, H, s, num_cus);
   prof_end(kMx4Down, s);
