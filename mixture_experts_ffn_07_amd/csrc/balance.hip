@@ -19,78 +19,133 @@ namespace moe {
 namespace {
 
 constexpr float kMaskedLogit = -3.3895313892515355e38f;   // BF16's lowest finite value
-constexpr int kRowWaves = 4;                              // waves of a workgroup, a row at a time each
+constexpr int kRowWaves = 8;                              // waves of a workgroup of rows
 
 inline size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
-// exp(x) within two units in the last place: the product x log2(e) in two parts, where the
-// hardware's exp2 of the rounded one alone is |x| 2^-25 off.  x <= 0 here.
+// exp(x), x <= 0, within two units in the last place: the product x log2(e) in two parts, where
+// the hardware's exp2 of the rounded one alone is |x| 2^-25 off.  (0 below -200.)
 __device__ __forceinline__ float exp_fine(float x) {
+  x = fmaxf(x, -200.f);
   const float h = x * 1.44269502f;
   const float l = fmaf(x, 1.92596300e-8f, fmaf(x, 1.44269502f, -h));
   return __builtin_amdgcn_exp2f(h) * fmaf(l, 0.693147182f, 1.0f);
 }
 __device__ __forceinline__ float log_fine(float x) { return __builtin_amdgcn_logf(x) * 0.693147182f; }
 
-__device__ __forceinline__ float wave_max(float v) {
+// Reductions of R values at once over the wave, the results uniform: within rows of 16 lanes by
+// lane permutations in the vector unit, then over the four rows.
+template <int CTRL>
+__device__ __forceinline__ float lanes(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float lane_of(float v, int l) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), l));
+}
+template <int R, bool MAX>
+__device__ __forceinline__ void reduce_rows(float (&v)[R]) {
+#define STEP(CTRL)                                                      \
+  _Pragma("unroll") for (int j = 0; j < R; ++j) {                       \
+    const float o = lanes<CTRL>(v[j]);                                  \
+    v[j] = MAX ? fmaxf(v[j], o) : v[j] + o;                             \
+  }
+  STEP(0xB1) STEP(0x4E) STEP(0x141) STEP(0x140)
+#undef STEP
 #pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v = fmaxf(v, __shfl_xor(v, m, kWave));
-  return v;
+  for (int j = 0; j < R; ++j) {
+    const float a = lane_of(v[j], 0), b = lane_of(v[j], 16), c = lane_of(v[j], 32), d = lane_of(v[j], 48);
+    v[j] = MAX ? fmaxf(fmaxf(a, b), fmaxf(c, d)) : (a + b) + (c + d);
+  }
 }
 
-// One row's scores: lane holds experts lane + 64 i in l (masked ones -inf).  p normalised
-// scores, q softmax, both 0 where masked; returns lse (0 for a row without experts).
-// Sigmoid scores are taken relative to exp(min(largest, 0)), so that they hold their digits
-// however low they are.
-template <bool SIG, int NV>
-__device__ __forceinline__ float row_scores(const float (&l)[NV], float (&p)[NV], float (&q)[NV]) {
-  float m = l[0];
+// Experts of a lane: pairs of neighbours (V = 2, even E) or single ones, NV in all.
+template <int V>
+__device__ __forceinline__ int expert_of(int i) {
+  return V == 2 ? 128 * (i >> 1) + 2 * lane_id() + (i & 1) : 64 * i + lane_id();
+}
+
+// A row's values, `rest` past its end.
+template <int V, int NV>
+__device__ __forceinline__ void load_row(const float* __restrict__ row, int E, float rest, float (&l)[NV]) {
 #pragma unroll
-  for (int i = 1; i < NV; ++i) m = fmaxf(m, l[i]);
-  m = wave_max(m);
-  if (m == -INFINITY) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) p[i] = q[i] = 0.f;
-    return 0.f;
+  for (int i = 0; i < NV; i += V) {
+    const int e = expert_of<V>(i);
+    if (V == 2) {
+      const float2 v = e < E ? *reinterpret_cast<const float2*>(row + e) : make_float2(rest, rest);
+      l[i] = v.x;
+      l[i + V - 1] = v.y;
+    } else {
+      l[i] = e < E ? row[e] : rest;
+    }
   }
-  float z = 0.f;
+}
+
+// Scores of R rows: p normalised scores, q softmax, both 0 where masked, slope 1 - sigma (sigmoid
+// scores), lse (0 for a row without experts).  Sigmoid scores are taken relative to
+// exp(min(largest, 0)), so that they hold their digits however low they are.
+template <bool SIG, int R, int NV>
+__device__ __forceinline__ void row_scores(float (&l)[R][NV], float (&p)[R][NV], float (&q)[R][NV],
+                                           float (&slope)[R][SIG ? NV : 1], float (&lse)[R]) {
+  float m[R], z[R], s[R];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    q[i] = exp_fine(fmaxf(l[i] - m, -200.f));             // (-200: exp is 0, and so are its parts)
-    z += q[i];
+  for (int j = 0; j < R; ++j) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)                          // (NaN too is masked)
+      l[j][i] = l[j][i] > kMaskedLogit ? fminf(l[j][i], FLT_MAX) : -INFINITY;
+    m[j] = l[j][0];
+#pragma unroll
+    for (int i = 1; i < NV; ++i) m[j] = fmaxf(m[j], l[j][i]);
   }
-  z = wave_sum(z);
-  const float rz = 1.0f / z;
+  reduce_rows<R, true>(m);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) q[i] *= rz;
-  if (SIG) {
-    const float t = fminf(m, 0.f);
-    float s = 0.f;
+  for (int j = 0; j < R; ++j) {
+    const float top = m[j] == -INFINITY ? 0.f : m[j];
+    z[j] = s[j] = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      p[i] = exp_fine(fmaxf(fminf(l[i], 0.f) - t, -200.f)) / (1.0f + exp_fine(fmaxf(-fabsf(l[i]), -200.f)));
-      s += p[i];
+      q[j][i] = exp_fine(l[j][i] - top);
+      z[j] += q[j][i];
     }
-    s = wave_sum(s);
-    const float rs = 1.0f / s;
+    if (SIG) {
+      const float t = fminf(top, 0.f);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) p[i] *= rs;
-  } else {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) p[i] = q[i];
+      for (int i = 0; i < NV; ++i) {
+        const float x = l[j][i], ea = exp_fine(-fabsf(x)), r = __builtin_amdgcn_rcpf(1.0f + ea);
+        // sigma(x) = exp(min(x, 0)) / (1 + exp(-|x|))
+        p[j][i] = (t < 0.f ? exp_fine(fminf(x, 0.f) - t) : x >= 0.f ? 1.f : ea) * r;
+        slope[j][SIG ? i : 0] = (x >= 0.f ? ea : 1.f) * r;
+        s[j] += p[j][i];
+      }
+    }
   }
-  return m + log_fine(z);
+  reduce_rows<R, false>(z);
+  if (SIG) reduce_rows<R, false>(s);
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    const bool any = m[j] != -INFINITY;
+    const float rz = any ? 1.0f / z[j] : 0.f, rs = any ? 1.0f / s[j] : 0.f;
+    lse[j] = any ? m[j] + log_fine(z[j]) : 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      q[j][i] *= rz;
+      if (SIG) p[j][i] *= rs;
+      else p[j][i] = q[j][i];
+    }
+  }
 }
 
-template <int NV>
-__device__ __forceinline__ void load_row(const float* __restrict__ row, int E, float (&l)[NV]) {
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = lane_id() + 64 * i;
-    l[i] = e < E ? row[e] : -INFINITY;
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i) l[i] = l[i] > kMaskedLogit ? fminf(l[i], FLT_MAX) : -INFINITY;   // (NaN too)
+// What 64 experts of a sequence add to the losses.
+struct BalanceShare {
+  double dot, z;
+  long long total, tokens;
+};
+
+// Registers of a lane for E experts, and rows that a wave takes at once (more of short ones, to
+// pass the latencies of loads and reductions together).
+constexpr int rows_at_once(int nv) { return nv <= 4 ? 4 : nv <= 8 ? 2 : 1; }
+inline int lane_values(int E) {
+  if (E & 1) return E <= 64 ? 1 : E <= 128 ? 2 : E <= 256 ? 4 : E <= 512 ? 8 : 16;
+  return E <= 128 ? 2 : E <= 256 ? 4 : E <= 384 ? 6 : E <= 512 ? 8 : E <= 768 ? 12 : 16;
 }
 
 }  // namespace
@@ -98,14 +153,17 @@ __device__ __forceinline__ void load_row(const float* __restrict__ row, int E, f
 BalanceWs balance_ws_layout(int T, int E, int S) {
   BalanceWs L{};
   const int len = T / S;
-  // chunks of a sequence's rows, one workgroup each: as many as fill the GPU, of a row a
-  // wave and more
-  const int most = S < 1024 ? 1024 / S : 1, want = (len + kRowWaves - 1) / kRowWaves;
-  L.chunks = want < most ? want : most;
+  // chunks of a sequence's rows, one workgroup each: two workgroups a CU, a step of rows each at least
+  const int step = kRowWaves * rows_at_once(lane_values(E));
+  const int most = S < 1024 ? 1024 / S : 1, want = (len + step - 1) / step;
+  const int room = want < 1 ? 1 : want < most ? want : most;   // (does not fall as T grows)
+  L.rows = (len + room * step - 1) / (room * step) * step;
+  if (L.rows < step) L.rows = step;
+  L.chunks = (len + L.rows - 1) / L.rows;
   if (L.chunks < 1) L.chunks = 1;
-  L.rows = (len + L.chunks - 1) / L.chunks;
-  const size_t n = static_cast<size_t>(S) * L.chunks;
+  const size_t n = static_cast<size_t>(S) * room;
   size_t o = 0;
+  L.share = o;   o = align256(o + sizeof(BalanceShare) * S * ((E + 63) / 64));
   L.probs = o;   o = align256(o + sizeof(float) * n * E);
   L.counts = o;  o = align256(o + sizeof(int) * n * E);
   L.z = o;       o = align256(o + sizeof(float) * n);
@@ -114,48 +172,64 @@ BalanceWs balance_ws_layout(int T, int E, int S) {
   return L;
 }
 
-// Workgroup = a chunk of a sequence's rows, a row at a time to each wave; its sums of p, its
+// Workgroup = a chunk of a sequence's rows, R rows at a time to each wave; its sums of p, its
 // counts, its sum of lse^2 and its tokens go to the workspace, to be joined in chunk order.
-template <bool SIG, int NV>
+template <bool SIG, int V, int NV>
 __global__ __launch_bounds__(kRowWaves * kWave) void balance_rows(
     const float* __restrict__ logits, const int32_t* __restrict__ idx, const uint8_t* __restrict__ mask,
     int E, int k, int len, int chunks, int rows, float* __restrict__ pp, int* __restrict__ pc,
-    float* __restrict__ pz, int* __restrict__ pn, uint32_t okey) {
+     float* __restrict__ pz, int* __restrict__ pn, uint32_t okey) {
+  constexpr int R = rows_at_once(NV);
   __shared__ float s_p[kRowWaves][NV * 64];
   __shared__ int s_c[NV * 64];
   __shared__ float s_z[kRowWaves];
   __shared__ int s_n[kRowWaves];
   const int wg = permute_item(blockIdx.x, gridDim.x, okey);
   const int s = wg / chunks, c = wg - s * chunks;
-  const int tid = threadIdx.x, lane = lane_id(), wv = wave_id();
-  for (int i = tid; i < E; i += blockDim.x) s_c[i] = 0;
+  const int tid = threadIdx.x, lane = lane_id();
+  const int wv = __builtin_amdgcn_readfirstlane(wave_id());
+  for (int i = tid; i < NV * 64; i += kRowWaves * kWave) s_c[i] = 0;
   __syncthreads();
   float acc[NV], z = 0.f;
   int n = 0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) acc[i] = 0.f;
   const int r_end = min(len, (c + 1) * rows);
-  for (int r = c * rows + wv; r < r_end; r += kRowWaves) {
-    const int t = s * len + r;
-    if (mask && !mask[t]) continue;
-    float l[NV], p[NV], q[NV];
-    load_row<NV>(logits + static_cast<size_t>(t) * E, E, l);
-    const int e = lane < k ? idx[static_cast<size_t>(t) * k + lane] : -1;
-    if (static_cast<unsigned>(e) < static_cast<unsigned>(E)) atomicAdd(&s_c[e], 1);
-    const float lse = row_scores<SIG, NV>(l, p, q);
+  for (int r = c * rows + wv * R; r < r_end; r += kRowWaves * R) {
+    float l[R][NV], p[R][NV], q[R][NV], slope[R][SIG ? NV : 1], lse[R];
+    bool on[R];
+    int e[R];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) acc[i] += p[i];
-    z = fmaf(lse, lse, z);
-    ++n;
+    for (int j = 0; j < R; ++j) {
+      const size_t t = static_cast<size_t>(s) * len + min(r + j, len - 1);
+      on[j] = r + j < r_end && (!mask || mask[t] != 0);
+      load_row<V, NV>(logits + t * E, E, -INFINITY, l[j]);
+      e[j] = lane < k ? idx[t * k + lane] : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      if (on[j] && static_cast<unsigned>(e[j]) < static_cast<unsigned>(E)) atomicAdd(&s_c[e[j]], 1);
+      if (!on[j])
+#pragma unroll
+        for (int i = 0; i < NV; ++i) l[j][i] = -INFINITY;
+    }
+    row_scores<SIG, R, NV>(l, p, q, slope, lse);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) acc[i] += p[j][i];
+      z = fmaf(lse[j], lse[j], z);
+      n += on[j];
+    }
   }
 #pragma unroll
-  for (int i = 0; i < NV; ++i) s_p[wv][lane + 64 * i] = acc[i];
+  for (int i = 0; i < NV; ++i) s_p[wv][expert_of<V>(i)] = acc[i];
   if (lane == 0) {
     s_z[wv] = z;
     s_n[wv] = n;
   }
   __syncthreads();
-  for (int e = tid; e < E; e += blockDim.x) {
+  for (int e = tid; e < E; e += kRowWaves * kWave) {
     float v = s_p[0][e];
 #pragma unroll
     for (int w = 1; w < kRowWaves; ++w) v += s_p[w][e];
@@ -174,102 +248,138 @@ __global__ __launch_bounds__(kRowWaves * kWave) void balance_rows(
   }
 }
 
-// Joins a sequence's chunks: workgroup = (sequence, 64 experts), four strips of chunks.
-__global__ __launch_bounds__(256) void balance_join(const float* __restrict__ pp, const int* __restrict__ pc,
-                                                    const int* __restrict__ pn, int E, int chunks,
-                                                    float* __restrict__ probs, int* __restrict__ counts,
-                                                    int* __restrict__ tokens) {
-  __shared__ double s_p[4][64];
-  __shared__ int s_c[4][64];
-  __shared__ int s_n[4];
-  const int s = blockIdx.x, lane = lane_id(), wv = wave_id(), e = blockIdx.y * 64 + lane;
-  double p = 0.0;
+// Joins the chunks: workgroup = (sequence, 64 experts), sixteen strips of chunks, in FP64, with the
+// share of its experts in sum c P and sum c (and the sequence's sum of lse^2 and its tokens).
+__global__ __launch_bounds__(1024) void balance_join(const float* __restrict__ pp, const int* __restrict__ pc,
+                                                     const float* __restrict__ pz, const int* __restrict__ pn,
+                                                     int E, int chunks, BalanceShare* __restrict__ share,
+                                                     float* __restrict__ probs, int* __restrict__ counts,
+                                                     int* __restrict__ tokens) {
+  __shared__ double s_p[16][64], s_z[16];
+  __shared__ int s_c[16][64], s_n[16];
+  const int lane = lane_id(), wv = wave_id();
+  const int blocks = gridDim.y;
+  const int s = blockIdx.x, e = blockIdx.y * 64 + lane, ee = min(e, E - 1);
+  const size_t row0 = static_cast<size_t>(s) * chunks;
+  double p = 0.0, z = 0.0;
   int c = 0, n = 0;
-  for (int j = wv; j < chunks; j += 4) {
-    const size_t row = static_cast<size_t>(s) * chunks + j;
-    if (e < E) {
-      p += pp[row * E + e];
-      c += pc[row * E + e];
+  for (int j = wv * 64 + lane; j < chunks; j += 1024) {
+    n += pn[row0 + j];
+    z += pz[row0 + j];
+  }
+  for (int j = wv; j < chunks; j += 16 * 8) {           // eight chunks' loads in flight
+    float pv[8];
+    int cv[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const size_t at = (row0 + min(j + 16 * u, chunks - 1)) * E + ee;
+      pv[u] = pp[at];
+      cv[u] = pc[at];
     }
-    n += pn[row];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (j + 16 * u < chunks) {
+        p += pv[u];
+        c += cv[u];
+      }
+  }
+  for (int m = 32; m >= 1; m >>= 1) {
+    n += __shfl_xor(n, m, kWave);
+    z += __shfl_xor(z, m, kWave);
   }
   s_p[wv][lane] = p;
   s_c[wv][lane] = c;
-  if (lane == 0) s_n[wv] = n;
-  __syncthreads();
-  if (wv) return;
-  n = s_n[0] + s_n[1] + s_n[2] + s_n[3];
-  if (e < E) {
-    p = (s_p[0][lane] + s_p[1][lane]) + (s_p[2][lane] + s_p[3][lane]);
-    probs[static_cast<size_t>(s) * E + e] = static_cast<float>(p / (n > 0 ? n : 1));
-    counts[static_cast<size_t>(s) * E + e] = s_c[0][lane] + s_c[1][lane] + s_c[2][lane] + s_c[3][lane];
+  if (lane == 0) {
+    s_n[wv] = n;
+    s_z[wv] = z;
   }
-  if (blockIdx.y == 0 && lane == 0) tokens[s] = n;
-}
-
-// Both losses, in one workgroup: a sequence at a time to each wave.
-__global__ __launch_bounds__(1024) void balance_losses(const float* __restrict__ probs,
-                                                       const int* __restrict__ counts,
-                                                       const int* __restrict__ tokens,
-                                                       const float* __restrict__ pz, int E, int S,
-                                                       int chunks, float* __restrict__ losses) {
-  __shared__ double s_l[16], s_z[16];
-  __shared__ long long s_n[16];
-  const int tid = threadIdx.x, lane = lane_id(), wv = wave_id();
-  double loss = 0.0, z = 0.0;
-  long long n = 0;
-  for (int s = wv; s < S; s += 16) {
-    double dot = 0.0;
-    long long total = 0;
-    for (int e = lane; e < E; e += 64) {
-      const int c = counts[static_cast<size_t>(s) * E + e];
-      total += c;
-      dot += static_cast<double>(c) * probs[static_cast<size_t>(s) * E + e];
+  __syncthreads();
+  if (wv == 0) {
+    p = z = 0.0;
+    c = n = 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) {
+      p += s_p[w][lane];
+      c += s_c[w][lane];
+      n += s_n[w];
+      z += s_z[w];
     }
+    const float mean = static_cast<float>(p / (n > 0 ? n : 1));
+    if (e < E) {
+      probs[static_cast<size_t>(s) * E + e] = mean;
+      counts[static_cast<size_t>(s) * E + e] = c;
+    }
+    double dot = e < E ? static_cast<double>(c) * mean : 0.0;
+    long long total = e < E ? c : 0;
     for (int m = 32; m >= 1; m >>= 1) {
       dot += __shfl_xor(dot, m, kWave);
       total += __shfl_xor(total, m, kWave);
     }
-    loss += total > 0 ? E * dot / static_cast<double>(total) : 0.0;
-    n += tokens[s];
+    if (lane == 0) {
+      if (blockIdx.y == 0) tokens[s] = n;
+      share[s * blocks + blockIdx.y] = BalanceShare{dot, z, total, n};
+    }
   }
-  const size_t parts = static_cast<size_t>(S) * chunks;
-  for (size_t i = tid; i < parts; i += 1024) z += pz[i];
-  for (int m = 32; m >= 1; m >>= 1) z += __shfl_xor(z, m, kWave);
+}
+
+// Both losses, from the shares: one workgroup.  (As the end of the join's last workgroup, found by
+// a counter, they took 9.2 us together where these two launches take 7: its fence writes the caches
+// back.)
+__global__ __launch_bounds__(256) void balance_losses(const BalanceShare* __restrict__ share, int E, int S,
+                                                      int blocks, float* __restrict__ losses) {
+  __shared__ double s_l[4], s_z[4];
+  __shared__ long long s_t[4];
+  const int lane = lane_id(), wv = wave_id(), tid = threadIdx.x;
+  double loss = 0.0, z = 0.0;
+  long long n = 0;
+  for (int s = tid; s < S; s += 256) {                    // a sequence a thread
+    double dot = 0.0;
+    long long total = 0;
+    for (int y = 0; y < blocks; ++y) {
+      dot += share[s * blocks + y].dot;
+      total += share[s * blocks + y].total;
+    }
+    z += share[s * blocks].z;
+    n += share[s * blocks].tokens;
+    loss += total > 0 ? E * dot / static_cast<double>(total) : 0.0;
+  }
+  for (int m = 32; m >= 1; m >>= 1) {
+    loss += __shfl_xor(loss, m, kWave);
+    z += __shfl_xor(z, m, kWave);
+    n += __shfl_xor(n, m, kWave);
+  }
   if (lane == 0) {
     s_l[wv] = loss;
     s_z[wv] = z;
-    s_n[wv] = n;
+    s_t[wv] = n;
   }
   __syncthreads();
   if (tid == 0) {
-    loss = z = 0.0;
-    n = 0;
-    for (int w = 0; w < 16; ++w) {
-      loss += s_l[w];
-      z += s_z[w];
-      n += s_n[w];
-    }
+    loss = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+    z = (s_z[0] + s_z[1]) + (s_z[2] + s_z[3]);
+    n = s_t[0] + s_t[1] + s_t[2] + s_t[3];
     losses[0] = static_cast<float>(loss / S);
     losses[1] = static_cast<float>(n > 0 ? z / static_cast<double>(n) : 0.0);
   }
 }
 
-// Gradient: workgroup = a chunk of a sequence's rows, a row at a time to each wave; the
+// Gradient: workgroup = a chunk of a sequence's rows, R rows at a time to each wave; the
 // sequence's counts and the sum of tokens are read once.
-template <bool SIG, int NV>
+template <bool SIG, int V, int NV>
 __global__ __launch_bounds__(kRowWaves * kWave) void balance_backward_rows(
     const float* __restrict__ logits, const uint8_t* __restrict__ mask, const int* __restrict__ counts,
     const int* __restrict__ tokens, const float* __restrict__ d_losses, const float* d_add, int E, int S,
     int len, int chunks, int rows, float* dlogits, uint32_t okey) {
+  constexpr int R = rows_at_once(NV);
   const int wg = permute_item(blockIdx.x, gridDim.x, okey);
   const int s = wg / chunks, c = wg - s * chunks;
-  const int lane = lane_id(), wv = wave_id();
+  const int lane = lane_id();
+  const int wv = __builtin_amdgcn_readfirstlane(wave_id());
   float up[NV];
   long long total = 0, n = 0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = lane + 64 * i, v = e < E ? counts[static_cast<size_t>(s) * E + e] : 0;
+    const int e = expert_of<V>(i), v = e < E ? counts[static_cast<size_t>(s) * E + e] : 0;
     up[i] = static_cast<float>(v);
     total += v;
   }
@@ -283,45 +393,73 @@ __global__ __launch_bounds__(kRowWaves * kWave) void balance_backward_rows(
       ? static_cast<float>(static_cast<double>(d_losses[0]) * E / (static_cast<double>(S) * ns * static_cast<double>(total))) : 0.f;
   const float c1 = n > 0 ? static_cast<float>(2.0 * d_losses[1] / static_cast<double>(n)) : 0.f;
   const int r_end = min(len, (c + 1) * rows);
-  for (int r = c * rows + wv; r < r_end; r += kRowWaves) {
-    const size_t t = static_cast<size_t>(s) * len + r;
-    float d[NV];
-    if (mask && !mask[t]) {
+  for (int r = c * rows + wv * R; r < r_end; r += kRowWaves * R) {
+    float l[R][NV], p[R][NV], q[R][NV], slope[R][SIG ? NV : 1], lse[R], add[R][NV], dot[R];
+    bool on[R];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) d[i] = 0.f;
-    } else {
-      float l[NV], p[NV], q[NV];
-      load_row<NV>(logits + t * E, E, l);
-      const float lse = row_scores<SIG, NV>(l, p, q);
-      float dot = 0.f;
+    for (int j = 0; j < R; ++j) {
+      const size_t t = static_cast<size_t>(s) * len + min(r + j, len - 1);
+      on[j] = !mask || mask[t] != 0;
+      load_row<V, NV>(logits + t * E, E, -INFINITY, l[j]);
+      if (d_add) load_row<V, NV>(d_add + t * E, E, 0.f, add[j]);
+      else
 #pragma unroll
-      for (int i = 0; i < NV; ++i) dot = fmaf(p[i], up[i], dot);
-      dot = wave_sum(dot);
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        float slope = 1.f;
-        if (SIG) {
-          const float ea = exp_fine(fmaxf(-fabsf(l[i]), -200.f));
-          slope = (l[i] >= 0.f ? ea : 1.f) / (1.f + ea);
-        }
-        d[i] = fmaf(c0 * p[i] * (up[i] - dot), slope, c1 * lse * q[i]);
-      }
+        for (int i = 0; i < NV; ++i) add[j][i] = 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int e = lane + 64 * i;
-      if (e < E) dlogits[t * E + e] = d[i] + (d_add ? d_add[t * E + e] : 0.f);
+    for (int j = 0; j < R; ++j)
+      if (!on[j])
+#pragma unroll
+        for (int i = 0; i < NV; ++i) l[j][i] = -INFINITY;
+    row_scores<SIG, R, NV>(l, p, q, slope, lse);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      dot[j] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) dot[j] = fmaf(p[j][i], up[i], dot[j]);
+    }
+    reduce_rows<R, false>(dot);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+      if (r + j >= r_end) break;
+      float* row = dlogits + (static_cast<size_t>(s) * len + r + j) * E;
+      const float cz = c1 * lse[j];
+      float d[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float g = c0 * p[j][i] * (up[i] - dot[j]);
+        if (SIG) g *= slope[j][SIG ? i : 0];
+        d[i] = fmaf(cz, q[j][i], g) + add[j][i];
+      }
+#pragma unroll
+      for (int i = 0; i < NV; i += V) {
+        const int e = expert_of<V>(i);
+        if (e >= E) continue;
+        if (V == 2) *reinterpret_cast<float2*>(row + e) = make_float2(d[i], d[i + V - 1]);
+        else row[e] = d[i];
+      }
     }
   }
 }
 
+// F(V, NV) for E experts
 #define BALANCE_FORMS(F)                                                       \
   do {                                                                         \
-    if (E <= 64) F(1);                                                         \
-    else if (E <= 128) F(2);                                                   \
-    else if (E <= 256) F(4);                                                   \
-    else if (E <= 512) F(8);                                                   \
-    else F(16);                                                                \
+    const int nv_ = lane_values(E);                                            \
+    if (E & 1) {                                                               \
+      if (nv_ == 1) F(1, 1);                                                   \
+      else if (nv_ == 2) F(1, 2);                                              \
+      else if (nv_ == 4) F(1, 4);                                              \
+      else if (nv_ == 8) F(1, 8);                                              \
+      else F(1, 16);                                                           \
+    } else {                                                                   \
+      if (nv_ == 2) F(2, 2);                                                   \
+      else if (nv_ == 4) F(2, 4);                                              \
+      else if (nv_ == 6) F(2, 6);                                              \
+      else if (nv_ == 8) F(2, 8);                                              \
+      else if (nv_ == 12) F(2, 12);                                            \
+      else F(2, 16);                                                           \
+    }                                                                          \
   } while (0)
 
 hipError_t launch_balance_loss(const float* logits, const int32_t* idx, const uint8_t* mask, int T, int E,
@@ -329,25 +467,26 @@ hipError_t launch_balance_loss(const float* logits, const int32_t* idx, const ui
                                int32_t* tokens, void* ws, hipStream_t s) {
   const BalanceWs L = balance_ws_layout(T, E, S);
   char* b = static_cast<char*>(ws);
+  BalanceShare* share = reinterpret_cast<BalanceShare*>(b + L.share);
   float* pp = reinterpret_cast<float*>(b + L.probs);
   int* pc = reinterpret_cast<int*>(b + L.counts);
   float* pz = reinterpret_cast<float*>(b + L.z);
   int* pn = reinterpret_cast<int*>(b + L.tokens);
   prof_begin(kBalance, s);
-#define ROWS(NV)                                                                                        \
+#define ROWS(V, NV)                                                                                        \
   do {                                                                                                  \
     if (sigmoid)                                                                                        \
-      hipLaunchKernelGGL((balance_rows<true, NV>), dim3(S * L.chunks), dim3(kRowWaves * kWave), 0, s,   \
+      hipLaunchKernelGGL((balance_rows<true, V, NV>), dim3(S * L.chunks), dim3(kRowWaves * kWave), 0, s,   \
                          logits, idx, mask, E, k, T / S, L.chunks, L.rows, pp, pc, pz, pn, order_key()); \
     else                                                                                                \
-      hipLaunchKernelGGL((balance_rows<false, NV>), dim3(S * L.chunks), dim3(kRowWaves * kWave), 0, s,  \
+      hipLaunchKernelGGL((balance_rows<false, V, NV>), dim3(S * L.chunks), dim3(kRowWaves * kWave), 0, s,  \
                          logits, idx, mask, E, k, T / S, L.chunks, L.rows, pp, pc, pz, pn, order_key()); \
   } while (0)
   BALANCE_FORMS(ROWS);
 #undef ROWS
-  hipLaunchKernelGGL(balance_join, dim3(S, (E + 63) / 64), dim3(256), 0, s, pp, pc, pn, E, L.chunks, probs,
-                     counts, tokens);
-  hipLaunchKernelGGL(balance_losses, dim3(1), dim3(1024), 0, s, probs, counts, tokens, pz, E, S, L.chunks, losses);
+  hipLaunchKernelGGL(balance_join, dim3(S, (E + 63) / 64), dim3(1024), 0, s, pp, pc, pz, pn, E, L.chunks, share,
+                     probs, counts, tokens);
+  hipLaunchKernelGGL(balance_losses, dim3(1), dim3(256), 0, s, share, E, S, (E + 63) / 64, losses);
   prof_end(kBalance, s);
   return hipGetLastError();
 }
@@ -357,14 +496,14 @@ hipError_t launch_balance_loss_backward(const float* logits, const uint8_t* mask
                                         int T, int E, int S, bool sigmoid, float* dlogits, hipStream_t s) {
   const BalanceWs L = balance_ws_layout(T, E, S);
   prof_begin(kBalanceBackward, s);
-#define ROWS(NV)                                                                                        \
+#define ROWS(V, NV)                                                                                        \
   do {                                                                                                  \
     if (sigmoid)                                                                                        \
-      hipLaunchKernelGGL((balance_backward_rows<true, NV>), dim3(S * L.chunks), dim3(kRowWaves * kWave), 0, s, \
+      hipLaunchKernelGGL((balance_backward_rows<true, V, NV>), dim3(S * L.chunks), dim3(kRowWaves * kWave), 0, s, \
                          logits, mask, counts, tokens, d_losses, d_add, E, S, T / S, L.chunks, L.rows,  \
                          dlogits, order_key());                                                         \
     else                                                                                                \
-      hipLaunchKernelGGL((balance_backward_rows<false, NV>), dim3(S * L.chunks), dim3(kRowWaves * kWave), 0, s, \
+      hipLaunchKernelGGL((balance_backward_rows<false, V, NV>), dim3(S * L.chunks), dim3(kRowWaves * kWave), 0, s, \
                          logits, mask, counts, tokens, d_losses, d_add, E, S, T / S, L.chunks, L.rows,  \
                          dlogits, order_key());                                                         \
   } while (0)

@@ -71,7 +71,7 @@ hipError_t launch_experts_mx4(const uint8_t* x, const uint8_t* xs, bool a4, cons
 // `rows` rows, `chunks` to a sequence.
 constexpr int kMaxSeqs = 4096;
 struct BalanceWs {
-  size_t probs, counts, z, tokens, total;
+  size_t share, probs, counts, z, tokens, total;
   int chunks, rows;
 };
 BalanceWs balance_ws_layout(int T, int E, int S);
