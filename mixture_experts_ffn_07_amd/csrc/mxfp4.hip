@@ -20,7 +20,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kBM4 = 64;                                 // rows (routed pairs) per M-tile
+constexpr int kShort4 = 32, kTall4 = 128;                // rows (routed pairs) per M-tile of the streaming form
 inline size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 inline int round_up(int v, int m) { return (v + m - 1) / m * m; }
 
@@ -35,6 +35,20 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
   v = v > a ? v : a;
   const uint32_t b = __builtin_amdgcn_update_dpp(0, static_cast<int>(v), 0x4E, 0xF, 0xF, true);   // [2,3,0,1]
   return v > b ? v : b;
+}
+
+// One slot (k = 1): the output rows of pairs without a row, which no tile of the down product
+// stores, are cleared: by the whole grid, a row a wave, 64 pairs looked at together.
+__device__ __forceinline__ void clear_rows(uint16_t* __restrict__ out, const int* __restrict__ row_of, int P, int H) {
+  const int lane = lane_id(), waves = gridDim.x * (blockDim.x / kWave);
+  for (int b0 = (blockIdx.x * (blockDim.x / kWave) + wave_id()) * kWave; b0 < P; b0 += waves * kWave) {
+    uint64_t none = __ballot(b0 + lane < P && row_of[b0 + lane] >= P);
+    while (none) {
+      const int b = b0 + __builtin_ctzll(none);
+      none &= none - 1;
+      for (int c = lane; c < H / 8; c += kWave) st16(out + static_cast<size_t>(b) * H + 8 * c, i32x4{0, 0, 0, 0});
+    }
+  }
 }
 
 }  // namespace
@@ -94,9 +108,9 @@ __global__ __launch_bounds__(256) void dequant_mx4_rows(const uint32_t* __restri
 Mx4Ws mx4_ws_layout(int T, int H, int I, int E, int k, bool a4) {
   Mx4Ws L{};
   const size_t P = static_cast<size_t>(T) * k;
-  L.bm = P >= 256 * static_cast<size_t>(E) ? kLargeBM : kBM4;
+  L.bm = P >= 256 * static_cast<size_t>(E) ? kLargeBM : P >= 32 * static_cast<size_t>(E) ? kTall4 : kShort4;
   L.max_tiles = static_cast<int>(E + (P + L.bm - 1) / L.bm);
-  const size_t tile_room = E + (P + kBM4 - 1) / kBM4;      // (as many as any smaller T takes)
+  const size_t tile_room = E + (P + kShort4 - 1) / kShort4;     // (as many as any smaller T takes)
   size_t o = 0;
   L.n_tiles = o;   o += 256;
   L.counts = o;    o = align256(o + sizeof(int) * E);
@@ -133,7 +147,7 @@ enum { kGateUp4 = 0, kDown4 = 1, kDownFused4 = 2 };
 // the next two chunks are in flight while one multiplies.  Rows past the tile's end load
 // the tile's first row; their columns are computed and discarded.
 template <int KIND, int NW, int BM, bool A4>
-__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == 64 ? 4 : 2, 8))) void gemm_mx4s(
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == kShort4 ? 4 : 2, 8))) void gemm_mx4s(
     const uint8_t* __restrict__ act, const uint8_t* __restrict__ acts,
     const uint8_t* __restrict__ wt, const uint8_t* __restrict__ wts,
     const int* __restrict__ perm, const int2* __restrict__ tiles, const int* __restrict__ n_tiles,
@@ -148,19 +162,17 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == 6
   constexpr int SB = 256;                                 // activation bytes of a row per stage
   constexpr int RS = SB + 16;                             // padded LDS row stride
   constexpr int CH = SB / 16;                             // 16-byte pieces of a row per stage
-  constexpr int LPT = BM * CH / NT;                       // 16-byte code loads per thread
+  constexpr int LPT = (BM * CH + NT - 1) / NT;            // 16-byte code loads per thread
   constexpr int SS = 8 * CPS;                             // scale bytes of a row per stage
+  constexpr int WD = BM == kShort4 ? 1 : 2;                    // chunks of weights in flight
+  constexpr int XD = BM == kShort4 ? 1 : 2;                    // stages of activations in flight
+  constexpr int BD = A4 || BM == kTall4 ? 4 : 2;               // activation operands held
   __shared__ __align__(16) uint8_t xl[2][BM * RS];
   __shared__ __align__(16) uint8_t sl[2][BM * SS];
   __shared__ __align__(16) i32x4 wtl[NW][16 * 8];         // per wave: [16 rows][8 pieces]
   __shared__ float s_amax[GU ? NW : 1][BM];
   const int tid = threadIdx.x;
-  // one slot: the down product stores whole output rows, those of pairs without a row are
-  // cleared here
-  if (GU && out)
-    for (int b = blockIdx.x; b < P; b += gridDim.x)
-      if (row_of[b] >= P)
-        for (int c = tid; c < H / 8; c += NT) st16(out + static_cast<size_t>(b) * H + 8 * c, i32x4{0, 0, 0, 0});
+  if (GU && out) clear_rows(out, row_of, P, H);           // (one slot: the down product stores whole rows)
   const int K = GU ? H : I;                               // reduction length
   const int N = GU ? I : H;                               // outputs
   const int RB = K / 2, KB = K / 32, AB = A4 ? K / 2 : K; // bytes of a row: weights, scales, activations
@@ -195,116 +207,128 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == 6
   const i32x4* asrc = tw + col * 8;
   const int sw = col & 7;
 
+  // activation loads: thread = 16-byte piece tid % CH of rows tid / CH + i NT / CH
+  const int piece = (tid % CH) * 16, xrow = tid / CH;
+  const bool xload = BM * CH >= NT || xrow < BM;
   uint32_t oxl[LPT];
-  int lrow[LPT], piece[LPT];
 #pragma unroll
   for (int i = 0; i < LPT; ++i) {
-    const int c = tid + i * NT, r = c / CH, rr = r < mcount ? r : 0;
-    piece[i] = (c % CH) * 16;
-    lrow[i] = r * RS + piece[i];
-    oxl[i] = static_cast<uint32_t>((GU ? perm[rbase + rr] / k : rbase + rr) * AB);
+    const int r = xrow + i * (NT / CH), rr = r < mcount ? r : 0;
+    oxl[i] = static_cast<uint32_t>((GU ? perm[rbase + rr] / k : rbase + rr) * AB + piece);
   }
   const bool sload = tid < BM;
   const int srow = tid < mcount ? tid : 0;
   const uint32_t osx = static_cast<uint32_t>(sload ? (GU ? perm[rbase + srow] / k : rbase + srow) * KB : 0);
-  i32x4 xr[LPT], wA[4], wB[4];
-  uint2 sr[CPS], sA[2], sB[2];
+  i32x4 xr[XD][LPT], W[WD][4];
+  uint2 sr[XD][CPS], sc[WD][2];
   // activations of stage st (a row's last stage may hold one chunk: its first one again)
-  auto fetch = [&](int st) {
+  auto fetch = [&](i32x4 (&x)[LPT], uint2 (&q)[CPS], int st) {
     if (st < nstage) {
+      const int b = st * SB, back = b + piece < AB ? 0 : 128;
+      if (xload)
 #pragma unroll
-      for (int i = 0; i < LPT; ++i) {
-        const int b = st * SB + piece[i];
-        xr[i] = ld16(act + oxl[i] + (b < AB ? b : b - 128));
-      }
+        for (int i = 0; i < LPT; ++i) x[i] = ld16(act + oxl[i] + (b - back));
       if (sload)
 #pragma unroll
         for (int c = 0; c < CPS; ++c)
-          sr[c] = *reinterpret_cast<const uint2*>(acts + osx + 8 * min(st * CPS + c, nchunk - 1));
+          q[c] = *reinterpret_cast<const uint2*>(acts + osx + 8 * min(st * CPS + c, nchunk - 1));
     }
   };
-  auto publish = [&](int st) {
+  auto publish = [&](i32x4 (&x)[LPT], uint2 (&q)[CPS], int st) {
     if (st < nstage) {
+      uint8_t* d = &xl[st & 1][xrow * RS + piece];
+      if (xload)
 #pragma unroll
-      for (int i = 0; i < LPT; ++i) *reinterpret_cast<i32x4*>(&xl[st & 1][lrow[i]]) = xr[i];
+        for (int i = 0; i < LPT; ++i) *reinterpret_cast<i32x4*>(d + i * (NT / CH) * RS) = x[i];
       if (sload)
 #pragma unroll
-        for (int c = 0; c < CPS; ++c) *reinterpret_cast<uint2*>(&sl[st & 1][tid * SS + 8 * c]) = sr[c];
+        for (int c = 0; c < CPS; ++c) *reinterpret_cast<uint2*>(&sl[st & 1][tid * SS + 8 * c]) = q[c];
     }
     __syncthreads();
   };
   // weights of chunk c and the scales of the lane's rows (past the end the last chunk again)
-  auto request = [&](i32x4 (&W)[4], uint2 (&sc)[2], int c) {
+  auto request = [&](int d, int c) {
     const uint32_t cc = static_cast<uint32_t>(min(c, nchunk - 1));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) W[i] = ld16_stream(wb + ow[i] + 128 * cc);
-    sc[0] = *reinterpret_cast<const uint2*>(wsb + os0 + 8 * cc);
-    sc[1] = *reinterpret_cast<const uint2*>(wsb + os1 + 8 * cc);
+    for (int i = 0; i < 4; ++i) W[d][i] = ld16_stream(wb + ow[i] + 128 * cc);
+    sc[d][0] = *reinterpret_cast<const uint2*>(wsb + os0 + 8 * cc);
+    sc[d][1] = *reinterpret_cast<const uint2*>(wsb + os1 + 8 * cc);
   };
-  fetch(0);
-  request(wA, sA, 0);
-  request(wB, sB, 1);
+  fetch(xr[0], sr[0], 0);
+#pragma unroll
+  for (int d = 0; d < WD; ++d) request(d, d);
   f32x4 acc0[G], acc1[G];
 #pragma unroll
   for (int g = 0; g < G; ++g) acc0[g] = acc1[g] = f32x4{0.f, 0.f, 0.f, 0.f};
-  publish(0);
+  publish(xr[0], sr[0], 0);
+  if (XD == 2) fetch(xr[XD - 1], sr[XD - 1], 1);
 
-  // One chunk: the weights through the wave's LDS tile into operands, the chunk after next
-  // on its way into the registers they left, then the products.
-  auto chunk = [&](i32x4 (&W)[4], uint2 (&sc)[2], int buf, int cc, int next) {
+  // One chunk (weights in set d): the weights through the wave's LDS tile into operands, the
+  // chunk WD further on its way into the registers they left, then the products.
+  auto chunk = [&](int d, int buf, int cc, int next) {
     i32x4 a[4];
     int sa[2];
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      wdst[0] = W[2 * m];
-      wdst[64] = W[2 * m + 1];
+      wdst[0] = W[d][2 * m];
+      wdst[64] = W[d][2 * m + 1];
       __builtin_amdgcn_wave_barrier();
       a[2 * m] = asrc[(2 * grp) ^ sw];
       a[2 * m + 1] = asrc[(2 * grp + 1) ^ sw];
       __builtin_amdgcn_wave_barrier();
-      sa[m] = static_cast<int>((grp < 2 ? sc[m].x : sc[m].y) >> (16 * (grp & 1)));
+      sa[m] = static_cast<int>((grp < 2 ? sc[d][m].x : sc[d][m].y) >> (16 * (grp & 1)));
     }
-    request(W, sc, next);
+    request(d, next);
     __builtin_amdgcn_sched_barrier(0);                    // (the compiler would sink the loads behind the products)
     const uint8_t* xcur = &xl[buf][col * RS + (A4 ? cc * 128 + 32 * grp : 64 * (grp >> 1) + 16 * (grp & 1))];
     const uint8_t* scur = &sl[buf][col * SS + cc * 8 + 2 * grp];
+    int sx[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) sx[g] = *reinterpret_cast<const uint16_t*>(scur + 16 * g * SS);
+    // operand i = 2 g + j of row group g and product j, read BD - 1 operands ahead
+    i32x8 b[BD];
+    auto rdb = [&](int i) {
+      const uint8_t* p = xcur + 16 * (i >> 1) * RS + (A4 ? 16 : 32) * (i & 1);
+      const i32x4 lo = *reinterpret_cast<const i32x4*>(p);
+      b[i % BD] = cat8(lo, A4 ? i32x4{0, 0, 0, 0} : *reinterpret_cast<const i32x4*>(p + 128));
+    };
+#pragma unroll
+    for (int i = 0; i < BD - 1 && i < 2 * G; ++i) rdb(i);
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       if (g && g >= ng) break;                            // (uniform: the tile has no rows there)
-      const uint8_t* p = xcur + 16 * g * RS;
-      i32x8 b[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const i32x4 lo = *reinterpret_cast<const i32x4*>(p + (A4 ? 16 : 32) * j);
-        const i32x4 hi = A4 ? i32x4{0, 0, 0, 0} : *reinterpret_cast<const i32x4*>(p + 128 + 32 * j);
-        b[j] = cat8(lo, hi);
+        if (2 * g + j + BD - 1 < 2 * G) rdb(2 * g + j + BD - 1);
+        const i32x8& x = b[(2 * g + j) % BD];
+        if (j == 0) {
+          acc0[g] = mfma_mx4_16<A4, 0>(a[0], x, sa[0], sx[g], acc0[g]);
+          acc1[g] = mfma_mx4_16<A4, 0>(a[2], x, sa[1], sx[g], acc1[g]);
+        } else {
+          acc0[g] = mfma_mx4_16<A4, 1>(a[1], x, sa[0], sx[g], acc0[g]);
+          acc1[g] = mfma_mx4_16<A4, 1>(a[3], x, sa[1], sx[g], acc1[g]);
+        }
+        // (kept at their place: sunk to the end of the stage they would hold every operand live)
+        asm volatile("" : "+v"(acc0[g]), "+v"(acc1[g]));
+        __builtin_amdgcn_sched_barrier(0);
       }
-      const int sx = *reinterpret_cast<const uint16_t*>(scur + 16 * g * SS);
-      acc0[g] = mfma_mx4_16<A4, 0>(a[0], b[0], sa[0], sx, acc0[g]);
-      acc1[g] = mfma_mx4_16<A4, 0>(a[2], b[0], sa[1], sx, acc1[g]);
-      acc0[g] = mfma_mx4_16<A4, 1>(a[1], b[1], sa[0], sx, acc0[g]);
-      acc1[g] = mfma_mx4_16<A4, 1>(a[3], b[1], sa[1], sx, acc1[g]);
-      // (kept at their place: sunk to the end of the stage they would hold every operand live)
-      asm volatile("" : "+v"(acc0[g]), "+v"(acc1[g]));
-      __builtin_amdgcn_sched_barrier(0);
     }
   };
-  for (int c = 0; c < nchunk; c += 2) {                   // chunk c in wA, c + 1 in wB
+  // Stage st, of parity par: its chunks, with the activations XD stages further requested first.
+  auto stage = [&](auto par_, int st) {
+    constexpr int par = decltype(par_)::value, xd = XD == 2 ? par : 0;
+    fetch(xr[xd], sr[xd], st + XD);
     if (A4) {
-      fetch(c / 2 + 1);
-      chunk(wA, sA, (c / 2) & 1, 0, c + 2);
-      if (c + 1 < nchunk) chunk(wB, sB, (c / 2) & 1, 1, c + 3);
-      publish(c / 2 + 1);
+      chunk(0, par, 0, 2 * st + WD);
+      if (2 * st + 1 < nchunk) chunk(WD - 1, par, 1, 2 * st + 1 + WD);
     } else {
-      fetch(c + 1);
-      chunk(wA, sA, 0, 0, c + 2);
-      publish(c + 1);
-      if (c + 1 < nchunk) {
-        fetch(c + 2);
-        chunk(wB, sB, 1, 0, c + 3);
-        publish(c + 2);
-      }
+      chunk(par % WD, par, 0, st + WD);
     }
+    publish(xr[XD == 2 ? par ^ 1 : 0], sr[XD == 2 ? par ^ 1 : 0], st + 1);
+  };
+  for (int st = 0; st < nstage; st += 2) {
+    stage(std::integral_constant<int, 0>{}, st);
+    if (st + 1 < nstage) stage(std::integral_constant<int, 1>{}, st + 1);
   }
   // lane: outputs row0 + 4grp + i (group 0) and row1 + 4grp + i (group 1) of tile row 16g + col
   if (GU) {
@@ -868,10 +892,7 @@ __global__ __launch_bounds__(256) void mx4_scales_t(
     uint16_t* __restrict__ out, uint32_t okey) {
   __shared__ uint2 tile[32][65];
   const int tid = threadIdx.x;
-  if (out)
-    for (int b = blockIdx.x; b < P; b += gridDim.x)
-      if (row_of[b] >= P)
-        for (int c = tid; c < H / 8; c += 256) st16(out + static_cast<size_t>(b) * H + 8 * c, i32x4{0, 0, 0, 0});
+  if (out) clear_rows(out, row_of, P, H);
   const int nh = H / 256, ni = I / 256;                   // steps of a row
   const int ch = (nh + 31) / 32, ci = (ni + 31) / 32;     // blocks of 32 steps
   const int gu = 2 * I / 64, dn = H / 64;                 // blocks of 64 rows (H and I multiples of 256)
@@ -1021,13 +1042,12 @@ hipError_t launch_experts_mx4(const uint8_t* x, const uint8_t* xs, bool a4, cons
 #define STREAM4(KD, A, AS, W, WS, Y, O, NBLK)                                                    \
   do {                                                                                           \
     const dim3 grid_(round_up((NBLK) * L.max_tiles, kXcds));                                     \
-    if (a4)                                                                                      \
-      hipLaunchKernelGGL((gemm_mx4s<KD, 8, kBM4, true>), grid_, dim3(512), 0, s, A, AS, W, WS, perm, tiles, \
-                         n_tiles, counts, offsets, row_of, w, H, I, k, P, hq, hs, Y, O, order_key()); \
-    else                                                                                         \
-      hipLaunchKernelGGL((gemm_mx4s<KD, 8, kBM4, false>), grid_, dim3(512), 0, s, A, AS, W, WS, perm, tiles, \
-                         n_tiles, counts, offsets, row_of, w, H, I, k, P, hq, hs, Y, O, order_key()); \
+    if (L.bm == kTall4) { if (a4) STREAM4_(KD, kTall4, true, A, AS, W, WS, Y, O); else STREAM4_(KD, kTall4, false, A, AS, W, WS, Y, O); } \
+    else { if (a4) STREAM4_(KD, kShort4, true, A, AS, W, WS, Y, O); else STREAM4_(KD, kShort4, false, A, AS, W, WS, Y, O); } \
   } while (0)
+#define STREAM4_(KD, BM, A4, A, AS, W, WS, Y, O)                                                 \
+  hipLaunchKernelGGL((gemm_mx4s<KD, 8, BM, A4>), grid_, dim3(512), 0, s, A, AS, W, WS, perm, tiles, n_tiles, \
+                     counts, offsets, row_of, w, H, I, k, P, hq, hs, Y, O, order_key())
     prof_begin(kMx4GateUp, s);
     STREAM4(kGateUp4, x, xs, wgu, wgus, nullptr, k == 1 ? out : nullptr, I / 128);
     prof_end(kMx4GateUp, s);
@@ -1035,6 +1055,7 @@ hipError_t launch_experts_mx4(const uint8_t* x, const uint8_t* xs, bool a4, cons
     if (k == 1) STREAM4(kDownFused4, hq, hs, wd, wds, nullptr, out, H / 256);
     else STREAM4(kDown4, hq, hs, wd, wds, y, nullptr, H / 256);
 #undef STREAM4
+#undef STREAM4_
   }
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && k > 1) e = launch_combine_slots(y, row_of, w, T, H, k, out, 0, H, H, s, num_cus);
