@@ -556,13 +556,14 @@ def moe_add_rmsnorm_backward_workspace_bytes(T: int, H: int) -> int:
     return int(lib.moe_add_rmsnorm_backward_workspace_bytes(T, H))
 
 
-def _ws_arg(ws, nbytes: int, dev, stream):
-    """(workspace, pointer, bytes): the caller's workspace, or a new one of nbytes.  Who calls
+def _ws_arg(ws, nbytes, dev, stream):
+    """(workspace, pointer, bytes): the caller's workspace, or a new one of nbytes (nbytes None: a
+    workspace is given, and the library checks its size).  Who calls
     holds the tensor until the kernels are enqueued: dropped before, its memory could be given
     to work of another thread that is enqueued ahead of them, or be unmapped."""
     if ws is None:
         ws = _new_ws(nbytes, dev, stream)
-    _need_ws(ws, nbytes)
+    _need_ws(ws, nbytes or 0)
     return ws, _arg(ws, "workspace", ws.shape, torch.uint8, dev), ws.numel()
 
 
@@ -721,7 +722,8 @@ def moe_experts_mxfp4(x, x_scales, w_gate_up, w_gate_up_scales, w_down, w_down_s
             _arg(topk_idx, "topk_idx", (T, k), torch.int32, dev),
             _arg(topk_w, "topk_w", (T, k), f32, dev))
     pout = _arg(out, "out", (T, H), _BF16, dev)
-    ws, pws, n = _ws_arg(ws, moe_experts_mxfp4_workspace_bytes(T, H, I, E, k, xtype), dev, stream)
+    need = moe_experts_mxfp4_workspace_bytes(T, H, I, E, k, xtype) if ws is None else None
+    ws, pws, n = _ws_arg(ws, need, dev, stream)
     _enqueue("moe_experts_mxfp4", dev, stream, *ptrs, T, H, I, E, k, pout, pws, n)
     return out
 
@@ -753,7 +755,8 @@ def moe_balance_loss(logits, topk_idx, score: int = MOE_SCORE_SOFTMAX, n_seqs: i
             _arg(token_mask, "token_mask", (T,), _MASK, dev))
     outs = (_arg(losses, "losses", (2,), f32, dev), _arg(counts, "counts", (S, E), i32, dev),
             _arg(probs, "probs", (S, E), f32, dev), _arg(tokens, "tokens", (S,), i32, dev))
-    ws, pws, n = _ws_arg(ws, moe_balance_loss_workspace_bytes(T, E, n_seqs), dev, stream)
+    need = moe_balance_loss_workspace_bytes(T, E, n_seqs) if ws is None else None
+    ws, pws, n = _ws_arg(ws, need, dev, stream)
     _enqueue("moe_balance_loss", dev, stream, *ptrs, T, E, k, n_seqs, score, *outs, pws, n)
     return losses, counts, probs, tokens
 

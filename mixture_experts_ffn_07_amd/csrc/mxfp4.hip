@@ -954,6 +954,183 @@ hipError_t mx4_set_attributes() {
   return e;
 }
 
+// ---------------------------------------------------------------------------
+// Few pairs (a decode step): two launches, every routed pair on its own, its weights straight
+// from HBM into the operands of the 16x16x128 MFMA, whose 16 activation columns all hold the
+// pair's one row.  Blocks, chunks and products follow in the streaming form's order, so a
+// pair has the bits that it has there.  The step is bound by the latency of two dependent
+// passes over memory and needs no grouping; pairs that share an expert read its weights from
+// the L2 the second time.
+namespace {
+// 16 (ROWS 8: 8, each twice) weight rows on their way into operands: U chunks of 256 positions,
+// loaded as 8 rows x 128 contiguous bytes (lane = row ln >> 3, piece ln & 7) and passed through
+// the wave's 2 KB of LDS, 16-byte pieces XOR-swizzled by row.  w, ws: row 0's codes and scales.
+template <bool A4, int ROWS, int U>
+struct PairRows {
+  static constexpr int L = ROWS / 8;                     // loads per chunk
+  i32x4 a[U][L];
+  int sa[U];
+  __device__ __forceinline__ void request(const uint8_t* __restrict__ w, const uint8_t* __restrict__ ws, int RB,
+                                          int KB, int c0, int nchunk) {
+    const int ln = lane_id(), lr = ln >> 3, lc = ln & 7, row = ln & (ROWS - 1) & 15, grp = ln >> 4;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c0 + u < nchunk) {
+#pragma unroll
+        for (int i = 0; i < L; ++i)
+          a[u][i] = ld16_stream(w + static_cast<uint32_t>((lr + 8 * i) * RB) + 128 * (c0 + u) + 16 * lc);
+        sa[u] = *reinterpret_cast<const uint16_t*>(ws + static_cast<uint32_t>(row * KB) + 8 * (c0 + u) + 2 * grp);
+      }
+  }
+  // times one activation row (x, xs: its codes and scales in global memory or LDS), added to acc:
+  // register i of lane (c, g) holds row 4 g + i
+  __device__ __forceinline__ f32x4 times(const uint8_t* x, const uint8_t* xs, int c0, int nchunk, i32x4* tile,
+                                         f32x4 acc) {
+    const int ln = lane_id(), lr = ln >> 3, lc = ln & 7, row = ln & (ROWS - 1) & 15, grp = ln >> 4;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c0 + u < nchunk) {
+        const uint8_t* p = x + (A4 ? 128 * (c0 + u) + 32 * grp : 256 * (c0 + u) + 64 * (grp >> 1) + 16 * (grp & 1));
+        const int sx = *reinterpret_cast<const uint16_t*>(xs + 8 * (c0 + u) + 2 * grp);
+        i32x8 b[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          b[j] = cat8(*reinterpret_cast<const i32x4*>(p + (A4 ? 16 : 32) * j),
+                      A4 ? i32x4{0, 0, 0, 0} : *reinterpret_cast<const i32x4*>(p + 128 + 32 * j));
+#pragma unroll
+        for (int i = 0; i < L; ++i) tile[(lr + 8 * i) * 8 + (lc ^ lr)] = a[u][i];
+        __builtin_amdgcn_wave_barrier();
+        const i32x4 a0 = tile[row * 8 + ((2 * grp) ^ (row & 7))], a1 = tile[row * 8 + ((2 * grp + 1) ^ (row & 7))];
+        __builtin_amdgcn_wave_barrier();
+        acc = mfma_mx4_16<A4, 0>(a0, b[0], sa[u], sx, acc);
+        acc = mfma_mx4_16<A4, 1>(a1, b[1], sa[u], sx, acc);
+      }
+    return acc;
+  }
+};
+constexpr int kPairsMax4 = 48;                           // pairs up to which this form may be taken
+constexpr int kPairCols4 = 8;                            // output columns per workgroup of the down pass
+constexpr int kPairWaves4 = 8;
+// Taken for 48 pairs at most, while the weights that it reads more than once (pairs that share an
+// expert; expected number of distinct experts E (1 - (1 - k/E)^T)) stay below 60 MB, about the
+// 12 us that grouping and its launches cost the streaming form, and all that it reads below 350 MB,
+// where that form's higher rate has made up for them.  Measured, us (this / streaming), MXFP8:
+// H 2048 I 768 E 128 k 8, T 1 14.7 / 24.4, T 6 29 / 35; H 2048 I 1024 E 8 k 2, T 8 14.9 / 25.6, T 24
+// (133 MB again) 29 / 26; H 7168 I 2048 E 32 k 4, T 2 43 / 58, T 4 (65 MB again) 78 / 71; H 7168 I 2048
+// E 384 k 8, T 1 44 / 61, T 2 (374 MB) 79 / 78; H 4096 I 1024 E 4 k 1, T 40 46 / 33.
+inline bool use_pairs4(int T, int H, int I, int E, int k) {
+  const int64_t P = static_cast<int64_t>(T) * k;
+  if (P > kPairsMax4) return false;
+  double miss = 1.0;                                     // (1 - k/E)^T
+  for (int t = 0; t < T; ++t) miss *= 1.0 - static_cast<double>(k) / E;
+  const double bytes = 3.0 * H * I * 17 / 32, again = static_cast<double>(P) - E * (1.0 - miss);
+  return again * bytes <= 60e6 && P * bytes <= 350e6;
+}
+}  // namespace
+
+// Gate/up, SwiGLU and the codes of one block: workgroup (pair, 32 neurons); waves 0, 1 the gate
+// rows, 2, 3 the up rows.
+template <bool A4>
+__global__ __launch_bounds__(256) void pairs_gate_up_mx4(
+    const uint8_t* __restrict__ x, const uint8_t* __restrict__ xs, const uint8_t* __restrict__ wgu,
+    const uint8_t* __restrict__ wgus, const int32_t* __restrict__ idx, int H, int I, int E, int k, int P,
+    uint8_t* __restrict__ hq, uint8_t* __restrict__ hs, uint32_t okey) {
+  extern __shared__ __align__(16) uint8_t ldp[];         // the token's codes, then its scales
+  __shared__ __align__(16) float s_v[2][32];
+  __shared__ __align__(16) i32x4 s_tile[4][16 * 8];
+  const int nblk = I / 32, AB = A4 ? H / 2 : H, KB = H / 32;
+  const int item = permute_item(blockIdx.x, nblk * P, okey);
+  const int p = item / nblk, n0 = (item - p * nblk) * 32;
+  const int e = idx[p];
+  if (static_cast<unsigned>(e) >= static_cast<unsigned>(E)) return;
+  const int t = p / k, tid = threadIdx.x, ln = lane_id(), col = ln & 15, grp = ln >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(wave_id());
+  const int nchunk = H / 256;
+  const size_t row = static_cast<size_t>(e) * 2 * I + (wv >> 1) * I + n0 + (wv & 1) * 16;
+  const uint8_t *wr = wgu + row * (H / 2), *wsr = wgus + row * KB;
+  constexpr int U = 8;
+  PairRows<A4, 16, U> r;
+  r.request(wr, wsr, H / 2, KB, 0, nchunk);              // on their way while the token is staged
+  __builtin_amdgcn_sched_barrier(0);
+  for (int c = 16 * tid; c < AB; c += 16 * 256) st16(ldp + c, ld16(x + static_cast<size_t>(t) * AB + c));
+  for (int c = 8 * tid; c < KB; c += 8 * 256)
+    *reinterpret_cast<uint2*>(ldp + AB + c) = *reinterpret_cast<const uint2*>(xs + static_cast<size_t>(t) * KB + c);
+  __syncthreads();
+  f32x4 d = {0.f, 0.f, 0.f, 0.f};
+  for (int c0 = 0; c0 < nchunk; c0 += U) {
+    if (c0) r.request(wr, wsr, H / 2, KB, c0, nchunk);
+    d = r.times(ldp, ldp + AB, c0, nchunk, s_tile[wv], d);
+  }
+  if (col == 0) *reinterpret_cast<f32x4*>(&s_v[wv >> 1][(wv & 1) * 16 + 4 * grp]) = d;
+  __syncthreads();
+  if (tid >= 8) return;                                  // eight lanes of four neurons
+  const f32x4 g = *reinterpret_cast<const f32x4*>(&s_v[0][4 * tid]), u = *reinterpret_cast<const f32x4*>(&s_v[1][4 * tid]);
+  float v[4], top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = swiglu4(g[i], u[i]);
+    top = fmaxf(top, fabsf(v[i]));
+  }
+#pragma unroll
+  for (int m = 1; m < 8; m <<= 1) top = fmaxf(top, __shfl_xor(top, m, kWave));
+  const int s = A4 ? mx4_scale_exp(top) : mx_scale_exp(top);
+  const float inv = exp2_neg(s);
+  const size_t at = static_cast<size_t>(p) * I + n0 + 4 * tid;
+  if (A4)
+    *reinterpret_cast<uint16_t*>(hq + at / 2) =
+        static_cast<uint16_t>(f32x4_to_e2m1x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(hq + at) = f32x4_to_e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+  if (tid == 0) hs[at / 32] = static_cast<uint8_t>(s + 127);
+}
+
+// Down and the weighted sum: workgroup = 8 output columns, a wave per pair in turn (the operand's
+// rows 8 to 15 repeat them); then out[t] from the pairs' values in slot order.
+template <bool A4>
+__global__ __launch_bounds__(kPairWaves4 * kWave) void pairs_down_mx4(
+    const uint8_t* __restrict__ hq, const uint8_t* __restrict__ hs, const uint8_t* __restrict__ wd,
+    const uint8_t* __restrict__ wds, const int32_t* __restrict__ idx, const float* __restrict__ w, int H, int I,
+    int E, int k, int P, uint16_t* __restrict__ out, uint32_t okey) {
+  __shared__ __align__(16) float val[kPairsMax4 * kPairCols4];
+  __shared__ float s_w[kPairsMax4];
+  __shared__ bool s_on[kPairsMax4];
+  __shared__ __align__(16) i32x4 s_tile[kPairWaves4][8 * 8];
+  const int tid = threadIdx.x, ln = lane_id(), col = ln & 15, grp = ln >> 4;
+  const int wv = __builtin_amdgcn_readfirstlane(wave_id());
+  const int n0 = permute_item(blockIdx.x, gridDim.x, okey) * kPairCols4;
+  const int nchunk = I / 256, KB = I / 32;
+  if (tid < P) {
+    s_on[tid] = static_cast<unsigned>(idx[tid]) < static_cast<unsigned>(E);
+    s_w[tid] = w[tid];
+  }
+  for (int p = wv; p < P; p += kPairWaves4) {
+    const int e = idx[p];
+    if (static_cast<unsigned>(e) >= static_cast<unsigned>(E)) continue;
+    const size_t row = static_cast<size_t>(e) * H + n0;
+    const uint8_t *x = hq + static_cast<size_t>(p) * (A4 ? I / 2 : I), *xs = hs + static_cast<size_t>(p) * KB;
+    constexpr int U = 4;
+    PairRows<A4, 8, U> r;
+    f32x4 d = {0.f, 0.f, 0.f, 0.f};
+    for (int c0 = 0; c0 < nchunk; c0 += U) {
+      r.request(wd + row * (I / 2), wds + row * KB, I / 2, KB, c0, nchunk);
+      d = r.times(x, xs, c0, nchunk, s_tile[wv], d);
+    }
+    if (col == 0 && grp < 2) *reinterpret_cast<f32x4*>(&val[p * kPairCols4 + 4 * grp]) = d;
+  }
+  __syncthreads();
+  const int T = P / k;
+  for (int i = tid; i < T * kPairCols4; i += kPairWaves4 * kWave) {
+    const int t = i / kPairCols4, c = i % kPairCols4;
+    float o = 0.f;
+    for (int j = 0; j < k; ++j) {
+      const int p = t * k + j;
+      // (one slot: the weighted value itself, the sign of a zero included, as in the other forms)
+      if (s_on[p]) o = k == 1 ? s_w[p] * val[p * kPairCols4 + c] : fmaf(s_w[p], val[p * kPairCols4 + c], o);
+    }
+    out[static_cast<size_t>(t) * H + n0 + c] = static_cast<uint16_t>(f32_to_bf16_rne(o));
+  }
+}
+
 // The MX rows' launches: grids of fewer than 2^32 threads.
 constexpr int64_t kMx4Launch = int64_t(1) << 31;
 
@@ -999,6 +1176,23 @@ hipError_t launch_experts_mx4(const uint8_t* x, const uint8_t* xs, bool a4, cons
   uint8_t* hq = reinterpret_cast<uint8_t*>(b + L.codes);
   uint8_t* hs = reinterpret_cast<uint8_t*>(b + L.scales);
   float* y = reinterpret_cast<float*>(b + L.y);
+  if (use_pairs4(T, H, I, E, k)) {
+#define PAIRS4(A4)                                                                                \
+  do {                                                                                            \
+    prof_begin(kMx4GateUp, s);                                                                    \
+    hipLaunchKernelGGL(pairs_gate_up_mx4<A4>, dim3(I / 32 * P), dim3(256), (A4 ? H / 2 : H) + H / 32, s, x, xs, \
+                       wgu, wgus, idx, H, I, E, k, P, hq, hs, order_key());                       \
+    prof_end(kMx4GateUp, s);                                                                      \
+    prof_begin(kMx4Down, s);                                                                      \
+    hipLaunchKernelGGL(pairs_down_mx4<A4>, dim3(H / kPairCols4), dim3(kPairWaves4 * kWave), 0, s, hq, hs, wd, wds, \
+                       idx, w, H, I, E, k, P, out, order_key());                                  \
+    prof_end(kMx4Down, s);                                                                        \
+  } while (0)
+    if (a4) PAIRS4(true);
+    else PAIRS4(false);
+#undef PAIRS4
+    return hipGetLastError();
+  }
   if (const hipError_t e = launch_group_experts(idx, P, E, L.bm, counts, offsets, tiles, n_tiles, perm, row_of, s);
       e != hipSuccess) return e;
   if (L.bm == kLargeBM) {
