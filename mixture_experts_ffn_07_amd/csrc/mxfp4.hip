@@ -118,8 +118,9 @@ Mx4Ws mx4_ws_layout(int T, int H, int I, int E, int k, bool a4) {
   L.tiles = o;     o = align256(o + sizeof(int) * 2 * tile_room);
   L.perm = o;      o = align256(o + sizeof(int) * P);
   L.row_of = o;    o = align256(o + sizeof(int) * P);
-  L.codes = o;     o = align256(o + P * (a4 ? I / 2 : I));
-  L.scales = o;    o = align256(o + P * (I / 32));
+  const size_t past = kLargeBM;                            // rows behind the last that a tile may read
+  L.codes = o;     o = align256(o + (P + past) * (a4 ? I / 2 : I));
+  L.scales = o;    o = align256(o + P * (I / 32) + past * 8);
   L.y = o;
   if (k > 1) o = align256(o + sizeof(float) * P * H);
   L.partial = L.wgu_t = L.wd_t = L.x_t = o;
@@ -127,7 +128,7 @@ Mx4Ws mx4_ws_layout(int T, int H, int I, int E, int k, bool a4) {
     o = align256(o + sizeof(float) * kLargeMaxSlices * kLargeBM * 256);
     L.wgu_t = o;   o = align256(o + static_cast<size_t>(E) * 2 * I * (H / 32));
     L.wd_t = o;    o = align256(o + static_cast<size_t>(E) * H * (I / 32));
-    L.x_t = o;     o = align256(o + P * (H / 32));
+    L.x_t = o;     o = align256(o + P * (H / 32) + past * 8);
   }
   L.total = o;
   return L;
@@ -567,12 +568,16 @@ __global__ __launch_bounds__(256) void gemm_large_mx4(
   const uint8_t* __restrict__ abase = wt + static_cast<size_t>(e) * wrows * RB;
   const int arow = GU ? (wv < 2 ? n0 + wv * 64 : I + n0 + (wv - 2) * 64) : nb * 256 + wv * 64;
   const uint32_t ao = static_cast<uint32_t>((arow + wrow) * RB + wc * 16);
-  uint32_t bo[8];
+  // gate_up: the tokens' rows, the tile's first one past its end; down: grouped rows, the next ones (or,
+  // behind the last, up to 255 rows of the workspace) past its end.  Columns of rows past the end are
+  // computed and discarded.
+  uint32_t bo[GU ? 8 : 1];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int r = wv * 64 + 8 * j + lrow, rr = r < mcount ? r : 0;
-    bo[j] = static_cast<uint32_t>((GU ? perm[rbase + rr] / k : rbase + rr) * AB + lc * 16);
+  for (int j = 0; j < (GU ? 8 : 1); ++j) {
+    const int r = wv * 64 + 8 * j + lrow;
+    bo[j] = static_cast<uint32_t>((GU ? perm[rbase + (r < mcount ? r : 0)] / k : r) * AB + lc * 16);
   }
+  const uint8_t* __restrict__ actb = GU ? act : act + static_cast<size_t>(rbase) * AB;
   // LDS: piece c of row r of 128 bytes at c ^ (r >> 1 & 7), of 64 bytes at c ^ (r >> 2 & 3): the
   // 16 rows that a read serves at once lie in 64 different banks
   const int lx0 = (wv * 64 + lrow) * 128 + ((lc ^ (lrow >> 1)) * 16);      // even j; odd j: the piece ^ 4
@@ -584,13 +589,10 @@ __global__ __launch_bounds__(256) void gemm_large_mx4(
     fa[i] = (GU ? (i >> 1) * 128 + wn * 64 + (i & 1) * 32 : wn * 128 + 32 * i) + l32;
   const int fb = wm * 128 + l32;
   const int swx = l32 >> 1 & 7, sww = A4 ? swx : l32 >> 2 & 3;
-  // scales: dword hi of row fa[i] of the weight tile, of row fb + 32 j of the activations
-  uint32_t osa[4], osb[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    osa[i] = static_cast<uint32_t>(GU ? (i >> 1) * I + n0 + wn * 64 + (i & 1) * 32 + l32 : nb * 256 + fa[i]) * 2 + hi;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) osb[j] = static_cast<uint32_t>(rbase + min(fb + 32 * j, mcount - 1)) * 2 + hi;
+  // scales: dword hi of the wave's weight rows and of its activation rows, the first blocks' (the
+  // others' lie a fixed distance on; past the tile's end the next rows', as above)
+  const uint32_t osa = static_cast<uint32_t>(GU ? n0 + wn * 64 + l32 : nb * 256 + wn * 128 + l32) * 2 + hi;
+  const uint32_t osb = static_cast<uint32_t>(rbase + fb) * 2 + hi;
   const uint32_t* __restrict__ sab = wts + static_cast<size_t>(e) * nk * wrows * 2;
 
   i32x4 stg[NS];   // [0, NW) weight rows, [NW, NS) activation rows
@@ -599,38 +601,39 @@ __global__ __launch_bounds__(256) void gemm_large_mx4(
   auto gload = [&](int q, int s) {
     const int ss = min(s, s_end - 1);
     if (q < NW) stg[q] = ld16(abase + ao + static_cast<uint32_t>(q * (A4 ? 8 : 16)) * RB + static_cast<uint32_t>(ss * WB));
-    else stg[q] = ld16(act + bo[(q - NW) & 7] + static_cast<uint32_t>(ss * 128));
+    else stg[q] = ld16(actb + bo[GU ? (q - NW) & 7 : 0] + (GU ? 0u : static_cast<uint32_t>((q - NW) * 8) * AB) + static_cast<uint32_t>(ss * 128));
   };
   auto lwrite = [&](int q, int s) {
     uint8_t* st = ldl + (s & 1) * kStage;
     if (q < NW) *reinterpret_cast<i32x4*>(st + (A4 ? (q & 1 ? lx1 : lx0) + q * 8 * 128 : lw0 + q * 16 * 64)) = stg[q];
     else *reinterpret_cast<i32x4*>(st + kWTile + (q & 1 ? lx1 : lx0) + ((q - NW) & 7) * 8 * 128) = stg[q];
   };
-  struct Frag {
-    i32x4 a[4];
-    i32x8 b[4];
-  };
-  // fragment g (0..3) of both operands, K step ks of stage s
-  auto rda = [&](Frag& f, int g, int s, int ks) {
+  // fragments: weights of this and of the next K step, activations of this one, each replaced by
+  // the next K step's once its products are issued
+  i32x4 fa0[4], fa1[4];
+  i32x8 fx[4];
+  // weight fragment g, activation fragment g of K step ks of stage s
+  auto rda = [&](i32x4 (&f)[4], int g, int s, int ks) {
     const uint8_t* st = ldl + (s & 1) * kStage;
-    f.a[g] = *reinterpret_cast<const i32x4*>(st + fa[g] * WB + (((A4 ? 4 * hi + ks : 2 * hi + ks) ^ sww) * 16));
+    f[g] = *reinterpret_cast<const i32x4*>(st + fa[g] * WB + (((A4 ? 4 * hi + ks : 2 * hi + ks) ^ sww) * 16));
   };
-  auto rdb = [&](Frag& f, int g, int s, int ks) {
+  auto rdb = [&](int g, int s, int ks) {
     const uint8_t* st = ldl + (s & 1) * kStage + kWTile + (fb + 32 * g) * 128;
     if (A4) {
-      f.b[g] = cat8(*reinterpret_cast<const i32x4*>(st + ((4 * hi + ks) ^ swx) * 16), i32x4{0, 0, 0, 0});
+      fx[g] = cat8(*reinterpret_cast<const i32x4*>(st + ((4 * hi + ks) ^ swx) * 16), i32x4{0, 0, 0, 0});
     } else {
-      f.b[g] = cat8(*reinterpret_cast<const i32x4*>(st + ((2 * ks + hi) ^ swx) * 16),
-                    *reinterpret_cast<const i32x4*>(st + ((4 + 2 * ks + hi) ^ swx) * 16));
+      fx[g] = cat8(*reinterpret_cast<const i32x4*>(st + ((2 * ks + hi) ^ swx) * 16),
+                   *reinterpret_cast<const i32x4*>(st + ((4 + 2 * ks + hi) ^ swx) * 16));
     }
   };
   uint32_t sa[4], sb[4], na[4], nbs[4];
   auto sload = [&](int kt) {
     const uint32_t kk = static_cast<uint32_t>(min(kt, ke - 1));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) na[i] = sab[kk * static_cast<uint32_t>(2 * wrows) + osa[i]];
+    for (int i = 0; i < 4; ++i)
+      na[i] = sab[kk * static_cast<uint32_t>(2 * wrows) + (GU ? (i >> 1) * 2 * I + (i & 1) * 64 : 64 * i) + osa];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) nbs[j] = acts[static_cast<size_t>(kk) * (2 * static_cast<size_t>(P)) + osb[j]];
+    for (int j = 0; j < 4; ++j) nbs[j] = acts[static_cast<size_t>(kk) * (2 * static_cast<size_t>(P)) + 64 * j + osb];
   };
   f32x16 acc[4][4];
 #pragma unroll
@@ -639,22 +642,21 @@ __global__ __launch_bounds__(256) void gemm_large_mx4(
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
-  // One MFMA K step on fragments f (scale byte SEL): 8 groups of 2 MFMAs; the first groups read the
-  // fragments of K step rks of stage rs into n, and write PER staged pieces of stage ws to LDS and
-  // reload them from stage ws + 1.  sched_barrier keeps this order.
-  auto phase = [&](auto sel, Frag& f, Frag& n, int rs, int rks, int ws, int q0) {
+  // One MFMA K step on weight fragments f (scale byte SEL): 8 groups of 2 MFMAs; the first groups read
+  // the weight fragments of K step rks of stage rs into n, every second one its activation fragment for
+  // that step, and the first PER write a staged piece of stage ws to LDS and reload it from stage ws + 1.
+  // sched_barrier keeps this order.
+  auto phase = [&](auto sel, i32x4 (&f)[4], i32x4 (&n)[4], int rs, int rks, int ws, int q0) {
     constexpr int SEL = decltype(sel)::value;
 #pragma unroll
     for (int g = 0; g < 8; ++g) {
-      const int i = g >> 1, j = (g & 1) * 2;
+      const int j = g >> 1, i = (g & 1) * 2;
 #pragma unroll
       for (int z = 0; z < 2; ++z)
-        acc[i][j + z] = mfma_mx4_32<A4, !GU, SEL>(f.a[i], f.b[j + z], sa[i], sb[j + z], acc[i][j + z]);
+        acc[i + z][j] = mfma_mx4_32<A4, !GU, SEL>(f[i + z], fx[j], sa[i + z], sb[j], acc[i + z][j]);
       __builtin_amdgcn_sched_barrier(0);
-      if (g < 4) {
-        rda(n, g, rs, rks);
-        rdb(n, g, rs, rks);
-      }
+      if (g < 4) rda(n, g, rs, rks);
+      if (g & 1) rdb(j, rs, rks);
       if (g < PER) {
         lwrite(q0 + g, ws);
         gload(q0 + g, ws + 1);
@@ -684,11 +686,10 @@ __global__ __launch_bounds__(256) void gemm_large_mx4(
     sb[i] = nbs[i];
   }
   __syncthreads();
-  Frag f0, f1;
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
-    rda(f0, g, s0, 0);
-    rdb(f0, g, s0, 0);
+    rda(fa0, g, s0, 0);
+    rdb(g, s0, 0);
   }
   // the epilogue's data (tile row tid's pair and weight)
   const int my_pr = GU ? 0 : perm[rbase + min(tid, mcount - 1)];
@@ -701,22 +702,22 @@ __global__ __launch_bounds__(256) void gemm_large_mx4(
   for (int kt = kb; kt < ke; ++kt) {
     sload(kt + 1);
     if (A4) {
-      phase(integral_constant<int, 0>{}, f0, f1, kt, 1, kt + 1, 0);
-      phase(integral_constant<int, 1>{}, f1, f0, kt, 2, kt + 1, PER);
-      phase(integral_constant<int, 2>{}, f0, f1, kt, 3, kt + 1, 2 * PER);
+      phase(integral_constant<int, 0>{}, fa0, fa1, kt, 1, kt + 1, 0);
+      phase(integral_constant<int, 1>{}, fa1, fa0, kt, 2, kt + 1, PER);
+      phase(integral_constant<int, 2>{}, fa0, fa1, kt, 3, kt + 1, 2 * PER);
       publish();
       // In the loop on purpose: a loop of one basic block would keep a copy of the accumulators
       // outside the AGPRs for the code after it.
       if (KIND == kDownFused4 && kt == kb) my_w = w[my_pr];          // k = 1: pair id == token
-      phase(integral_constant<int, 3>{}, f1, f0, kt + 1, 0, kt + 2, 3 * PER);
+      phase(integral_constant<int, 3>{}, fa1, fa0, kt + 1, 0, kt + 2, 3 * PER);
     } else {
-      phase(integral_constant<int, 0>{}, f0, f1, 2 * kt, 1, 2 * kt + 1, 0);
+      phase(integral_constant<int, 0>{}, fa0, fa1, 2 * kt, 1, 2 * kt + 1, 0);
       publish();
-      phase(integral_constant<int, 1>{}, f1, f0, 2 * kt + 1, 0, 2 * kt + 2, PER);
+      phase(integral_constant<int, 1>{}, fa1, fa0, 2 * kt + 1, 0, 2 * kt + 2, PER);
       if (KIND == kDownFused4 && kt == kb) my_w = w[my_pr];
-      phase(integral_constant<int, 2>{}, f0, f1, 2 * kt + 1, 1, 2 * kt + 2, 0);
+      phase(integral_constant<int, 2>{}, fa0, fa1, 2 * kt + 1, 1, 2 * kt + 2, 0);
       publish();
-      phase(integral_constant<int, 3>{}, f1, f0, 2 * kt + 2, 0, 2 * kt + 3, PER);
+      phase(integral_constant<int, 3>{}, fa1, fa0, 2 * kt + 2, 0, 2 * kt + 3, PER);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
