@@ -108,7 +108,25 @@ __global__ __launch_bounds__(256) void dequant_mx4_rows(const uint32_t* __restri
 Mx4Ws mx4_ws_layout(int T, int H, int I, int E, int k, bool a4) {
   Mx4Ws L{};
   const size_t P = static_cast<size_t>(T) * k;
-  L.bm = P >= 256 * static_cast<size_t>(E) ? kLargeBM : P >= 32 * static_cast<size_t>(E) ? kTall4 : kShort4;
+  // 256-row tiles where the products are bound by the matrix cores and LDS: 300 rows an expert, and
+  // tiles of gate/up for half of the CUs (a round and the split tail then run full), or, where
+  // reductions are short against a tile's start and end, for two and a half rounds.  Measured, us
+  // (256-row / 128-row tiles, MXFP8; MXFP4):
+  //   H 7168 I 2048 E 6 k 1: 200 rows an expert 125 / 118; 112 / 98, 320 150 / 182; 117 / 147, 1500 408 / 572;
+  //     320 / 460
+  //   H 4096 I 1024 E 32 k 6: 320 rows 269 / 269; 232 / 230, 640 436 / 499; 370 / 419
+  //   H 4096 I 1024 E 4 k 2: 640 rows (80 tiles of gate/up) 96 / 86; 87 / 74, 1500 (187) 140 / 171; 121 / 142
+  //   H 2048 I 768 E 64 k 8: 320 rows (480) 246 / 235; 216 / 202, 640 (960) 418 / 441; 369 / 378
+  //   H 2048 I 1024 E 16 k 4: 640 rows (320) 164 / 145; 147 / 120, 1024 (512) 219 / 221; 195 / 181, 1500 (750)
+  //     287 / 318; 252 / 265
+  // 128-row tiles from 32 rows an expert, below it 32-row ones (32 / 128):
+  //   H 7168 I 2048 E 32 k 4, 38 rows 272 / 198; 267 / 187;  H 2048 I 1024 E 128 k 4, 31 rows, MXFP4 132 / 131;
+  //   H 2048 I 768 E 128 k 8, 25 rows, MXFP8 98 / 106, 4 rows 65 / 84; E 64, 50 rows 75 / 77; 73 / 69
+  // (64-row ones won nowhere by more than 4 %.)
+  const size_t gu_tiles = P / kLargeBM * (I / 128);
+  const bool large = P >= 300 * static_cast<size_t>(E) &&
+                     gu_tiles >= (static_cast<size_t>(H) * I >= (size_t(4) << 20) ? 128u : 640u);
+  L.bm = large ? kLargeBM : P >= 32 * static_cast<size_t>(E) ? kTall4 : kShort4;
   L.max_tiles = static_cast<int>(E + (P + L.bm - 1) / L.bm);
   const size_t tile_room = E + (P + kShort4 - 1) / kShort4;     // (as many as any smaller T takes)
   size_t o = 0;

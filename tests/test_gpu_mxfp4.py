@@ -178,7 +178,10 @@ SIZES = [
     (17, 768, 512, 4, 2), (33, 512, 768, 6, 1), (64, 1024, 256, 32, 8), (65, 512, 256, 5, 2), (130, 256, 256, 2, 2),
     (300, 512, 512, 3, 1), (777, 256, 512, 16, 6), (600, 512, 256, 1, 1), (513, 768, 256, 2, 2), (1025, 1024, 512, 4, 1),
     (700, 4096, 1024, 1, 1), (1300, 2048, 2048, 2, 1), (900, 4096, 1024, 4, 2), (1500, 1024, 2048, 4, 2),
-    (2601, 1792, 1792, 2, 1)]
+    # 256-row tiles: k = 1 and more, ragged experts, odd numbers of steps, slices of the last round's tiles on
+    # either product
+    (2200, 2048, 2048, 3, 1), (1300, 2048, 2048, 4, 2), (2048, 2048, 2048, 1, 1), (2305, 2304, 2048, 1, 1),
+    (1100, 1024, 4096, 2, 1), (700, 1280, 4096, 2, 2), (1200, 1792, 3840, 3, 1)]
 
 
 @pytest.mark.parametrize("T,H,I,E,k", SIZES)
@@ -200,7 +203,7 @@ def test_experts_skewed(M, T, four):
 @pytest.mark.parametrize("T,E,k,H,I", [
     (6, 4, 2, 512, 256), (50, 8, 3, 512, 256), (200, 8, 3, 512, 256), (9, 4, 1, 512, 256), (300, 4, 1, 512, 256),
     (900, 3, 1, 512, 256), (1200, 3, 2, 512, 256), (1100, 3, 1, 2048, 2048), (600, 3, 2, 4096, 1024),
-    (2200, 3, 1, 1024, 2048), (1100, 3, 2, 1024, 2048)])
+    (2200, 3, 1, 2048, 2048), (1100, 3, 2, 2048, 2048), (1100, 2, 1, 1024, 4096)])
 @pytest.mark.parametrize("four", [False, True])
 def test_experts_ids_out_of_range(M, T, E, k, H, I, four):
     print(f"[mxfp4] ids out of range T={T} E={E} k={k} H={H} four={four}", flush=True)
@@ -250,10 +253,10 @@ def test_experts_same_expert_twice(M, four):
         check(d, call(M, d))
 
 
-@pytest.mark.parametrize("T", [4, 90, 700])
+@pytest.mark.parametrize("T,H,I", [(4, 512, 256), (90, 512, 256), (700, 512, 256), (1200, 2048, 2048)])
 @pytest.mark.parametrize("four", [False, True])
-def test_experts_zero_rows(M, T, four):
-    d = make(M, T, 512, 256, 4, 2, four, seed=4)
+def test_experts_zero_rows(M, T, H, I, four):
+    d = make(M, T, H, I, 4, 2, four, seed=4)
     d["x"][0] = 0
     d["xs"][0] = 0                                          # as a row of zeros is coded
     d["xs"][1] = 0                                          # values of 2^-127
@@ -263,11 +266,11 @@ def test_experts_zero_rows(M, T, four):
     check(d, out)
 
 
+@pytest.mark.parametrize("T,H,I", [(6, 512, 512), (70, 512, 512), (300, 512, 512), (1100, 2048, 2048)])
 @pytest.mark.parametrize("four", [False, True])
-def test_experts_far_apart_scales(M, four):
+def test_experts_far_apart_scales(M, T, H, I, four):
     """Blocks whose scales lie far apart, on both operands; activations that saturate silu."""
-    T, H, I, E, k = 70, 512, 512, 3, 2
-    d = make(M, T, H, I, E, k, four, seed=5)
+    d = make(M, T, H, I, 3, 2, four, seed=5)
     g = torch.Generator(device="cuda").manual_seed(1)
     d["sg"] = (d["sg"].int() + torch.randint(-18, 3, d["sg"].shape, generator=g, device="cuda")).to(torch.uint8)
     d["xs"] = (d["xs"].int() + torch.randint(-12, 4, d["xs"].shape, generator=g, device="cuda")).to(torch.uint8)
@@ -276,7 +279,7 @@ def test_experts_far_apart_scales(M, four):
 
 
 @pytest.mark.parametrize("T,E,k,H,I", [(3, 8, 2, 512, 256), (90, 8, 2, 512, 256), (700, 4, 2, 512, 256),
-                                       (1500, 3, 1, 1024, 2048), (1500, 3, 2, 2048, 1024)])
+                                       (2200, 3, 1, 2048, 2048), (1300, 3, 2, 2048, 2048)])
 @pytest.mark.parametrize("four", [False, True])
 def test_experts_bad_token_leaves_the_others(M, T, E, k, H, I, four):
     """A token with a NaN scale, and an expert with one: only that token's, and that expert's tokens'
@@ -296,7 +299,8 @@ def test_experts_bad_token_leaves_the_others(M, T, E, k, H, I, four):
 
 
 @pytest.mark.parametrize("T,E,k,H,I", [(1, 8, 2, 512, 512), (40, 8, 2, 512, 512), (500, 8, 2, 512, 512), (900, 2, 1, 2048, 2048),
-                                       (700, 2, 2, 4096, 1024), (2100, 2, 1, 1024, 2048), (1050, 2, 2, 1024, 2048)])
+                                       (700, 2, 2, 4096, 1024), (2100, 2, 1, 2048, 2048), (1050, 2, 2, 2048, 2048),
+                                       (1100, 2, 1, 1024, 4096), (2305, 1, 1, 2304, 2048)])
 @pytest.mark.parametrize("four", [False, True])
 def test_experts_deterministic_and_order_free(M, T, E, k, H, I, four):
     print(f"[mxfp4] order T={T} E={E} k={k} four={four}", flush=True)
@@ -312,7 +316,7 @@ def test_experts_deterministic_and_order_free(M, T, E, k, H, I, four):
     M.moe_set_debug_options(0, 0)
 
 
-@pytest.mark.parametrize("T", [4, 90, 600])
+@pytest.mark.parametrize("T", [4, 90, 600, 160000])
 @pytest.mark.parametrize("four", [False, True])
 def test_experts_large_offsets(M, T, four):
     """An expert array beyond 2^32 bytes and the last experts in it."""
@@ -325,13 +329,21 @@ def test_experts_large_offsets(M, T, four):
     for n, t in big.items():
         t[E - 2:] = d[n]
     moved = dict(d, **big, idx=d["idx"] + (E - 2))
-    out = call(M, moved)
-    check(d, out, rows=slice(0, 40))
+    out = call(M, moved)                                    # (160000: 256-row tiles)
+    check(d, out, rows=slice(T - 40 if T > 40 else 0, T))
     assert E * I * H >= 2 ** 32
 
 
+@pytest.mark.parametrize("four", [False, True])
+def test_experts_many_rows_and_short_reductions(M, four):
+    d = make(M, 41000, 512, 512, 2, 1, four, seed=16)
+    out = call(M, d)
+    check(d, out, rows=slice(0, 200))
+    check(d, out, rows=slice(40800, 41000))
+
+
 @pytest.mark.parametrize("T,E,k,H,I", [(1, 16, 4, 512, 256), (60, 16, 4, 512, 256), (300, 8, 2, 512, 256), (900, 2, 1, 2048, 2048),
-                                       (700, 2, 2, 4096, 1024), (2100, 2, 1, 1024, 2048), (1050, 2, 2, 1024, 2048)])
+                                       (700, 2, 2, 4096, 1024), (2100, 2, 1, 2048, 2048), (1050, 2, 2, 2048, 2048)])
 @pytest.mark.parametrize("four", [False, True])
 def test_experts_graph_replays(M, T, E, k, H, I, four):
     """Captured and replayed, with eager work of the program's own between the replays; two
@@ -371,7 +383,7 @@ def test_experts_graph_replays(M, T, E, k, H, I, four):
 def test_experts_one_slot_zero_and_negative_weights(M, H, I, E, four):
     """k = 1: a weight of 0 or less; a zero's sign is that of the product in every form."""
     print(f"[mxfp4] one slot H={H} I={I} E={E} four={four}", flush=True)
-    d = make(M, 2100, H, I, E, 1, four, seed=13)
+    d = make(M, 2100, H, I, E, 1, four, seed=13)                # (256-row tiles at H 2048 I 2048)
     d["w"][::3] = 0
     d["w"][1::3] *= -1
     full = call(M, d)
@@ -404,6 +416,14 @@ def test_experts_empty_batch(M):
     for four in (False, True):
         d = make(M, 4, 512, 256, 4, 2, four)
         assert call(M, part_of(d, slice(0, 0))).shape == (0, 512)
+
+
+def test_experts_small_workspace_is_refused(M):
+    d = make(M, 100, 512, 256, 4, 2, True)
+    n = M.moe_experts_mxfp4_workspace_bytes(100, 512, 256, 4, 2, M.MOE_MXFP4)
+    with pytest.raises(M.MoeError) as e:
+        call(M, d, ws=M.workspace(n - 1))
+    assert e.value.status == M.MOE_ERR_WORKSPACE
 
 
 def test_experts_against_the_batched_mxfp8_layer(M):
