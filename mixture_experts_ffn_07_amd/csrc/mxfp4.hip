@@ -108,25 +108,27 @@ __global__ __launch_bounds__(256) void dequant_mx4_rows(const uint32_t* __restri
 Mx4Ws mx4_ws_layout(int T, int H, int I, int E, int k, bool a4) {
   Mx4Ws L{};
   const size_t P = static_cast<size_t>(T) * k;
-  // 256-row tiles where the products are bound by the matrix cores and LDS: 300 rows an expert, and
-  // tiles of gate/up for half of the CUs (a round and the split tail then run full), or, where
-  // reductions are short against a tile's start and end, for two and a half rounds.  Measured, us
-  // (256-row / 128-row tiles, MXFP8; MXFP4):
-  //   H 7168 I 2048 E 6 k 1: 200 rows an expert 125 / 118; 112 / 98, 320 150 / 182; 117 / 147, 1500 408 / 572;
-  //     320 / 460
-  //   H 4096 I 1024 E 32 k 6: 320 rows 269 / 269; 232 / 230, 640 436 / 499; 370 / 419
-  //   H 4096 I 1024 E 4 k 2: 640 rows (80 tiles of gate/up) 96 / 86; 87 / 74, 1500 (187) 140 / 171; 121 / 142
-  //   H 2048 I 768 E 64 k 8: 320 rows (480) 246 / 235; 216 / 202, 640 (960) 418 / 441; 369 / 378
-  //   H 2048 I 1024 E 16 k 4: 640 rows (320) 164 / 145; 147 / 120, 1024 (512) 219 / 221; 195 / 181, 1500 (750)
-  //     287 / 318; 252 / 265
-  // 128-row tiles from 32 rows an expert, below it 32-row ones (32 / 128):
-  //   H 7168 I 2048 E 32 k 4, 38 rows 272 / 198; 267 / 187;  H 2048 I 1024 E 128 k 4, 31 rows, MXFP4 132 / 131;
-  //   H 2048 I 768 E 128 k 8, 25 rows, MXFP8 98 / 106, 4 rows 65 / 84; E 64, 50 rows 75 / 77; 73 / 69
-  // (64-row ones won nowhere by more than 4 %.)
-  const size_t gu_tiles = P / kLargeBM * (I / 128);
-  const bool large = P >= 300 * static_cast<size_t>(E) &&
-                     gu_tiles >= (static_cast<size_t>(H) * I >= (size_t(4) << 20) ? 128u : 640u);
-  L.bm = large ? kLargeBM : P >= 32 * static_cast<size_t>(E) ? kTall4 : kShort4;
+  // 256-row tiles where the products are bound by the matrix cores and LDS: with long reductions
+  // (weights of 8 M values a matrix) from 192 rows an expert, else from 320, and enough tiles of
+  // gate/up that the rounds and the split tail run full: half of the CUs, or five rounds where
+  // reductions are short (below 4 M) against a tile's start and end.  Measured, us (256-row /
+  // 128-row tiles, MXFP4; MXFP8):
+  //   H 7168 I 2048 E 32 k 4: 192 rows an expert 391 / 444; 484 / 498, 512 rows 743 / 928; 922 / 1089
+  //   H 4096 I 14336 E 8 k 2: 128 rows 297 / 283, 192 rows 313 / 354, 512 rows 583 / 849
+  //   H 2048 I 5632 E 8 k 2: 256 rows 132 / 126, 512 rows MXFP8 229 / 267
+  //   H 4096 I 1024 E 64 k 6: 256 rows 365 / 341; 426 / 395, 384 rows 472 / 508; 557 / 588, 1536 rows 1550 / 1853
+  //   H 4096 I 1024 E 16 k 4: 512 rows 194 / 188, 1024 rows 293 / 324; 340 / 384
+  //   H 2048 I 768 E 64 k 8, 1024 rows (1536 tiles) 544 / 576; 621 / 669
+  //   H 2048 I 1024 k 4, 1024 rows: E 16 (512 tiles) 192 / 179; 218 / 215, E 32 (1024) 349 / 336; 398 / 398
+  // 128-row tiles from 18 rows an expert, below it 32-row ones (32 / 128):
+  //   H 4096 I 1024 E 64 k 6: 19 rows 123 / 110; 122 / 120, 73 rows 252 / 170; 259 / 189
+  //   H 2048 I 768 E 128 k 8: 4 rows 66 / 76; 65 / 82, 16 rows MXFP8 86 / 93, 25 rows 95 / 92; 98 / 100
+  //   H 2048 I 768 E 64 k 8, 50 rows MXFP8 76 / 73;  H 7168 I 2048 E 32 k 4, 38 rows MXFP8 273 / 196
+  // (64-row ones lie within 8 % of the better of the two, on both sides, from 16 to 75 rows.)
+  const size_t gu_tiles = P / kLargeBM * (I / 128), HI = static_cast<size_t>(H) * I;
+  const bool large = P >= (HI >= (size_t(8) << 20) ? 192 : 320) * static_cast<size_t>(E) &&
+                     gu_tiles >= (HI >= (size_t(4) << 20) ? 128u : 1280u);
+  L.bm = large ? kLargeBM : P >= 18 * static_cast<size_t>(E) ? kTall4 : kShort4;
   L.max_tiles = static_cast<int>(E + (P + L.bm - 1) / L.bm);
   const size_t tile_room = E + (P + kShort4 - 1) / kShort4;     // (as many as any smaller T takes)
   size_t o = 0;
@@ -162,9 +164,12 @@ enum { kGateUp4 = 0, kDown4 = 1, kDownFused4 = 2 };
 // XOR-swizzled by row), and reads back two operands of the 16x16x128 MFMA: product j takes
 // blocks 2g + j of the chunk's eight in lane group g, so a lane's two scales are neighbours.
 // The activations are staged in LDS, 256 bytes of each row a stage (two chunks of MXFP4,
-// one of MXFP8) with their scales, double-buffered and shared by the waves; the weights of
-// the next two chunks are in flight while one multiplies.  Rows past the tile's end load
-// the tile's first row; their columns are computed and discarded.
+// one of MXFP8) with their scales, double-buffered and shared by the waves; the next
+// chunk's weights and the next stage's activations are in flight while one multiplies, and
+// other workgroups of the CU (two of 128 rows, four of 32) cover what that does not: a second
+// chunk and stage in flight in the 128-row tiles took the registers and LDS of the second
+// workgroup and 4 % more time.  Rows past the tile's end load the tile's first row; their
+// columns are computed and discarded.
 template <int KIND, int NW, int BM, bool A4>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == kShort4 ? 4 : 2, 8))) void gemm_mx4s(
     const uint8_t* __restrict__ act, const uint8_t* __restrict__ acts,
@@ -181,15 +186,12 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == k
   constexpr int SB = 256;                                 // activation bytes of a row per stage
   constexpr int RS = SB + 16;                             // padded LDS row stride
   constexpr int CH = SB / 16;                             // 16-byte pieces of a row per stage
-  constexpr int LPT = (BM * CH + NT - 1) / NT;            // 16-byte code loads per thread
+  constexpr int LPT = BM * CH / NT;                       // 16-byte code loads per thread
   constexpr int SS = 8 * CPS;                             // scale bytes of a row per stage
-  constexpr int WD = BM == kShort4 ? 1 : 2;                    // chunks of weights in flight
-  constexpr int XD = BM == kShort4 ? 1 : 2;                    // stages of activations in flight
-  constexpr int BD = A4 || BM == kTall4 ? 4 : 2;               // activation operands held
+  constexpr int BD = A4 ? 4 : 2;                          // activation operands held
   __shared__ __align__(16) uint8_t xl[2][BM * RS];
   __shared__ __align__(16) uint8_t sl[2][BM * SS];
   __shared__ __align__(16) i32x4 wtl[NW][16 * 8];         // per wave: [16 rows][8 pieces]
-  __shared__ float s_amax[GU ? NW : 1][BM];
   const int tid = threadIdx.x;
   if (GU && out) clear_rows(out, row_of, P, H);           // (one slot: the down product stores whole rows)
   const int K = GU ? H : I;                               // reduction length
@@ -228,7 +230,6 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == k
 
   // activation loads: thread = 16-byte piece tid % CH of rows tid / CH + i NT / CH
   const int piece = (tid % CH) * 16, xrow = tid / CH;
-  const bool xload = BM * CH >= NT || xrow < BM;
   uint32_t oxl[LPT];
 #pragma unroll
   for (int i = 0; i < LPT; ++i) {
@@ -238,66 +239,62 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == k
   const bool sload = tid < BM;
   const int srow = tid < mcount ? tid : 0;
   const uint32_t osx = static_cast<uint32_t>(sload ? (GU ? perm[rbase + srow] / k : rbase + srow) * KB : 0);
-  i32x4 xr[XD][LPT], W[WD][4];
-  uint2 sr[XD][CPS], sc[WD][2];
+  i32x4 xr[LPT], W[4];
+  uint2 sr[CPS], sc[2];
   // activations of stage st (a row's last stage may hold one chunk: its first one again)
-  auto fetch = [&](i32x4 (&x)[LPT], uint2 (&q)[CPS], int st) {
+  auto fetch = [&](int st) {
     if (st < nstage) {
       const int b = st * SB, back = b + piece < AB ? 0 : 128;
-      if (xload)
 #pragma unroll
-        for (int i = 0; i < LPT; ++i) x[i] = ld16(act + oxl[i] + (b - back));
+      for (int i = 0; i < LPT; ++i) xr[i] = ld16(act + oxl[i] + (b - back));
       if (sload)
 #pragma unroll
         for (int c = 0; c < CPS; ++c)
-          q[c] = *reinterpret_cast<const uint2*>(acts + osx + 8 * min(st * CPS + c, nchunk - 1));
+          sr[c] = *reinterpret_cast<const uint2*>(acts + osx + 8 * min(st * CPS + c, nchunk - 1));
     }
   };
-  auto publish = [&](i32x4 (&x)[LPT], uint2 (&q)[CPS], int st) {
+  auto publish = [&](int st) {
     if (st < nstage) {
       uint8_t* d = &xl[st & 1][xrow * RS + piece];
-      if (xload)
 #pragma unroll
-        for (int i = 0; i < LPT; ++i) *reinterpret_cast<i32x4*>(d + i * (NT / CH) * RS) = x[i];
+      for (int i = 0; i < LPT; ++i) *reinterpret_cast<i32x4*>(d + i * (NT / CH) * RS) = xr[i];
       if (sload)
 #pragma unroll
-        for (int c = 0; c < CPS; ++c) *reinterpret_cast<uint2*>(&sl[st & 1][tid * SS + 8 * c]) = q[c];
+        for (int c = 0; c < CPS; ++c) *reinterpret_cast<uint2*>(&sl[st & 1][tid * SS + 8 * c]) = sr[c];
     }
     __syncthreads();
   };
   // weights of chunk c and the scales of the lane's rows (past the end the last chunk again)
-  auto request = [&](int d, int c) {
+  auto request = [&](int c) {
     const uint32_t cc = static_cast<uint32_t>(min(c, nchunk - 1));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) W[d][i] = ld16_stream(wb + ow[i] + 128 * cc);
-    sc[d][0] = *reinterpret_cast<const uint2*>(wsb + os0 + 8 * cc);
-    sc[d][1] = *reinterpret_cast<const uint2*>(wsb + os1 + 8 * cc);
+    for (int i = 0; i < 4; ++i) W[i] = ld16_stream(wb + ow[i] + 128 * cc);
+    sc[0] = *reinterpret_cast<const uint2*>(wsb + os0 + 8 * cc);
+    sc[1] = *reinterpret_cast<const uint2*>(wsb + os1 + 8 * cc);
   };
-  fetch(xr[0], sr[0], 0);
-#pragma unroll
-  for (int d = 0; d < WD; ++d) request(d, d);
+  fetch(0);
+  request(0);
   f32x4 acc0[G], acc1[G];
 #pragma unroll
   for (int g = 0; g < G; ++g) acc0[g] = acc1[g] = f32x4{0.f, 0.f, 0.f, 0.f};
-  publish(xr[0], sr[0], 0);
-  if (XD == 2) fetch(xr[XD - 1], sr[XD - 1], 1);
+  publish(0);
 
-  // One chunk (weights in set d): the weights through the wave's LDS tile into operands, the
-  // chunk WD further on its way into the registers they left, then the products.
-  auto chunk = [&](int d, int buf, int cc, int next) {
+  // One chunk: the weights through the wave's LDS tile into operands, the next chunk's on their
+  // way into the registers they left, then the products.
+  auto chunk = [&](int buf, int cc, int next) {
     i32x4 a[4];
     int sa[2];
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      wdst[0] = W[d][2 * m];
-      wdst[64] = W[d][2 * m + 1];
+      wdst[0] = W[2 * m];
+      wdst[64] = W[2 * m + 1];
       __builtin_amdgcn_wave_barrier();
       a[2 * m] = asrc[(2 * grp) ^ sw];
       a[2 * m + 1] = asrc[(2 * grp + 1) ^ sw];
       __builtin_amdgcn_wave_barrier();
-      sa[m] = static_cast<int>((grp < 2 ? sc[d][m].x : sc[d][m].y) >> (16 * (grp & 1)));
+      sa[m] = static_cast<int>((grp < 2 ? sc[m].x : sc[m].y) >> (16 * (grp & 1)));
     }
-    request(d, next);
+    request(next);
     __builtin_amdgcn_sched_barrier(0);                    // (the compiler would sink the loads behind the products)
     const uint8_t* xcur = &xl[buf][col * RS + (A4 ? cc * 128 + 32 * grp : 64 * (grp >> 1) + 16 * (grp & 1))];
     const uint8_t* scur = &sl[buf][col * SS + cc * 8 + 2 * grp];
@@ -333,23 +330,14 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == k
       }
     }
   };
-  // Stage st, of parity par: its chunks, with the activations XD stages further requested first.
-  auto stage = [&](auto par_, int st) {
-    constexpr int par = decltype(par_)::value, xd = XD == 2 ? par : 0;
-    fetch(xr[xd], sr[xd], st + XD);
-    if (A4) {
-      chunk(0, par, 0, 2 * st + WD);
-      if (2 * st + 1 < nchunk) chunk(WD - 1, par, 1, 2 * st + 1 + WD);
-    } else {
-      chunk(par % WD, par, 0, st + WD);
-    }
-    publish(xr[XD == 2 ? par ^ 1 : 0], sr[XD == 2 ? par ^ 1 : 0], st + 1);
-  };
-  for (int st = 0; st < nstage; st += 2) {
-    stage(std::integral_constant<int, 0>{}, st);
-    if (st + 1 < nstage) stage(std::integral_constant<int, 1>{}, st + 1);
+  for (int st = 0; st < nstage; ++st) {
+    fetch(st + 1);
+    chunk(st & 1, 0, st * CPS + 1);
+    if (CPS == 2 && 2 * st + 1 < nchunk) chunk(st & 1, 1, 2 * st + 2);
+    publish(st + 1);
   }
   // lane: outputs row0 + 4grp + i (group 0) and row1 + 4grp + i (group 1) of tile row 16g + col
+  float* s_amax = reinterpret_cast<float*>(xl[0]);        // (every wave is done with the stages)
   if (GU) {
     // SwiGLU into acc0; a row's largest magnitude over the wave's 16 neurons, met in LDS with
     // the other half of the 32-neuron block (wave wv ^ 1), gives the block's scale
@@ -363,14 +351,14 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == k
       }
       top = fmaxf(top, __shfl_xor(top, 16, kWave));
       top = fmaxf(top, __shfl_xor(top, 32, kWave));
-      if (grp == 0) s_amax[GU ? wv : 0][16 * g + col] = top;
+      if (grp == 0) s_amax[wv * BM + 16 * g + col] = top;
     }
     __syncthreads();
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const int r = 16 * g + col;
       if (r >= mcount) continue;
-      const float top = fmaxf(s_amax[GU ? wv : 0][r], s_amax[GU ? wv ^ 1 : 0][r]);
+      const float top = fmaxf(s_amax[wv * BM + r], s_amax[(wv ^ 1) * BM + r]);
       const int s = A4 ? mx4_scale_exp(top) : mx_scale_exp(top);
       const float inv = exp2_neg(s);
       const f32x4 v = acc0[g];
