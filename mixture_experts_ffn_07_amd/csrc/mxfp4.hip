@@ -20,7 +20,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kShort4 = 32, kTall4 = 128;                // rows (routed pairs) per M-tile of the streaming form
+constexpr int kShort4 = 32, kTall4 = 96;                 // rows (routed pairs) per M-tile of the streaming form
 inline size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 inline int round_up(int v, int m) { return (v + m - 1) / m * m; }
 
@@ -112,19 +112,24 @@ Mx4Ws mx4_ws_layout(int T, int H, int I, int E, int k, bool a4) {
   // (weights of 8 M values a matrix) from 192 rows an expert, else from 320, and enough tiles of
   // gate/up that the rounds and the split tail run full: half of the CUs, or five rounds where
   // reductions are short (below 4 M) against a tile's start and end.  Measured, us (256-row /
-  // 128-row tiles, MXFP4; MXFP8):
-  //   H 7168 I 2048 E 32 k 4: 192 rows an expert 391 / 444; 484 / 498, 512 rows 743 / 928; 922 / 1089
-  //   H 4096 I 14336 E 8 k 2: 128 rows 297 / 283, 192 rows 313 / 354, 512 rows 583 / 849
-  //   H 2048 I 5632 E 8 k 2: 256 rows 132 / 126, 512 rows MXFP8 229 / 267
-  //   H 4096 I 1024 E 64 k 6: 256 rows 365 / 341; 426 / 395, 384 rows 472 / 508; 557 / 588, 1536 rows 1550 / 1853
-  //   H 4096 I 1024 E 16 k 4: 512 rows 194 / 188, 1024 rows 293 / 324; 340 / 384
-  //   H 2048 I 768 E 64 k 8, 1024 rows (1536 tiles) 544 / 576; 621 / 669
-  //   H 2048 I 1024 k 4, 1024 rows: E 16 (512 tiles) 192 / 179; 218 / 215, E 32 (1024) 349 / 336; 398 / 398
-  // 128-row tiles from 18 rows an expert, below it 32-row ones (32 / 128):
-  //   H 4096 I 1024 E 64 k 6: 19 rows 123 / 110; 122 / 120, 73 rows 252 / 170; 259 / 189
-  //   H 2048 I 768 E 128 k 8: 4 rows 66 / 76; 65 / 82, 16 rows MXFP8 86 / 93, 25 rows 95 / 92; 98 / 100
-  //   H 2048 I 768 E 64 k 8, 50 rows MXFP8 76 / 73;  H 7168 I 2048 E 32 k 4, 38 rows MXFP8 273 / 196
-  // (64-row ones lie within 8 % of the better of the two, on both sides, from 16 to 75 rows.)
+  // 96-row tiles, MXFP4; MXFP8):
+  //   H 7168 I 2048 E 32 k 4: 192 rows an expert 386 / 468; 477 / 503, 512 rows 726 / 1098; 903 / 1178
+  //   H 7168 I 2048 E 6 k 1, MXFP8: 171 rows (64 tiles) 116 / 104, 320 rows (112) 146 / 174
+  //   H 4096 I 14336 E 8 k 2: 128 rows 294 / 317; 353 / 361, 192 rows 310 / 475; 403 / 536
+  //   H 2048 I 5632 E 8 k 2: 256 rows MXFP8 151 / 146, 512 rows 184 / 228; 223 / 253
+  //   H 4096 I 1024 E 64 k 6: 256 rows MXFP8 415 / 413, 384 rows 463 / 551; 541 / 593, 1536 rows 1523 / 2047
+  //   H 4096 I 1024 E 16 k 4: 512 rows (256 tiles) 193 / 180, 1024 rows 287 / 334; 334 / 368
+  //   H 2048 I 768 E 64 k 8, 1024 rows (1536 tiles) 535 / 567; 612 / 626
+  //   H 2048 I 1024 k 4, 1024 rows: E 16 (512 tiles) 191 / 169; 215 / 193, E 32 (1024) 345 / 326, E 64 (2048)
+  //     604 / 672
+  // 96-row tiles from 18 rows an expert, below it 32-row ones (32 / 96):
+  //   H 4096 I 1024 E 64 k 6: 19 rows 115 / 103; 121 / 108, 73 rows 265 / 164; 284 / 179
+  //   H 2048 I 768 E 128 k 8: 4 rows 65 / 68; 66 / 70, 16 rows 82 / 79; 86 / 84
+  //   H 4096 I 14336 E 8 k 2, MXFP8: 16 rows 169 / 184, 32 rows 264 / 195
+  //   H 7168 I 2048, MXFP8: E 32 k 4, 6 rows 151 / 156, 12 rows 174 / 163, 19 rows 193 / 167; E 6 k 1, 21 rows
+  //     51 / 56
+  // (64-row ones lie within 8 % of the better of the two, on both sides, from 16 to 75 rows; 128-row ones leave
+  // registers for half as many weight rows a wave: E 64, 73 rows 171; 188, E 16, 1024 rows 179; 215.)
   const size_t gu_tiles = P / kLargeBM * (I / 128), HI = static_cast<size_t>(H) * I;
   const bool large = P >= (HI >= (size_t(8) << 20) ? 192 : 320) * static_cast<size_t>(E) &&
                      gu_tiles >= (HI >= (size_t(4) << 20) ? 128u : 1280u);
@@ -157,30 +162,36 @@ Mx4Ws mx4_ws_layout(int T, int H, int I, int E, int k, bool a4) {
 enum { kGateUp4 = 0, kDown4 = 1, kDownFused4 = 2 };
 
 // Batched products with a whole-line weight stream: workgroup = (M-tile of BM routed rows,
-// NW waves), each wave owning two groups of 16 weight rows (gate_up: 16 neurons' gate and up
-// rows; down: 32 output channels).  A chunk is 256 positions of K, 128 bytes of a weight
-// row: the wave reads its 32 rows as four loads of 8 rows x 128 contiguous bytes
+// 4 waves), each wave owning 2 R groups of 16 weight rows (gate_up: 16 R neurons' gate and up
+// rows; down: 32 R output channels).  A chunk is 256 positions of K, 128 bytes of a weight
+// row: the wave reads a group as two loads of 8 rows x 128 contiguous bytes
 // (non-temporal), passes them through a wave-private 2 KB LDS tile (16-byte pieces
 // XOR-swizzled by row), and reads back two operands of the 16x16x128 MFMA: product j takes
 // blocks 2g + j of the chunk's eight in lane group g, so a lane's two scales are neighbours.
 // The activations are staged in LDS, 256 bytes of each row a stage (two chunks of MXFP4,
 // one of MXFP8) with their scales, double-buffered and shared by the waves; the next
 // chunk's weights and the next stage's activations are in flight while one multiplies, and
-// other workgroups of the CU (two of 128 rows, four of 32) cover what that does not: a second
-// chunk and stage in flight in the 128-row tiles took the registers and LDS of the second
-// workgroup and 4 % more time.  Rows past the tile's end load the tile's first row; their
-// columns are computed and discarded.
-template <int KIND, int NW, int BM, bool A4>
-__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == kShort4 ? 4 : 2, 8))) void gemm_mx4s(
+// the CU's other workgroups cover what that does not.  Rows past the tile's end load the
+// tile's first row; their columns are computed and discarded.
+//
+// 32-row tiles are bound by the weights' bytes: R = 1, 100-106 registers, four workgroups a
+// CU (8 experts of 4096 x 14336, 64 tokens: 748 MB in 160-169 us, 4.4-4.7 TB/s; 8 waves a
+// workgroup 196, R = 2 198).  96-row tiles are bound by LDS, where every wave reads the whole
+// stage: R = 2 halves that per product, 246-252 registers, two workgroups a CU (E 16, 4095
+// tokens, MXFP8: 215 us with R = 1 and 8 waves, 191 with R = 2, 1.08 PFLOP/s of the whole
+// call).  A second chunk and stage in flight cost the second workgroup and 4 %; stages of 128
+// bytes, twice the barriers, 2-10 %; weights loaded straight to LDS, 3-9 %.
+template <int KIND, int BM, int R, bool A4>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM == kShort4 ? 4 : 2, 8))) void gemm_mx4s(
     const uint8_t* __restrict__ act, const uint8_t* __restrict__ acts,
     const uint8_t* __restrict__ wt, const uint8_t* __restrict__ wts,
     const int* __restrict__ perm, const int2* __restrict__ tiles, const int* __restrict__ n_tiles,
     const int* __restrict__ counts, const int* __restrict__ offsets, const int* __restrict__ row_of,
     const float* __restrict__ w, int H, int I, int k, int P, uint8_t* __restrict__ hq,
     uint8_t* __restrict__ hs, float* __restrict__ y, uint16_t* __restrict__ out, uint32_t okey) {
-  constexpr int NT = NW * 64;
+  constexpr int NW = 4, NT = NW * 64;
   constexpr bool GU = KIND == kGateUp4;
-  constexpr int RPW = GU ? 16 : 32;                       // outputs per wave
+  constexpr int RPW = (GU ? 16 : 32) * R;                       // outputs per wave
   constexpr int G = BM / 16;                              // 16-row groups of the tile
   constexpr int CPS = A4 ? 2 : 1;                         // chunks per stage
   constexpr int SB = 256;                                 // activation bytes of a row per stage
@@ -188,7 +199,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == k
   constexpr int CH = SB / 16;                             // 16-byte pieces of a row per stage
   constexpr int LPT = BM * CH / NT;                       // 16-byte code loads per thread
   constexpr int SS = 8 * CPS;                             // scale bytes of a row per stage
-  constexpr int BD = A4 ? 4 : 2;                          // activation operands held
+  constexpr int BD = 2;                           // activation operands held
   __shared__ __align__(16) uint8_t xl[2][BM * RS];
   __shared__ __align__(16) uint8_t sl[2][BM * SS];
   __shared__ __align__(16) i32x4 wtl[NW][16 * 8];         // per wave: [16 rows][8 pieces]
@@ -211,18 +222,15 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == k
   const int ln = tid & 63, col = ln & 15, grp = ln >> 4;
   const int wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int nb = nb_i * NW * RPW + wv * RPW;              // the wave's first output
-  const int row0 = nb, row1 = GU ? I + nb : nb + 16;
+  // first weight row of group m (gate_up: gate and up rows in turn)
+  auto grow = [&](int m) { return GU ? (m & 1) * I + nb + 16 * (m >> 1) : nb + 16 * m; };
   const size_t wrows = GU ? 2 * static_cast<size_t>(I) : static_cast<size_t>(N);
 
   // whole-line loads: lane = (row lr of an 8-row group, 16-byte piece lc)
   const int lr = ln >> 3, lc = ln & 7;
   const uint8_t* __restrict__ wb = wt + static_cast<size_t>(e) * wrows * RB;
   const uint8_t* __restrict__ wsb = wts + static_cast<size_t>(e) * wrows * KB;
-  uint32_t ow[4];                                         // group 0 rows 0-7, 8-15, group 1 rows 0-7, 8-15
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    ow[i] = static_cast<uint32_t>(((i < 2 ? row0 : row1) + 8 * (i & 1) + lr) * RB + lc * 16);
-  const uint32_t os0 = static_cast<uint32_t>((row0 + col) * KB), os1 = static_cast<uint32_t>((row1 + col) * KB);
+  const uint32_t ow = static_cast<uint32_t>(lr * RB + lc * 16), os = static_cast<uint32_t>(col * KB);
   i32x4* tw = wtl[wv];
   i32x4* wdst = tw + lr * 8 + (lc ^ lr);                  // + 64 for rows 8-15
   const i32x4* asrc = tw + col * 8;
@@ -239,8 +247,8 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == k
   const bool sload = tid < BM;
   const int srow = tid < mcount ? tid : 0;
   const uint32_t osx = static_cast<uint32_t>(sload ? (GU ? perm[rbase + srow] / k : rbase + srow) * KB : 0);
-  i32x4 xr[LPT], W[4];
-  uint2 sr[CPS], sc[2];
+  i32x4 xr[LPT], W[4 * R];
+  uint2 sr[CPS], sc[2 * R];
   // activations of stage st (a row's last stage may hold one chunk: its first one again)
   auto fetch = [&](int st) {
     if (st < nstage) {
@@ -264,28 +272,31 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == k
     }
     __syncthreads();
   };
-  // weights of chunk c and the scales of the lane's rows (past the end the last chunk again)
-  auto request = [&](int c) {
+  // weights of group m of chunk c and the scales of the lane's row (past the end the last chunk again)
+  auto request = [&](int m, int c) {
     const uint32_t cc = static_cast<uint32_t>(min(c, nchunk - 1));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) W[i] = ld16_stream(wb + ow[i] + 128 * cc);
-    sc[0] = *reinterpret_cast<const uint2*>(wsb + os0 + 8 * cc);
-    sc[1] = *reinterpret_cast<const uint2*>(wsb + os1 + 8 * cc);
+    const uint8_t* p = wb + (static_cast<uint32_t>(grow(m) * RB) + 128 * cc);
+    W[2 * m] = ld16_stream(p + ow);
+    W[2 * m + 1] = ld16_stream(p + 8 * RB + ow);
+    sc[m] = *reinterpret_cast<const uint2*>(wsb + (static_cast<uint32_t>(grow(m) * KB) + 8 * cc) + os);
   };
   fetch(0);
-  request(0);
-  f32x4 acc0[G], acc1[G];
 #pragma unroll
-  for (int g = 0; g < G; ++g) acc0[g] = acc1[g] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int m = 0; m < 2 * R; ++m) request(m, 0);
+  f32x4 acc[2 * R][G];
+#pragma unroll
+  for (int g = 0; g < G; ++g)
+#pragma unroll
+    for (int m = 0; m < 2 * R; ++m) acc[m][g] = f32x4{0.f, 0.f, 0.f, 0.f};
   publish(0);
 
   // One chunk: the weights through the wave's LDS tile into operands, the next chunk's on their
   // way into the registers they left, then the products.
   auto chunk = [&](int buf, int cc, int next) {
-    i32x4 a[4];
-    int sa[2];
+    i32x4 a[4 * R];
+    int sa[2 * R];
 #pragma unroll
-    for (int m = 0; m < 2; ++m) {
+    for (int m = 0; m < 2 * R; ++m) {
       wdst[0] = W[2 * m];
       wdst[64] = W[2 * m + 1];
       __builtin_amdgcn_wave_barrier();
@@ -293,8 +304,8 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == k
       a[2 * m + 1] = asrc[(2 * grp + 1) ^ sw];
       __builtin_amdgcn_wave_barrier();
       sa[m] = static_cast<int>((grp < 2 ? sc[m].x : sc[m].y) >> (16 * (grp & 1)));
+      request(m, next);
     }
-    request(next);
     __builtin_amdgcn_sched_barrier(0);                    // (the compiler would sink the loads behind the products)
     const uint8_t* xcur = &xl[buf][col * RS + (A4 ? cc * 128 + 32 * grp : 64 * (grp >> 1) + 16 * (grp & 1))];
     const uint8_t* scur = &sl[buf][col * SS + cc * 8 + 2 * grp];
@@ -317,15 +328,14 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == k
       for (int j = 0; j < 2; ++j) {
         if (2 * g + j + BD - 1 < 2 * G) rdb(2 * g + j + BD - 1);
         const i32x8& x = b[(2 * g + j) % BD];
-        if (j == 0) {
-          acc0[g] = mfma_mx4_16<A4, 0>(a[0], x, sa[0], sx[g], acc0[g]);
-          acc1[g] = mfma_mx4_16<A4, 0>(a[2], x, sa[1], sx[g], acc1[g]);
-        } else {
-          acc0[g] = mfma_mx4_16<A4, 1>(a[1], x, sa[0], sx[g], acc0[g]);
-          acc1[g] = mfma_mx4_16<A4, 1>(a[3], x, sa[1], sx[g], acc1[g]);
+#pragma unroll
+        for (int m = 0; m < 2 * R; ++m) {
+          if (j == 0) acc[m][g] = mfma_mx4_16<A4, 0>(a[2 * m], x, sa[m], sx[g], acc[m][g]);
+          else acc[m][g] = mfma_mx4_16<A4, 1>(a[2 * m + 1], x, sa[m], sx[g], acc[m][g]);
         }
         // (kept at their place: sunk to the end of the stage they would hold every operand live)
-        asm volatile("" : "+v"(acc0[g]), "+v"(acc1[g]));
+#pragma unroll
+        for (int m = 0; m < 2 * R; ++m) asm volatile("" : "+v"(acc[m][g]));
         __builtin_amdgcn_sched_barrier(0);
       }
     }
@@ -336,40 +346,47 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == k
     if (CPS == 2 && 2 * st + 1 < nchunk) chunk(st & 1, 1, 2 * st + 2);
     publish(st + 1);
   }
-  // lane: outputs row0 + 4grp + i (group 0) and row1 + 4grp + i (group 1) of tile row 16g + col
-  float* s_amax = reinterpret_cast<float*>(xl[0]);        // (every wave is done with the stages)
+  // lane: outputs 4 grp + i of every weight group and tile row 16 g + col
   if (GU) {
-    // SwiGLU into acc0; a row's largest magnitude over the wave's 16 neurons, met in LDS with
-    // the other half of the 32-neuron block (wave wv ^ 1), gives the block's scale
+    // SwiGLU into the gate groups; a row's largest magnitude over the block of 32 neurons gives
+    // its scale: the wave's own two groups, or its one and, through LDS, that of wave wv ^ 1
+    float* s_amax = reinterpret_cast<float*>(xl[0]);      // (every wave is done with the stages)
+    float top[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      float top = 0.f;
+      top[g] = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc0[g][i] = swiglu4(acc0[g][i], acc1[g][i]);
-        top = fmaxf(top, fabsf(acc0[g][i]));
-      }
-      top = fmaxf(top, __shfl_xor(top, 16, kWave));
-      top = fmaxf(top, __shfl_xor(top, 32, kWave));
-      if (grp == 0) s_amax[wv * BM + 16 * g + col] = top;
+      for (int m = 0; m < 2 * R; m += 2)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          acc[m][g][i] = swiglu4(acc[m][g][i], acc[m + 1][g][i]);
+          top[g] = fmaxf(top[g], fabsf(acc[m][g][i]));
+        }
+      top[g] = fmaxf(top[g], __shfl_xor(top[g], 16, kWave));
+      top[g] = fmaxf(top[g], __shfl_xor(top[g], 32, kWave));
+      if (R == 1 && grp == 0) s_amax[wv * BM + 16 * g + col] = top[g];
     }
-    __syncthreads();
+    if (R == 1) __syncthreads();
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const int r = 16 * g + col;
       if (r >= mcount) continue;
-      const float top = fmaxf(s_amax[wv * BM + r], s_amax[(wv ^ 1) * BM + r]);
-      const int s = A4 ? mx4_scale_exp(top) : mx_scale_exp(top);
+      const int s = [&](float m) { return A4 ? mx4_scale_exp(m) : mx_scale_exp(m); }(
+          R == 1 ? fmaxf(top[g], s_amax[(wv ^ 1) * BM + r]) : top[g]);
       const float inv = exp2_neg(s);
-      const f32x4 v = acc0[g];
       const size_t row = static_cast<size_t>(rbase + r);
-      if (A4)
-        *reinterpret_cast<uint16_t*>(hq + row * (I / 2) + (nb + 4 * grp) / 2) =
-            static_cast<uint16_t>(f32x4_to_e2m1x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv));
-      else
-        *reinterpret_cast<uint32_t*>(hq + row * I + nb + 4 * grp) =
-            f32x4_to_e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-      if (grp == 0 && (wv & 1) == 0) hs[row * (I / 32) + nb / 32] = static_cast<uint8_t>(s + 127);
+#pragma unroll
+      for (int m = 0; m < 2 * R; m += 2) {
+        const f32x4 v = acc[m][g];
+        const int n = nb + 8 * m + 4 * grp;
+        if (A4)
+          *reinterpret_cast<uint16_t*>(hq + row * (I / 2) + n / 2) =
+              static_cast<uint16_t>(f32x4_to_e2m1x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv));
+        else
+          *reinterpret_cast<uint32_t*>(hq + row * I + n) =
+              f32x4_to_e4m3x4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+      }
+      if (grp == 0 && (R == 2 || (wv & 1) == 0)) hs[row * (I / 32) + nb / 32] = static_cast<uint8_t>(s + 127);
     }
     return;
   }
@@ -381,14 +398,14 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(BM == k
       const int t = perm[rbase + r];                      // k = 1: pair id == token
       const float wj = w[t];
       uint16_t* orow = out + static_cast<size_t>(t) * H + nb + 4 * grp;
-      *reinterpret_cast<uint2*>(orow) = make_uint2(pack_bf16x2(wj * acc0[g][0], wj * acc0[g][1]),
-                                                   pack_bf16x2(wj * acc0[g][2], wj * acc0[g][3]));
-      *reinterpret_cast<uint2*>(orow + 16) = make_uint2(pack_bf16x2(wj * acc1[g][0], wj * acc1[g][1]),
-                                                        pack_bf16x2(wj * acc1[g][2], wj * acc1[g][3]));
+#pragma unroll
+      for (int m = 0; m < 2 * R; ++m)
+        *reinterpret_cast<uint2*>(orow + 16 * m) = make_uint2(pack_bf16x2(wj * acc[m][g][0], wj * acc[m][g][1]),
+                                                              pack_bf16x2(wj * acc[m][g][2], wj * acc[m][g][3]));
     } else {
       float* yr = y + static_cast<size_t>(rbase + r) * H + nb + 4 * grp;
-      *reinterpret_cast<f32x4*>(yr) = acc0[g];            // (read back by the slot sum)
-      *reinterpret_cast<f32x4*>(yr + 16) = acc1[g];
+#pragma unroll
+      for (int m = 0; m < 2 * R; ++m) *reinterpret_cast<f32x4*>(yr + 16 * m) = acc[m][g];
     }
   }
 }
@@ -1240,22 +1257,32 @@ hipError_t launch_experts_mx4(const uint8_t* x, const uint8_t* xs, bool a4, cons
     else FIXUP4(kDown4);
 #undef FIXUP4
   } else {
-#define STREAM4(KD, A, AS, W, WS, Y, O, NBLK)                                                    \
+    // 96-row tiles: R = 1 gives twice the workgroups where R = 2 would leave half of the CUs idle (us, R = 1 for
+    // few / R = 2: E 8, H 4096, I 14336, 64 tokens 184 / 207; E 6, H 7168, I 2048, 256 tokens 62 / 78; with 192
+    // tiles of the down product, E 8, H 2048, I 5632, 1024 tokens 135 / 126)
+    const int64_t each = P / (kTall4 * E) + 1;                // about as many tiles an expert
+#define STREAM4_(KD, BM, R, A4, A, AS, W, WS, Y, O, N)                                           \
+  hipLaunchKernelGGL((gemm_mx4s<KD, BM, R, A4>), dim3(round_up((N) / (128 * (R)) * L.max_tiles, kXcds)), dim3(256), 0, \
+                     s, A, AS, W, WS, perm, tiles, n_tiles, counts, offsets, row_of, w, H, I, k, P, hq, hs, Y, O, order_key())
+#define STREAM4R(KD, BM, R, A, AS, W, WS, Y, O, N)                                               \
   do {                                                                                           \
-    const dim3 grid_(round_up((NBLK) * L.max_tiles, kXcds));                                     \
-    if (L.bm == kTall4) { if (a4) STREAM4_(KD, kTall4, true, A, AS, W, WS, Y, O); else STREAM4_(KD, kTall4, false, A, AS, W, WS, Y, O); } \
-    else { if (a4) STREAM4_(KD, kShort4, true, A, AS, W, WS, Y, O); else STREAM4_(KD, kShort4, false, A, AS, W, WS, Y, O); } \
+    if (a4) STREAM4_(KD, BM, R, true, A, AS, W, WS, Y, O, N);                                    \
+    else STREAM4_(KD, BM, R, false, A, AS, W, WS, Y, O, N);                                      \
   } while (0)
-#define STREAM4_(KD, BM, A4, A, AS, W, WS, Y, O)                                                 \
-  hipLaunchKernelGGL((gemm_mx4s<KD, 8, BM, A4>), grid_, dim3(512), 0, s, A, AS, W, WS, perm, tiles, n_tiles, \
-                     counts, offsets, row_of, w, H, I, k, P, hq, hs, Y, O, order_key())
+#define STREAM4(KD, A, AS, W, WS, Y, O, N)                                                       \
+  do {                                                                                           \
+    if (L.bm == kShort4) STREAM4R(KD, kShort4, 1, A, AS, W, WS, Y, O, N);                        \
+    else if (each * E * ((N) / 256) <= 128) STREAM4R(KD, kTall4, 1, A, AS, W, WS, Y, O, N);          \
+    else STREAM4R(KD, kTall4, 2, A, AS, W, WS, Y, O, N);                                         \
+  } while (0)
     prof_begin(kMx4GateUp, s);
-    STREAM4(kGateUp4, x, xs, wgu, wgus, nullptr, k == 1 ? out : nullptr, I / 128);
+    STREAM4(kGateUp4, x, xs, wgu, wgus, nullptr, k == 1 ? out : nullptr, 2 * I);
     prof_end(kMx4GateUp, s);
     prof_begin(kMx4Down, s);
-    if (k == 1) STREAM4(kDownFused4, hq, hs, wd, wds, nullptr, out, H / 256);
-    else STREAM4(kDown4, hq, hs, wd, wds, y, nullptr, H / 256);
+    if (k == 1) STREAM4(kDownFused4, hq, hs, wd, wds, nullptr, out, H);
+    else STREAM4(kDown4, hq, hs, wd, wds, y, nullptr, H);
 #undef STREAM4
+#undef STREAM4R
 #undef STREAM4_
   }
   hipError_t e = hipGetLastError();

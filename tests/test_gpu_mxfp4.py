@@ -178,6 +178,8 @@ SIZES = [
     (17, 768, 512, 4, 2), (33, 512, 768, 6, 1), (64, 1024, 256, 32, 8), (65, 512, 256, 5, 2), (130, 256, 256, 2, 2),
     (300, 512, 512, 3, 1), (777, 256, 512, 16, 6), (600, 512, 256, 1, 1), (513, 768, 256, 2, 2), (1025, 1024, 512, 4, 1),
     (700, 4096, 1024, 1, 1), (1300, 2048, 2048, 2, 1), (900, 4096, 1024, 4, 2), (1500, 1024, 2048, 4, 2),
+    # 96-row tiles with enough of them for 64 weight rows a wave: on the gate/up product, on the down product, on both
+    (700, 512, 512, 72, 2), (1900, 512, 512, 72, 1), (500, 512, 1280, 18, 2), (333, 2304, 256, 15, 3), (2500, 256, 2048, 24, 1),
     # 256-row tiles: k = 1 and more, ragged experts, odd numbers of steps, slices of the last round's tiles on
     # either product
     (2200, 2048, 2048, 3, 1), (1300, 2048, 2048, 4, 2), (2048, 2048, 2048, 1, 1), (2305, 2304, 2048, 1, 1),
@@ -202,8 +204,9 @@ def test_experts_skewed(M, T, four):
 
 @pytest.mark.parametrize("T,E,k,H,I", [
     (6, 4, 2, 512, 256), (50, 8, 3, 512, 256), (200, 8, 3, 512, 256), (9, 4, 1, 512, 256), (300, 4, 1, 512, 256),
-    (900, 3, 1, 512, 256), (1200, 3, 2, 512, 256), (1100, 3, 1, 2048, 2048), (600, 3, 2, 4096, 1024),
-    (2200, 3, 1, 2048, 2048), (1100, 3, 2, 2048, 2048), (1100, 2, 1, 1024, 4096)])
+    (900, 3, 1, 512, 256), (1200, 3, 2, 512, 256), (1100, 3, 1, 2048, 2048),
+    (600, 3, 2, 4096, 1024),
+    (2200, 3, 1, 2048, 2048), (1100, 3, 2, 2048, 2048), (1100, 2, 1, 1024, 4096), (1200, 72, 2, 512, 512), (2500, 72, 1, 512, 512)])
 @pytest.mark.parametrize("four", [False, True])
 def test_experts_ids_out_of_range(M, T, E, k, H, I, four):
     print(f"[mxfp4] ids out of range T={T} E={E} k={k} H={H} four={four}", flush=True)
@@ -279,7 +282,7 @@ def test_experts_far_apart_scales(M, T, H, I, four):
 
 
 @pytest.mark.parametrize("T,E,k,H,I", [(3, 8, 2, 512, 256), (90, 8, 2, 512, 256), (700, 4, 2, 512, 256),
-                                       (2200, 3, 1, 2048, 2048), (1300, 3, 2, 2048, 2048)])
+                                       (2200, 3, 1, 2048, 2048), (1300, 3, 2, 2048, 2048), (800, 72, 2, 512, 512), (1800, 72, 1, 512, 512)])
 @pytest.mark.parametrize("four", [False, True])
 def test_experts_bad_token_leaves_the_others(M, T, E, k, H, I, four):
     """A token with a NaN scale, and an expert with one: only that token's, and that expert's tokens'
@@ -300,7 +303,7 @@ def test_experts_bad_token_leaves_the_others(M, T, E, k, H, I, four):
 
 @pytest.mark.parametrize("T,E,k,H,I", [(1, 8, 2, 512, 512), (40, 8, 2, 512, 512), (500, 8, 2, 512, 512), (900, 2, 1, 2048, 2048),
                                        (700, 2, 2, 4096, 1024), (2100, 2, 1, 2048, 2048), (1050, 2, 2, 2048, 2048),
-                                       (1100, 2, 1, 1024, 4096), (2305, 1, 1, 2304, 2048)])
+                                       (1100, 2, 1, 1024, 4096), (2305, 1, 1, 2304, 2048), (800, 72, 2, 512, 512), (1800, 72, 1, 512, 512)])
 @pytest.mark.parametrize("four", [False, True])
 def test_experts_deterministic_and_order_free(M, T, E, k, H, I, four):
     print(f"[mxfp4] order T={T} E={E} k={k} four={four}", flush=True)
@@ -316,7 +319,7 @@ def test_experts_deterministic_and_order_free(M, T, E, k, H, I, four):
     M.moe_set_debug_options(0, 0)
 
 
-@pytest.mark.parametrize("T", [4, 90, 600, 160000])
+@pytest.mark.parametrize("T", [4, 90, 600, 164000])
 @pytest.mark.parametrize("four", [False, True])
 def test_experts_large_offsets(M, T, four):
     """An expert array beyond 2^32 bytes and the last experts in it."""
