@@ -53,7 +53,9 @@ __device__ __forceinline__ void clear_rows(uint16_t* __restrict__ out, const int
 
 }  // namespace
 
-// moe_quantize_mxfp4: four lanes per block of 32, eight BF16 values each.  n pieces of eight.
+// moe_quantize_mxfp4: four lanes per block of 32, eight BF16 values each, so that a wave reads
+// 1 KB and writes 256 bytes of codes in one piece; the block's scale from the largest of the four
+// lanes.  n pieces of eight.  Bound by memory: 16384 x 4096 in 29.7 us, 5.7 TB/s (6.1 from 900 MB on).
 __global__ __launch_bounds__(256) void quant_mx4_rows(const uint16_t* __restrict__ src, int64_t n,
                                                       uint32_t* __restrict__ codes,
                                                       uint8_t* __restrict__ scales, int64_t base, uint32_t okey) {
@@ -79,7 +81,9 @@ __global__ __launch_bounds__(256) void quant_mx4_rows(const uint16_t* __restrict
   if ((i & 3) == 0) scales[i >> 2] = static_cast<uint8_t>(s + 127);
 }
 
-// moe_dequantize_mxfp4: eight codes a lane.
+// moe_dequantize_mxfp4: eight codes a lane.  Bound by memory, above all by its stores, which are
+// streaming ones (451 MB, 43520 x 4096: plain 110 us, streaming 88, 5.1 TB/s; 16384 x 4096 41 and 26;
+// streaming loads of the codes take the gain back, 105).
 __global__ __launch_bounds__(256) void dequant_mx4_rows(const uint32_t* __restrict__ codes,
                                                         const uint8_t* __restrict__ scales, int64_t n,
                                                         uint16_t* __restrict__ dst, int64_t base,
@@ -102,7 +106,7 @@ __global__ __launch_bounds__(256) void dequant_mx4_rows(const uint32_t* __restri
     }
     o[j] = static_cast<int>(pack_bf16x2(f[0], f[1]));
   }
-  st16(dst + 8 * i, o);
+  st16_stream(dst + 8 * i, o);
 }
 
 Mx4Ws mx4_ws_layout(int T, int H, int I, int E, int k, bool a4) {
@@ -984,7 +988,9 @@ hipError_t mx4_set_attributes() {
 // pair's one row.  Blocks, chunks and products follow in the streaming form's order, so a
 // pair has the bits that it has there.  The step is bound by the latency of two dependent
 // passes over memory and needs no grouping; pairs that share an expert read its weights from
-// the L2 the second time.
+// the L2 the second time.  One token, 8 of 128 experts, H 2048, I 768: 20 MB of weights in
+// 5.0 + 5.3 us of kernels, 12 us a call (grouped and streamed 21); 8 of 384 experts, H 7168,
+// I 2048: 187 MB in 44 us, 4.3 TB/s.
 namespace {
 // 16 (ROWS 8: 8, each twice) weight rows on their way into operands: U chunks of 256 positions,
 // loaded as 8 rows x 128 contiguous bytes (lane = row ln >> 3, piece ln & 7) and passed through
@@ -1037,11 +1043,11 @@ constexpr int kPairCols4 = 8;                            // output columns per w
 constexpr int kPairWaves4 = 8;
 // Taken for 48 pairs at most, while the weights that it reads more than once (pairs that share an
 // expert; expected number of distinct experts E (1 - (1 - k/E)^T)) stay below 60 MB, about the
-// 12 us that grouping and its launches cost the streaming form, and all that it reads below 350 MB,
+// 8 to 12 us that grouping and its launches cost the streaming form, and all that it reads below 350 MB,
 // where that form's higher rate has made up for them.  Measured, us (this / streaming), MXFP8:
-// H 2048 I 768 E 128 k 8, T 1 14.7 / 24.4, T 6 29 / 35; H 2048 I 1024 E 8 k 2, T 8 14.9 / 25.6, T 24
-// (133 MB again) 29 / 26; H 7168 I 2048 E 32 k 4, T 2 43 / 58, T 4 (65 MB again) 78 / 71; H 7168 I 2048
-// E 384 k 8, T 1 44 / 61, T 2 (374 MB) 79 / 78; H 4096 I 1024 E 4 k 1, T 40 46 / 33.
+// H 2048 I 768 E 128 k 8, T 1 13.3 / 21.3, T 6 29 / 32; H 2048 I 1024 E 8 k 2, T 8 14.9 / 22.7, T 24
+// (133 MB again) 29 / 23; H 7168 I 2048 E 32 k 4, T 2 43 / 50, T 4 (65 MB again) 78 / 70; H 7168 I 2048
+// E 384 k 8, T 1 44 / 52, T 2 (374 MB) 79 / 80; H 4096 I 1024 E 4 k 1, T 40 46 / 27.
 inline bool use_pairs4(int T, int H, int I, int E, int k) {
   const int64_t P = static_cast<int64_t>(T) * k;
   if (P > kPairsMax4) return false;
