@@ -580,7 +580,8 @@ size_t moe_experts_mxfp4_workspace_bytes(int T, int H, int I, int E, int k, moe_
  *   losses     [2] float32 out,  counts [n_seqs, E] int32 out,  probs [n_seqs, E] float32 out,
  *   tokens     [n_seqs] int32 out: N_s
  *   workspace  >= moe_balance_loss_workspace_bytes(T, E, n_seqs), contents ignored
- * Scores and sums are FP32 (a few units in the last place; sums over workgroups FP64).
+ * Scores are FP32: a few units in the last place, and 2^-25 |logit - largest| beside that from
+ * the logits' difference.  Sums within a workgroup are FP32, over workgroups FP64.
  * Limits: 0 <= T < 2^22, 1 <= n_seqs <= 4096 and a divisor of T, E <= 1024, 1 <= k <=
  * min(E, 32).  T = 0 writes zeros.
  */

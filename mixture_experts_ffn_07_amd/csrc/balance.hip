@@ -153,7 +153,9 @@ inline int lane_values(int E) {
 BalanceWs balance_ws_layout(int T, int E, int S) {
   BalanceWs L{};
   const int len = T / S;
-  // chunks of a sequence's rows, one workgroup each: two workgroups a CU, a step of rows each at least
+  // chunks of a sequence's rows, one workgroup each, a step of rows each at least: 1024, four workgroups a CU
+  // (32768 x 256 in 8 sequences, us of the rows' kernel / of the gradient's: 256 chunks 16.1 / 29, 512 15.6 / 25,
+  // 1024 13.6 / 21.7)
   const int step = kRowWaves * rows_at_once(lane_values(E));
   const int most = S < 1024 ? 1024 / S : 1, want = (len + step - 1) / step;
   const int room = want < 1 ? 1 : want < most ? want : most;   // (does not fall as T grows)
@@ -174,6 +176,10 @@ BalanceWs balance_ws_layout(int T, int E, int S) {
 
 // Workgroup = a chunk of a sequence's rows, R rows at a time to each wave; its sums of p, its
 // counts, its sum of lse^2 and its tokens go to the workspace, to be joined in chunk order.
+// 2048 x 384 sigmoid: 5.5 us, the latency of one pass.  32768 x 256 softmax, k 8: 13.3 us for 35 MB,
+// 2.6 TB/s, bound by vector instructions (an exponential, a product and a sum for each score, their
+// reductions, and the pairs' counters in LDS).  With one row at a time to a wave the calls took 59
+// and 30 us, now 13 to 15 and 18.
 template <bool SIG, int V, int NV>
 __global__ __launch_bounds__(kRowWaves * kWave) void balance_rows(
     const float* __restrict__ logits, const int32_t* __restrict__ idx, const uint8_t* __restrict__ mask,
@@ -364,7 +370,8 @@ __global__ __launch_bounds__(256) void balance_losses(const BalanceShare* __rest
 }
 
 // Gradient: workgroup = a chunk of a sequence's rows, R rows at a time to each wave; the
-// sequence's counts and the sum of tokens are read once.
+// sequence's counts and the sum of tokens are read once.  32768 x 256, added to a given gradient:
+// 101 MB in 20-22 us, 4.6-5.1 TB/s, bound by memory; 2048 x 384 6.8 us, a launch and one pass.
 template <bool SIG, int V, int NV>
 __global__ __launch_bounds__(kRowWaves * kWave) void balance_backward_rows(
     const float* __restrict__ logits, const uint8_t* __restrict__ mask, const int* __restrict__ counts,

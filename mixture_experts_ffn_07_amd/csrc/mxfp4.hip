@@ -432,6 +432,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM == kShor
 // The scales come straight to registers, a dword a row and step, from copies with the step
 // outside and the row inside (mx4_scales_t; the gate/up epilogue writes h's that way): from
 // rows as they are given, a wave's load would touch 32 lines.
+//
+// Measured, 16384 rows, 6 experts, H 7168, I 2048: MXFP4 gate/up 275 us, 3.5 PFLOP/s (matrix
+// cores busy half of the time), down 199, 2.4 (8 steps a tile against its start, and 235 MB of
+// output).  With two stages of loads in flight instead of one the whole call took 536 us for 530.
 namespace {
 constexpr int kLTile = kLargeBM * 128;                   // bytes of an operand's stage
 
@@ -911,7 +915,8 @@ __global__ __launch_bounds__(256) void gemm_large_mx4_fixup_down(
 // Scales with the step of 256 positions outside and the row inside, 8 bytes each in the order of
 // scale_place, of both weights and of the routed activations (gathered into grouped order):
 // workgroup = 64 rows x 32 steps through LDS, reads and writes along their own rows.  With one
-// slot, output rows of pairs without an expert are cleared here.
+// slot, output rows of pairs without an expert are cleared here.  (16384 rows, 6 experts, H 7168,
+// I 2048: 12 MB in and out in 13 us.)
 template <bool A4>
 __global__ __launch_bounds__(256) void mx4_scales_t(
     const uint2* __restrict__ wgus, const uint2* __restrict__ wds, const uint2* __restrict__ xs,
