@@ -112,20 +112,19 @@ __global__ __launch_bounds__(256) void dequant_mx4_rows(const uint32_t* __restri
 Mx4Ws mx4_ws_layout(int T, int H, int I, int E, int k, bool a4) {
   Mx4Ws L{};
   const size_t P = static_cast<size_t>(T) * k;
-  // 256-row tiles where the products are bound by the matrix cores and LDS: with long reductions
-  // (weights of 8 M values a matrix) from 192 rows an expert, else from 320, and enough tiles of
-  // gate/up that the rounds and the split tail run full: half of the CUs, or five rounds where
-  // reductions are short (below 4 M) against a tile's start and end.  Measured, us (256-row /
-  // 96-row tiles, MXFP4; MXFP8):
-  //   H 7168 I 2048 E 32 k 4: 192 rows an expert 386 / 468; 477 / 503, 512 rows 726 / 1098; 903 / 1178
-  //   H 7168 I 2048 E 6 k 1, MXFP8: 171 rows (64 tiles) 116 / 104, 320 rows (112) 146 / 174
-  //   H 4096 I 14336 E 8 k 2: 128 rows 294 / 317; 353 / 361, 192 rows 310 / 475; 403 / 536
-  //   H 2048 I 5632 E 8 k 2: 256 rows MXFP8 151 / 146, 512 rows 184 / 228; 223 / 253
-  //   H 4096 I 1024 E 64 k 6: 256 rows MXFP8 415 / 413, 384 rows 463 / 551; 541 / 593, 1536 rows 1523 / 2047
-  //   H 4096 I 1024 E 16 k 4: 512 rows (256 tiles) 193 / 180, 1024 rows 287 / 334; 334 / 368
-  //   H 2048 I 768 E 64 k 8, 1024 rows (1536 tiles) 535 / 567; 612 / 626
-  //   H 2048 I 1024 k 4, 1024 rows: E 16 (512 tiles) 191 / 169; 215 / 193, E 32 (1024) 345 / 326, E 64 (2048)
-  //     604 / 672
+  // 256-row tiles where the products are bound by the matrix cores and LDS: from 192 rows an
+  // expert, where an expert's rows times H I reach 3 G (long reductions or many rows, against a
+  // tile's start and end and the scales' transposition), with tiles of gate/up for half of the CUs.
+  // Measured, us (256-row / 96-row tiles, MXFP4; MXFP8):
+  //   H 4096 I 14336 E 8 k 2: 128 rows an expert 298 / 323; 372 / 376, 192 rows 315 / 428; 414 / 486
+  //   H 7168 I 2048 E 32 k 4: 192 rows (2.8 G) 393 / 396; 489 / 443, 256 rows 431 / 498; 540 / 563, 512 rows 746 / 853;
+  //     924 / 974
+  //   H 7168 I 2048 E 6 k 1, MXFP8: 171 rows 116 / 101, 320 rows (112 tiles) 150 / 148
+  //   H 2048 I 5632 E 8 k 2: 256 rows MXFP8 154 / 132, 512 rows 187 / 176; 229 / 210
+  //   H 4096 I 1024 E 64 k 6: 256 rows MXFP8 429 / 375, 384 rows 477 / 471; 557 / 533, 1536 rows 1555 / 1659
+  //   H 4096 I 1024 E 16 k 4: 512 rows 198 / 161, 1024 rows 296 / 287; 342 / 329, 2048 rows 556 / 564; 642 / 651
+  //   H 2048 I 768 E 64 k 8: 1024 rows 545 / 522; 620 / 587, 2048 rows 1007 / 1013; 1155 / 1146
+  //   H 2048 I 1024 k 4: E 16, 1024 rows 197 / 156; 219 / 181, E 64, 2048 rows 1140 / 1161; 1328 / 1357
   // 96-row tiles from 18 rows an expert, below it 32-row ones (32 / 96):
   //   H 4096 I 1024 E 64 k 6: 19 rows 115 / 103; 121 / 108, 73 rows 265 / 164; 284 / 179
   //   H 2048 I 768 E 128 k 8: 4 rows 65 / 68; 66 / 70, 16 rows 82 / 79; 86 / 84
@@ -134,9 +133,8 @@ Mx4Ws mx4_ws_layout(int T, int H, int I, int E, int k, bool a4) {
   //     51 / 56
   // (64-row ones lie within 8 % of the better of the two, on both sides, from 16 to 75 rows; 128-row ones leave
   // registers for half as many weight rows a wave: E 64, 73 rows 171; 188, E 16, 1024 rows 179; 215.)
-  const size_t gu_tiles = P / kLargeBM * (I / 128), HI = static_cast<size_t>(H) * I;
-  const bool large = P >= (HI >= (size_t(8) << 20) ? 192 : 320) * static_cast<size_t>(E) &&
-                     gu_tiles >= (HI >= (size_t(4) << 20) ? 128u : 1280u);
+  const bool large = P >= 192 * static_cast<size_t>(E) && P * H * I >= (size_t(3) << 30) * E &&
+                     P / kLargeBM * (I / 128) >= 128;
   L.bm = large ? kLargeBM : P >= 18 * static_cast<size_t>(E) ? kTall4 : kShort4;
   L.max_tiles = static_cast<int>(E + (P + L.bm - 1) / L.bm);
   const size_t tile_room = E + (P + kShort4 - 1) / kShort4;     // (as many as any smaller T takes)
@@ -176,16 +174,16 @@ enum { kGateUp4 = 0, kDown4 = 1, kDownFused4 = 2 };
 // one of MXFP8) with their scales, double-buffered and shared by the waves; the next
 // chunk's weights and the next stage's activations are in flight while one multiplies, and
 // the CU's other workgroups cover what that does not.  Rows past the tile's end load the
-// tile's first row; their columns are computed and discarded.
+// tile's first row; their columns are computed and discarded.  KEEP: plain loads of the weights.
 //
 // 32-row tiles are bound by the weights' bytes: R = 1, 100-106 registers, four workgroups a
 // CU (8 experts of 4096 x 14336, 64 tokens: 748 MB in 160-169 us, 4.4-4.7 TB/s; 8 waves a
 // workgroup 196, R = 2 198).  96-row tiles are bound by LDS, where every wave reads the whole
 // stage: R = 2 halves that per product, 246-252 registers, two workgroups a CU (E 16, 4095
-// tokens, MXFP8: 215 us with R = 1 and 8 waves, 191 with R = 2, 1.08 PFLOP/s of the whole
-// call).  A second chunk and stage in flight cost the second workgroup and 4 %; stages of 128
+// tokens, MXFP8: 215 us with R = 1 and 8 waves, 191 with R = 2, 176 with KEEP, 1.17 PFLOP/s of
+// the whole call).  A second chunk and stage in flight cost the second workgroup and 4 %; stages of 128
 // bytes, twice the barriers, 2-10 %; weights loaded straight to LDS, 3-9 %.
-template <int KIND, int BM, int R, bool A4>
+template <int KIND, int BM, int R, bool KEEP, bool A4>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM == kShort4 ? 4 : 2, 8))) void gemm_mx4s(
     const uint8_t* __restrict__ act, const uint8_t* __restrict__ acts,
     const uint8_t* __restrict__ wt, const uint8_t* __restrict__ wts,
@@ -203,7 +201,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM == kShor
   constexpr int CH = SB / 16;                             // 16-byte pieces of a row per stage
   constexpr int LPT = BM * CH / NT;                       // 16-byte code loads per thread
   constexpr int SS = 8 * CPS;                             // scale bytes of a row per stage
-  constexpr int BD = 2;                           // activation operands held
+  constexpr int BD = 2;                                   // activation operands held
   __shared__ __align__(16) uint8_t xl[2][BM * RS];
   __shared__ __align__(16) uint8_t sl[2][BM * SS];
   __shared__ __align__(16) i32x4 wtl[NW][16 * 8];         // per wave: [16 rows][8 pieces]
@@ -280,8 +278,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM == kShor
   auto request = [&](int m, int c) {
     const uint32_t cc = static_cast<uint32_t>(min(c, nchunk - 1));
     const uint8_t* p = wb + (static_cast<uint32_t>(grow(m) * RB) + 128 * cc);
-    W[2 * m] = ld16_stream(p + ow);
-    W[2 * m + 1] = ld16_stream(p + 8 * RB + ow);
+    W[2 * m] = KEEP ? ld16(p + ow) : ld16_stream(p + ow);
+    W[2 * m + 1] = KEEP ? ld16(p + 8 * RB + ow) : ld16_stream(p + 8 * RB + ow);
     sc[m] = *reinterpret_cast<const uint2*>(wsb + (static_cast<uint32_t>(grow(m) * KB) + 8 * cc) + os);
   };
   fetch(0);
@@ -1271,20 +1269,25 @@ hipError_t launch_experts_mx4(const uint8_t* x, const uint8_t* xs, bool a4, cons
     // 96-row tiles: R = 1 gives twice the workgroups where R = 2 would leave half of the CUs idle (us, R = 1 for
     // few / R = 2: E 8, H 4096, I 14336, 64 tokens 184 / 207; E 6, H 7168, I 2048, 256 tokens 62 / 78; with 192
     // tiles of the down product, E 8, H 2048, I 5632, 1024 tokens 135 / 126)
+    // (weights are loaded for once, or, from 64 rows an expert, kept in the caches for the expert's other tiles; us, for
+    // once / kept, MXFP8: E 64, H 2048, I 768, 50 rows an expert 71 / 75, 75 rows 80 / 83, 100 rows 101 / 100; E 64,
+    // H 4096, I 1024, 60 rows 166 / 161, 73 rows 179 / 169, 192 rows 341 / 296; E 16, H 2048, I 1024, 1024 rows 191 / 176)
+    const bool keep = P >= static_cast<int64_t>(64) * E;
     const int64_t each = P / (kTall4 * E) + 1;                // about as many tiles an expert
-#define STREAM4_(KD, BM, R, A4, A, AS, W, WS, Y, O, N)                                           \
-  hipLaunchKernelGGL((gemm_mx4s<KD, BM, R, A4>), dim3(round_up((N) / (128 * (R)) * L.max_tiles, kXcds)), dim3(256), 0, \
+#define STREAM4_(KD, BM, R, KEEP, A4, A, AS, W, WS, Y, O, N)                                           \
+  hipLaunchKernelGGL((gemm_mx4s<KD, BM, R, KEEP, A4>), dim3(round_up((N) / (128 * (R)) * L.max_tiles, kXcds)), dim3(256), 0, \
                      s, A, AS, W, WS, perm, tiles, n_tiles, counts, offsets, row_of, w, H, I, k, P, hq, hs, Y, O, order_key())
-#define STREAM4R(KD, BM, R, A, AS, W, WS, Y, O, N)                                               \
+#define STREAM4R(KD, BM, R, KEEP, A, AS, W, WS, Y, O, N)                                               \
   do {                                                                                           \
-    if (a4) STREAM4_(KD, BM, R, true, A, AS, W, WS, Y, O, N);                                    \
-    else STREAM4_(KD, BM, R, false, A, AS, W, WS, Y, O, N);                                      \
+    if (a4) STREAM4_(KD, BM, R, KEEP, true, A, AS, W, WS, Y, O, N);                                    \
+    else STREAM4_(KD, BM, R, KEEP, false, A, AS, W, WS, Y, O, N);                                      \
   } while (0)
 #define STREAM4(KD, A, AS, W, WS, Y, O, N)                                                       \
   do {                                                                                           \
-    if (L.bm == kShort4) STREAM4R(KD, kShort4, 1, A, AS, W, WS, Y, O, N);                        \
-    else if (each * E * ((N) / 256) <= 128) STREAM4R(KD, kTall4, 1, A, AS, W, WS, Y, O, N);          \
-    else STREAM4R(KD, kTall4, 2, A, AS, W, WS, Y, O, N);                                         \
+    if (L.bm == kShort4) STREAM4R(KD, kShort4, 1, false, A, AS, W, WS, Y, O, N);                        \
+    else if (each * E * ((N) / 256) <= 128) STREAM4R(KD, kTall4, 1, false, A, AS, W, WS, Y, O, N);          \
+    else if (keep) STREAM4R(KD, kTall4, 2, true, A, AS, W, WS, Y, O, N);                         \
+    else STREAM4R(KD, kTall4, 2, false, A, AS, W, WS, Y, O, N);                                  \
   } while (0)
     prof_begin(kMx4GateUp, s);
     STREAM4(kGateUp4, x, xs, wgu, wgus, nullptr, k == 1 ? out : nullptr, 2 * I);

@@ -179,11 +179,11 @@ SIZES = [
     (300, 512, 512, 3, 1), (777, 256, 512, 16, 6), (600, 512, 256, 1, 1), (513, 768, 256, 2, 2), (1025, 1024, 512, 4, 1),
     (700, 4096, 1024, 1, 1), (1300, 2048, 2048, 2, 1), (900, 4096, 1024, 4, 2), (1500, 1024, 2048, 4, 2),
     # 96-row tiles with enough of them for 64 weight rows a wave: on the gate/up product, on the down product, on both
-    (700, 512, 512, 72, 2), (1900, 512, 512, 72, 1), (500, 512, 1280, 18, 2), (333, 2304, 256, 15, 3), (2500, 256, 2048, 24, 1),
+    (700, 512, 512, 72, 2), (1900, 512, 512, 72, 1), (500, 512, 1280, 18, 2), (333, 2304, 256, 15, 3), (2500, 256, 2048, 24, 1), (2600, 512, 512, 40, 1), (1500, 512, 768, 40, 2),
     # 256-row tiles: k = 1 and more, ragged experts, odd numbers of steps, slices of the last round's tiles on
     # either product
-    (2200, 2048, 2048, 3, 1), (1300, 2048, 2048, 4, 2), (2048, 2048, 2048, 1, 1), (2305, 2304, 2048, 1, 1),
-    (1100, 1024, 4096, 2, 1), (700, 1280, 4096, 2, 2), (1200, 1792, 3840, 3, 1)]
+    (2400, 2048, 2048, 3, 1), (1600, 2048, 2048, 4, 2), (2048, 2048, 2048, 1, 1), (2305, 2304, 2048, 1, 1),
+    (1600, 1024, 4096, 2, 1), (700, 1280, 4096, 2, 2), (1500, 1792, 3840, 3, 1)]
 
 
 @pytest.mark.parametrize("T,H,I,E,k", SIZES)
@@ -206,7 +206,7 @@ def test_experts_skewed(M, T, four):
     (6, 4, 2, 512, 256), (50, 8, 3, 512, 256), (200, 8, 3, 512, 256), (9, 4, 1, 512, 256), (300, 4, 1, 512, 256),
     (900, 3, 1, 512, 256), (1200, 3, 2, 512, 256), (1100, 3, 1, 2048, 2048),
     (600, 3, 2, 4096, 1024),
-    (2200, 3, 1, 2048, 2048), (1100, 3, 2, 2048, 2048), (1100, 2, 1, 1024, 4096), (1200, 72, 2, 512, 512), (2500, 72, 1, 512, 512)])
+    (2400, 3, 1, 2048, 2048), (1200, 3, 2, 2048, 2048), (1600, 2, 1, 1024, 4096), (1200, 72, 2, 512, 512), (2500, 72, 1, 512, 512)])
 @pytest.mark.parametrize("four", [False, True])
 def test_experts_ids_out_of_range(M, T, E, k, H, I, four):
     print(f"[mxfp4] ids out of range T={T} E={E} k={k} H={H} four={four}", flush=True)
@@ -256,7 +256,7 @@ def test_experts_same_expert_twice(M, four):
         check(d, call(M, d))
 
 
-@pytest.mark.parametrize("T,H,I", [(4, 512, 256), (90, 512, 256), (700, 512, 256), (1200, 2048, 2048)])
+@pytest.mark.parametrize("T,H,I", [(4, 512, 256), (90, 512, 256), (700, 512, 256), (1600, 2048, 2048)])
 @pytest.mark.parametrize("four", [False, True])
 def test_experts_zero_rows(M, T, H, I, four):
     d = make(M, T, H, I, 4, 2, four, seed=4)
@@ -269,7 +269,7 @@ def test_experts_zero_rows(M, T, H, I, four):
     check(d, out)
 
 
-@pytest.mark.parametrize("T,H,I", [(6, 512, 512), (70, 512, 512), (300, 512, 512), (1100, 2048, 2048)])
+@pytest.mark.parametrize("T,H,I", [(6, 512, 512), (70, 512, 512), (300, 512, 512), (1200, 2048, 2048)])
 @pytest.mark.parametrize("four", [False, True])
 def test_experts_far_apart_scales(M, T, H, I, four):
     """Blocks whose scales lie far apart, on both operands; activations that saturate silu."""
@@ -282,7 +282,7 @@ def test_experts_far_apart_scales(M, T, H, I, four):
 
 
 @pytest.mark.parametrize("T,E,k,H,I", [(3, 8, 2, 512, 256), (90, 8, 2, 512, 256), (700, 4, 2, 512, 256),
-                                       (2200, 3, 1, 2048, 2048), (1300, 3, 2, 2048, 2048), (800, 72, 2, 512, 512), (1800, 72, 1, 512, 512)])
+                                       (2400, 3, 1, 2048, 2048), (1300, 3, 2, 2048, 2048), (800, 72, 2, 512, 512), (1800, 72, 1, 512, 512)])
 @pytest.mark.parametrize("four", [False, True])
 def test_experts_bad_token_leaves_the_others(M, T, E, k, H, I, four):
     """A token with a NaN scale, and an expert with one: only that token's, and that expert's tokens'
@@ -303,7 +303,8 @@ def test_experts_bad_token_leaves_the_others(M, T, E, k, H, I, four):
 
 @pytest.mark.parametrize("T,E,k,H,I", [(1, 8, 2, 512, 512), (40, 8, 2, 512, 512), (500, 8, 2, 512, 512), (900, 2, 1, 2048, 2048),
                                        (700, 2, 2, 4096, 1024), (2100, 2, 1, 2048, 2048), (1050, 2, 2, 2048, 2048),
-                                       (1100, 2, 1, 1024, 4096), (2305, 1, 1, 2304, 2048), (800, 72, 2, 512, 512), (1800, 72, 1, 512, 512)])
+                                       (1600, 2, 1, 1024, 4096), (2305, 1, 1, 2304, 2048), (800, 72, 2, 512, 512), (1800, 72, 1, 512, 512),
+                                       (2400, 72, 2, 512, 512), (5000, 72, 1, 512, 512)])
 @pytest.mark.parametrize("four", [False, True])
 def test_experts_deterministic_and_order_free(M, T, E, k, H, I, four):
     print(f"[mxfp4] order T={T} E={E} k={k} four={four}", flush=True)
@@ -319,7 +320,7 @@ def test_experts_deterministic_and_order_free(M, T, E, k, H, I, four):
     M.moe_set_debug_options(0, 0)
 
 
-@pytest.mark.parametrize("T", [4, 90, 600, 164000])
+@pytest.mark.parametrize("T", [4, 90, 600, 164000, 404000])
 @pytest.mark.parametrize("four", [False, True])
 def test_experts_large_offsets(M, T, four):
     """An expert array beyond 2^32 bytes and the last experts in it."""
@@ -332,7 +333,7 @@ def test_experts_large_offsets(M, T, four):
     for n, t in big.items():
         t[E - 2:] = d[n]
     moved = dict(d, **big, idx=d["idx"] + (E - 2))
-    out = call(M, moved)                                    # (160000: 256-row tiles)
+    out = call(M, moved)                                    # (404000: 256-row tiles)
     check(d, out, rows=slice(T - 40 if T > 40 else 0, T))
     assert E * I * H >= 2 ** 32
 
