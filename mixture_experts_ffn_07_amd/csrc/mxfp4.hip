@@ -167,22 +167,22 @@ enum { kGateUp4 = 0, kDown4 = 1, kDownFused4 = 2 };
 // 4 waves), each wave owning 2 R groups of 16 weight rows (gate_up: 16 R neurons' gate and up
 // rows; down: 32 R output channels).  A chunk is 256 positions of K, 128 bytes of a weight
 // row: the wave reads a group as two loads of 8 rows x 128 contiguous bytes
-// (non-temporal), passes them through a wave-private 2 KB LDS tile (16-byte pieces
+// (non-temporal, KEEP: plain), passes them through a wave-private 2 KB LDS tile (16-byte pieces
 // XOR-swizzled by row), and reads back two operands of the 16x16x128 MFMA: product j takes
 // blocks 2g + j of the chunk's eight in lane group g, so a lane's two scales are neighbours.
 // The activations are staged in LDS, 256 bytes of each row a stage (two chunks of MXFP4,
 // one of MXFP8) with their scales, double-buffered and shared by the waves; the next
 // chunk's weights and the next stage's activations are in flight while one multiplies, and
 // the CU's other workgroups cover what that does not.  Rows past the tile's end load the
-// tile's first row; their columns are computed and discarded.  KEEP: plain loads of the weights.
+// tile's first row; their columns are computed and discarded.
 //
 // 32-row tiles are bound by the weights' bytes: R = 1, 100-106 registers, four workgroups a
 // CU (8 experts of 4096 x 14336, 64 tokens: 748 MB in 160-169 us, 4.4-4.7 TB/s; 8 waves a
 // workgroup 196, R = 2 198).  96-row tiles are bound by LDS, where every wave reads the whole
 // stage: R = 2 halves that per product, 246-252 registers, two workgroups a CU (E 16, 4095
 // tokens, MXFP8: 215 us with R = 1 and 8 waves, 191 with R = 2, 176 with KEEP, 1.17 PFLOP/s of
-// the whole call).  A second chunk and stage in flight cost the second workgroup and 4 %; stages of 128
-// bytes, twice the barriers, 2-10 %; weights loaded straight to LDS, 3-9 %.
+// the whole call).  A second chunk and stage in flight cost the second workgroup and 4 %; stages
+// of 128 bytes, twice the barriers, 2-10 %; weights loaded straight to LDS, 3-9 %.
 template <int KIND, int BM, int R, bool KEEP, bool A4>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM == kShort4 ? 4 : 2, 8))) void gemm_mx4s(
     const uint8_t* __restrict__ act, const uint8_t* __restrict__ acts,
@@ -1269,23 +1269,25 @@ hipError_t launch_experts_mx4(const uint8_t* x, const uint8_t* xs, bool a4, cons
     // 96-row tiles: R = 1 gives twice the workgroups where R = 2 would leave half of the CUs idle (us, R = 1 for
     // few / R = 2: E 8, H 4096, I 14336, 64 tokens 184 / 207; E 6, H 7168, I 2048, 256 tokens 62 / 78; with 192
     // tiles of the down product, E 8, H 2048, I 5632, 1024 tokens 135 / 126)
-    // (weights are loaded for once, or, from 64 rows an expert, kept in the caches for the expert's other tiles; us, for
-    // once / kept, MXFP8: E 64, H 2048, I 768, 50 rows an expert 71 / 75, 75 rows 80 / 83, 100 rows 101 / 100; E 64,
-    // H 4096, I 1024, 60 rows 166 / 161, 73 rows 179 / 169, 192 rows 341 / 296; E 16, H 2048, I 1024, 1024 rows 191 / 176)
+    // KEEP: from 64 rows an expert some have several tiles, and the caches keep the weights for the others (us,
+    // streamed / kept, MXFP8: E 64, H 2048, I 768, 50 rows an expert 71 / 75, 75 rows 80 / 83, 100 rows 101 / 100;
+    // E 64, H 4096, I 1024, 60 rows 166 / 161, 73 rows 179 / 169, 192 rows 341 / 296; E 16, H 2048, I 1024, 1024 rows
+    // 191 / 176)
     const bool keep = P >= static_cast<int64_t>(64) * E;
     const int64_t each = P / (kTall4 * E) + 1;                // about as many tiles an expert
-#define STREAM4_(KD, BM, R, KEEP, A4, A, AS, W, WS, Y, O, N)                                           \
-  hipLaunchKernelGGL((gemm_mx4s<KD, BM, R, KEEP, A4>), dim3(round_up((N) / (128 * (R)) * L.max_tiles, kXcds)), dim3(256), 0, \
-                     s, A, AS, W, WS, perm, tiles, n_tiles, counts, offsets, row_of, w, H, I, k, P, hq, hs, Y, O, order_key())
-#define STREAM4R(KD, BM, R, KEEP, A, AS, W, WS, Y, O, N)                                               \
+#define STREAM4_(KD, BM, R, KEEP, A4, A, AS, W, WS, Y, O, N)                                     \
+  hipLaunchKernelGGL((gemm_mx4s<KD, BM, R, KEEP, A4>), dim3(round_up((N) / (128 * (R)) * L.max_tiles, kXcds)), \
+                     dim3(256), 0, s, A, AS, W, WS, perm, tiles, n_tiles, counts, offsets, row_of, w, H, I, k, P, \
+                     hq, hs, Y, O, order_key())
+#define STREAM4R(KD, BM, R, KEEP, A, AS, W, WS, Y, O, N)                                         \
   do {                                                                                           \
-    if (a4) STREAM4_(KD, BM, R, KEEP, true, A, AS, W, WS, Y, O, N);                                    \
-    else STREAM4_(KD, BM, R, KEEP, false, A, AS, W, WS, Y, O, N);                                      \
+    if (a4) STREAM4_(KD, BM, R, KEEP, true, A, AS, W, WS, Y, O, N);                              \
+    else STREAM4_(KD, BM, R, KEEP, false, A, AS, W, WS, Y, O, N);                                \
   } while (0)
 #define STREAM4(KD, A, AS, W, WS, Y, O, N)                                                       \
   do {                                                                                           \
-    if (L.bm == kShort4) STREAM4R(KD, kShort4, 1, false, A, AS, W, WS, Y, O, N);                        \
-    else if (each * E * ((N) / 256) <= 128) STREAM4R(KD, kTall4, 1, false, A, AS, W, WS, Y, O, N);          \
+    if (L.bm == kShort4) STREAM4R(KD, kShort4, 1, false, A, AS, W, WS, Y, O, N);                 \
+    else if (each * E * ((N) / 256) <= 128) STREAM4R(KD, kTall4, 1, false, A, AS, W, WS, Y, O, N); \
     else if (keep) STREAM4R(KD, kTall4, 2, true, A, AS, W, WS, Y, O, N);                         \
     else STREAM4R(KD, kTall4, 2, false, A, AS, W, WS, Y, O, N);                                  \
   } while (0)
