@@ -382,19 +382,27 @@ __global__ __launch_bounds__(kRowWaves * kWave) void balance_backward_rows(
   const int s = wg / chunks, c = wg - s * chunks;
   const int lane = lane_id();
   const int wv = __builtin_amdgcn_readfirstlane(wave_id());
-  float up[NV];
+  // sum p = 1, so a number taken from every count changes nothing: less their mean (over the experts that
+  // have any), level counts are exactly 0, and the rounding of up - dot goes by how far they lie apart
+  int cnt[NV], live = 0;
   long long total = 0, n = 0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = expert_of<V>(i), v = e < E ? counts[static_cast<size_t>(s) * E + e] : 0;
-    up[i] = static_cast<float>(v);
-    total += v;
+    const int e = expert_of<V>(i);
+    cnt[i] = e < E ? counts[static_cast<size_t>(s) * E + e] : 0;
+    total += cnt[i];
+    live += cnt[i] > 0;
   }
   for (int i = lane; i < S; i += 64) n += tokens[i];
   for (int m = 32; m >= 1; m >>= 1) {
     total += __shfl_xor(total, m, kWave);
     n += __shfl_xor(n, m, kWave);
+    live += __shfl_xor(live, m, kWave);
   }
+  const int mid = live > 0 ? static_cast<int>(static_cast<double>(total) / live) : 0;
+  float up[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) up[i] = static_cast<float>(cnt[i] - mid);
   const int ns = tokens[s];
   const float c0 = total > 0 && ns > 0
       ? static_cast<float>(static_cast<double>(d_losses[0]) * E / (static_cast<double>(S) * ns * static_cast<double>(total))) : 0.f;
