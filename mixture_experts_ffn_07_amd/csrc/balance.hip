@@ -438,13 +438,13 @@ __global__ __launch_bounds__(kRowWaves * kWave) void balance_backward_rows(
     for (int j = 0; j < R; ++j) {
       if (r + j >= r_end) break;
       float* row = dlogits + (static_cast<size_t>(s) * len + r + j) * E;
-      const float cz = c1 * lse[j];
       float d[NV];
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         float g = c0 * p[j][i] * (up[i] - dot[j]);
         if (SIG) g *= slope[j][SIG ? i : 0];
-        d[i] = fmaf(cz, q[j][i], g) + add[j][i];
+        // (lse q first: c1 lse may pass the range, and times a q of 0 would be NaN)
+        d[i] = fmaf(c1, lse[j] * q[j][i], g) + add[j][i];
       }
 #pragma unroll
       for (int i = 0; i < NV; i += V) {
