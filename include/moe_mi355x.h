@@ -581,7 +581,8 @@ size_t moe_experts_mxfp4_workspace_bytes(int T, int H, int I, int E, int k, moe_
  *   tokens     [n_seqs] int32 out: N_s
  *   workspace  >= moe_balance_loss_workspace_bytes(T, E, n_seqs), contents ignored
  * Scores are FP32: a few units in the last place, and 2^-25 |logit - largest| beside that from
- * the logits' difference.  Sums within a workgroup are FP32, over workgroups FP64.
+ * the logits' difference.  Sums of p within a workgroup are FP32, over workgroups FP64; those of
+ * lse^2 are FP64 throughout.
  * Limits: 0 <= T < 2^22, 1 <= n_seqs <= 4096 and a divisor of T, E <= 1024, 1 <= k <=
  * min(E, 32).  T = 0 writes zeros.
  */

@@ -168,7 +168,7 @@ BalanceWs balance_ws_layout(int T, int E, int S) {
   L.share = o;   o = align256(o + sizeof(BalanceShare) * S * ((E + 63) / 64));
   L.probs = o;   o = align256(o + sizeof(float) * n * E);
   L.counts = o;  o = align256(o + sizeof(int) * n * E);
-  L.z = o;       o = align256(o + sizeof(float) * n);
+  L.z = o;       o = align256(o + sizeof(double) * n);
   L.tokens = o;  o = align256(o + sizeof(int) * n);
   L.total = o;
   return L;
@@ -184,11 +184,11 @@ template <bool SIG, int V, int NV>
 __global__ __launch_bounds__(kRowWaves * kWave) void balance_rows(
     const float* __restrict__ logits, const int32_t* __restrict__ idx, const uint8_t* __restrict__ mask,
     int E, int k, int len, int chunks, int rows, float* __restrict__ pp, int* __restrict__ pc,
-     float* __restrict__ pz, int* __restrict__ pn, uint32_t okey) {
+    double* __restrict__ pz, int* __restrict__ pn, uint32_t okey) {
   constexpr int R = rows_at_once(NV);
   __shared__ float s_p[kRowWaves][NV * 64];
   __shared__ int s_c[NV * 64];
-  __shared__ float s_z[kRowWaves];
+  __shared__ double s_z[kRowWaves];
   __shared__ int s_n[kRowWaves];
   const int wg = permute_item(blockIdx.x, gridDim.x, okey);
   const int s = wg / chunks, c = wg - s * chunks;
@@ -196,7 +196,8 @@ __global__ __launch_bounds__(kRowWaves * kWave) void balance_rows(
   const int wv = __builtin_amdgcn_readfirstlane(wave_id());
   for (int i = tid; i < NV * 64; i += kRowWaves * kWave) s_c[i] = 0;
   __syncthreads();
-  float acc[NV], z = 0.f;
+  float acc[NV];
+  double z = 0.0;                                         // (squares whose sum may pass FP32's range)
   int n = 0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) acc[i] = 0.f;
@@ -224,7 +225,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void balance_rows(
     for (int j = 0; j < R; ++j) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) acc[i] += p[j][i];
-      z = fmaf(lse[j], lse[j], z);
+      z = fma(static_cast<double>(lse[j]), static_cast<double>(lse[j]), z);
       n += on[j];
     }
   }
@@ -243,7 +244,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void balance_rows(
     pc[static_cast<size_t>(wg) * E + e] = s_c[e];
   }
   if (tid == 0) {
-    float v = s_z[0];
+    double v = s_z[0];
     int m = s_n[0];
     for (int w = 1; w < kRowWaves; ++w) {
       v += s_z[w];
@@ -257,7 +258,7 @@ __global__ __launch_bounds__(kRowWaves * kWave) void balance_rows(
 // Joins the chunks: workgroup = (sequence, 64 experts), sixteen strips of chunks, in FP64, with the
 // share of its experts in sum c P and sum c (and the sequence's sum of lse^2 and its tokens).
 __global__ __launch_bounds__(1024) void balance_join(const float* __restrict__ pp, const int* __restrict__ pc,
-                                                     const float* __restrict__ pz, const int* __restrict__ pn,
+                                                     const double* __restrict__ pz, const int* __restrict__ pn,
                                                      int E, int chunks, BalanceShare* __restrict__ share,
                                                      float* __restrict__ probs, int* __restrict__ counts,
                                                      int* __restrict__ tokens) {
@@ -485,7 +486,7 @@ hipError_t launch_balance_loss(const float* logits, const int32_t* idx, const ui
   BalanceShare* share = reinterpret_cast<BalanceShare*>(b + L.share);
   float* pp = reinterpret_cast<float*>(b + L.probs);
   int* pc = reinterpret_cast<int*>(b + L.counts);
-  float* pz = reinterpret_cast<float*>(b + L.z);
+  double* pz = reinterpret_cast<double*>(b + L.z);
   int* pn = reinterpret_cast<int*>(b + L.tokens);
   prof_begin(kBalance, s);
 #define ROWS(V, NV)                                                                                        \
