@@ -24,7 +24,9 @@ constexpr int kShort4 = 32, kTall4 = 96;                 // rows (routed pairs) 
 inline size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 inline int round_up(int v, int m) { return (v + m - 1) / m * m; }
 
-// silu(g) u on the hardware's reciprocal, one unit in the last place off.
+// silu(g) u on the hardware's exponential and reciprocal, one unit in the last place each; the
+// exponential's argument is rounded before it, which moves it by about |g| 2^-24 of it.  A code of a
+// keeps 2^-2 or 2^-4 of it, so this shows only next to the border of two codes.
 __device__ __forceinline__ float swiglu4(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
