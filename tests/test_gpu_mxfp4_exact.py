@@ -13,6 +13,11 @@ from tests.test_gpu_mxfp4 import SIZES, M, _f64, Lazy, call, make, part_of, refe
 pytestmark = pytest.mark.gpu
 
 
+# The longest reductions of either product, with few pairs, on 32- and 96-row tiles; many slots
+LONG = [(1, 16384, 256, 4, 1), (1, 256, 16384, 4, 2), (3, 16384, 512, 64, 2), (1, 7168, 2048, 40, 8), (3, 4096, 14336, 2, 1),
+        (70, 16384, 256, 2, 1), (70, 256, 16384, 2, 2), (40, 7168, 2048, 3, 2), (9, 512, 256, 64, 32), (300, 512, 256, 40, 32)]
+
+
 def make_runs(M, T, H, I, E, k, seed, **kw):  # noqa: F811
     d = make(M, T, H, I, E, k, False, seed=seed, **kw)
     rng = np.random.default_rng(seed)
@@ -32,11 +37,20 @@ def check_runs(d, out, rows=slice(None)):
     assert np.all(np.isfinite(got)) and np.all(over <= 0), f"{over.max():.3e} over, |ref| {np.abs(ref).max():.3e}"
 
 
-@pytest.mark.parametrize("T,H,I,E,k", SIZES + [(3, 4096, 14336, 2, 1), (70, 16384, 256, 2, 1), (70, 256, 16384, 2, 2), (40, 7168, 2048, 3, 2)])
+@pytest.mark.parametrize("T,H,I,E,k", SIZES + LONG)
 def test_exact_runs(M, T, H, I, E, k):  # noqa: F811
     print(f"[mxfp4 runs] T={T} H={H} I={I} E={E} k={k}", flush=True)
     d = make_runs(M, T, H, I, E, k, seed=T + H)
     check_runs(d, call(M, d))
+
+
+@pytest.mark.parametrize("T,H,I", [(16500, 16384, 256), (1500, 256, 16384)])
+def test_exact_runs_on_large_tiles_and_the_longest_reductions(M, T, H, I):  # noqa: F811
+    print(f"[mxfp4 runs] large T={T} H={H} I={I}", flush=True)
+    d = make_runs(M, T, H, I, 1, 1, seed=T)
+    out = call(M, d)
+    for rows in (slice(0, 40), slice(T - 40, T)):
+        check_runs(d, out, rows)
 
 
 @pytest.mark.parametrize("T,H,I,E,k", [(6, 512, 256, 4, 2), (200, 512, 256, 8, 3), (900, 512, 256, 3, 1), (2400, 2048, 2048, 3, 1),
