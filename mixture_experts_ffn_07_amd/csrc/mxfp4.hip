@@ -449,7 +449,7 @@ template <bool A4>
 constexpr size_t large4_lds() {
   return A4 ? 2 * 2 * kLTile : 2 * (kLTile + kLTile / 2);
 }
-constexpr size_t kLSide = 3 * sizeof(int) * kLargeBM;    // (down: the rows' pair ids and weights)
+constexpr size_t kLSide = 2 * sizeof(int) * kLargeBM;    // (down: the rows' pair ids and weights)
 
 // 32x32x64 with weights w (E2M1) and activations x (E2M1 or E4M3); XW: the activation rows
 // along the result's registers and the weight rows along its lanes, else the other way.
