@@ -530,7 +530,8 @@ int moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t ro
  * Sums in FP32, out rounded once to BF16.  (With MXFP8 activations the matrix instruction
  * adds eight neighbours along H or I at a time, dropping what lies below 2^-13 of the largest
  * of their products: up to 2^-10.2 of it.  An activation that this moves past the border of
- * two codes takes the other code.  With MXFP4 ones the sums are exact to FP32.)
+ * two codes takes the other code.  With MXFP4 ones the sums are exact to FP32, and so are the
+ * gate/up sums of MXFP8 ones where T k is below 18 E.)
  * silu is off by about (|g| + 4) 2^-24 of it; below -87 (where it is above -1.5e-36) it may be 0.
  *
  *   x         xtype MOE_MXFP8: [T, H] E4M3 codes (moe_quantize_mxfp8, moe_add_rmsnorm);

@@ -133,7 +133,8 @@ Mx4Ws mx4_ws_layout(int T, int H, int I, int E, int k, bool a4) {
   //   H 4096 I 14336 E 8 k 2, MXFP8: 16 rows 169 / 184, 32 rows 264 / 195
   //   H 7168 I 2048, MXFP8: E 32 k 4, 6 rows 151 / 156, 12 rows 174 / 163, 19 rows 193 / 167; E 6 k 1, 21 rows
   //     51 / 56
-  // (64-row ones lie within 8 % of the better of the two, on both sides, from 16 to 75 rows; 128-row ones leave
+  // (The 32-row figures with MXFP8 activations are from before its gate/up sums were exact: now 2 to 4 % more.
+  // 64-row ones lie within 8 % of the better of the two, on both sides, from 16 to 75 rows; 128-row ones leave
   // registers for half as many weight rows a wave: E 64, 73 rows 171; 188, E 16, 1024 rows 179; 215.)
   const bool large = P >= 192 * static_cast<size_t>(E) && P * H * I >= (size_t(3) << 30) * E &&
                      P / kLargeBM * (I / 128) >= 128;
@@ -204,6 +205,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM == kShor
   constexpr int LPT = BM * CH / NT;                       // 16-byte code loads per thread
   constexpr int SS = 8 * CPS;                             // scale bytes of a row per stage
   constexpr int BD = 2;                                   // activation operands held
+  // gate/up sums of E4M3 activations exact to FP32 (split_e4m3: twice the products), so that no activation
+  // takes the other of two codes: where a token's output rests on few of them and the weights' bytes leave
+  // the matrix cores room (16 rows an expert, H 2048 I 768 E 128: 85.6 -> 89.0 us; 64 tokens, 8 experts of
+  // 4096 x 14336 168 -> 172).  The taller tiles have none (777 tokens 172 -> 256, 4095 179 -> 246; with
+  // R = 1, E 6, 256 tokens 64 -> 98).
+  constexpr bool EXACT = GU && !A4 && BM == kShort4;
   __shared__ __align__(16) uint8_t xl[2][BM * RS];
   __shared__ __align__(16) uint8_t sl[2][BM * SS];
   __shared__ __align__(16) i32x4 wtl[NW][16 * 8];         // per wave: [16 rows][8 pieces]
@@ -331,12 +338,26 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM == kShor
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         if (2 * g + j + BD - 1 < 2 * G) rdb(2 * g + j + BD - 1);
-        const i32x8& x = b[(2 * g + j) % BD];
+        i32x8 x = b[(2 * g + j) % BD], high;
+        if (EXACT)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            int lo, hi;
+            split_e4m3(x[i], lo, hi);
+            x[i] = lo;
+            high[i] = hi;
+          }
 #pragma unroll
         for (int m = 0; m < 2 * R; ++m) {
           if (j == 0) acc[m][g] = mfma_mx4_16<A4, 0>(a[2 * m], x, sa[m], sx[g], acc[m][g]);
           else acc[m][g] = mfma_mx4_16<A4, 1>(a[2 * m + 1], x, sa[m], sx[g], acc[m][g]);
         }
+        if (EXACT)
+#pragma unroll
+          for (int m = 0; m < 2 * R; ++m) {
+            if (j == 0) acc[m][g] = mfma_mx4_16<A4, 0>(a[2 * m], high, sa[m], sx[g], acc[m][g]);
+            else acc[m][g] = mfma_mx4_16<A4, 1>(a[2 * m + 1], high, sa[m], sx[g], acc[m][g]);
+          }
         // (kept at their place: sunk to the end of the stage they would hold every operand live)
 #pragma unroll
         for (int m = 0; m < 2 * R; ++m) asm volatile("" : "+v"(acc[m][g]));
@@ -990,12 +1011,13 @@ hipError_t mx4_set_attributes() {
 // ---------------------------------------------------------------------------
 // Few pairs (a decode step): two launches, every routed pair on its own, its weights straight
 // from HBM into the operands of the 16x16x128 MFMA, whose 16 activation columns all hold the
-// pair's one row.  Blocks, chunks and products follow in the streaming form's order, so a
-// pair has the bits that it has there.  The step is bound by the latency of two dependent
-// passes over memory and needs no grouping; pairs that share an expert read its weights from
-// the L2 the second time.  One token, 8 of 128 experts, H 2048, I 768: 20 MB of weights in
-// 5.0 + 5.3 us of kernels, 12 us a call (grouped and streamed 21); 8 of 384 experts, H 7168,
-// I 2048: 187 MB in 44 us, 4.3 TB/s.
+// pair's one row.  Blocks, chunks and products follow in the order of the streaming form's 32-row
+// tiles, gate/up sums of E4M3 activations in two parts too (one token, 8 of 128 experts 10.6 ->
+// 11.0 us), so a pair has the bits that it has there.  The step is bound by the latency of two
+// dependent passes over memory and needs no grouping; pairs that share an expert read its weights
+// from the L2 the second time.  One token, 8 of 128 experts, H 2048, I 768: 20 MB of weights in
+// 6.6 + 5.4 us of kernels, 13 us a call (grouped and streamed 21); 8 of 384 experts, H 7168,
+// I 2048: 187 MB in 45 us, 4.1 TB/s.
 namespace {
 // 16 (ROWS 8: 8, each twice) weight rows on their way into operands: U chunks of 256 positions,
 // loaded as 8 rows x 128 contiguous bytes (lane = row ln >> 3, piece ln & 7) and passed through
@@ -1017,28 +1039,34 @@ struct PairRows {
         sa[u] = *reinterpret_cast<const uint16_t*>(ws + static_cast<uint32_t>(row * KB) + 8 * (c0 + u) + 2 * grp);
       }
   }
-  // times one activation row (x, xs: its codes and scales in global memory or LDS), added to acc:
-  // register i of lane (c, g) holds row 4 g + i
+  // times one activation row (x, xs: its codes and scales in global memory or LDS; high > 0: the codes of
+  // 2 and above lie that far behind x, split_e4m3), added to acc: register i of lane (c, g) holds row 4 g + i
   __device__ __forceinline__ f32x4 times(const uint8_t* x, const uint8_t* xs, int c0, int nchunk, i32x4* tile,
-                                         f32x4 acc) {
+                                         f32x4 acc, int high = 0) {
     const int ln = lane_id(), lr = ln >> 3, lc = ln & 7, row = ln & (ROWS - 1) & 15, grp = ln >> 4;
 #pragma unroll
     for (int u = 0; u < U; ++u)
       if (c0 + u < nchunk) {
         const uint8_t* p = x + (A4 ? 128 * (c0 + u) + 32 * grp : 256 * (c0 + u) + 64 * (grp >> 1) + 16 * (grp & 1));
         const int sx = *reinterpret_cast<const uint16_t*>(xs + 8 * (c0 + u) + 2 * grp);
-        i32x8 b[2];
+        i32x8 b[2], h[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2; ++j) {
           b[j] = cat8(*reinterpret_cast<const i32x4*>(p + (A4 ? 16 : 32) * j),
                       A4 ? i32x4{0, 0, 0, 0} : *reinterpret_cast<const i32x4*>(p + 128 + 32 * j));
+          if (high)
+            h[j] = cat8(*reinterpret_cast<const i32x4*>(p + high + 32 * j),
+                        *reinterpret_cast<const i32x4*>(p + high + 128 + 32 * j));
+        }
 #pragma unroll
         for (int i = 0; i < L; ++i) tile[(lr + 8 * i) * 8 + (lc ^ lr)] = a[u][i];
         __builtin_amdgcn_wave_barrier();
         const i32x4 a0 = tile[row * 8 + ((2 * grp) ^ (row & 7))], a1 = tile[row * 8 + ((2 * grp + 1) ^ (row & 7))];
         __builtin_amdgcn_wave_barrier();
         acc = mfma_mx4_16<A4, 0>(a0, b[0], sa[u], sx, acc);
+        if (high) acc = mfma_mx4_16<A4, 0>(a0, h[0], sa[u], sx, acc);
         acc = mfma_mx4_16<A4, 1>(a1, b[1], sa[u], sx, acc);
+        if (high) acc = mfma_mx4_16<A4, 1>(a1, h[1], sa[u], sx, acc);
       }
     return acc;
   }
@@ -1070,10 +1098,12 @@ __global__ __launch_bounds__(256) void pairs_gate_up_mx4(
     const uint8_t* __restrict__ x, const uint8_t* __restrict__ xs, const uint8_t* __restrict__ wgu,
     const uint8_t* __restrict__ wgus, const int32_t* __restrict__ idx, int H, int I, int E, int k, int P,
     uint8_t* __restrict__ hq, uint8_t* __restrict__ hs, uint32_t okey) {
-  extern __shared__ __align__(16) uint8_t ldp[];         // the token's codes, then its scales
+  extern __shared__ __align__(16) uint8_t ldp[];         // the token's codes (MXFP8: low, high), then its scales
   __shared__ __align__(16) float s_v[2][32];
   __shared__ __align__(16) i32x4 s_tile[4][16 * 8];
   const int nblk = I / 32, AB = A4 ? H / 2 : H, KB = H / 32;
+  const int high = A4 ? 0 : AB;
+  uint8_t* lds = ldp + AB + high;
   const int item = permute_item(blockIdx.x, nblk * P, okey);
   const int p = item / nblk, n0 = (item - p * nblk) * 32;
   const int e = idx[p];
@@ -1087,14 +1117,27 @@ __global__ __launch_bounds__(256) void pairs_gate_up_mx4(
   PairRows<A4, 16, U> r;
   r.request(wr, wsr, H / 2, KB, 0, nchunk);              // on their way while the token is staged
   __builtin_amdgcn_sched_barrier(0);
-  for (int c = 16 * tid; c < AB; c += 16 * 256) st16(ldp + c, ld16(x + static_cast<size_t>(t) * AB + c));
+  for (int c = 16 * tid; c < AB; c += 16 * 256) {
+    i32x4 v = ld16(x + static_cast<size_t>(t) * AB + c), hi;
+    if (!A4) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        int l, h;
+        split_e4m3(v[i], l, h);
+        v[i] = l;
+        hi[i] = h;
+      }
+      st16(ldp + AB + c, hi);
+    }
+    st16(ldp + c, v);
+  }
   for (int c = 8 * tid; c < KB; c += 8 * 256)
-    *reinterpret_cast<uint2*>(ldp + AB + c) = *reinterpret_cast<const uint2*>(xs + static_cast<size_t>(t) * KB + c);
+    *reinterpret_cast<uint2*>(lds + c) = *reinterpret_cast<const uint2*>(xs + static_cast<size_t>(t) * KB + c);
   __syncthreads();
   f32x4 d = {0.f, 0.f, 0.f, 0.f};
   for (int c0 = 0; c0 < nchunk; c0 += U) {
     if (c0) r.request(wr, wsr, H / 2, KB, c0, nchunk);
-    d = r.times(ldp, ldp + AB, c0, nchunk, s_tile[wv], d);
+    d = r.times(ldp, lds, c0, nchunk, s_tile[wv], d, high);
   }
   if (col == 0) *reinterpret_cast<f32x4*>(&s_v[wv >> 1][(wv & 1) * 16 + 4 * grp]) = d;
   __syncthreads();
@@ -1215,7 +1258,7 @@ hipError_t launch_experts_mx4(const uint8_t* x, const uint8_t* xs, bool a4, cons
 #define PAIRS4(A4)                                                                                \
   do {                                                                                            \
     prof_begin(kMx4GateUp, s);                                                                    \
-    hipLaunchKernelGGL(pairs_gate_up_mx4<A4>, dim3(I / 32 * P), dim3(256), (A4 ? H / 2 : H) + H / 32, s, x, xs, \
+    hipLaunchKernelGGL(pairs_gate_up_mx4<A4>, dim3(I / 32 * P), dim3(256), (A4 ? H / 2 : 2 * H) + H / 32, s, x, xs, \
                        wgu, wgus, idx, H, I, E, k, P, hq, hs, order_key());                       \
     prof_end(kMx4GateUp, s);                                                                      \
     prof_begin(kMx4Down, s);                                                                      \
