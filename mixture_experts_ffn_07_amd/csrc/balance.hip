@@ -176,10 +176,11 @@ BalanceWs balance_ws_layout(int T, int E, int S) {
 
 // Workgroup = a chunk of a sequence's rows, R rows at a time to each wave; its sums of p, its
 // counts, its sum of lse^2 and its tokens go to the workspace, to be joined in chunk order.
-// 2048 x 384 sigmoid: 5.5 us, the latency of one pass.  32768 x 256 softmax, k 8: 13.3 us for 35 MB,
-// 2.6 TB/s, bound by vector instructions (an exponential, a product and a sum for each score, their
-// reductions, and the pairs' counters in LDS).  With one row at a time to a wave the calls took 59
-// and 30 us, now 13 to 15 and 18.
+// 2048 x 384 sigmoid: 5.6 us, the latency of one pass.  32768 x 256 softmax, k 8: 13.3 to 13.9 us for
+// 35 MB, 2.6 TB/s: the vector units issue in 69 % of the CUs' busy cycles (556 instructions a wave:
+// an exponential, a product and a sum for each score, reductions, the pairs' counters), and the rest
+// is the latency of the one step of four rows that a wave has, 47 % of its time.  With one row at a
+// time to a wave the calls took 59 and 30 us, now 14 to 16 and 18.5.
 template <bool SIG, int V, int NV>
 __global__ __launch_bounds__(kRowWaves * kWave) void balance_rows(
     const float* __restrict__ logits, const int32_t* __restrict__ idx, const uint8_t* __restrict__ mask,
@@ -330,7 +331,7 @@ __global__ __launch_bounds__(1024) void balance_join(const float* __restrict__ p
 }
 
 // Both losses, from the shares: one workgroup.  (As the end of the join's last workgroup, found by
-// a counter, they took 9.2 us together where these two launches take 7: its fence writes the caches
+// a counter, they took 9.2 us together where these two launches take 6.2 to 7.4: its fence writes the caches
 // back.)
 __global__ __launch_bounds__(256) void balance_losses(const BalanceShare* __restrict__ share, int E, int S,
                                                       int blocks, float* __restrict__ losses) {
@@ -372,7 +373,7 @@ __global__ __launch_bounds__(256) void balance_losses(const BalanceShare* __rest
 
 // Gradient: workgroup = a chunk of a sequence's rows, R rows at a time to each wave; the
 // sequence's counts and the sum of tokens are read once.  32768 x 256, added to a given gradient:
-// 101 MB in 20-22 us, 4.6-5.1 TB/s, bound by memory; 2048 x 384 6.8 us, a launch and one pass.
+// 101 MB in 20-22 us, 4.6-5.1 TB/s, bound by memory; 2048 x 384 7.1 us, a launch and one pass.
 template <bool SIG, int V, int NV>
 __global__ __launch_bounds__(kRowWaves * kWave) void balance_backward_rows(
     const float* __restrict__ logits, const uint8_t* __restrict__ mask, const int* __restrict__ counts,

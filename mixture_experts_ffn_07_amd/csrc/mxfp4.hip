@@ -179,13 +179,16 @@ enum { kGateUp4 = 0, kDown4 = 1, kDownFused4 = 2 };
 // the CU's other workgroups cover what that does not.  Rows past the tile's end load the
 // tile's first row; their columns are computed and discarded.
 //
-// 32-row tiles are bound by the weights' bytes: R = 1, 100-106 registers, four workgroups a
-// CU (8 experts of 4096 x 14336, 64 tokens: 748 MB in 160-169 us, 4.4-4.7 TB/s; 8 waves a
-// workgroup 196, R = 2 198).  96-row tiles are bound by LDS, where every wave reads the whole
-// stage: R = 2 halves that per product, 246-252 registers, two workgroups a CU (E 16, 4095
-// tokens, MXFP8: 215 us with R = 1 and 8 waves, 191 with R = 2, 176 with KEEP, 1.17 PFLOP/s of
-// the whole call).  A second chunk and stage in flight cost the second workgroup and 4 %; stages
-// of 128 bytes, twice the barriers, 2-10 %; weights loaded straight to LDS, 3-9 %.
+// 32-row tiles are bound by the weights' bytes: R = 1, 100-106 registers (gate/up with E4M3
+// activations 126), four workgroups a CU (8 experts of 4096 x 14336, 64 tokens: 748 MB in
+// 160-169 us, 4.4-4.7 TB/s, 172 with exact sums; 8 waves a workgroup 196, R = 2 198).  96-row
+// tiles fill no unit (E 16, 4095 tokens, MXFP8, gate/up and down: matrix cores busy 40 and 29 %
+// of the CUs' cycles, LDS 42 and 29, a third of that bank conflicts; a wave waits for memory or a
+// barrier a fifth of its time and stands behind instructions issued before for half of it).  Every
+// wave reads the whole stage from LDS: R = 2 halves that per product, 246-252 registers, two
+// workgroups a CU (the same call: 215 us with R = 1 and 8 waves, 191 with R = 2, 176 to 180 with
+// KEEP, 1.15 PFLOP/s).  A second chunk and stage in flight cost the second workgroup and 4 %;
+// stages of 128 bytes, twice the barriers, 2-10 %; weights loaded straight to LDS, 3-9 %.
 template <int KIND, int BM, int R, bool KEEP, bool A4>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(BM == kShort4 ? 4 : 2, 8))) void gemm_mx4s(
     const uint8_t* __restrict__ act, const uint8_t* __restrict__ acts,
@@ -1016,7 +1019,7 @@ hipError_t mx4_set_attributes() {
 // 11.0 us), so a pair has the bits that it has there.  The step is bound by the latency of two
 // dependent passes over memory and needs no grouping; pairs that share an expert read its weights
 // from the L2 the second time.  One token, 8 of 128 experts, H 2048, I 768: 20 MB of weights in
-// 6.6 + 5.4 us of kernels, 13 us a call (grouped and streamed 21); 8 of 384 experts, H 7168,
+// 6.8 + 5.2 us of kernels, 12.3 us a call (grouped and streamed 21); 8 of 384 experts, H 7168,
 // I 2048: 187 MB in 45 us, 4.1 TB/s.
 namespace {
 // 16 (ROWS 8: 8, each twice) weight rows on their way into operands: U chunks of 256 positions,
