@@ -602,8 +602,8 @@ size_t moe_balance_loss_workspace_bytes(int T, int E, int n_seqs);
  *   dlogits[t, e] = d_add[t, e] + d_losses[0] / (n_seqs * N_s) * p_e * (f_e - sum_m p_m f_m) *
  *                   (MOE_SCORE_SIGMOID: 1 - sigma(l_e)) + d_losses[1] * 2 lse_t / N * exp(l_e - lse_t)
  * A masked expert and a token that takes no part get d_add alone.  The counts are taken less their
- * mean: rounding goes by how far they lie apart, and where all experts that are not masked have the
- * same count only the second loss's part and d_add are left, exactly.
+ * mean: rounding goes by how far they lie apart, and where all experts have the same count (those
+ * masked for every token, none) only the second loss's part and d_add are left, exactly.
  *
  *   logits, token_mask  as given to moe_balance_loss
  *   counts, tokens      as returned by it, or their sums over several GPUs (the loss of the
